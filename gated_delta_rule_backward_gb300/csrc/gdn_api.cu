@@ -591,11 +591,16 @@ int gdn_backward_launches(const gdn_params_t* p)
 
 gdn_status_t gdn_device_status(void* stream)
 {
-    int a = 0, b = 0;
+    int a = 0, b = 0, c = 0;
     int e = gdn::tc_take_status(stream, &a);
     if (!e) e = gdn::tc_grad_take_status(stream, &b);
+    if (!e) e = gdn::decode_take_status(stream, &c);
     if (e) return cuda_status(e, "device status");
-    if (!a && !b) return GDN_OK;
+    if (!a && !b && !c) return GDN_OK;
+    if (!a && !b)
+        return fail(GDN_ERR_INVALID_ARG, "%s%s%s met a slot outside the pool%s; what it named was skipped",
+                    c & 1 ? "gdn_decode" : "", c == 3 ? " and " : "", c & 2 ? "gdn_states_move" : "",
+                    c & 1 ? " or a bad cu_tokens" : "");
     // chain status word: 6 | kernel << 4 | wait-site bits << 8 (gdn_tc_chain.cu)
     static const char* const kernels[] = {"?", "state chain", "?", "dM chain", "selftest"};
     const int ker = (a >> 4) & 15;

@@ -1,0 +1,476 @@
+// gdn_decode.cu -- the gated delta rule's serving form (include/gdn_decode.h): the recurrence
+// over a pool of states, a few tokens a sequence.
+//
+// Mathematics.  Only rows of the state meet the tokens, M[j] . k and M[j] . q, so every row of a
+// state goes its own way: a warp takes 4 RT rows, keeps them in registers over the sequence's tokens, and
+// reads and writes them once.  Both dots are taken of the state before the token, u = M k, o = M q, and
+//     delta = beta (v - a u),   y = scale (a o + delta (k . q)),   M <- a M + delta k^T
+// so that one pass over the row and one exchange between lanes serve a token (the KDA gate puts
+// its a into k and q: M (a k), M (a q)).
+//
+// What bounds it: the states' bytes, 8 S_k S_v a head against 7 S_k S_v flops a token.  So the
+// layout follows the reads: 8 lanes a row, each with float4 blocks 32 columns apart (whole 128-byte
+// lines), 4 rows across the warp, all of a warp's state in flight before its first use.  No shared
+// memory and no barrier: the warps of a head read the same q, k and gates from L1.
+#include <climits>
+#include <cstdio>
+
+#include "../../include/gdn_decode.h"
+#include "gdn_device.cuh"
+#include "gdn_elem.cuh"
+
+namespace gdn {
+namespace {
+
+// Bit 0: gdn_decode met a bad slot or token range; bit 1: gdn_states_move a bad slot.
+__device__ int g_decode_status;
+
+typedef unsigned long long f2;  // two fp32 in one 64-bit register, the operand of the packed fp32 pipe
+
+__device__ __forceinline__ f2 pack2(float x, float y)
+{
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 x)
+{
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+    return a + b;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+struct DecodeArgs {
+    const void *q, *k, *v, *g, *beta;
+    const int* cu;
+    float* pool;
+    const int *slot_in, *slot_out;
+    void* y;
+    long long slot_stride, qs0, qs1, ks0, ks1, vs0, vs1;
+    int T, n_tok, n_slots, H_k, H_v, SK, SV;
+    int gate_dtype, y_dtype, vec;
+    unsigned warps;  // n_seq H_v S_v / rows of a warp
+    float scale;
+};
+
+// One token's operands as they arrive: a lane's blocks of q, k (and the KDA gate), one v, beta, g.
+template <typename T, int NV, bool KDA>
+struct Token {
+    Pack<T, 4> q[NV], k[NV];
+    float g[KDA ? NV : 1][KDA ? 4 : 1];
+    float v, beta;
+};
+
+template <typename T, int NV, bool KDA>
+__device__ __forceinline__ void load_token(Token<T, NV, KDA>& x, const DecodeArgs& A, long long row, int h, int j, int cl)
+{
+    const int hk = h % A.H_k;
+    const T* q = (const T*)A.q + row * A.qs0 + hk * A.qs1;
+    const T* k = (const T*)A.k + row * A.ks0 + hk * A.ks1;
+    const long long gh = row * A.H_v + h;
+#pragma unroll
+    for (int b = 0; b < NV; ++b) {
+        const int c = 32 * b + 4 * cl;
+        if (c < A.SK) {
+            x.k[b] = ld_pack<T, 4>(k + c, A.vec);
+            x.q[b] = ld_pack<T, 4>(q + c, A.vec);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x.k[b].x[i] = x.q[b].x[i] = from_f32<T>(0.f);
+        }
+    }
+    if (KDA) {
+#pragma unroll
+        for (int b = 0; b < NV; ++b) {
+            const int c = 32 * b + 4 * cl;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x.g[b][KDA ? i : 0] = c < A.SK ? ld_any(A.g, gh * A.SK + c + i, A.gate_dtype) : 0.f;
+        }
+    } else {
+        x.g[0][0] = ld_any(A.g, gh, A.gate_dtype);
+    }
+    x.beta = ld_any(A.beta, gh, A.gate_dtype);
+    x.v = to_f32(__ldg((const T*)A.v + row * A.vs0 + h * A.vs1 + j));
+}
+
+// RT: rows of a lane (4 RT a warp); NV: its float4 blocks of a row.
+template <typename T, int NV, int RT, bool KDA>
+__global__ void __launch_bounds__(128) gdn_decode_kernel(const DecodeArgs A)
+{
+    const unsigned w = blockIdx.x * 4u + (threadIdx.x >> 5);
+    if (w >= A.warps) return;
+    const int lane = threadIdx.x & 31, cl = lane & 7, grp = lane >> 3;
+    const unsigned per_head = A.SV / (4 * RT);
+    const unsigned nh = w / per_head;
+    const int row0 = (int)(w - nh * per_head) * 4 * RT;
+    const int n = nh / A.H_v, h = nh - n * A.H_v;
+
+    const int s_in = __ldg(A.slot_in + n), s_out = __ldg(A.slot_out + n);
+    long long lo, hi;
+    if (A.cu) {
+        lo = __ldg(A.cu + n);
+        hi = __ldg(A.cu + n + 1);
+    } else {
+        lo = (long long)n * A.T;
+        hi = lo + A.T;
+    }
+    if (s_in < -1 || s_in >= A.n_slots || s_out < -1 || s_out >= A.n_slots || lo < 0 || hi < lo || hi > A.n_tok) {
+        if (lane == 0) atomicOr(&g_decode_status, 1);
+        return;
+    }
+
+    // rows row0 + grp RT + r of the state, r < RT
+    const long long at = ((long long)h * A.SV + row0 + grp * RT) * A.SK;
+    f2 m[RT][NV][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int b = 0; b < NV; ++b) {
+            const int c = 32 * b + 4 * cl;
+            ulonglong2 x = make_ulonglong2(0, 0);
+            if (s_in >= 0 && c < A.SK)
+                x = *reinterpret_cast<const ulonglong2*>(A.pool + s_in * A.slot_stride + at + r * A.SK + c);
+            m[r][b][0] = x.x;
+            m[r][b][1] = x.y;
+        }
+
+    // After the exchange between a row's 8 lanes, lanes 0-3 hold u and lanes 4-7 o; row mine of the RT.
+    constexpr int kShare = 4 / RT;  // lanes that hold the same sum
+    const int mine = (cl & 3) / kShare;
+    const int j = row0 + grp * RT + mine;
+
+    Token<T, NV, KDA> x, nx;
+    if (lo < hi) load_token<T, NV, KDA>(x, A, lo, h, j, cl);
+    for (long long t = lo; t < hi; ++t) {
+        if (t + 1 < hi) load_token<T, NV, KDA>(nx, A, t + 1, h, j, cl);
+        f2 k[NV][2], q[NV][2], a[KDA ? NV : 1][2];
+        f2 kqs = 0;
+        float as = 1.f;
+#pragma unroll
+        for (int b = 0; b < NV; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                k[b][i] = pack2(x.k[b].get(2 * i), x.k[b].get(2 * i + 1));
+                q[b][i] = pack2(x.q[b].get(2 * i), x.q[b].get(2 * i + 1));
+                kqs = fma2(k[b][i], q[b][i], kqs);
+                if (KDA) a[KDA ? b : 0][i] = pack2(expf(x.g[KDA ? b : 0][KDA ? 2 * i : 0]), expf(x.g[KDA ? b : 0][KDA ? 2 * i + 1 : 0]));
+            }
+        if (!KDA) {
+            as = expf(x.g[0][0]);
+            a[0][0] = pack2(as, as);
+        }
+        const float kq = rowsum8(sum2(kqs));
+        float s[2 * RT];
+        {
+            f2 u2[RT], o2[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) u2[r] = o2[r] = 0;
+#pragma unroll
+            for (int b = 0; b < NV; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const f2 ka = KDA ? mul2(k[b][i], a[KDA ? b : 0][i]) : k[b][i];
+                    const f2 qa = KDA ? mul2(q[b][i], a[KDA ? b : 0][i]) : q[b][i];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        u2[r] = fma2(m[r][b][i], ka, u2[r]);
+                        o2[r] = fma2(m[r][b][i], qa, o2[r]);
+                    }
+                }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                s[r] = sum2(u2[r]);
+                s[RT + r] = sum2(o2[r]);
+            }
+        }
+        // reduce-scatter of the 2 RT sums over the 8 lanes, then a butterfly over the lanes that share one
+#pragma unroll
+        for (int n2 = RT, bit = 4; n2 >= 1; n2 >>= 1, bit >>= 1) {
+            const bool up = (cl & bit) != 0;
+#pragma unroll
+            for (int i = 0; i < n2; ++i) {
+                const float send = up ? s[i] : s[n2 + i], keep = up ? s[n2 + i] : s[i];
+                s[i] = keep + __shfl_xor_sync(kFull, send, bit);
+            }
+        }
+#pragma unroll
+        for (int bit = kShare / 2; bit >= 1; bit >>= 1) s[0] += __shfl_xor_sync(kFull, s[0], bit);
+        const float sum = KDA ? s[0] : as * s[0];
+        float delta = x.beta * (x.v - sum);  // on lanes 0-3
+        float d[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) d[r] = __shfl_sync(kFull, delta, (lane & 24) + r * kShare);
+        delta = __shfl_xor_sync(kFull, delta, 4);
+        if (cl >= 4 && (cl & (kShare - 1)) == 0)
+            st_any(A.y, (t * A.H_v + h) * A.SV + j, A.y_dtype, A.scale * fmaf(delta, kq, sum));
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const f2 dd = pack2(d[r], d[r]);
+#pragma unroll
+            for (int b = 0; b < NV; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    m[r][b][i] = fma2(k[b][i], dd, mul2(m[r][b][i], a[KDA ? b : 0][KDA ? i : 0]));
+        }
+        x = nx;
+    }
+
+    if (s_out < 0) return;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int b = 0; b < NV; ++b) {
+            const int c = 32 * b + 4 * cl;
+            if (c < A.SK)
+                *reinterpret_cast<ulonglong2*>(A.pool + s_out * A.slot_stride + at + r * A.SK + c) =
+                    make_ulonglong2(m[r][b][0], m[r][b][1]);
+        }
+}
+
+template <typename T, int NV, int RT>
+int launch_decode_g(DecodeArgs& A, long long heads, bool kda, cudaStream_t st)
+{
+    A.warps = (unsigned)(heads * (A.SV / (4 * RT)));
+    const unsigned ctas = (A.warps + 3) / 4;
+    if (kda) gdn_decode_kernel<T, NV, RT, true><<<ctas, 128, 0, st>>>(A);
+    else gdn_decode_kernel<T, NV, RT, false><<<ctas, 128, 0, st>>>(A);
+    return (int)cudaGetLastError();
+}
+
+template <typename T>
+int launch_decode_t(DecodeArgs& A, long long heads, bool kda, cudaStream_t st)
+{
+    // Few heads are spread over more warps of one row a lane; many take more rows a lane, so
+    // that a token's q and k serve them all.
+    const bool wide = heads * A.SV >= 16 * 4 * kNumSMs;
+    if (A.SK <= 32) return wide ? launch_decode_g<T, 1, 4>(A, heads, kda, st) : launch_decode_g<T, 1, 1>(A, heads, kda, st);
+    if (A.SK == 64) return wide ? launch_decode_g<T, 2, 4>(A, heads, kda, st) : launch_decode_g<T, 2, 1>(A, heads, kda, st);
+    if (A.SK == 128) return wide ? launch_decode_g<T, 4, 4>(A, heads, kda, st) : launch_decode_g<T, 4, 1>(A, heads, kda, st);
+    return wide ? launch_decode_g<T, 8, 2>(A, heads, kda, st) : launch_decode_g<T, 8, 1>(A, heads, kda, st);
+}
+
+gdn_status_t fail(gdn_status_t s, const char* msg)
+{
+    set_last_error(msg);
+    return s;
+}
+
+gdn_status_t cuda_fail(int e, const char* what)
+{
+    char msg[256];
+    snprintf(msg, sizeof msg, "%s: %s", what, cudaGetErrorString((cudaError_t)e));
+    return fail(GDN_ERR_CUDA, msg);
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb)
+{
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+// Bytes that rows of H heads of S elements reach over.
+size_t span(int64_t rows, int64_t H, int64_t S, const int64_t s[2], size_t es)
+{
+    return rows < 1 ? 0 : (size_t)((rows - 1) * s[0] + (H - 1) * s[1] + S) * es;
+}
+
+gdn_status_t check_decode(const gdn_decode_params_t* p)
+{
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "gdn_decode: params is NULL");
+    if (p->n_seq < 0 || p->T < 0 || p->n_tok < 0 || p->n_slots < 0)
+        return fail(GDN_ERR_INVALID_ARG, "gdn_decode: negative n_seq, T, n_tok or n_slots");
+    if (p->H_k < 1 || p->H_v < 1 || p->S_k < 1 || p->S_v < 1)
+        return fail(GDN_ERR_INVALID_ARG, "gdn_decode: heads and head sizes must be >= 1");
+    if (p->H_v % p->H_k != 0) return fail(GDN_ERR_INVALID_ARG, "gdn_decode: H_v is not a multiple of H_k");
+    if (p->gate != GDN_GATE_SCALAR && p->gate != GDN_GATE_KDA) return fail(GDN_ERR_INVALID_ARG, "gdn_decode: unknown gate kind");
+    if (!known_dtype(p->in_dtype) || !known_dtype(p->gate_dtype) || !known_dtype(p->y_dtype))
+        return fail(GDN_ERR_INVALID_ARG, "gdn_decode: unknown dtype");
+    for (int i = 0; i < 2; ++i)
+        if (p->q_s[i] < 0 || p->k_s[i] < 0 || p->v_s[i] < 0) return fail(GDN_ERR_INVALID_ARG, "gdn_decode: negative stride");
+    if (p->S_k != 16 && p->S_k != 32 && p->S_k != 64 && p->S_k != 128 && p->S_k != 256)
+        return fail(GDN_ERR_UNSUPPORTED, "gdn_decode: S_k must be 16, 32, 64, 128 or 256");
+    if (p->S_v % 16 != 0 || p->S_v > 256) return fail(GDN_ERR_UNSUPPORTED, "gdn_decode: S_v must be a multiple of 16 up to 256");
+    if (p->H_v > 65535 || p->n_tok > INT_MAX || p->T > INT_MAX || p->n_slots > INT_MAX ||
+        p->n_seq > (int64_t)UINT_MAX / (p->H_v * (p->S_v / 4)))
+        return fail(GDN_ERR_UNSUPPORTED, "gdn_decode: sizes beyond the kernel's index range");
+    if (p->slot_stride < p->H_v * p->S_v * p->S_k || p->slot_stride % 4 != 0)
+        return fail(GDN_ERR_INVALID_ARG, "gdn_decode: slot_stride must be a multiple of 4 of at least H_v S_v S_k");
+    return GDN_OK;
+}
+
+bool vec4(const void* ptr, const int64_t s[2], size_t es)
+{
+    return (uintptr_t)ptr % (4 * es) == 0 && s[0] % 4 == 0 && s[1] % 4 == 0;
+}
+
+}  // namespace
+
+int decode_take_status(void* stream, int* status)
+{
+    cudaStream_t s = (cudaStream_t)stream;
+    int v = 0;
+    int e = (int)cudaMemcpyFromSymbolAsync(&v, g_decode_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (!e) e = (int)cudaStreamSynchronize(s);
+    if (e) return e;
+    if (v) {
+        const int zero = 0;
+        e = (int)cudaMemcpyToSymbolAsync(g_decode_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+        if (!e) e = (int)cudaStreamSynchronize(s);
+    }
+    *status = v;
+    return e;
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" gdn_status_t gdn_decode_supported(const gdn_decode_params_t* p) { return check_decode(p); }
+
+extern "C" gdn_status_t gdn_decode(const gdn_decode_params_t* p, const void* q, const void* k, const void* v, const void* g,
+                                   const void* beta, const int32_t* cu_tokens, float* pool, const int32_t* slot_in,
+                                   const int32_t* slot_out, void* y, void* stream)
+{
+    const gdn_status_t st = check_decode(p);
+    if (st != GDN_OK) return st;
+    if (!cu_tokens && p->n_tok != p->n_seq * p->T)
+        return fail(GDN_ERR_INVALID_ARG, "gdn_decode: without cu_tokens, n_tok must be n_seq T");
+    if (p->n_seq == 0) return GDN_OK;
+    if (!slot_in || !slot_out || (p->n_slots > 0 && !pool) || (p->n_tok > 0 && (!q || !k || !v || !g || !beta || !y)))
+        return fail(GDN_ERR_INVALID_ARG, "gdn_decode: NULL pointer");
+    const size_t es = elem_size(p->in_dtype), gs = elem_size(p->gate_dtype), ys = elem_size(p->y_dtype);
+    if ((uintptr_t)pool % 16 != 0) return fail(GDN_ERR_INVALID_ARG, "gdn_decode: the pool must be 16-byte aligned");
+    if ((uintptr_t)q % es || (uintptr_t)k % es || (uintptr_t)v % es || (uintptr_t)g % gs || (uintptr_t)beta % gs ||
+        (uintptr_t)y % ys || (uintptr_t)slot_in % 4 || (uintptr_t)slot_out % 4 || (uintptr_t)cu_tokens % 4)
+        return fail(GDN_ERR_INVALID_ARG, "gdn_decode: a pointer is not aligned to its element");
+    const bool kda = p->gate == GDN_GATE_KDA;
+    const size_t n_pool = p->n_slots > 0 ? (size_t)((p->n_slots - 1) * p->slot_stride + p->H_v * p->S_v * p->S_k) * 4 : 0;
+    const size_t n_y = (size_t)(p->n_tok * p->H_v * p->S_v) * ys, n_b = (size_t)(p->n_tok * p->H_v) * gs;
+    const struct { const void* ptr; size_t n; } in[] = {
+        {q, span(p->n_tok, p->H_k, p->S_k, p->q_s, es)}, {k, span(p->n_tok, p->H_k, p->S_k, p->k_s, es)},
+        {v, span(p->n_tok, p->H_v, p->S_v, p->v_s, es)}, {g, n_b * (kda ? (size_t)p->S_k : 1)}, {beta, n_b},
+        {cu_tokens, (size_t)(p->n_seq + 1) * 4}, {slot_in, (size_t)p->n_seq * 4}, {slot_out, (size_t)p->n_seq * 4}};
+    for (const auto& i : in)
+        if (overlap(i.ptr, i.n, y, n_y) || overlap(i.ptr, i.n, pool, n_pool))
+            return fail(GDN_ERR_ALIAS, "gdn_decode: y or the pool overlaps an input");
+    if (overlap(y, n_y, pool, n_pool)) return fail(GDN_ERR_ALIAS, "gdn_decode: y overlaps the pool");
+
+    DecodeArgs A{};
+    A.q = q; A.k = k; A.v = v; A.g = g; A.beta = beta; A.cu = cu_tokens; A.pool = pool;
+    A.slot_in = slot_in; A.slot_out = slot_out; A.y = y;
+    A.slot_stride = p->slot_stride;
+    A.qs0 = p->q_s[0]; A.qs1 = p->q_s[1]; A.ks0 = p->k_s[0]; A.ks1 = p->k_s[1]; A.vs0 = p->v_s[0]; A.vs1 = p->v_s[1];
+    A.T = (int)p->T; A.n_tok = (int)p->n_tok; A.n_slots = (int)p->n_slots;
+    A.H_k = (int)p->H_k; A.H_v = (int)p->H_v; A.SK = (int)p->S_k; A.SV = (int)p->S_v;
+    A.gate_dtype = p->gate_dtype; A.y_dtype = p->y_dtype; A.scale = p->scale;
+    A.vec = vec4(q, p->q_s, es) && vec4(k, p->k_s, es);
+    const long long heads = p->n_seq * p->H_v;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int e = p->in_dtype == GDN_F32    ? launch_decode_t<float>(A, heads, kda, s)
+                  : p->in_dtype == GDN_BF16 ? launch_decode_t<__nv_bfloat16>(A, heads, kda, s)
+                                            : launch_decode_t<__half>(A, heads, kda, s);
+    return e ? cuda_fail(e, "gdn_decode launch") : GDN_OK;
+}
+
+namespace gdn {
+namespace {
+
+struct MoveArgs {
+    char* pool;
+    const int *src, *dst;
+    long long layer_stride, slot_stride, state_bytes;
+    int n_slots, n_moves, group, piece;  // piece: bytes of a state that one CTA moves, for every move of its group
+    unsigned pieces, groups;
+};
+
+// One CTA: one piece of the states of one group in one layer.  Every source piece is in shared
+// memory before the first destination is written, so the group's moves are simultaneous.
+__global__ void __launch_bounds__(256) gdn_states_move_kernel(const MoveArgs A)
+{
+    extern __shared__ uint4 buf[];
+    const unsigned pc = blockIdx.x % A.pieces, gl = blockIdx.x / A.pieces;
+    const unsigned gr = gl % A.groups, layer = gl / A.groups;
+    const long long at = (long long)pc * A.piece;
+    const int bytes = (int)(A.state_bytes - at < A.piece ? A.state_bytes - at : A.piece);
+    const int n16 = bytes / 16, per = A.piece / 16;
+    const int m0 = gr * A.group, nm = A.n_moves - m0 < A.group ? A.n_moves - m0 : A.group;
+    char* base = A.pool + layer * A.layer_stride + at;
+    for (int i = threadIdx.x; i < nm * n16; i += blockDim.x) {
+        const int m = i / n16, e = i - m * n16;
+        const int s = __ldg(A.src + m0 + m), d = __ldg(A.dst + m0 + m);
+        if (s < -1 || s >= A.n_slots || d < -1 || d >= A.n_slots) {
+            if (e == 0) atomicOr(&g_decode_status, 2);
+            continue;
+        }
+        if (d < 0 || s == d) continue;
+        buf[m * per + e] = s < 0 ? make_uint4(0, 0, 0, 0) : reinterpret_cast<const uint4*>(base + s * A.slot_stride)[e];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nm * n16; i += blockDim.x) {
+        const int m = i / n16, e = i - m * n16;
+        const int s = __ldg(A.src + m0 + m), d = __ldg(A.dst + m0 + m);
+        if (s < -1 || s >= A.n_slots || d < 0 || d >= A.n_slots || s == d) continue;
+        reinterpret_cast<uint4*>(base + d * A.slot_stride)[e] = buf[m * per + e];
+    }
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" gdn_status_t gdn_states_move(void* pool, int64_t n_layers, int64_t layer_stride, int64_t n_slots,
+                                        int64_t slot_stride, int64_t state_bytes, const int32_t* src, const int32_t* dst,
+                                        int64_t n_moves, int64_t group, void* stream)
+{
+    if (n_layers < 0 || n_slots < 0 || state_bytes < 0 || n_moves < 0 || layer_stride < 0 || slot_stride < 0 || group < 1)
+        return fail(GDN_ERR_INVALID_ARG, "gdn_states_move: negative size or stride, or group < 1");
+    if (group > n_moves) group = n_moves > 0 ? n_moves : 1;
+    if (group > 1024) return fail(GDN_ERR_UNSUPPORTED, "gdn_states_move: more than 1024 moves in a group");
+    if (n_layers == 0 || n_moves == 0 || state_bytes == 0 || n_slots == 0) return GDN_OK;
+    if (!pool || !src || !dst) return fail(GDN_ERR_INVALID_ARG, "gdn_states_move: NULL pointer");
+    if ((uintptr_t)pool % 16 || layer_stride % 16 || slot_stride % 16 || state_bytes % 16 || (uintptr_t)src % 4 || (uintptr_t)dst % 4)
+        return fail(GDN_ERR_INVALID_ARG, "gdn_states_move: the pool, its strides and state_bytes must be multiples of 16 bytes");
+    if ((n_slots > 1 && slot_stride < state_bytes) || n_slots > INT_MAX || n_moves > INT_MAX)
+        return fail(GDN_ERR_INVALID_ARG, "gdn_states_move: slots overlap, or too many of them");
+    // layers lie one after the other, or inside one another's slots ([slot][layer] order)
+    const int64_t slots_span = (n_slots - 1) * slot_stride + state_bytes, layers_span = (n_layers - 1) * layer_stride + state_bytes;
+    if (n_layers > 1 && layer_stride < slots_span && !(layer_stride >= state_bytes && (n_slots == 1 || slot_stride >= layers_span)))
+        return fail(GDN_ERR_INVALID_ARG, "gdn_states_move: layers overlap");
+    const size_t n_pool = (size_t)((n_layers - 1) * layer_stride + slots_span);
+    if (overlap(src, (size_t)n_moves * 4, pool, n_pool) || overlap(dst, (size_t)n_moves * 4, pool, n_pool))
+        return fail(GDN_ERR_ALIAS, "gdn_states_move: src or dst inside the pool");
+
+    MoveArgs A{};
+    A.pool = (char*)pool; A.src = src; A.dst = dst;
+    A.layer_stride = layer_stride; A.slot_stride = slot_stride; A.state_bytes = state_bytes;
+    A.n_slots = (int)n_slots; A.n_moves = (int)n_moves; A.group = (int)group;
+    int64_t piece = 32 * 1024 / group / 16 * 16;
+    if (piece > 8192) piece = 8192;
+    if (piece < 128) piece = 128;
+    if (piece > state_bytes) piece = state_bytes;
+    A.piece = (int)piece;
+    A.pieces = (unsigned)((state_bytes + piece - 1) / piece);
+    A.groups = (unsigned)((n_moves + group - 1) / group);
+    const int64_t ctas = (int64_t)A.pieces * A.groups * n_layers;
+    if (ctas > INT_MAX) return fail(GDN_ERR_UNSUPPORTED, "gdn_states_move: too many pieces for one launch");
+    const size_t smem = (size_t)(piece * group);
+    int e = 0;
+    if (smem > 48 * 1024)
+        e = (int)cudaFuncSetAttribute(gdn_states_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (!e) {
+        gdn_states_move_kernel<<<(unsigned)ctas, 256, smem, (cudaStream_t)stream>>>(A);
+        e = (int)cudaGetLastError();
+    }
+    return e ? cuda_fail(e, "gdn_states_move launch") : GDN_OK;
+}

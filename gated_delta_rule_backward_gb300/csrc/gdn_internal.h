@@ -289,6 +289,10 @@ int launch_reduce(const ReduceArgs& a, void* stream);
 int launch_widen(const void* src, int in_dtype, const long long s[3], int N, int T, int H, int D, float* dst,
                  void* stream);
 
+// Reads and clears the status word of gdn_decode.cu (bad slots or token ranges met on the
+// device).  Returns a cudaError_t as int.
+int decode_take_status(void* stream, int* status);
+
 // Sets the text gdn_last_error() returns on the calling thread.
 void set_last_error(const char* msg);
 
