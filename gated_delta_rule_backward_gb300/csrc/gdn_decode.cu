@@ -10,47 +10,22 @@
 //
 // What bounds it: the states' bytes, 8 S_k S_v a head against 7 S_k S_v flops a token.  So the
 // layout follows the reads: 8 lanes a row, each with float4 blocks 32 columns apart (whole 128-byte
-// lines), 4 rows across the warp, all of a warp's state in flight before its first use.  No shared
-// memory and no barrier: the warps of a head read the same q, k and gates from L1.
+// lines), 4 rows across the warp, all of a warp's state in flight before its first use.  Warps do
+// not meet: each keeps the token's vectors in fp32 in shared memory of its own, a lane widening
+// (and for KDA exponentiating) its share of the columns once for all rows.
 #include <climits>
 #include <cstdio>
 
 #include "../../include/gdn_decode.h"
 #include "gdn_device.cuh"
 #include "gdn_elem.cuh"
+#include "gdn_f32x2.cuh"
 
 namespace gdn {
 namespace {
 
 // Bit 0: gdn_decode met a bad slot or token range; bit 1: gdn_states_move a bad slot.
 __device__ int g_decode_status;
-
-typedef unsigned long long f2;  // two fp32 in one 64-bit register, the operand of the packed fp32 pipe
-
-__device__ __forceinline__ f2 pack2(float x, float y)
-{
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float sum2(f2 x)
-{
-    float a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-    return a + b;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
-{
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b)
-{
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 struct DecodeArgs {
     const void *q, *k, *v, *g, *beta;
@@ -60,55 +35,53 @@ struct DecodeArgs {
     void* y;
     long long slot_stride, qs0, qs1, ks0, ks1, vs0, vs1;
     int T, n_tok, n_slots, H_k, H_v, SK, SV;
-    int gate_dtype, y_dtype, vec;
+    int gate_dtype, y_dtype, vec, vec_g;
     unsigned warps;  // n_seq H_v S_v / rows of a warp
     float scale;
 };
 
-// One token's operands as they arrive: a lane's blocks of q, k (and the KDA gate), one v, beta, g.
-template <typename T, int NV, bool KDA>
+// Four consecutive gates as fp32.
+__device__ __forceinline__ float4 ld_gate4(const void* p, long long i, int dtype, bool vec)
+{
+    if (vec && dtype == GDN_F32) return __ldg(reinterpret_cast<const float4*>((const float*)p + i));
+    return make_float4(ld_any(p, i, dtype), ld_any(p, i + 1, dtype), ld_any(p, i + 2, dtype), ld_any(p, i + 3, dtype));
+}
+
+// One token's operands as they arrive: a lane's share of q, k (and the KDA gate), one v, beta, g.
+template <typename T, int SHARE, bool KDA>
 struct Token {
-    Pack<T, 4> q[NV], k[NV];
-    float g[KDA ? NV : 1][KDA ? 4 : 1];
+    Pack<T, 4> q[SHARE], k[SHARE];
+    float4 g[SHARE];  // scalar gate: g[0].x
     float v, beta;
 };
 
-template <typename T, int NV, bool KDA>
-__device__ __forceinline__ void load_token(Token<T, NV, KDA>& x, const DecodeArgs& A, long long row, int h, int j, int cl)
+template <typename T, int SHARE, bool KDA>
+__device__ __forceinline__ void load_token(Token<T, SHARE, KDA>& x, const DecodeArgs& A, const T* q, const T* k, const T* v, long long row,
+                                           int h, int lane)
 {
-    const int hk = h % A.H_k;
-    const T* q = (const T*)A.q + row * A.qs0 + hk * A.qs1;
-    const T* k = (const T*)A.k + row * A.ks0 + hk * A.ks1;
     const long long gh = row * A.H_v + h;
-#pragma unroll
-    for (int b = 0; b < NV; ++b) {
-        const int c = 32 * b + 4 * cl;
-        if (c < A.SK) {
-            x.k[b] = ld_pack<T, 4>(k + c, A.vec);
-            x.q[b] = ld_pack<T, 4>(q + c, A.vec);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x.k[b].x[i] = x.q[b].x[i] = from_f32<T>(0.f);
-        }
-    }
-    if (KDA) {
-#pragma unroll
-        for (int b = 0; b < NV; ++b) {
-            const int c = 32 * b + 4 * cl;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x.g[b][KDA ? i : 0] = c < A.SK ? ld_any(A.g, gh * A.SK + c + i, A.gate_dtype) : 0.f;
-        }
-    } else {
-        x.g[0][0] = ld_any(A.g, gh, A.gate_dtype);
-    }
     x.beta = ld_any(A.beta, gh, A.gate_dtype);
-    x.v = to_f32(__ldg((const T*)A.v + row * A.vs0 + h * A.vs1 + j));
+    if (!KDA) x.g[0].x = ld_any(A.g, gh, A.gate_dtype);
+    x.v = to_f32(__ldg(v + row * A.vs0));
+#pragma unroll
+    for (int s = 0; s < SHARE; ++s) {
+        const int c = 128 * s + 4 * lane;
+        if (c < A.SK) {
+            x.k[s] = ld_pack<T, 4>(k + row * A.ks0 + c, A.vec);
+            x.q[s] = ld_pack<T, 4>(q + row * A.qs0 + c, A.vec);
+            if (KDA) x.g[s] = ld_gate4(A.g, gh * A.SK + c, A.gate_dtype, A.vec_g);
+        }
+    }
 }
 
 // RT: rows of a lane (4 RT a warp); NV: its float4 blocks of a row.
 template <typename T, int NV, int RT, bool KDA>
 __global__ void __launch_bounds__(128) gdn_decode_kernel(const DecodeArgs A)
 {
+    constexpr int COLS = 32 * NV, SHARE = (COLS + 127) / 128;
+    // The token's row vectors in fp32, for each warp: what the dots take of the state (k, q; times the gate
+    // for KDA), and for KDA also k and the gate itself.
+    __shared__ float4 rows[4][KDA ? 4 : 2][COLS / 4];
     const unsigned w = blockIdx.x * 4u + (threadIdx.x >> 5);
     if (w >= A.warps) return;
     const int lane = threadIdx.x & 31, cl = lane & 7, grp = lane >> 3;
@@ -150,45 +123,58 @@ __global__ void __launch_bounds__(128) gdn_decode_kernel(const DecodeArgs A)
     constexpr int kShare = 4 / RT;  // lanes that hold the same sum
     const int mine = (cl & 3) / kShare;
     const int j = row0 + grp * RT + mine;
+    const int hk = h % A.H_k;
+    const T *qh = (const T*)A.q + hk * A.qs1, *kh = (const T*)A.k + hk * A.ks1, *vh = (const T*)A.v + h * A.vs1 + j;
+    float4(*mem)[COLS / 4] = rows[threadIdx.x >> 5];
 
-    Token<T, NV, KDA> x, nx;
-    if (lo < hi) load_token<T, NV, KDA>(x, A, lo, h, j, cl);
+    Token<T, SHARE, KDA> x;
+    if (lo < hi) load_token<T, SHARE, KDA>(x, A, qh, kh, vh, lo, h, lane);
     for (long long t = lo; t < hi; ++t) {
-        if (t + 1 < hi) load_token<T, NV, KDA>(nx, A, t + 1, h, j, cl);
-        f2 k[NV][2], q[NV][2], a[KDA ? NV : 1][2];
-        f2 kqs = 0;
-        float as = 1.f;
+        // this lane's four columns (or twice four): fp32, and the gate
+        float kq = 0.f;
+        const float as = KDA ? 1.f : expf(x.g[0].x), beta = x.beta, vj = x.v;
 #pragma unroll
-        for (int b = 0; b < NV; ++b)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                k[b][i] = pack2(x.k[b].get(2 * i), x.k[b].get(2 * i + 1));
-                q[b][i] = pack2(x.q[b].get(2 * i), x.q[b].get(2 * i + 1));
-                kqs = fma2(k[b][i], q[b][i], kqs);
-                if (KDA) a[KDA ? b : 0][i] = pack2(expf(x.g[KDA ? b : 0][KDA ? 2 * i : 0]), expf(x.g[KDA ? b : 0][KDA ? 2 * i + 1 : 0]));
+        for (int s = 0; s < SHARE; ++s) {
+            const int c = 128 * s + 4 * lane;
+            float4 k = make_float4(0.f, 0.f, 0.f, 0.f), q = k, a = k;
+            if (c < A.SK) {
+                k = make_float4(x.k[s].get(0), x.k[s].get(1), x.k[s].get(2), x.k[s].get(3));
+                q = make_float4(x.q[s].get(0), x.q[s].get(1), x.q[s].get(2), x.q[s].get(3));
+                if (KDA) a = make_float4(expf(x.g[s].x), expf(x.g[s].y), expf(x.g[s].z), expf(x.g[s].w));
             }
-        if (!KDA) {
-            as = expf(x.g[0][0]);
-            a[0][0] = pack2(as, as);
+            kq += (k.x * q.x + k.y * q.y) + (k.z * q.z + k.w * q.w);
+            if (c < COLS) {
+                if (KDA) {
+                    mem[2][c / 4] = k;
+                    mem[3][c / 4] = a;
+                    k = make_float4(k.x * a.x, k.y * a.y, k.z * a.z, k.w * a.w);
+                    q = make_float4(q.x * a.x, q.y * a.y, q.z * a.z, q.w * a.w);
+                }
+                mem[0][c / 4] = k;
+                mem[1][c / 4] = q;
+            }
         }
-        const float kq = rowsum8(sum2(kqs));
+        if (t + 1 < hi) load_token<T, SHARE, KDA>(x, A, qh, kh, vh, t + 1, h, lane);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) kq += __shfl_xor_sync(kFull, kq, o);
+        __syncwarp();
         float s[2 * RT];
         {
             f2 u2[RT], o2[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r) u2[r] = o2[r] = 0;
 #pragma unroll
-            for (int b = 0; b < NV; ++b)
+            for (int b = 0; b < NV; ++b) {
+                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&mem[0][8 * b + cl]);
+                const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&mem[1][8 * b + cl]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const f2 ka = KDA ? mul2(k[b][i], a[KDA ? b : 0][i]) : k[b][i];
-                    const f2 qa = KDA ? mul2(q[b][i], a[KDA ? b : 0][i]) : q[b][i];
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        u2[r] = fma2(m[r][b][i], ka, u2[r]);
-                        o2[r] = fma2(m[r][b][i], qa, o2[r]);
-                    }
+                for (int r = 0; r < RT; ++r) {
+                    u2[r] = fma2(m[r][b][0], k.x, u2[r]);
+                    o2[r] = fma2(m[r][b][0], q.x, o2[r]);
+                    u2[r] = fma2(m[r][b][1], k.y, u2[r]);
+                    o2[r] = fma2(m[r][b][1], q.y, o2[r]);
                 }
+            }
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 s[r] = sum2(u2[r]);
@@ -208,23 +194,27 @@ __global__ void __launch_bounds__(128) gdn_decode_kernel(const DecodeArgs A)
 #pragma unroll
         for (int bit = kShare / 2; bit >= 1; bit >>= 1) s[0] += __shfl_xor_sync(kFull, s[0], bit);
         const float sum = KDA ? s[0] : as * s[0];
-        float delta = x.beta * (x.v - sum);  // on lanes 0-3
+        float delta = beta * (vj - sum);  // on lanes 0-3
         float d[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) d[r] = __shfl_sync(kFull, delta, (lane & 24) + r * kShare);
         delta = __shfl_xor_sync(kFull, delta, 4);
         if (cl >= 4 && (cl & (kShare - 1)) == 0)
             st_any(A.y, (t * A.H_v + h) * A.SV + j, A.y_dtype, A.scale * fmaf(delta, kq, sum));
+        const f2 as2 = pack2(as, as);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const f2 dd = pack2(d[r], d[r]);
+        for (int b = 0; b < NV; ++b) {
+            const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&mem[KDA ? 2 : 0][8 * b + cl]);
+            ulonglong2 a = make_ulonglong2(as2, as2);
+            if (KDA) a = *reinterpret_cast<const ulonglong2*>(&mem[KDA ? 3 : 0][8 * b + cl]);
 #pragma unroll
-            for (int b = 0; b < NV; ++b)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    m[r][b][i] = fma2(k[b][i], dd, mul2(m[r][b][i], a[KDA ? b : 0][KDA ? i : 0]));
+            for (int r = 0; r < RT; ++r) {
+                const f2 dd = pack2(d[r], d[r]);
+                m[r][b][0] = fma2(k.x, dd, mul2(m[r][b][0], a.x));
+                m[r][b][1] = fma2(k.y, dd, mul2(m[r][b][1], a.y));
+            }
         }
-        x = nx;
+        __syncwarp();
     }
 
     if (s_out < 0) return;
@@ -376,6 +366,7 @@ extern "C" gdn_status_t gdn_decode(const gdn_decode_params_t* p, const void* q, 
     A.H_k = (int)p->H_k; A.H_v = (int)p->H_v; A.SK = (int)p->S_k; A.SV = (int)p->S_v;
     A.gate_dtype = p->gate_dtype; A.y_dtype = p->y_dtype; A.scale = p->scale;
     A.vec = vec4(q, p->q_s, es) && vec4(k, p->k_s, es);
+    A.vec_g = (uintptr_t)g % 16 == 0;
     const long long heads = p->n_seq * p->H_v;
     cudaStream_t s = (cudaStream_t)stream;
     const int e = p->in_dtype == GDN_F32    ? launch_decode_t<float>(A, heads, kda, s)
