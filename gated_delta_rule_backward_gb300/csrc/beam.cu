@@ -8,16 +8,18 @@
 //
 // Selecting n of a CTA's items: the n-th largest of the threads' maxima is a bound that at
 // least n items reach, and for items in no particular order few more do.  So: every warp
-// gives its R largest thread maxima, the n-th largest of all of those is the bound, the
-// items that reach it go to a list (in any order), and each listed item's rank is the number
-// of listed keys above its own.  Keys are (value, lowest index first) in one 64-bit number, so
-// ranks do not depend on the list's order.  Where more items reach the bound than the list
-// holds (many equal values), n rounds of a block-wide maximum select instead.
+// gives its R largest thread maxima, the n-th largest of all of those is the bound, and the
+// items that reach it go to a list (in any order).  A list that is still long goes through the same once
+// more, now spread evenly over the threads.  Each listed item's rank is the number of
+// listed keys above its own; keys are (value, lowest index first) in one 64-bit number, so ranks do not
+// depend on the list's order.  Where more items reach the bound than the list holds (many
+// equal values), n rounds of a block-wide maximum select instead.
 #include <climits>
 #include <cstdio>
 
 #include "../../include/beam.h"
 #include "gdn_elem.cuh"
+#include "gdn_f32x2.cuh"
 #include "gdn_internal.h"
 #include "gdn_tc.cuh"
 
@@ -26,7 +28,8 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxOut = 64, kMaxBeams = 64;
-constexpr int kList = 256;
+constexpr int kList = 1024, kLong = 96;  // items a list holds; items from which a second bound pays
+constexpr int kItems = 16;               // keys that a thread of the join holds
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -70,73 +73,95 @@ __device__ __forceinline__ float ex2(float x)
 __device__ __forceinline__ float exp_diff(float a, float b) { return a == b ? 1.f : ex2((a - b) * kLog2e); }
 
 struct SelectSmem {
-    unsigned top[kWarps * 16];
-    u64 list[kList];
+    u64 list[2][kList];
     u64 warp_best[kWarps];
     u64 out[kMaxOut];
-    int count;
+    __align__(16) unsigned top[kWarps * 8];
+    int count[2];
 };
 
 // R: thread maxima that a warp gives for a selection of n.
-__device__ __forceinline__ int tops_of(int n) { return n <= 16 ? 4 : n <= 32 ? 8 : 16; }
+__device__ __forceinline__ int tops_of(int n) { return n <= 16 ? 4 : 8; }
 
-// A warp's R largest of its lanes' v (0: none), from high to low.
-__device__ __forceinline__ void warp_tops(unsigned v, int R, unsigned* out, int lane)
+// A warp's R largest of its lanes' v (0: none), from high to low; returns the first.
+__device__ __forceinline__ unsigned warp_tops(unsigned v, int R, unsigned* out, int lane)
 {
+    unsigned first = 0;
     for (int r = 0; r < R; ++r) {
         const unsigned best = __reduce_max_sync(kAll, v);
+        if (r == 0) first = best;
         if (lane == 0) out[r] = best;
         const unsigned who = __ballot_sync(kAll, v == best);
         if (lane == __ffs(who) - 1) v = 0;
     }
+    return first;
 }
 
-// The n-th largest of the kWarps R values (0 when there are fewer): every warp finds it by itself.
-__device__ __forceinline__ unsigned nth_top(const unsigned* top, int R, int n, int lane)
+// The largest of the tops that n of them reach (0 when there is none): every warp finds it by itself.
+__device__ __forceinline__ unsigned nth_top(const unsigned* top, int n, int lane)
 {
-    unsigned v[4];
-    const int per = R / 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < per ? top[i * 32 + lane] : 0u;
+    const uint4* all = reinterpret_cast<const uint4*>(top);
     unsigned best = 0;
-    for (int r = 0; r < n; ++r) {
-        const unsigned mine = max(max(v[0], v[1]), max(v[2], v[3]));
-        best = __reduce_max_sync(kAll, mine);
-        if (best == 0) return 0;
-        const unsigned who = __ballot_sync(kAll, mine == best);
-        if (lane == __ffs(who) - 1) {
-            if (v[0] == best) v[0] = 0;
-            else if (v[1] == best) v[1] = 0;
-            else if (v[2] == best) v[2] = 0;
-            else v[3] = 0;
+    if (tops_of(n) == 4) {
+        const unsigned v = top[lane];
+        int reach = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const uint4 t = all[i];
+            reach += (t.x >= v) + (t.y >= v) + (t.z >= v) + (t.w >= v);
         }
+        best = reach >= n ? v : 0;
+    } else {
+        const unsigned v = top[lane], w = top[32 + lane];
+        int rv = 0, rw = 0;
+#pragma unroll
+        for (int i = 0; i < 2 * kWarps; ++i) {
+            const uint4 t = all[i];
+            rv += (t.x >= v) + (t.y >= v) + (t.z >= v) + (t.w >= v);
+            rw += (t.x >= w) + (t.y >= w) + (t.z >= w) + (t.w >= w);
+        }
+        best = max(rv >= n ? v : 0, rw >= n ? w : 0);
     }
-    return best;
+    best = __reduce_max_sync(kAll, best);
+    return best > kNegInf ? best : kNegInf + 1;  // an item at -inf is none
 }
 
-// The n best keys of the CTA's items into S.out (0 past their number), from high to low.  `each`
-// calls its argument with every item's (order(value), index) of this thread; S.top holds the warps' tops and
-// S.count 0, a barrier ago.  Ends with a barrier.
+// The n best keys of the CTA's items into S.out (0 past their number), from high to low.  `each(bound, take)`
+// calls take(order(value), index) for every item of this thread whose order reaches bound; `mine` is the largest.
+// S.top holds the warps' tops and S.count 0, a barrier ago.  Ends with a barrier.
 template <typename Each>
 __device__ __forceinline__ void select_n(SelectSmem& S, int n, unsigned mine, const Each& each)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned bound = nth_top(S.top, tops_of(n), n, lane);
-    if (bound <= kNegInf) bound = kNegInf + 1;  // an item at -inf is none
+    const unsigned bound = nth_top(S.top, n, lane);
     if (mine >= bound)
-        each([&](unsigned o, unsigned index) {
-            if (o >= bound) {
-                const int at = atomicAdd(&S.count, 1);
-                if (at < kList) S.list[at] = key_of(o, index);
-            }
+        each(bound, [&](unsigned o, unsigned index) {
+            const int at = atomicAdd(&S.count[0], 1);
+            if (at < kList) S.list[0][at] = key_of(o, index);
         });
     __syncthreads();
-    const int listed = S.count;
+    int listed = S.count[0];
     if (listed <= kList) {
-        if (tid < listed) {
-            const u64 key = S.list[tid];
+        const u64* list = S.list[0];
+        if (listed > kLong) {
+            unsigned best = 0;
+            for (int t = tid; t < listed; t += kThreads) best = max(best, (unsigned)(S.list[0][t] >> 32));
+            const int R = tops_of(n);
+            warp_tops(best, R, S.top + warp * R, lane);
+            __syncthreads();
+            const unsigned closer = nth_top(S.top, n, lane);
+            for (int t = tid; t < listed; t += kThreads) {
+                const u64 key = S.list[0][t];
+                if ((unsigned)(key >> 32) >= closer) S.list[1][atomicAdd(&S.count[1], 1)] = key;
+            }
+            __syncthreads();
+            listed = S.count[1];
+            list = S.list[1];
+        }
+        for (int t = tid; t < listed; t += kThreads) {
+            const u64 key = list[t];
             int rank = 0;
-            for (int i = 0; i < listed; ++i) rank += S.list[i] > key;
+            for (int i = 0; i < listed; ++i) rank += list[i] > key;
             if (rank < n) S.out[rank] = key;
         }
         for (int i = listed + tid; i < n; i += kThreads) S.out[i] = 0;
@@ -147,9 +172,9 @@ __device__ __forceinline__ void select_n(SelectSmem& S, int n, unsigned mine, co
     for (int r = 0; r < n; ++r) {
         u64 best = 0;
         if (mine >= bound)
-            each([&](unsigned o, unsigned index) {
+            each(bound, [&](unsigned o, unsigned index) {
                 const u64 key = key_of(o, index);
-                if (o >= bound && key < last && key > best) best = key;
+                if (key < last && key > best) best = key;
             });
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
@@ -165,11 +190,29 @@ __device__ __forceinline__ void select_n(SelectSmem& S, int n, unsigned mine, co
     }
 }
 
+// The largest of a pack's elements; one that is NaN does not count.
+__device__ __forceinline__ float pack_max(const Pack<float, 4>& v)
+{
+    return fmaxf(fmaxf(v.x[0], v.x[1]), fmaxf(v.x[2], v.x[3]));
+}
+__device__ __forceinline__ float pack_max(const Pack<__nv_bfloat16, 8>& v)
+{
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(v.x);
+    const float2 m = __bfloat1622float2(__hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3])));
+    return fmaxf(m.x, m.y);
+}
+__device__ __forceinline__ float pack_max(const Pack<__half, 8>& v)
+{
+    const __half2* w = reinterpret_cast<const __half2*>(v.x);
+    const float2 m = __half22float2(__hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3])));
+    return fmaxf(m.x, m.y);
+}
+
 // PACKS loads of 16 bytes a thread.
 template <typename T, int PACKS>
-__global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamArgs A)
+__global__ void __launch_bounds__(kThreads, PACKS == 8 ? 3 : 4) beam_segment_kernel(const BeamArgs A)
 {
-    constexpr int VEC = 16 / (int)sizeof(T), E = PACKS * VEC;
+    constexpr int VEC = 16 / (int)sizeof(T);
     __shared__ SelectSmem S;
     __shared__ float2 part[kWarps];
     const int row = blockIdx.x / A.splits, split = blockIdx.x - row * A.splits;
@@ -181,40 +224,51 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamArgs A
     const T* base = (const T*)A.logits + row * A.row_stride;
     const int lead = (int)(((uintptr_t)base & 15) / sizeof(T));
     const int first = split * A.seg - lead;
-    float x[E];
+    Pack<T, VEC> x[PACKS];
 #pragma unroll
     for (int p = 0; p < PACKS; ++p) {
         const int in = (p * kThreads + tid) * VEC, at = first + in;
         if (in < A.seg && at >= 0 && at + VEC <= A.V) {
-            const Pack<T, VEC> v = ld_pack<T, VEC>(base + at, true);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) x[p * VEC + i] = v.get(i);
+            x[p] = ld_pack<T, VEC>(base + at, true);
         } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                x[p * VEC + i] = in < A.seg && at + i >= 0 && at + i < A.V ? to_f32(base[at + i]) : -INFINITY;
+            for (int i = 0; i < VEC; ++i) x[p].x[i] = in < A.seg && at + i >= 0 && at + i < A.V ? base[at + i] : from_f32<T>(-INFINITY);
         }
     }
-    float m = -INFINITY;
+    float top[PACKS], m = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        x[e] = fmaxf(x[e], -INFINITY) + 0.f;  // NaN to -inf, -0 to 0
-        m = fmaxf(m, x[e]);
+    for (int p = 0; p < PACKS; ++p) {
+        top[p] = fmaxf(pack_max(x[p]), -INFINITY);  // a pack of NaNs
+        m = fmaxf(m, top[p]);
     }
+    // The sum against the thread's own maximum: (x - m) log2 e in two roundings, then the exponential.
     float s = 0.f;
-    if (fabsf(m) < INFINITY) {
+    if (m < INFINITY && m > -INFINITY) {
+        f2 s2 = 0;
+        const f2 mm = pack2(-m, -m), ll = pack2(kLog2e, kLog2e);
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += ex2((x[e] - m) * kLog2e);
-    } else if (m > 0.f) {
+        for (int p = 0; p < PACKS; ++p)
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += x[e] == m ? 1.f : 0.f;
+            for (int i = 0; i < VEC; i += 2) {
+                const float2 v = unpack2(mul2(add2(pack2(x[p].get(i), x[p].get(i + 1)), mm), ll));
+                s2 = add2(s2, pack2(ex2(v.x), ex2(v.y)));
+            }
+        s = sum2(s2);
     }
-    const unsigned mine = order(m);
+    if (m == INFINITY || s != s) {  // infinities share the probability; NaNs are left out
+        s = 0.f;
+#pragma unroll
+        for (int p = 0; p < PACKS; ++p)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float v = x[p].get(i);
+                s += v == m ? 1.f : v < m ? ex2((v - m) * kLog2e) : 0.f;
+            }
+    }
+    const unsigned mine = order(m + 0.f);  // + 0: -0 becomes 0
     const int R = tops_of(A.n);
-    warp_tops(mine, R, S.top + warp * R, lane);
-    if (tid == 0) S.count = 0;
-    __syncwarp();
-    const float wm = unorder(S.top[warp * R]);
+    if (tid < 2) S.count[tid] = 0;
+    const float wm = unorder(warp_tops(mine, R, S.top + warp * R, lane));
     s = m > -INFINITY ? s * exp_diff(m, wm) : 0.f;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
@@ -226,10 +280,17 @@ __global__ void __launch_bounds__(kThreads) beam_segment_kernel(const BeamArgs A
         for (int w = 0; w < kWarps; ++w) total += part[w].x > -INFINITY ? part[w].y * exp_diff(part[w].x, M) : 0.f;
         A.sums[blockIdx.x] = make_float2(M, total);
     }
-    select_n(S, A.n, mine, [&](auto&& take) {
+    select_n(S, A.n, mine, [&](unsigned bound, auto&& take) {
+        const float b = unorder(bound);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            take(order(x[e]), (unsigned)(first + ((e / VEC) * kThreads + tid) * VEC + e % VEC));
+        for (int p = 0; p < PACKS; ++p)
+            if (top[p] >= b) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float v = x[p].get(i);
+                    if (v >= b) take(order(v + 0.f), (unsigned)(first + (p * kThreads + tid) * VEC + i));
+                }
+            }
     });
     for (int i = tid; i < A.n; i += kThreads) A.best[(long long)blockIdx.x * A.n + i] = S.out[i];
 }
@@ -238,105 +299,128 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs A)
 {
     __shared__ SelectSmem S;
     __shared__ float row_score[kMaxBeams], row_max[kMaxBeams], row_log[kMaxBeams];
-    __shared__ int rows_on[kMaxBeams], rows_done[kMaxBeams], n_on, n_done;  // beams that go on, and finished ones
+    __shared__ int kind[kMaxBeams], rows_on[kMaxBeams], rows_done[kMaxBeams], n_on, n_done;  // beams that go on, and finished ones
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row0 = (long long)blockIdx.x * A.K;
-    tc::grid_dep_wait();
-    for (int k = warp; k < A.K; k += kWarps) {
-        const float score = A.scores[row0 + k];
-        const bool dead = !(score > -INFINITY), done = A.done && A.done[row0 + k];
-        float m = -INFINITY, s = 0.f;
-        if (!dead && !done) {
-            for (int i = lane; i < A.splits; i += 32) {
-                const float2 p = A.sums[(row0 + k) * A.splits + i];
-                const float big = fmaxf(m, p.x);
-                s = (m > -INFINITY ? s * exp_diff(m, big) : 0.f) + (p.x > -INFINITY ? p.y * exp_diff(p.x, big) : 0.f);
-                m = big;
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) {
-                const float m2 = __shfl_xor_sync(kAll, m, o), s2 = __shfl_xor_sync(kAll, s, o), big = fmaxf(m, m2);
-                s = (m > -INFINITY ? s * exp_diff(m, big) : 0.f) + (m2 > -INFINITY ? s2 * exp_diff(m2, big) : 0.f);
-                m = big;
-            }
-        }
-        if (lane == 0) {
-            row_score[k] = score;
-            row_max[k] = m;
-            row_log[k] = dead ? 0.f : done ? 1.f : logf(s);
-            rows_done[k] = dead ? -1 : done;
-        }
+    if (tid < A.K) {
+        const float score = A.scores[row0 + tid];
+        row_score[tid] = score;
+        kind[tid] = !(score > -INFINITY) ? -1 : A.done && A.done[row0 + tid] ? 1 : 0;
     }
     __syncthreads();
     if (tid == 0) {
         int on = 0, ended = 0;
         for (int k = 0; k < A.K; ++k) {
-            const int what = rows_done[k];  // entry k is read before any entry above ended <= k is written
-            if (what == 0) rows_on[on++] = k;
-            else if (what > 0) rows_done[ended++] = k;
+            if (kind[k] == 0) rows_on[on++] = k;
+            else if (kind[k] > 0) rows_done[ended++] = k;
         }
         n_on = on;
         n_done = ended;
-        S.count = 0;
     }
     __syncthreads();
+    tc::grid_dep_wait();
 
-    // A thread takes items that follow one another: whole lists, best first, so that the threads'
-    // maxima are the lists' best and few other items reach the bound.
-    const int per = A.splits * A.n, kept = n_on * per, total = kept + n_done, q = (total + kThreads - 1) / kThreads;
-    auto each = [&](auto&& take) {
-        for (int i = tid * q; i < total && i < (tid + 1) * q; ++i) {
-            int k;
-            float c;
-            unsigned token;
-            if (i < kept) {
-                const int r = i / per;
-                k = rows_on[r];
-                const u64 key = A.best[(row0 + k) * per + (i - r * per)];
-                if (key == 0) continue;
-                const float x = unorder((unsigned)(key >> 32)), m = row_max[k];
-                c = row_score[k] + ((x == m ? 0.f : x - m) - row_log[k]);
-                token = 0xffffffffu - (unsigned)key;
-            } else {
-                k = rows_done[i - kept];
-                c = row_score[k];
-                token = A.pad;
+    // A thread takes items that follow one another (whole lists, best first, so that its largest is a list's
+    // best), and threads next to one another are in different warps, so that each beam's are spread over all warps.
+    const int place = lane * kWarps + warp;
+    const int per = A.splits * A.n, kept = n_on * per, total = kept + n_done;
+    const u64* best = A.best + row0 * per;
+    int carried = 0;
+    for (int from = 0; from < total || from == 0;) {
+        // as many items as the threads hold, with the n best of those before
+        const int left = total - from, most = kThreads * kItems - carried, now = left < most ? left : most;
+        const int q = (now + carried + kThreads - 1) / kThreads;
+        u64 key[kItems];
+        int row[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int at = place * q + i;  // among this round's items: new ones, then the carried
+            key[i] = 0;
+            row[i] = -1;
+            if (i < q && at < now + carried) {
+                if (at >= now) {
+                    key[i] = S.out[at - now];
+                } else if (from + at < kept) {
+                    const int r = (from + at) / per;
+                    row[i] = rows_on[r];
+                    key[i] = best[(long long)row[i] * per + (from + at - r * per)];
+                } else {
+                    const int k = rows_done[from + at - kept];
+                    key[i] = key_of(order(row_score[k] + 0.f), (unsigned)k * (unsigned)A.V + (unsigned)A.pad);
+                }
             }
-            c += 0.f;
-            if (c > -INFINITY) take(order(c), (unsigned)k * (unsigned)A.V + token);
         }
-    };
-    unsigned mine = 0;
-    each([&](unsigned o, unsigned) { mine = max(mine, o); });
-    const int R = tops_of(A.n);
-    warp_tops(mine, R, S.top + warp * R, lane);
-    __syncthreads();
-    select_n(S, A.n, mine, each);
+        if (from == 0) {
+            for (int r = warp; r < n_on; r += kWarps) {  // a row's log-sum-exp
+                const int k = rows_on[r];
+                float m = -INFINITY, s = 0.f;
+                for (int i = lane; i < A.splits; i += 32) {
+                    const float2 p = A.sums[(row0 + k) * A.splits + i];
+                    const float big = fmaxf(m, p.x);
+                    s = (m > -INFINITY ? s * exp_diff(m, big) : 0.f) + (p.x > -INFINITY ? p.y * exp_diff(p.x, big) : 0.f);
+                    m = big;
+                }
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) {
+                    const float m2 = __shfl_xor_sync(kAll, m, o), s2 = __shfl_xor_sync(kAll, s, o), big = fmaxf(m, m2);
+                    s = (m > -INFINITY ? s * exp_diff(m, big) : 0.f) + (m2 > -INFINITY ? s2 * exp_diff(m2, big) : 0.f);
+                    m = big;
+                }
+                if (lane == 0) {
+                    row_max[k] = m;
+                    row_log[k] = logf(s);
+                }
+            }
+        }
+        if (tid < 2) S.count[tid] = 0;
+        __syncthreads();  // the carried keys have been read, too
+        unsigned mine = 0;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            if (row[i] >= 0 && key[i] != 0) {
+                const int k = row[i];
+                const float x = unorder((unsigned)(key[i] >> 32)), m = row_max[k];
+                const float c = row_score[k] + ((x == m ? 0.f : x - m) - row_log[k]) + 0.f;
+                key[i] = c > -INFINITY ? key_of(order(c), (unsigned)k * (unsigned)A.V + (0xffffffffu - (unsigned)key[i])) : 0;
+            }
+            mine = max(mine, (unsigned)(key[i] >> 32));
+        }
+        const int R = tops_of(A.n);
+        warp_tops(mine, R, S.top + warp * R, lane);
+        __syncthreads();
+        select_n(S, A.n, mine, [&](unsigned bound, auto&& take) {
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                if ((unsigned)(key[i] >> 32) >= bound) take((unsigned)(key[i] >> 32), 0xffffffffu - (unsigned)key[i]);
+        });
+        carried = A.n;
+        from += now > 0 ? now : 1;
+    }
 
-    int found = 0;
-    for (int i = 0; i < A.n; ++i) found += S.out[i] != 0;
     const long long at = (long long)blockIdx.x * A.n;
-    for (int i = tid; i < A.n; i += kThreads) {
+    if (tid < A.n) {
+        int found = 0;
+        for (int i = 0; i < A.n; ++i) found += S.out[i] != 0;
         unsigned flat;
         float c = -INFINITY;
-        if (i < found) {
-            flat = 0xffffffffu - (unsigned)S.out[i];
-            c = unorder((unsigned)(S.out[i] >> 32));
+        if (tid < found) {
+            flat = 0xffffffffu - (unsigned)S.out[tid];
+            c = unorder((unsigned)(S.out[tid] >> 32));
         } else {
-            // the (i - found)-th lowest index that is not among the found ones
-            flat = i - found;
+            // the (tid - found)-th lowest index that is not among the found ones
+            flat = tid - found;
             for (bool again = true; again;) {
                 unsigned below = 0;
                 for (int j = 0; j < found; ++j) below += 0xffffffffu - (unsigned)S.out[j] <= flat;
-                again = flat != (unsigned)(i - found) + below;
-                flat = (unsigned)(i - found) + below;
+                again = flat != (unsigned)(tid - found) + below;
+                flat = (unsigned)(tid - found) + below;
             }
         }
         const int k = flat / (unsigned)A.V;
-        A.scores_out[at + i] = c;
-        A.parent[at + i] = k;
-        A.token[at + i] = flat - (unsigned)k * (unsigned)A.V;
-        if (A.src_slots) A.src_slots[at + i] = A.slots[row0 + k];
+        A.scores_out[at + tid] = c;
+        A.parent[at + tid] = k;
+        A.token[at + tid] = flat - (unsigned)k * (unsigned)A.V;
+        if (A.src_slots) A.src_slots[at + tid] = A.slots[row0 + k];
     }
 }
 
@@ -376,18 +460,18 @@ int check(const beam_params_t* p)
     return GDN_OK;
 }
 
-// Segments of 32 elements a thread; of 8 where that would leave SMs without one.
+// Segments of 8 packs a thread; of fewer where that would leave SMs without one.
 BeamPlan plan_of(const beam_params_t* p)
 {
     BeamPlan pl{};
     const int vec = 16 / (int)elem_size(p->dtype);
-    int el = 32;
-    if (p->N * p->K * ((p->V + 32 * kThreads - 1) / (32 * kThreads)) < 2 * kNumSMs) el = 8;
-    pl.packs = el / vec;
     // a row may start vec - 1 elements into its first pack; segments of one size leave no small last one,
     // whose few threads would give a low bound
     const int64_t span = p->V + vec - 1;
-    pl.splits = (int)((span + el * kThreads - 1) / (el * kThreads));
+    pl.packs = 8;
+    while (pl.packs > 2 && p->N * p->K * ((span + pl.packs * vec * kThreads - 1) / (pl.packs * vec * kThreads)) < 4 * kNumSMs) pl.packs /= 2;
+    const int64_t most = (int64_t)pl.packs * vec * kThreads;
+    pl.splits = (int)((span + most - 1) / most);
     pl.seg = (int)((span + (int64_t)pl.splits * vec - 1) / ((int64_t)pl.splits * vec)) * vec;
     const size_t segs = (size_t)(p->N * p->K) * pl.splits;
     pl.off_best = (segs * sizeof(float2) + 15) / 16 * 16;
@@ -398,9 +482,9 @@ BeamPlan plan_of(const beam_params_t* p)
 template <typename T>
 void launch_segments(const BeamArgs& A, int packs, unsigned ctas, cudaStream_t st)
 {
-    constexpr int VEC = 16 / (int)sizeof(T);
-    if (packs * VEC == 32) beam_segment_kernel<T, 32 / VEC><<<ctas, kThreads, 0, st>>>(A);
-    else beam_segment_kernel<T, 8 / VEC><<<ctas, kThreads, 0, st>>>(A);
+    if (packs == 8) beam_segment_kernel<T, 8><<<ctas, kThreads, 0, st>>>(A);
+    else if (packs == 4) beam_segment_kernel<T, 4><<<ctas, kThreads, 0, st>>>(A);
+    else beam_segment_kernel<T, 2><<<ctas, kThreads, 0, st>>>(A);
 }
 
 }  // namespace
