@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import gdn
-from .decode import DTYPE_CODES
+from .decode import DTYPE_CODES, _stream
 
 _lib = gdn._lib
 
@@ -66,7 +66,7 @@ def beam_select(p: BeamParams, logits, scores, done, slots, scores_out, parent, 
     """Raw C-ABI call; done (uint8 or bool), slots and src_slots may be None."""
     st = _lib.beam_select(ctypes.byref(p), logits.data_ptr(), scores.data_ptr(), _ptr(done), _ptr(slots), scores_out.data_ptr(),
                           parent.data_ptr(), token.data_ptr(), _ptr(src_slots), workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), gdn._stream_handle(stream))
+                          workspace.numel() * workspace.element_size(), _stream(stream))
     if st != gdn.GDN_OK:
         raise gdn.GdnError(st, "beam_select")
 

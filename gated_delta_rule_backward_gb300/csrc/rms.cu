@@ -1,21 +1,23 @@
 // rms.cu -- root-mean-square norm with the residual's addition, forward and backward (include/rms.h).
 //
-// Both directions are one pass over their rows: what is read once is held in registers until
-// the row's sums are known.  TPR threads share a row, each with VPT packs of VEC elements, and a
-// CTA holds blockDim.y such rows, whose threads meet at a named barrier of their own (a row of one
-// warp needs none).  Bytes bound both: a row's loads are all in flight before its first sum.
+// Both directions are one pass over their rows: what is read once is held in registers, as it is
+// stored, until the row's sums are known.  TPR threads share a row, each with VPT packs of VEC
+// elements; rows of one warp's width go several to a CTA, others have a CTA each.  Bytes bound
+// both: a row's loads are all in flight before its first sum.
 #include <climits>
 #include <cstdio>
 #include <cuda_fp8.h>
 
 #include "../../include/rms.h"
 #include "gdn_elem.cuh"
+#include "gdn_f32x2.cuh"
 #include "gdn_internal.h"
+#include "gdn_tc.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kMaxThreads = 512;  // of a CTA: 128 registers a thread
+constexpr int kMaxThreads = 1024, kRingThreads = 512;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kE4m3Max = 448.f;
 constexpr float kTinyScale = 1.17549435e-38f;  // 2^-126
@@ -25,7 +27,7 @@ struct RmsFwd {
     void *h, *y;
     float *scales, *rstd;
     long long xs, rs;
-    int rows, D, w_dtype, y_dtype, group, vec;
+    int rows, D, w_dtype, y_dtype, lg_group, vec;
     float eps, inv_D;
 };
 
@@ -39,315 +41,444 @@ struct RmsBwd {
     float inv_D;
 };
 
-// Sums (and a maximum) over the threads of a row.  buf: two sets of 32 pairs a row of the CTA; successive
-// calls alternate between them, so one barrier a call is enough.
-__device__ __forceinline__ float2 row_reduce(float s, float m, float2* buf, int tid, int tpr, int bar)
+// A sum (MAX: a maximum too) over the threads of a row: a warp, a CTA, or (GROUPS) one of several rows of a CTA,
+// which meet at a named barrier of their own.  buf: 32 pairs for each row; successive calls use different
+// ones, so one barrier a call is enough.
+template <bool MAX, bool GROUPS>
+__device__ __forceinline__ float2 row_reduce(float s, float m, float2* buf)
 {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
         s += __shfl_xor_sync(kAll, s, o);
-        m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        if (MAX) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     }
-    if (tpr > 32) {
-        const int lane = tid & 31, warps = tpr >> 5;
-        if (lane == 0) buf[tid >> 5] = make_float2(s, m);
-        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(tpr) : "memory");
-        const float2 v = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
-        s = v.x;
-        m = v.y;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            s += __shfl_xor_sync(kAll, s, o);
-            m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    if (blockDim.x > 32) {
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(s, m);
+        if (GROUPS) asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+        else __syncthreads();
+        s = m = 0.f;
+        for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
+            const float2 v = buf[i];
+            s += v.x;
+            if (MAX) m = fmaxf(m, v.y);
         }
     }
     return make_float2(s, m);
 }
 
-// VEC elements at column c of a row of D (zero past its end).
-template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> ld_cols(const T* row, int c, int D, bool vec)
-{
-    Pack<T, VEC> r;
-    if (VEC == 1) {
-        r.x[0] = c < D ? row[c] : from_f32<T>(0.f);
-    } else if (vec) {
-        if (c < D) {
-            *reinterpret_cast<uint4*>(&r) = *reinterpret_cast<const uint4*>(row + c);
-        } else {
-            *reinterpret_cast<uint4*>(&r) = make_uint4(0, 0, 0, 0);
-        }
-    } else {
+// VEC fp32 numbers, in pairs for the packed fp32 pipe.
+template <int VEC>
+struct Nums {
+    f2 v[VEC / 2];
+    __device__ __forceinline__ void fill(float x)
+    {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) r.x[i] = c + i < D ? row[c + i] : from_f32<T>(0.f);
+        for (int i = 0; i < VEC / 2; ++i) v[i] = pack2(x, x);
+    }
+    __device__ __forceinline__ void set(int i, float x, float y) { v[i / 2] = pack2(x, y); }
+    __device__ __forceinline__ float2 pair(int i) const { return unpack2(v[i / 2]); }
+    __device__ __forceinline__ float sum() const
+    {
+        f2 t = v[0];
+#pragma unroll
+        for (int i = 1; i < VEC / 2; ++i) t = add2(t, v[i]);
+        return sum2(t);
+    }
+    __device__ __forceinline__ float max_abs() const
+    {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const float2 x = unpack2(v[i]);
+            m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+        }
+        return m;
+    }
+};
+template <>
+struct Nums<1> {
+    float v;
+    __device__ __forceinline__ void fill(float x) { v = x; }
+    __device__ __forceinline__ void set(int, float x, float) { v = x; }
+    __device__ __forceinline__ float2 pair(int) const { return make_float2(v, 0.f); }
+    __device__ __forceinline__ float sum() const { return v; }
+    __device__ __forceinline__ float max_abs() const { return fabsf(v); }
+};
+template <int VEC>
+__device__ __forceinline__ Nums<VEC> add(const Nums<VEC>& a, const Nums<VEC>& b)
+{
+    Nums<VEC> r;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) r.v[i] = add2(a.v[i], b.v[i]);
+    return r;
+}
+__device__ __forceinline__ Nums<1> add(const Nums<1>& a, const Nums<1>& b) { return {a.v + b.v}; }
+template <int VEC>
+__device__ __forceinline__ Nums<VEC> mul(const Nums<VEC>& a, const Nums<VEC>& b)
+{
+    Nums<VEC> r;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) r.v[i] = mul2(a.v[i], b.v[i]);
+    return r;
+}
+__device__ __forceinline__ Nums<1> mul(const Nums<1>& a, const Nums<1>& b) { return {a.v * b.v}; }
+template <int VEC>
+__device__ __forceinline__ Nums<VEC> mul(const Nums<VEC>& a, float b)
+{
+    Nums<VEC> r;
+    const f2 bb = pack2(b, b);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) r.v[i] = mul2(a.v[i], bb);
+    return r;
+}
+__device__ __forceinline__ Nums<1> mul(const Nums<1>& a, float b) { return {a.v * b}; }
+template <int VEC>
+__device__ __forceinline__ Nums<VEC> fma(const Nums<VEC>& a, const Nums<VEC>& b, const Nums<VEC>& c)
+{
+    Nums<VEC> r;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) r.v[i] = fma2(a.v[i], b.v[i], c.v[i]);
+    return r;
+}
+__device__ __forceinline__ Nums<1> fma(const Nums<1>& a, const Nums<1>& b, const Nums<1>& c) { return {fmaf(a.v, b.v, c.v)}; }
+template <int VEC>
+__device__ __forceinline__ Nums<VEC> fma(const Nums<VEC>& a, float b, const Nums<VEC>& c)
+{
+    Nums<VEC> r;
+    const f2 bb = pack2(b, b);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) r.v[i] = fma2(a.v[i], bb, c.v[i]);
+    return r;
+}
+__device__ __forceinline__ Nums<1> fma(const Nums<1>& a, float b, const Nums<1>& c) { return {fmaf(a.v, b, c.v)}; }
+
+__device__ __forceinline__ float2 widen2(uint32_t w, __nv_bfloat16) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ float2 widen2(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ uint32_t narrow2(float2 x, __nv_bfloat16)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t narrow2(float2 x, __half)
+{
+    const __half2 v = __floats2half2_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A thread's VEC elements of a row (16 bytes of T, or one element) as they are stored.
+template <typename T, int VEC>
+__device__ __forceinline__ uint4 ld_cols(const T* row, int c, int D, bool vec)
+{
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (VEC == 1) {
+        if (c < D) r.x = sizeof(T) == 4 ? reinterpret_cast<const uint32_t*>(row)[c] : reinterpret_cast<const uint16_t*>(row)[c];
+    } else if (vec) {
+        if (c < D) r = *reinterpret_cast<const uint4*>(row + c);
+    } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (c + i < D) {
+                if (sizeof(T) == 4) w[i & 3] = reinterpret_cast<const uint32_t*>(row)[c + i];
+                else w[(i / 2) & 3] |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[c + i] << (16 * (i & 1));
+            }
+        r = make_uint4(w[0], w[1], w[2], w[3]);
     }
     return r;
 }
 
 template <typename T, int VEC>
-__device__ __forceinline__ void st_cols(T* row, int c, int D, bool vec, const float (&v)[VEC])
+__device__ __forceinline__ Nums<VEC> widen(const uint4& x)
 {
-    if (VEC == 1) {
-        if (c < D) row[c] = from_f32<T>(v[0]);
+    Nums<VEC> r;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) r.set(i, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < (VEC + 1) / 2; ++i) {
+            const float2 v = widen2(w[i], T());
+            r.set(2 * i, v.x, v.y);
+        }
+    }
+    return r;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void st_cols(T* row, int c, int D, bool vec, const Nums<VEC>& v)
+{
+    if constexpr (VEC == 1) {
+        if (c < D) row[c] = from_f32<T>(v.v);
     } else if (vec) {
-        constexpr int PER = 16 / (int)sizeof(T);  // elements of one 16-byte store
-        if (c < D) {
+        if (c >= D) return;
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int b = 0; b < VEC; b += PER < VEC ? PER : VEC) {
-                Pack<T, PER < VEC ? PER : VEC> r;
-#pragma unroll
-                for (int i = 0; i < (PER < VEC ? PER : VEC); ++i) r.x[i] = from_f32<T>(v[b + i]);
-                if (PER <= VEC) *reinterpret_cast<uint4*>(row + c + b) = *reinterpret_cast<const uint4*>(&r);
-                else *reinterpret_cast<uint2*>(row + c + b) = *reinterpret_cast<const uint2*>(&r);
+            for (int i = 0; i < VEC; i += 4) {
+                const float2 a = v.pair(i), b = v.pair(i + 2);
+                *reinterpret_cast<float4*>(row + c + i) = make_float4(a.x, a.y, b.x, b.y);
             }
+        } else if constexpr (VEC == 8) {
+            *reinterpret_cast<uint4*>(row + c) = make_uint4(narrow2(v.pair(0), T()), narrow2(v.pair(2), T()), narrow2(v.pair(4), T()), narrow2(v.pair(6), T()));
+        } else {
+            *reinterpret_cast<uint2*>(row + c) = make_uint2(narrow2(v.pair(0), T()), narrow2(v.pair(2), T()));
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if (c + i < D) row[c + i] = from_f32<T>(v[i]);
-    }
-}
-
-template <int VEC>
-__device__ __forceinline__ void ld_weight(float (&w)[VEC], const void* p, int dtype, int c, int D, bool vec)
-{
-    if (!p) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) w[i] = 1.f;
-    } else if (VEC > 1 && vec && c < D && dtype == GDN_F32) {
-#pragma unroll
-        for (int b = 0; b < VEC; b += 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>((const float*)p + c + (VEC > 1 ? b : 0)));
-            w[b] = v.x;
-            if (VEC > 1) {
-                w[b + 1 < VEC ? b + 1 : 0] = v.y;
-                w[b + 2 < VEC ? b + 2 : 0] = v.z;
-                w[b + 3 < VEC ? b + 3 : 0] = v.w;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) w[i] = c + i < D ? ld_any(p, c + i, dtype) : 0.f;
-    }
-}
-
-template <int VEC>
-__device__ __forceinline__ void st_e4m3(uint8_t* row, int c, int D, bool vec, const float (&v)[VEC])
-{
-    if (VEC == 1) {
-        if (c < D) row[c] = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
-    } else {
-        uint8_t q[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
-            const __nv_fp8x2_storage_t two =
-                __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[VEC > 1 ? i + 1 : 0]), __NV_SATFINITE, __NV_E4M3);
-            q[i] = (uint8_t)(two & 0xff);
-            q[VEC > 1 ? i + 1 : 0] = (uint8_t)(two >> 8);
+            const float2 a = v.pair(i);
+            if (c + i < D) row[c + i] = from_f32<T>(a.x);
+            if (c + i + 1 < D) row[c + i + 1] = from_f32<T>(a.y);
+        }
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ Nums<VEC> ld_weight(const void* p, int dtype, int c, int D, bool vec)
+{
+    Nums<VEC> w;
+    if (!p) {
+        w.fill(1.f);
+    } else if (VEC >= 4 && vec && dtype == GDN_F32) {
+#pragma unroll
+        for (int b = 0; b + 3 < VEC; b += 4) {
+            const float4 v = c < D ? __ldg(reinterpret_cast<const float4*>((const float*)p + c + b)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            w.set(b, v.x, v.y);
+            w.set(b + 2, v.z, v.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) w.set(i, c + i < D ? ld_any(p, c + i, dtype) : 0.f, VEC > 1 && c + i + 1 < D ? ld_any(p, c + i + 1, dtype) : 0.f);
+    }
+    return w;
+}
+
+template <int VEC>
+__device__ __forceinline__ void st_e4m3(uint8_t* row, int c, int D, bool vec, const Nums<VEC>& v)
+{
+    if constexpr (VEC == 1) {
+        if (c < D) row[c] = __nv_cvt_float_to_fp8(v.v, __NV_SATFINITE, __NV_E4M3);
+    } else {
+        uint32_t w[VEC / 4];
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(v.pair(i), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(v.pair(i + 2), __NV_SATFINITE, __NV_E4M3);
+            w[i / 4] = lo | hi << 16;
         }
         if (vec) {
-            if (c < D) {
-                uint32_t a = 0;
-#pragma unroll
-                for (int b = 0; b < VEC; b += 4) {
-                    a = 0;
-#pragma unroll
-                    for (int i = 0; i < 4 && i < VEC; ++i) a |= (uint32_t)q[b + i < VEC ? b + i : 0] << (8 * i);
-                    *reinterpret_cast<uint32_t*>(row + c + b) = a;
-                }
-            }
+            if (c >= D) return;
+            if constexpr (VEC == 8) *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t*>(row + c) = w[0];
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (c + i < D) row[c + i] = q[i];
+                if (c + i < D) row[c + i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
         }
     }
 }
 
-// h of one pack: x + residual in fp32.
-template <typename T, int VEC>
-__device__ __forceinline__ void sum_pack(float (&h)[VEC], const Pack<T, VEC>& x, const Pack<T, VEC>& r, bool res)
-{
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) h[i] = res ? x.get(i) + r.get(i) : x.get(i);
-}
+// The forms of y: a type of its own, 8-bit codes with a scale a row, or a scale a group of columns.
+enum { kPlain = 0, kRowCodes = 1, kGroupCodes = 2 };
 
 // What follows the sums, for one pack: h and y (or its codes and scale) to memory.
-template <typename T, int VEC>
-__device__ __forceinline__ void finish_pack(const RmsFwd& A, const float (&h)[VEC], const float (&w)[VEC], long long row, int c,
-                                            float rstd, float inv_scale)
+template <typename T, int VEC, int OUT>
+__device__ __forceinline__ void finish_pack(const RmsFwd& A, const Nums<VEC>& h, long long row, int c, float rstd, float inv)
 {
     const bool vec = A.vec;
-    if (A.h) st_cols<T, VEC>((T*)A.h + row * A.D, c, A.D, vec, h);
-    float y[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) y[i] = (h[i] * w[i]) * rstd;
     const long long at = row * A.D;
-    if (A.y_dtype == RMS_E4M3) {
-        float inv = inv_scale;
-        if (VEC > 1 && A.group) {
-            float m = 0.f;
+    if (A.h) st_cols<T, VEC>((T*)A.h + at, c, A.D, vec, h);
+    const Nums<VEC> y = mul(mul(h, ld_weight<VEC>(A.w, A.w_dtype, c, A.D, vec)), rstd);
+    if (OUT == kGroupCodes) {
+        float m = y.max_abs();
+        // the lanes of a group (a power of two; every lane of the warp is here)
+        if (A.lg_group == 7) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(y[i]));
-            const int lanes = A.group / VEC;  // a power of two; every lane of the warp is here
-            for (int o = lanes >> 1; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-            const float scale = fmaxf(m / kE4m3Max, kTinyScale);
-            inv = 1.f / scale;
-            if (c < A.D && (c & (A.group - 1)) == 0) A.scales[row * (A.D / A.group) + c / A.group] = scale;
+            for (int o = 64 / VEC; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        } else {
+            for (int o = (1 << A.lg_group) / VEC / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
         }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) y[i] *= inv;
-        st_e4m3<VEC>((uint8_t*)A.y + at, c, A.D, vec, y);
-    } else if (A.y_dtype == GDN_F32) {
-        st_cols<float, VEC>((float*)A.y + at, c, A.D, vec, y);
+        const float scale = fmaxf(m * (1.f / kE4m3Max), kTinyScale);
+        inv = __frcp_rn(scale);
+        if (c < A.D && (c & ((1 << A.lg_group) - 1)) == 0) A.scales[row * (A.D >> A.lg_group) + (c >> A.lg_group)] = scale;
+    }
+    if (OUT != kPlain) {
+        st_e4m3<VEC>((uint8_t*)A.y + at, c, A.D, vec, mul(y, inv));
     } else if (A.y_dtype == GDN_BF16) {
         st_cols<__nv_bfloat16, VEC>((__nv_bfloat16*)A.y + at, c, A.D, vec, y);
+    } else if (A.y_dtype == GDN_F32) {
+        st_cols<float, VEC>((float*)A.y + at, c, A.D, vec, y);
     } else {
         st_cols<__half, VEC>((__half*)A.y + at, c, A.D, vec, y);
     }
 }
 
 // VPT packs a thread; VPT = 0: rows that registers do not hold, read again (from L2) after the sums.
-template <typename T, int VEC, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) rms_forward_kernel(const RmsFwd A)
+// Rows of fewer than the most packs have 256 threads at most, five CTAs an SM: 4096 rows of 6144
+// to codes take 28 us so, 30 us with the four that the compiler's own choice of registers leaves.
+template <typename T, int VEC, int VPT, int OUT>
+__global__ void __launch_bounds__(VPT > 0 && VPT < (VEC > 1 ? 4 : 16) ? 256 : kMaxThreads, VPT > 0 && VPT < (VEC > 1 ? 4 : 16) ? 5 : 1)
+    rms_forward_kernel(const RmsFwd A)
 {
-    __shared__ float2 buf[32 * 16];
-    const int tid = threadIdx.x, tpr = blockDim.x;
+    __shared__ float2 buf[32];
+    const int tid = threadIdx.x, step = blockDim.x * VEC;
     const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     if (row >= A.rows) return;  // the whole row's threads leave together
     const T* x = (const T*)A.x + row * A.xs;
     const T* r = A.res ? (const T*)A.res + row * A.rs : x;
-    const bool res = A.res != nullptr;
-    float s = 0.f, m = 0.f;
-    float h[VPT ? VPT : 1][VEC], w[VPT ? VPT : 1][VEC];
-    const int step = tpr * VEC;
+    Nums<VEC> h[VPT ? VPT : 1], acc;
+    acc.fill(0.f);
+    float m = 0.f;
+    auto sum_at = [&](int c) {
+        const uint4 a = ld_cols<T, VEC>(x, c, A.D, A.vec);
+        if (!A.res) return widen<T, VEC>(a);
+        return add(widen<T, VEC>(a), widen<T, VEC>(ld_cols<T, VEC>(r, c, A.D, A.vec)));
+    };
+    auto take = [&](const Nums<VEC>& hv, int c) {
+        acc = fma(hv, hv, acc);
+        if (OUT == kRowCodes) m = fmaxf(m, mul(hv, ld_weight<VEC>(A.w, A.w_dtype, c, A.D, A.vec)).max_abs());
+    };
     if (VPT) {
-        Pack<T, VEC> px[VPT ? VPT : 1], pr[VPT ? VPT : 1];
+        uint4 px[VPT ? VPT : 1], pr[VPT ? VPT : 1];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            px[v] = ld_cols<T, VEC>(x, tid * VEC + v * step, A.D, A.vec);
-            if (res) pr[v] = ld_cols<T, VEC>(r, tid * VEC + v * step, A.D, A.vec);
+        for (int v = 0; v < VPT; ++v) px[v] = ld_cols<T, VEC>(x, tid * VEC + v * step, A.D, A.vec);
+        if (A.res) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) pr[v] = ld_cols<T, VEC>(r, tid * VEC + v * step, A.D, A.vec);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) h[v] = add(widen<T, VEC>(px[v]), widen<T, VEC>(pr[v]));
+        } else {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) h[v] = widen<T, VEC>(px[v]);
         }
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) ld_weight<VEC>(w[v], A.w, A.w_dtype, tid * VEC + v * step, A.D, A.vec);
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            sum_pack<T, VEC>(h[v], px[v], pr[v], res);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                s = fmaf(h[v][i], h[v][i], s);
-                m = fmaxf(m, fabsf(h[v][i] * w[v][i]));
-            }
-        }
+        for (int v = 0; v < VPT; ++v) take(h[v], tid * VEC + v * step);
     } else {
-        for (int c = tid * VEC; c < A.D; c += step) {
-            const Pack<T, VEC> px = ld_cols<T, VEC>(x, c, A.D, A.vec), pr = ld_cols<T, VEC>(r, c, A.D, A.vec);
-            sum_pack<T, VEC>(h[0], px, pr, res);
-            ld_weight<VEC>(w[0], A.w, A.w_dtype, c, A.D, A.vec);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                s = fmaf(h[0][i], h[0][i], s);
-                m = fmaxf(m, fabsf(h[0][i] * w[0][i]));
-            }
-        }
+        for (int c = tid * VEC; c < A.D; c += step) take(sum_at(c), c);
     }
-    const float2 sm = row_reduce(s, m, buf + 32 * threadIdx.y, tid, tpr, 1 + threadIdx.y);
-    const float rstd = 1.f / sqrtf(sm.x * A.inv_D + A.eps);
-    const float scale = fmaxf(sm.y * rstd / kE4m3Max, kTinyScale), inv = 1.f / scale;
+    const float2 sm = row_reduce<OUT == kRowCodes, false>(acc.sum(), m, buf);
+    const float rstd = rsqrtf(sm.x * A.inv_D + A.eps);
+    const float scale = fmaxf(sm.y * rstd * (1.f / kE4m3Max), kTinyScale), inv = __frcp_rn(scale);
     if (tid == 0) {
         if (A.rstd) A.rstd[row] = rstd;
-        if (A.y_dtype == RMS_E4M3 && !A.group) A.scales[row] = scale;
+        if (OUT == kRowCodes) A.scales[row] = scale;
     }
     if (VPT) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) finish_pack<T, VEC>(A, h[v], w[v], row, tid * VEC + v * step, rstd, inv);
+        for (int v = 0; v < VPT; ++v) finish_pack<T, VEC, OUT>(A, h[v], row, tid * VEC + v * step, rstd, inv);
     } else {
         // whole steps, so that the lanes that share a scale stay together
-        for (int c0 = 0; c0 < A.D; c0 += step) {
-            const int c = c0 + tid * VEC;
-            const Pack<T, VEC> px = ld_cols<T, VEC>(x, c, A.D, A.vec), pr = ld_cols<T, VEC>(r, c, A.D, A.vec);
-            sum_pack<T, VEC>(h[0], px, pr, res);
-            ld_weight<VEC>(w[0], A.w, A.w_dtype, c, A.D, A.vec);
-            finish_pack<T, VEC>(A, h[0], w[0], row, c, rstd, inv);
-        }
+        for (int c0 = 0; c0 < A.D; c0 += step) finish_pack<T, VEC, OUT>(A, sum_at(c0 + tid * VEC), row, c0 + tid * VEC, rstd, inv);
     }
 }
 
-// Rows blockIdx.x blockDim.y + threadIdx.y, then a whole grid of rows further: a thread keeps its columns,
-// their weights and their part of dweight in registers over all its rows.
-template <typename T, int VEC, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) rms_backward_kernel(const RmsBwd A)
+__device__ __forceinline__ void copy_async(uint4* to, const void* from, bool there)
 {
-    extern __shared__ float sums[];  // [blockDim.y][D] at the end
-    __shared__ float2 buf[2][32 * 16];
-    const int tid = threadIdx.x, tpr = blockDim.x, step = tpr * VEC;
-    float w[VPT][VEC], dw[VPT][VEC];
+    const uint32_t bytes = there ? 16 : 0;  // 0: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(bytes) : "memory");
+}
+
+// Rows blockIdx.x blockDim.y + threadIdx.y, then a whole grid of rows further: a thread keeps its columns,
+// their weights and their part of dweight in registers over all its rows.  Whole packs come through a
+// ring of rows in shared memory, where every thread copies and reads places of its own, so that
+// the rows in flight need neither registers nor barriers.
+template <typename T, int VEC, int VPT, int RING>
+__global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
+{
+    extern __shared__ uint4 ring[];  // [RING][3 VPT][threads]; at the end, as floats, [blockDim.y][D]
+    __shared__ float2 buf[2][kRingThreads / 32];
+    const int tid = threadIdx.x, step = blockDim.x * VEC;
+    const int threads = blockDim.x * blockDim.y, own = threadIdx.y * blockDim.x + tid;
+    const bool vec = VEC > 1 && A.vec;
+    tc::grid_dep_launch();
+    Nums<VEC> w[VPT], dw[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        ld_weight<VEC>(w[v], A.w, A.w_dtype, tid * VEC + v * step, A.D, A.vec);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) dw[v][i] = 0.f;
+        w[v] = ld_weight<VEC>(A.w, A.w_dtype, tid * VEC + v * step, A.D, A.vec);
+        dw[v].fill(0.f);
     }
-    int set = 0;
-    for (long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y; row < A.rows;
-         row += (long long)gridDim.x * blockDim.y, set ^= 1) {
-        const T *h = (const T*)A.h + row * A.hs, *dy = (const T*)A.dy + row * A.dys;
-        const T* dh = A.dh ? (const T*)A.dh + row * A.D : nullptr;
-        const float rstd = __ldg(A.rstd + row);
-        Pack<T, VEC> ph[VPT], pd[VPT], pg[VPT];
+    const long long all = (long long)gridDim.x * blockDim.y, row0 = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    const T *h = (const T*)A.h, *dy = (const T*)A.dy, *dh = (const T*)A.dh;
+    auto fetch = [&](long long row, int slot) {
+        if (row < A.rows) {
+            uint4* to = ring + (size_t)slot * 3 * VPT * threads + own;
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int c = tid * VEC + v * step;
-            ph[v] = ld_cols<T, VEC>(h, c, A.D, A.vec);
-            pd[v] = ld_cols<T, VEC>(dy, c, A.D, A.vec);
-            if (dh) pg[v] = ld_cols<T, VEC>(dh, c, A.D, A.vec);
+            for (int v = 0; v < VPT; ++v) {
+                const int c = tid * VEC + v * step, cc = c < A.D ? c : 0;
+                copy_async(to + (3 * v) * threads, h + row * A.hs + cc, c < A.D);
+                copy_async(to + (3 * v + 1) * threads, dy + row * A.dys + cc, c < A.D);
+                if (dh) copy_async(to + (3 * v + 2) * threads, dh + row * A.D + cc, c < A.D);
+            }
         }
-        float s = 0.f;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (vec) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float n = ph[v].get(i) * rstd, d = pd[v].get(i);
-                s = fmaf(d * w[v][i], n, s);
-                dw[v][i] = fmaf(d, n, dw[v][i]);
-            }
-        const float c = row_reduce(s, 0.f, buf[set] + 32 * threadIdx.y, tid, tpr, 1 + threadIdx.y).x * A.inv_D;
+        for (int i = 0; i < RING - 1; ++i) fetch(row0 + i * all, i);
+    }
+    int set = 0, slot = 0;
+    for (long long row = row0; row < A.rows; row += all, set ^= 1, slot = (slot + 1) % RING) {
+        const float rstd = __ldg(A.rstd + row);
+        if (vec) {
+            fetch(row + (RING - 1) * all, (slot + RING - 1) % RING);
+            asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+        }
+        Nums<VEC> n[VPT], t[VPT], acc;
+        uint4 pg[VPT];
+        acc.fill(0.f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            float o[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                o[i] = rstd * fmaf(-(ph[v].get(i) * rstd), c, pd[v].get(i) * w[v][i]);
-                if (dh) o[i] += pg[v].get(i);
+            uint4 a, b;
+            const int c = tid * VEC + v * step;
+            if (vec) {
+                const uint4* from = ring + ((size_t)slot * 3 * VPT + 3 * v) * threads + own;
+                a = from[0];
+                b = from[threads];
+                if (dh) pg[v] = from[2 * threads];
+            } else {
+                a = ld_cols<T, VEC>(h + row * A.hs, c, A.D, false);
+                b = ld_cols<T, VEC>(dy + row * A.dys, c, A.D, false);
+                if (dh) pg[v] = ld_cols<T, VEC>(dh + row * A.D, c, A.D, false);
             }
-            st_cols<T, VEC>((T*)A.dx + row * A.D, tid * VEC + v * step, A.D, A.vec, o);
+            n[v] = mul(widen<T, VEC>(a), rstd);
+            t[v] = widen<T, VEC>(b);
+            dw[v] = fma(t[v], n[v], dw[v]);
+            t[v] = mul(t[v], w[v]);
+            acc = fma(t[v], n[v], acc);
+        }
+        const float c = -rstd * (row_reduce<false, true>(acc.sum(), 0.f, buf[set] + threadIdx.y * (blockDim.x >> 5)).x * A.inv_D);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            Nums<VEC> o;
+            if (dh) o = fma(t[v], rstd, widen<T, VEC>(pg[v]));
+            else o = mul(t[v], rstd);
+            st_cols<T, VEC>((T*)A.dx + row * A.D, tid * VEC + v * step, A.D, A.vec, fma(n[v], c, o));
         }
     }
     if (!A.part) return;
-    float* mine = sums + (size_t)threadIdx.y * A.D;
     float* out = A.part + (size_t)blockIdx.x * A.D;
     if (blockDim.y > 1) {
+        float* sums = reinterpret_cast<float*>(ring);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();  // the ring is read
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
+            for (int i = 0; i < VEC; i += 2) {
                 const int c = tid * VEC + v * step + i;
-                if (c < A.D) mine[c] = dw[v][i];
+                const float2 x = dw[v].pair(i);
+                if (c < A.D) sums[(size_t)threadIdx.y * A.D + c] = x.x;
+                if (VEC > 1 && c + 1 < A.D) sums[(size_t)threadIdx.y * A.D + c + 1] = x.y;
             }
         __syncthreads();
-        for (int c = threadIdx.y * tpr + tid; c < A.D; c += tpr * blockDim.y) {
+        for (int c = own; c < A.D; c += threads) {
             float t = 0.f;
             for (int r = 0; r < (int)blockDim.y; ++r) t += sums[(size_t)r * A.D + c];
             out[c] = t;
         }
     } else {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int c = tid * VEC + v * step + i;
-                if (c < A.D) out[c] = dw[v][i];
-            }
+        for (int v = 0; v < VPT; ++v) st_cols<float, VEC>(out, tid * VEC + v * step, A.D, A.vec, dw[v]);
     }
 }
 
@@ -363,7 +494,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_backward_long_kernel(const Rm
     float s = 0.f;
     for (int c = threadIdx.x; c < A.D; c += blockDim.x)
         s = fmaf(to_f32(dy[c]) * (A.w ? ld_any(A.w, c, A.w_dtype) : 1.f), to_f32(h[c]) * rstd, s);
-    const float m = row_reduce(s, 0.f, buf, threadIdx.x, blockDim.x, 1).x * A.inv_D;
+    const float m = row_reduce<false, false>(s, 0.f, buf).x * A.inv_D;
     for (int c = threadIdx.x; c < A.D; c += blockDim.x) {
         float o = rstd * fmaf(-(to_f32(h[c]) * rstd), m, to_f32(dy[c]) * (A.w ? ld_any(A.w, c, A.w_dtype) : 1.f));
         if (dh) o += to_f32(dh[c]);
@@ -382,19 +513,24 @@ __global__ void __launch_bounds__(256) rms_dweight_long_kernel(const RmsBwd A)
     A.part[(size_t)blockIdx.x * A.D + c] = t;
 }
 
-// dweight = the parts' sum, 32 columns a CTA, 8 warps over the parts.
-__global__ void __launch_bounds__(256) rms_dweight_sum_kernel(const float* part, int parts, int D, float* dweight)
+// dweight = the parts' sum, 8 columns a CTA, 16 threads over the parts of each.  Small CTAs: they are
+// resident beside the rows' CTAs (which leave them an eighth of the registers) before those end.
+__global__ void __launch_bounds__(128) rms_dweight_sum_kernel(const float* part, int parts, int D, float* dweight)
 {
-    __shared__ float s[8][32];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+    __shared__ float s[16][9];
+    const int col = threadIdx.x & 7, g = threadIdx.x >> 3, c = blockIdx.x * 8 + col;
+    tc::grid_dep_wait();
     float t = 0.f;
-    if (c < D)
-        for (int p = g; p < parts; p += 8) t += part[(size_t)p * D + c];
-    s[g][threadIdx.x & 31] = t;
+    if (c < D) {
+#pragma unroll 10
+        for (int p = g; p < parts; p += 16) t += __ldcg(part + (size_t)p * D + c);
+    }
+    s[g][col] = t;
     __syncthreads();
-    if (g == 0 && c < D) {
+    if (threadIdx.x < 8 && c < D) {
+        t = 0.f;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) t += s[i][threadIdx.x];
+        for (int i = 0; i < 16; ++i) t += s[i][threadIdx.x];
         dweight[c] = t;
     }
 }
@@ -405,80 +541,115 @@ struct Shape {
 };
 
 // The layout, and with it the order of every sum, goes by D, the rows and the types alone: the same numbers give the
-// same bits whatever their alignment (packs off their 16 bytes are loaded one by one).
-Shape shape_of(const rms_params_t* p, int max_regs)
+// same bits whatever their alignment (packs off their 16 bytes are loaded one by one).  `most`: elements
+// of a thread; `threads`: below so many, a thread takes one pack more only when its row has more than that.
+Shape shape_of(const rms_params_t* p, int most, int threads, int max_threads)
 {
-    const int64_t D = p->D, rows = p->rows;
     const int vecn = 16 / (int)elem_size(p->x_dtype);
     Shape s{};
-    s.vec = D % vecn == 0 ? vecn : 1;
-    const int64_t packs = (D + s.vec - 1) / s.vec;
-    const int most = max_regs / s.vec;  // packs that a thread's registers hold
+    s.vec = p->D % vecn == 0 ? vecn : 1;
+    const int64_t packs = (p->D + s.vec - 1) / s.vec;
+    most /= s.vec;
+    s.ry = 1;
     s.vpt = 1;
-    while (s.vpt < most && packs > 256 * (int64_t)s.vpt) s.vpt *= 2;
-    int64_t t = (packs + s.vpt - 1) / s.vpt;
-    t = (t + 31) / 32 * 32;
-    if (t > kMaxThreads) {
-        s.vpt = 0;
-        t = kMaxThreads;
-    }
-    s.tpr = (int)t;
-    s.ry = s.tpr >= 256 ? 1 : 256 / s.tpr;
-    while (s.ry > 1 && rows < (int64_t)s.ry * kNumSMs) s.ry /= 2;
+    while (s.vpt < most && packs > threads * (int64_t)s.vpt) s.vpt = s.vec > 1 && s.vpt < 4 ? s.vpt + 1 : 2 * s.vpt;
+    const int64_t t = ((packs + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+    if (t > max_threads) s.vpt = 0;
+    s.tpr = t > max_threads ? max_threads : (int)t;
     return s;
+}
+
+// Forward: a CTA a row, 256 threads before a thread takes a second pack; short rows (up to 16 elements a
+// lane) a warp each, several to a CTA where there are many.
+Shape fwd_shape(const rms_params_t* p)
+{
+    const int vecn = 16 / (int)elem_size(p->x_dtype);
+    const bool shorter = p->D <= 512;
+    Shape s = shape_of(p, p->D % vecn == 0 ? 4 * vecn : 16, shorter ? 32 : 256, kMaxThreads);
+    if (shorter && s.tpr == 32) {
+        s.ry = 8;
+        while (s.ry > 1 && p->rows < (int64_t)s.ry * 2 * kNumSMs) s.ry /= 2;
+    }
+    return s;
+}
+
+// Backward: a row's exchange between threads costs as much as 16 elements' arithmetic, so 16 elements a
+// thread; one CTA of up to 512 threads an SM.
+Shape bwd_shape(const rms_params_t* p)
+{
+    Shape s = shape_of(p, 16, 32, kRingThreads);
+    if (s.vpt > 0) {
+        s.ry = kRingThreads / s.tpr;
+        while (s.ry > 1 && p->rows < (int64_t)s.ry * kNumSMs) s.ry /= 2;
+    }
+    return s;
+}
+
+template <typename T, int VEC, int VPT>
+int launch_fwd_v(const RmsFwd& A, const Shape& s, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)((A.rows + s.ry - 1) / s.ry);
+    const dim3 block(s.tpr, s.ry);
+    if (A.y_dtype != RMS_E4M3) rms_forward_kernel<T, VEC, VPT, kPlain><<<grid, block, 0, st>>>(A);
+    else if (!A.lg_group) rms_forward_kernel<T, VEC, VPT, kRowCodes><<<grid, block, 0, st>>>(A);
+    else if constexpr (VEC > 1) rms_forward_kernel<T, VEC, VPT, kGroupCodes><<<grid, block, 0, st>>>(A);
+    return (int)cudaGetLastError();
 }
 
 template <typename T, int VEC>
 int launch_fwd(const RmsFwd& A, const Shape& s, cudaStream_t st)
 {
-    const dim3 block(s.tpr, s.ry);
-    const unsigned grid = (unsigned)((A.rows + s.ry - 1) / s.ry);
-    constexpr int M = 32 / VEC;  // most packs of a thread
-    if (s.vpt == 0) rms_forward_kernel<T, VEC, 0><<<grid, block, 0, st>>>(A);
-    else if (s.vpt == 1) rms_forward_kernel<T, VEC, 1><<<grid, block, 0, st>>>(A);
-    else if (s.vpt == 2) rms_forward_kernel<T, VEC, 2><<<grid, block, 0, st>>>(A);
-    else if (s.vpt == 4) rms_forward_kernel<T, VEC, 4><<<grid, block, 0, st>>>(A);
-    else if (s.vpt == 8) rms_forward_kernel<T, VEC, M < 8 ? M : 8><<<grid, block, 0, st>>>(A);
-    else if (s.vpt == 16) rms_forward_kernel<T, VEC, M < 16 ? M : 16><<<grid, block, 0, st>>>(A);
-    else rms_forward_kernel<T, VEC, M><<<grid, block, 0, st>>>(A);
-    return (int)cudaGetLastError();
+    switch (s.vpt) {
+        case 1: return launch_fwd_v<T, VEC, 1>(A, s, st);
+        case 2: return launch_fwd_v<T, VEC, 2>(A, s, st);
+        case 3: if constexpr (VEC > 1) return launch_fwd_v<T, VEC, 3>(A, s, st); break;
+        case 4: return launch_fwd_v<T, VEC, 4>(A, s, st);
+        case 8: if constexpr (VEC == 1) return launch_fwd_v<T, VEC, 8>(A, s, st); break;
+        case 16: if constexpr (VEC == 1) return launch_fwd_v<T, VEC, 16>(A, s, st); break;
+        default: return launch_fwd_v<T, VEC, 0>(A, s, st);
+    }
+    return (int)cudaErrorInvalidValue;
 }
 
 template <typename T, int VEC, int VPT>
 int launch_bwd_v(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
 {
-    const size_t smem = A.part && s.ry > 1 ? (size_t)s.ry * A.D * 4 : 0;
+    const size_t row = (size_t)3 * VPT * s.tpr * s.ry * 16;  // of a ring: 96 KB at most
+    const bool deep = 4 * row <= 200 * 1024;
+    size_t smem = VEC > 1 && A.vec ? (deep ? 4 : 2) * row : 0;
+    if (A.part && s.ry > 1 && smem < (size_t)s.ry * A.D * 4) smem = (size_t)s.ry * A.D * 4;
+    const auto kernel = deep ? rms_backward_kernel<T, VEC, VPT, 4> : rms_backward_kernel<T, VEC, VPT, 2>;
     if (smem > 40 * 1024) {
-        const int e = (int)cudaFuncSetAttribute(rms_backward_kernel<T, VEC, VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const int e = (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e) return e;
     }
-    rms_backward_kernel<T, VEC, VPT><<<ctas, dim3(s.tpr, s.ry), smem, st>>>(A);
+    kernel<<<ctas, dim3(s.tpr, s.ry), smem, st>>>(A);
     return (int)cudaGetLastError();
 }
 
 template <typename T, int VEC>
 int launch_bwd(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
 {
-    constexpr int M = 16 / VEC < 1 ? 1 : 16 / VEC;
-    if (s.vpt == 0) {
-        rms_backward_long_kernel<T><<<(unsigned)A.rows, kMaxThreads, 0, st>>>(A);
-        if (A.part) rms_dweight_long_kernel<T><<<dim3(ctas, (A.D + 255) / 256), 256, 0, st>>>(A);
-        return (int)cudaGetLastError();
+    switch (s.vpt) {
+        case 1: return launch_bwd_v<T, VEC, 1>(A, s, ctas, st);
+        case 2: return launch_bwd_v<T, VEC, 2>(A, s, ctas, st);
+        case 3: if constexpr (VEC == 4) return launch_bwd_v<T, VEC, 3>(A, s, ctas, st); break;
+        case 4: if constexpr (VEC <= 4) return launch_bwd_v<T, VEC, 4>(A, s, ctas, st); break;
+        case 8: if constexpr (VEC == 1) return launch_bwd_v<T, VEC, 8>(A, s, ctas, st); break;
+        case 16: if constexpr (VEC == 1) return launch_bwd_v<T, VEC, 16>(A, s, ctas, st); break;
+        default:
+            rms_backward_long_kernel<T><<<(unsigned)A.rows, kMaxThreads, 0, st>>>(A);
+            if (A.part) rms_dweight_long_kernel<T><<<dim3(ctas, (A.D + 255) / 256), 256, 0, st>>>(A);
+            return (int)cudaGetLastError();
     }
-    if (s.vpt == 1) return launch_bwd_v<T, VEC, 1>(A, s, ctas, st);
-    if (s.vpt == 2) return launch_bwd_v<T, VEC, 2>(A, s, ctas, st);
-    if (s.vpt == 4) return launch_bwd_v<T, VEC, M < 4 ? M : 4>(A, s, ctas, st);
-    if (s.vpt == 8) return launch_bwd_v<T, VEC, M < 8 ? M : 8>(A, s, ctas, st);
-    return launch_bwd_v<T, VEC, M>(A, s, ctas, st);
+    return (int)cudaErrorInvalidValue;
 }
 
-// CTAs of the backward, each with its own part of dweight: every SM's registers once.
+// CTAs of the backward, each with its own part of dweight.
 int bwd_ctas(const rms_params_t* p, const Shape& s)
 {
-    int64_t per_sm = 1024 / (s.tpr * s.ry);
-    if (per_sm < 1) per_sm = 1;
     const int64_t need = (p->rows + s.ry - 1) / s.ry;
-    return (int)(need < kNumSMs * per_sm ? need : kNumSMs * per_sm);
+    return (int)(need < kNumSMs ? need : kNumSMs);
 }
 
 int fail(int code, const char* msg)
@@ -530,7 +701,7 @@ using namespace gdn;
 extern "C" size_t rms_backward_workspace_bytes(const rms_params_t* p)
 {
     if (check(p) != GDN_OK || p->rows == 0) return 0;
-    return (size_t)bwd_ctas(p, shape_of(p, 16)) * p->D * 4;
+    return (size_t)bwd_ctas(p, bwd_shape(p)) * p->D * 4;
 }
 
 extern "C" int rms_forward(const rms_params_t* p, const void* x, const void* residual, const void* weight, void* h, void* y,
@@ -560,10 +731,10 @@ extern "C" int rms_forward(const rms_params_t* p, const void* x, const void* res
     RmsFwd A{};
     A.x = x; A.res = residual; A.w = weight; A.h = h; A.y = y; A.scales = e4 ? scales : nullptr; A.rstd = rstd;
     A.xs = p->x_s; A.rs = p->res_s; A.rows = (int)p->rows; A.D = (int)p->D;
-    A.w_dtype = p->w_dtype; A.y_dtype = p->y_dtype; A.group = e4 ? p->group : 0;
+    A.w_dtype = p->w_dtype; A.y_dtype = p->y_dtype; A.lg_group = e4 && p->group ? (p->group == 16 ? 4 : p->group == 32 ? 5 : p->group == 64 ? 6 : 7) : 0;
     A.eps = p->eps; A.inv_D = 1.f / (float)p->D;
     A.vec = wide_ok(p, {x, residual, weight, h, y});
-    const Shape s = shape_of(p, 32);
+    const Shape s = fwd_shape(p);
     cudaStream_t cs = (cudaStream_t)stream;
     int e;
     if (p->x_dtype == GDN_F32) e = s.vec > 1 ? launch_fwd<float, 4>(A, s, cs) : launch_fwd<float, 1>(A, s, cs);
@@ -607,15 +778,24 @@ extern "C" int rms_backward(const rms_params_t* p, const void* h, const void* we
     A.hs = p->x_s; A.dys = p->res_s; A.rows = (int)p->rows; A.D = (int)p->D; A.w_dtype = p->w_dtype;
     A.inv_D = 1.f / (float)p->D;
     A.vec = wide_ok(p, {h, weight, dy, dh, dx});
-    const Shape s = shape_of(p, 16);
+    const Shape s = bwd_shape(p);
     const int ctas = bwd_ctas(p, s);
     int e;
     if (p->x_dtype == GDN_F32) e = s.vec > 1 ? launch_bwd<float, 4>(A, s, ctas, cs) : launch_bwd<float, 1>(A, s, ctas, cs);
     else if (p->x_dtype == GDN_BF16) e = s.vec > 1 ? launch_bwd<__nv_bfloat16, 8>(A, s, ctas, cs) : launch_bwd<__nv_bfloat16, 1>(A, s, ctas, cs);
     else e = s.vec > 1 ? launch_bwd<__half, 8>(A, s, ctas, cs) : launch_bwd<__half, 1>(A, s, ctas, cs);
     if (!e && dweight) {
-        rms_dweight_sum_kernel<<<(unsigned)((p->D + 31) / 32), 256, 0, cs>>>(A.part, ctas, A.D, dweight);
-        e = (int)cudaGetLastError();
+        // starts while the rows run and waits on the device for their end
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)((p->D + 7) / 8));
+        cfg.blockDim = dim3(128);
+        cfg.stream = cs;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = (int)cudaLaunchKernelEx(&cfg, rms_dweight_sum_kernel, (const float*)A.part, ctas, A.D, dweight);
     }
     return e ? cuda_fail(e, "rms_backward launch") : GDN_OK;
 }

@@ -109,8 +109,16 @@ def supported(p: DecodeParams) -> int:
     return int(_lib.gdn_decode_supported(ctypes.byref(p)))
 
 
+def _stream(stream):
+    """A stream's handle as a number (default: the current device's current stream)."""
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle itself: torch.cuda.current_stream() makes an object around it, 3 us a call
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _index(t, what):
-    if t.dtype != torch.int32 or (t.numel() and not t.is_contiguous()):
+    if t.dtype != torch.int32 or not t.is_contiguous():
         raise TypeError(f"{what} must be contiguous int32")
     return t.data_ptr()
 
@@ -121,7 +129,7 @@ def gdn_decode(p: DecodeParams, q, k, v, g, beta, cu_tokens, pool, slot_in, slot
         raise ValueError("slot_in and slot_out must have n_seq entries, cu_tokens n_seq + 1")
     st = _lib.gdn_decode(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                          None if cu_tokens is None else _index(cu_tokens, "cu_tokens"), pool.data_ptr(),
-                         _index(slot_in, "slot_in"), _index(slot_out, "slot_out"), y.data_ptr(), gdn._stream_handle(stream))
+                         _index(slot_in, "slot_in"), _index(slot_out, "slot_out"), y.data_ptr(), _stream(stream))
     if st != gdn.GDN_OK:
         raise gdn.GdnError(st, "gdn_decode")
 
@@ -146,6 +154,6 @@ def gdn_states_move(pool, src, dst, group=1, stream=None):
     state = pool.numel() // (L * S) * es if L * S else 0
     st = _lib.gdn_states_move(pool.data_ptr(), L, pool.stride(0) * es if L > 1 else 0, S,
                               pool.stride(1) * es if S > 1 else state, state, _index(src, "src"), _index(dst, "dst"),
-                              src.numel(), group, gdn._stream_handle(stream))
+                              src.numel(), group, _stream(stream))
     if st != gdn.GDN_OK:
         raise gdn.GdnError(st, "gdn_states_move")

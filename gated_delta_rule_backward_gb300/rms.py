@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import gdn
-from .decode import DTYPE_CODES
+from .decode import DTYPE_CODES, _stream
 
 _lib = gdn._lib
 
@@ -87,7 +87,7 @@ def _ptr(t):
 def rms_forward(p: RmsParams, x, residual, weight, h, y, scales, rstd, stream=None):
     """Raw C-ABI call; residual, weight, h, scales and rstd may be None."""
     st = _lib.rms_forward(ctypes.byref(p), x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(h), y.data_ptr(), _ptr(scales), _ptr(rstd),
-                          gdn._stream_handle(stream))
+                          _stream(stream))
     if st != gdn.GDN_OK:
         raise gdn.GdnError(st, "rms_forward")
 
@@ -96,7 +96,7 @@ def rms_backward(p: RmsParams, h, weight, rstd, dy, dh, dx, dweight, workspace, 
     """Raw C-ABI call; weight, dh, dweight (and then the workspace) may be None."""
     st = _lib.rms_backward(ctypes.byref(p), h.data_ptr(), _ptr(weight), rstd.data_ptr(), dy.data_ptr(), _ptr(dh), dx.data_ptr(), _ptr(dweight),
                            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                           gdn._stream_handle(stream))
+                           _stream(stream))
     if st != gdn.GDN_OK:
         raise gdn.GdnError(st, "rms_backward")
 
