@@ -1,19 +1,19 @@
 // beam.cu -- a beam search's selection over beams and vocabulary (include/beam.h).
 //
-// Two kernels.  The first cuts every beam's row into segments, one a CTA, each read once into
-// registers: the segment's maximum, the sum of exponentials against it, and its n best logits
-// (the order within a row does not need the row's normaliser).  The second, one CTA a
-// sequence, joins the segments' sums into each row's log-sum-exp, turns the K x segments x n
-// kept logits into scores and selects among them.
+// Two kernels.  The first cuts every beam's row into segments, one a CTA, and reads each once:
+// every 1 to 32 threads leave the maximum of their share (a chunk: their packs of 16 bytes),
+// every CTA its maximum and the sum of exponentials against it.  The second, one CTA a sequence, joins the sums
+// into each row's log-sum-exp, turns chunk maxima into scores, and looks at the few chunks alone that can
+// hold one of the n best: an element among them is at least the n-th largest chunk maximum.
 //
-// Selecting n of a CTA's items: the n-th largest of the threads' maxima is a bound that at
-// least n items reach, and for items in no particular order few more do.  So: every warp
-// gives its R largest thread maxima, the n-th largest of all of those is the bound, and the
-// items that reach it go to a list (in any order).  A list that is still long goes through the same once
-// more, now spread evenly over the threads.  Each listed item's rank is the number of
-// listed keys above its own; keys are (value, lowest index first) in one 64-bit number, so ranks do not
-// depend on the list's order.  Where more items reach the bound than the list holds (many
-// equal values), n rounds of a block-wide maximum select instead.
+// The n-th largest chunk maximum is found in two steps.  The largest that n of the warps' few
+// largest thread maxima reach is a bound that n chunks reach at least, and for chunks in no
+// particular order few more do; those go to a list, and each listed chunk that fewer than n
+// others exceed is read again.  Elements that reach the last of these go to a list of their own,
+// and each one's rank is the number of listed keys above its own.  Keys are (score, lowest
+// index first) in one 64-bit number, so ranks do not depend on the lists' order.  Where a list
+// does not hold all that reach the bound (very many equal scores), n rounds of a CTA-wide
+// maximum over the chunks that reach it select instead.
 #include <climits>
 #include <cstdio>
 
@@ -26,10 +26,11 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;           // of a segment
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxOut = 64, kMaxBeams = 64;
-constexpr int kList = 1024, kLong = 96;  // items a list holds; items from which a second bound pays
-constexpr int kItems = 16;               // keys that a thread of the join holds
+constexpr int kList = 1024;  // items a list holds
+constexpr int kFew = 32;     // chunks that are read without a closer bound
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -42,10 +43,10 @@ struct BeamArgs {
     const int* slots;
     float* scores_out;
     int *parent, *token, *src_slots;
-    float2* sums;  // [N K][splits] maximum and sum of a segment
-    u64* best;     // [N K][splits][n_out] its best (order(logit), ~index) keys, 0 past their number
+    float2* sums;   // [N K][splits] maximum and sum of a segment
+    float* chunks;  // [N K][splits][kThreads >> lg] the maximum of 1 << lg threads
     long long row_stride;
-    int K, V, splits, seg, n, pad;
+    int K, V, splits, seg, lg_packs, lg, n, pad;
 };
 
 // Floats as whole numbers of the same order; -0 and +0 have to be the same float before.
@@ -72,124 +73,6 @@ __device__ __forceinline__ float ex2(float x)
 // exp(a - b) for a <= b, 1 where both are the same infinity.
 __device__ __forceinline__ float exp_diff(float a, float b) { return a == b ? 1.f : ex2((a - b) * kLog2e); }
 
-struct SelectSmem {
-    u64 list[2][kList];
-    u64 warp_best[kWarps];
-    u64 out[kMaxOut];
-    __align__(16) unsigned top[kWarps * 8];
-    int count[2];
-};
-
-// R: thread maxima that a warp gives for a selection of n.
-__device__ __forceinline__ int tops_of(int n) { return n <= 16 ? 4 : 8; }
-
-// A warp's R largest of its lanes' v (0: none), from high to low; returns the first.
-__device__ __forceinline__ unsigned warp_tops(unsigned v, int R, unsigned* out, int lane)
-{
-    unsigned first = 0;
-    for (int r = 0; r < R; ++r) {
-        const unsigned best = __reduce_max_sync(kAll, v);
-        if (r == 0) first = best;
-        if (lane == 0) out[r] = best;
-        const unsigned who = __ballot_sync(kAll, v == best);
-        if (lane == __ffs(who) - 1) v = 0;
-    }
-    return first;
-}
-
-// The largest of the tops that n of them reach (0 when there is none): every warp finds it by itself.
-__device__ __forceinline__ unsigned nth_top(const unsigned* top, int n, int lane)
-{
-    const uint4* all = reinterpret_cast<const uint4*>(top);
-    unsigned best = 0;
-    if (tops_of(n) == 4) {
-        const unsigned v = top[lane];
-        int reach = 0;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const uint4 t = all[i];
-            reach += (t.x >= v) + (t.y >= v) + (t.z >= v) + (t.w >= v);
-        }
-        best = reach >= n ? v : 0;
-    } else {
-        const unsigned v = top[lane], w = top[32 + lane];
-        int rv = 0, rw = 0;
-#pragma unroll
-        for (int i = 0; i < 2 * kWarps; ++i) {
-            const uint4 t = all[i];
-            rv += (t.x >= v) + (t.y >= v) + (t.z >= v) + (t.w >= v);
-            rw += (t.x >= w) + (t.y >= w) + (t.z >= w) + (t.w >= w);
-        }
-        best = max(rv >= n ? v : 0, rw >= n ? w : 0);
-    }
-    best = __reduce_max_sync(kAll, best);
-    return best > kNegInf ? best : kNegInf + 1;  // an item at -inf is none
-}
-
-// The n best keys of the CTA's items into S.out (0 past their number), from high to low.  `each(bound, take)`
-// calls take(order(value), index) for every item of this thread whose order reaches bound; `mine` is the largest.
-// S.top holds the warps' tops and S.count 0, a barrier ago.  Ends with a barrier.
-template <typename Each>
-__device__ __forceinline__ void select_n(SelectSmem& S, int n, unsigned mine, const Each& each)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned bound = nth_top(S.top, n, lane);
-    if (mine >= bound)
-        each(bound, [&](unsigned o, unsigned index) {
-            const int at = atomicAdd(&S.count[0], 1);
-            if (at < kList) S.list[0][at] = key_of(o, index);
-        });
-    __syncthreads();
-    int listed = S.count[0];
-    if (listed <= kList) {
-        const u64* list = S.list[0];
-        if (listed > kLong) {
-            unsigned best = 0;
-            for (int t = tid; t < listed; t += kThreads) best = max(best, (unsigned)(S.list[0][t] >> 32));
-            const int R = tops_of(n);
-            warp_tops(best, R, S.top + warp * R, lane);
-            __syncthreads();
-            const unsigned closer = nth_top(S.top, n, lane);
-            for (int t = tid; t < listed; t += kThreads) {
-                const u64 key = S.list[0][t];
-                if ((unsigned)(key >> 32) >= closer) S.list[1][atomicAdd(&S.count[1], 1)] = key;
-            }
-            __syncthreads();
-            listed = S.count[1];
-            list = S.list[1];
-        }
-        for (int t = tid; t < listed; t += kThreads) {
-            const u64 key = list[t];
-            int rank = 0;
-            for (int i = 0; i < listed; ++i) rank += list[i] > key;
-            if (rank < n) S.out[rank] = key;
-        }
-        for (int i = listed + tid; i < n; i += kThreads) S.out[i] = 0;
-        __syncthreads();
-        return;
-    }
-    u64 last = ~0ull;
-    for (int r = 0; r < n; ++r) {
-        u64 best = 0;
-        if (mine >= bound)
-            each(bound, [&](unsigned o, unsigned index) {
-                const u64 key = key_of(o, index);
-                if (key < last && key > best) best = key;
-            });
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            const u64 other = __shfl_xor_sync(kAll, best, o);
-            best = other > best ? other : best;
-        }
-        if (lane == 0) S.warp_best[warp] = best;
-        __syncthreads();
-        last = 0;
-        for (int i = 0; i < kWarps; ++i) last = S.warp_best[i] > last ? S.warp_best[i] : last;
-        if (tid == 0) S.out[r] = last;
-        __syncthreads();
-    }
-}
-
 // The largest of a pack's elements; one that is NaN does not count.
 __device__ __forceinline__ float pack_max(const Pack<float, 4>& v)
 {
@@ -208,39 +91,56 @@ __device__ __forceinline__ float pack_max(const Pack<__half, 8>& v)
     return fmaxf(m.x, m.y);
 }
 
+// A row's packs lie on 16-byte boundaries: it starts `lead` elements into the first.  Pack p of thread t of segment
+// `split` begins at element split seg - lead + (256 p + t) VEC; what is outside the row or the segment reads as -inf.
+template <typename T>
+__device__ __forceinline__ int lead_of(const T* row)
+{
+    return (int)(((uintptr_t)row & 15) / sizeof(T));
+}
+// N packs whose first elements are at first + in(p): the whole ones all in flight at once, then the few elements of a
+// pack that the row's ends cut.
+template <typename T, int VEC, int N, typename In>
+__device__ __forceinline__ void ld_chunk_packs(Pack<T, VEC> (&x)[N], const T* row, int first, int seg, int V, const In& in)
+{
+    Pack<T, VEC> none;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) none.x[i] = from_f32<T>(-INFINITY);
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        const int at = first + in(p);
+        x[p] = none;
+        if (in(p) < seg && at >= 0 && at + VEC <= V) x[p] = ld_pack<T, VEC>(row + at, true);
+    }
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        const int at = first + in(p);
+        if (in(p) < seg && ((at < 0 && at + VEC > 0) || (at < V && at + VEC > V))) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (at + i >= 0 && at + i < V) x[p].x[i] = row[at + i];
+        }
+    }
+}
+
 // PACKS loads of 16 bytes a thread.
 template <typename T, int PACKS>
-__global__ void __launch_bounds__(kThreads, PACKS == 8 ? 3 : 4) beam_segment_kernel(const BeamArgs A)
+__global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamArgs A)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
-    __shared__ SelectSmem S;
     __shared__ float2 part[kWarps];
     const int row = blockIdx.x / A.splits, split = blockIdx.x - row * A.splits;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     tc::grid_dep_launch();
+    const T* base = (const T*)A.logits + row * A.row_stride;
+    const int first = split * A.seg - lead_of(base);
     if ((A.done && A.done[row]) || !(A.scores[row] > -INFINITY)) return;
 
-    // The segment's packs lie on 16-byte boundaries: the row starts `lead` elements into the first.
-    const T* base = (const T*)A.logits + row * A.row_stride;
-    const int lead = (int)(((uintptr_t)base & 15) / sizeof(T));
-    const int first = split * A.seg - lead;
     Pack<T, VEC> x[PACKS];
+    ld_chunk_packs<T, VEC, PACKS>(x, base, first, A.seg, A.V, [&](int p) { return (p * kThreads + tid) * VEC; });
+    float m = -INFINITY;
 #pragma unroll
-    for (int p = 0; p < PACKS; ++p) {
-        const int in = (p * kThreads + tid) * VEC, at = first + in;
-        if (in < A.seg && at >= 0 && at + VEC <= A.V) {
-            x[p] = ld_pack<T, VEC>(base + at, true);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) x[p].x[i] = in < A.seg && at + i >= 0 && at + i < A.V ? base[at + i] : from_f32<T>(-INFINITY);
-        }
-    }
-    float top[PACKS], m = -INFINITY;
-#pragma unroll
-    for (int p = 0; p < PACKS; ++p) {
-        top[p] = fmaxf(pack_max(x[p]), -INFINITY);  // a pack of NaNs
-        m = fmaxf(m, top[p]);
-    }
+    for (int p = 0; p < PACKS; ++p) m = fmaxf(m, pack_max(x[p]));  // a pack of NaNs: -inf stays
     // The sum against the thread's own maximum: (x - m) log2 e in two roundings, then the exponential.
     float s = 0.f;
     if (m < INFINITY && m > -INFINITY) {
@@ -265,10 +165,10 @@ __global__ void __launch_bounds__(kThreads, PACKS == 8 ? 3 : 4) beam_segment_ker
                 s += v == m ? 1.f : v < m ? ex2((v - m) * kLog2e) : 0.f;
             }
     }
-    const unsigned mine = order(m + 0.f);  // + 0: -0 becomes 0
-    const int R = tops_of(A.n);
-    if (tid < 2) S.count[tid] = 0;
-    const float wm = unorder(warp_tops(mine, R, S.top + warp * R, lane));
+    float cm = m;
+    for (int o = 1; o < 1 << A.lg; o <<= 1) cm = fmaxf(cm, __shfl_xor_sync(kAll, cm, o));
+    if ((lane & ((1 << A.lg) - 1)) == 0) A.chunks[((long long)blockIdx.x * kThreads + tid) >> A.lg] = cm;
+    const float wm = unorder(__reduce_max_sync(kAll, order(m + 0.f)));
     s = m > -INFINITY ? s * exp_diff(m, wm) : 0.f;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
@@ -276,142 +176,269 @@ __global__ void __launch_bounds__(kThreads, PACKS == 8 ? 3 : 4) beam_segment_ker
     __syncthreads();
     if (tid == 0) {
         float M = -INFINITY, total = 0.f;
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part[w].x);
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) total += part[w].x > -INFINITY ? part[w].y * exp_diff(part[w].x, M) : 0.f;
         A.sums[blockIdx.x] = make_float2(M, total);
     }
-    select_n(S, A.n, mine, [&](unsigned bound, auto&& take) {
-        const float b = unorder(bound);
-#pragma unroll
-        for (int p = 0; p < PACKS; ++p)
-            if (top[p] >= b) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float v = x[p].get(i);
-                    if (v >= b) take(order(v + 0.f), (unsigned)(first + (p * kThreads + tid) * VEC + i));
-                }
-            }
-    });
-    for (int i = tid; i < A.n; i += kThreads) A.best[(long long)blockIdx.x * A.n + i] = S.out[i];
 }
 
-__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs A)
+// Thread maxima that a warp of the join gives for a bound on the n-th: 32 or 64 in all.
+__device__ __forceinline__ int tops_of(int n) { return (n <= 16 ? 32 : 64) / kJoinWarps; }
+
+// The largest of the tops that n of them reach, by one warp.
+__device__ __forceinline__ unsigned nth_top(const unsigned* top, int n, int lane)
 {
-    __shared__ SelectSmem S;
+    const uint4* all = reinterpret_cast<const uint4*>(top);
+    const int tops = tops_of(n) * kJoinWarps;
+    unsigned best = 0;
+    for (int at = lane; at < tops; at += 32) {
+        const unsigned v = top[at];
+        int reach = 0;
+#pragma unroll 4
+        for (int i = 0; i < tops / 4; ++i) {
+            const uint4 t = all[i];
+            reach += (t.x >= v) + (t.y >= v) + (t.z >= v) + (t.w >= v);
+        }
+        if (reach >= n) best = max(best, v);
+    }
+    best = __reduce_max_sync(kAll, best);
+    return best > kNegInf ? best : kNegInf + 1;  // an item at -inf is none
+}
+
+constexpr int kHeld = 2;  // chunks whose maxima a thread of the join keeps in registers
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs A)
+{
+    constexpr int VEC = 16 / (int)sizeof(T);
+    __shared__ u64 list[2][kList];
+    __shared__ u64 out[kMaxOut], warp_best[kJoinWarps];
+    __shared__ __align__(16) unsigned top[64];
     __shared__ float row_score[kMaxBeams], row_max[kMaxBeams], row_log[kMaxBeams];
-    __shared__ int kind[kMaxBeams], rows_on[kMaxBeams], rows_done[kMaxBeams], n_on, n_done;  // beams that go on, and finished ones
+    __shared__ int kind[kMaxBeams], rows_on[kMaxBeams], row_slot[kMaxBeams], n_on, chunk_count, element_count, kept_count;
+    __shared__ unsigned the_bound, least_kept;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row0 = (long long)blockIdx.x * A.K;
+    const int per = A.splits * (kThreads >> A.lg);  // chunks of a row
     if (tid < A.K) {
         const float score = A.scores[row0 + tid];
         row_score[tid] = score;
+        row_slot[tid] = A.src_slots ? A.slots[row0 + tid] : 0;
         kind[tid] = !(score > -INFINITY) ? -1 : A.done && A.done[row0 + tid] ? 1 : 0;
     }
-    __syncthreads();
     if (tid == 0) {
-        int on = 0, ended = 0;
-        for (int k = 0; k < A.K; ++k) {
-            if (kind[k] == 0) rows_on[on++] = k;
-            else if (kind[k] > 0) rows_done[ended++] = k;
-        }
-        n_on = on;
-        n_done = ended;
+        chunk_count = element_count = kept_count = 0;
+        least_kept = 0xffffffffu;
     }
     __syncthreads();
+    if (warp == 0) {  // the beams that go on, in order
+        int on = 0;
+        for (int k0 = 0; k0 < A.K; k0 += 32) {
+            const bool goes = k0 + lane < A.K && kind[k0 + lane] == 0;
+            const unsigned all = __ballot_sync(kAll, goes);
+            if (goes) rows_on[on + __popc(all & ((1u << lane) - 1))] = k0 + lane;
+            on += __popc(all);
+        }
+        if (lane == 0) n_on = on;
+    }
+    __syncthreads();
+    const int all_chunks = n_on * per;
     tc::grid_dep_wait();
+    // A thread's chunks are tid + j kJoinThreads of the going beams' chunks; the first kHeld stay in registers.
+    float held[kHeld];
+    int held_row[kHeld];
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+        const int i = tid + j * kJoinThreads;
+        held[j] = -INFINITY;
+        held_row[j] = 0;
+        if (i < all_chunks) {
+            const int r = i / per;
+            held_row[j] = rows_on[r];
+            held[j] = __ldcg(A.chunks + (row0 + held_row[j]) * per + (i - r * per));
+        }
+    }
+    for (int r = warp; r < n_on; r += kJoinWarps) {  // a row's log-sum-exp
+        const int k = rows_on[r];
+        float m = -INFINITY, s = 0.f;
+        for (int i = lane; i < A.splits; i += 32) {
+            const float2 p = A.sums[(row0 + k) * A.splits + i];
+            const float big = fmaxf(m, p.x);
+            s = (m > -INFINITY ? s * exp_diff(m, big) : 0.f) + (p.x > -INFINITY ? p.y * exp_diff(p.x, big) : 0.f);
+            m = big;
+        }
+        const float big = unorder(__reduce_max_sync(kAll, order(m + 0.f)));
+        s = m > -INFINITY ? s * exp_diff(m, big) : 0.f;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+        if (lane == 0) {
+            row_max[k] = big;
+            row_log[k] = logf(s);
+        }
+    }
+    __syncthreads();
 
-    // A thread takes items that follow one another (whole lists, best first, so that its largest is a list's
-    // best), and threads next to one another are in different warps, so that each beam's are spread over all warps.
-    const int place = lane * kWarps + warp;
-    const int per = A.splits * A.n, kept = n_on * per, total = kept + n_done;
-    const u64* best = A.best + row0 * per;
-    int carried = 0;
-    for (int from = 0; from < total || from == 0;) {
-        // as many items as the threads hold, with the n best of those before
-        const int left = total - from, most = kThreads * kItems - carried, now = left < most ? left : most;
-        const int q = (now + carried + kThreads - 1) / kThreads;
-        u64 key[kItems];
-        int row[kItems];
+    // order(score) of a logit of beam k; 0 for one that is none
+    auto score_of = [&](int k, float x) -> unsigned {
+        if (!(x > -INFINITY)) return 0u;
+        const float m = row_max[k];
+        const float c = row_score[k] + ((x == m ? 0.f : x - m) - row_log[k]) + 0.f;  // + 0: -0 becomes 0
+        return c > -INFINITY ? order(c) : 0u;
+    };
+    // every chunk of this thread: (its number among the going beams' chunks, order(its maximum's score))
+    auto each_chunk = [&](auto&& take) {
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int at = place * q + i;  // among this round's items: new ones, then the carried
-            key[i] = 0;
-            row[i] = -1;
-            if (i < q && at < now + carried) {
-                if (at >= now) {
-                    key[i] = S.out[at - now];
-                } else if (from + at < kept) {
-                    const int r = (from + at) / per;
-                    row[i] = rows_on[r];
-                    key[i] = best[(long long)row[i] * per + (from + at - r * per)];
-                } else {
-                    const int k = rows_done[from + at - kept];
-                    key[i] = key_of(order(row_score[k] + 0.f), (unsigned)k * (unsigned)A.V + (unsigned)A.pad);
+        for (int j = 0; j < kHeld; ++j) take(tid + j * kJoinThreads, score_of(held_row[j], held[j]));
+        for (int i = tid + kHeld * kJoinThreads; i < all_chunks; i += kJoinThreads) {
+            const int r = i / per, k = rows_on[r];
+            take(i, score_of(k, __ldcg(A.chunks + (row0 + k) * per + (i - r * per))));
+        }
+    };
+    // every element of the going beams' chunk i that reaches `least`, shared by LC threads: (order(score), index)
+    auto each_element = [&](int i, int LC, unsigned least, auto&& take) {
+        const int r = i / per, c = i - r * per, k = rows_on[r];
+        const T* base = (const T*)A.logits + (row0 + k) * A.row_stride;
+        const int split = c / (kThreads >> A.lg), t0 = (c - split * (kThreads >> A.lg)) << A.lg, first = split * A.seg - lead_of(base);
+        for (int q0 = tid & (LC - 1); q0 < 1 << (A.lg_packs + A.lg); q0 += 4 * LC) {
+            Pack<T, VEC> x[4];
+            auto in = [&](int p) {
+                const int q = q0 + LC * p;
+                return q < 1 << (A.lg_packs + A.lg) ? ((q >> A.lg) * kThreads + t0 + (q & ((1 << A.lg) - 1))) * VEC : A.seg;
+            };
+            ld_chunk_packs<T, VEC, 4>(x, base, first, A.seg, A.V, in);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                if (score_of(k, pack_max(x[p])) < least) continue;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const unsigned o = score_of(k, x[p].get(e));
+                    if (o >= least) take(o, (unsigned)k * (unsigned)A.V + (unsigned)(first + in(p) + e));
                 }
             }
         }
-        if (from == 0) {
-            for (int r = warp; r < n_on; r += kWarps) {  // a row's log-sum-exp
-                const int k = rows_on[r];
-                float m = -INFINITY, s = 0.f;
-                for (int i = lane; i < A.splits; i += 32) {
-                    const float2 p = A.sums[(row0 + k) * A.splits + i];
-                    const float big = fmaxf(m, p.x);
-                    s = (m > -INFINITY ? s * exp_diff(m, big) : 0.f) + (p.x > -INFINITY ? p.y * exp_diff(p.x, big) : 0.f);
-                    m = big;
-                }
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) {
-                    const float m2 = __shfl_xor_sync(kAll, m, o), s2 = __shfl_xor_sync(kAll, s, o), big = fmaxf(m, m2);
-                    s = (m > -INFINITY ? s * exp_diff(m, big) : 0.f) + (m2 > -INFINITY ? s2 * exp_diff(m2, big) : 0.f);
-                    m = big;
-                }
-                if (lane == 0) {
-                    row_max[k] = m;
-                    row_log[k] = logf(s);
-                }
-            }
-        }
-        if (tid < 2) S.count[tid] = 0;
-        __syncthreads();  // the carried keys have been read, too
-        unsigned mine = 0;
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            if (row[i] >= 0 && key[i] != 0) {
-                const int k = row[i];
-                const float x = unorder((unsigned)(key[i] >> 32)), m = row_max[k];
-                const float c = row_score[k] + ((x == m ? 0.f : x - m) - row_log[k]) + 0.f;
-                key[i] = c > -INFINITY ? key_of(order(c), (unsigned)k * (unsigned)A.V + (0xffffffffu - (unsigned)key[i])) : 0;
-            }
-            mine = max(mine, (unsigned)(key[i] >> 32));
-        }
+    };
+
+    unsigned mine = 0;
+    each_chunk([&](int, unsigned o) { mine = max(mine, o); });
+    {
+        unsigned v = mine;
         const int R = tops_of(A.n);
-        warp_tops(mine, R, S.top + warp * R, lane);
-        __syncthreads();
-        select_n(S, A.n, mine, [&](unsigned bound, auto&& take) {
-#pragma unroll
-            for (int i = 0; i < kItems; ++i)
-                if ((unsigned)(key[i] >> 32) >= bound) take((unsigned)(key[i] >> 32), 0xffffffffu - (unsigned)key[i]);
+        for (int r = 0; r < R; ++r) {
+            const unsigned best = __reduce_max_sync(kAll, v);
+            if (lane == 0) top[warp * R + r] = best;
+            const unsigned who = __ballot_sync(kAll, v == best);
+            if (lane == __ffs(who) - 1) v = 0;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const unsigned b = nth_top(top, A.n, lane);
+        if (lane == 0) the_bound = b;
+    }
+    __syncthreads();
+    const unsigned bound = the_bound;
+    if (mine >= bound)
+        each_chunk([&](int i, unsigned o) {
+            if (o >= bound) {
+                const int at = atomicAdd(&chunk_count, 1);
+                if (at < kList) list[0][at] = key_of(o, (unsigned)i);
+            }
         });
-        carried = A.n;
-        from += now > 0 ? now : 1;
+    __syncthreads();
+    const int chunks = chunk_count;
+    bool fits = chunks <= kList;
+    int found = 0;  // candidates above -inf among the n best
+    unsigned least = bound;  // what an element has to reach
+    if (fits) {
+        const u64* chunk = list[0];
+        int kept = chunks;
+        u64* elements = list[1];
+        if (chunks > kFew && chunks > A.n) {
+            // the chunks that fewer than n others exceed, and with them a closer bound
+            for (int t = tid; t < chunks; t += kJoinThreads) {
+                const unsigned v = (unsigned)(list[0][t] >> 32);
+                int above = 0;
+                for (int i = 0; i < chunks; ++i) above += (unsigned)(list[0][i] >> 32) > v;
+                if (above < A.n) {
+                    list[1][atomicAdd(&kept_count, 1)] = list[0][t];
+                    atomicMin(&least_kept, v);
+                }
+            }
+            __syncthreads();
+            kept = kept_count;
+            least = least_kept;
+            chunk = list[1];
+            elements = list[0];
+        }
+        auto push = [&](unsigned o, unsigned index) {
+            const int at = atomicAdd(&element_count, 1);
+            if (at < kList) elements[at] = key_of(o, index);
+        };
+        // a warp a chunk, or as many threads as there are for each
+        int lg_lanes = 5;
+        while (lg_lanes > 2 && kept << lg_lanes > kJoinThreads) --lg_lanes;
+        for (int t = tid >> lg_lanes; t < kept; t += kJoinThreads >> lg_lanes)
+            each_element((int)(0xffffffffu - (unsigned)chunk[t]), 1 << lg_lanes, least, push);
+        if (tid < A.K && kind[tid] > 0 && order(row_score[tid] + 0.f) >= least) push(order(row_score[tid] + 0.f), (unsigned)tid * (unsigned)A.V + (unsigned)A.pad);
+        __syncthreads();
+        const int listed = element_count;
+        fits = listed <= kList;
+        if (fits) {
+            found = listed < A.n ? listed : A.n;
+            for (int t = tid; t < listed; t += kJoinThreads) {
+                const u64 key = elements[t];
+                int rank = 0;
+#pragma unroll 4
+                for (int i = 0; i < listed; ++i) rank += elements[i] > key;
+                if (rank < A.n) out[rank] = key;
+            }
+            __syncthreads();
+        }
+    }
+    if (!fits) {
+        found = 0;
+        u64 last = ~0ull;
+        for (int r = 0; r < A.n; ++r) {
+            u64 best = 0;
+            auto better = [&](unsigned o, unsigned index) {
+                const u64 key = key_of(o, index);
+                if (key < last && key > best) best = key;
+            };
+            for (int i = warp; i < all_chunks; i += kJoinWarps) {
+                const int r = i / per, c = i - r * per, k = rows_on[r];
+                if (score_of(k, __ldcg(A.chunks + (row0 + k) * per + c)) >= bound) each_element(i, 32, max(bound, (unsigned)(best >> 32)), better);
+            }
+            if (tid < A.K && kind[tid] > 0) better(order(row_score[tid] + 0.f), (unsigned)tid * (unsigned)A.V + (unsigned)A.pad);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) {
+                const u64 other = __shfl_xor_sync(kAll, best, o);
+                best = other > best ? other : best;
+            }
+            if (lane == 0) warp_best[warp] = best;
+            __syncthreads();
+            last = 0;
+            for (int i = 0; i < kJoinWarps; ++i) last = warp_best[i] > last ? warp_best[i] : last;
+            if (tid == 0) out[r] = last;
+            found += last != 0;
+            __syncthreads();
+        }
     }
 
     const long long at = (long long)blockIdx.x * A.n;
     if (tid < A.n) {
-        int found = 0;
-        for (int i = 0; i < A.n; ++i) found += S.out[i] != 0;
         unsigned flat;
         float c = -INFINITY;
         if (tid < found) {
-            flat = 0xffffffffu - (unsigned)S.out[tid];
-            c = unorder((unsigned)(S.out[tid] >> 32));
+            flat = 0xffffffffu - (unsigned)out[tid];
+            c = unorder((unsigned)(out[tid] >> 32));
         } else {
             // the (tid - found)-th lowest index that is not among the found ones
             flat = tid - found;
             for (bool again = true; again;) {
                 unsigned below = 0;
-                for (int j = 0; j < found; ++j) below += 0xffffffffu - (unsigned)S.out[j] <= flat;
+                for (int j = 0; j < found; ++j) below += 0xffffffffu - (unsigned)out[j] <= flat;
                 again = flat != (unsigned)(tid - found) + below;
                 flat = (unsigned)(tid - found) + below;
             }
@@ -420,13 +447,13 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs A)
         A.scores_out[at + tid] = c;
         A.parent[at + tid] = k;
         A.token[at + tid] = flat - (unsigned)k * (unsigned)A.V;
-        if (A.src_slots) A.src_slots[at + tid] = A.slots[row0 + k];
+        if (A.src_slots) A.src_slots[at + tid] = row_slot[k];
     }
 }
 
 struct BeamPlan {
-    int packs, seg, splits;
-    size_t off_best, bytes;
+    int lg_packs, seg, splits, lg;
+    size_t off_chunks, bytes;
 };
 
 int fail(int code, const char* msg)
@@ -465,26 +492,41 @@ BeamPlan plan_of(const beam_params_t* p)
 {
     BeamPlan pl{};
     const int vec = 16 / (int)elem_size(p->dtype);
-    // a row may start vec - 1 elements into its first pack; segments of one size leave no small last one,
-    // whose few threads would give a low bound
+    // a row may start vec - 1 elements into its first pack; segments of one size leave no small last one
     const int64_t span = p->V + vec - 1;
-    pl.packs = 8;
-    while (pl.packs > 2 && p->N * p->K * ((span + pl.packs * vec * kThreads - 1) / (pl.packs * vec * kThreads)) < 4 * kNumSMs) pl.packs /= 2;
-    const int64_t most = (int64_t)pl.packs * vec * kThreads;
-    pl.splits = (int)((span + most - 1) / most);
+    pl.lg_packs = 3;
+    auto most = [&]() { return (int64_t)vec * kThreads << pl.lg_packs; };
+    while (pl.lg_packs > 1 && p->N * p->K * ((span + most() - 1) / most()) < 4 * kNumSMs) --pl.lg_packs;
+    pl.splits = (int)((span + most() - 1) / most());
     pl.seg = (int)((span + (int64_t)pl.splits * vec - 1) / ((int64_t)pl.splits * vec)) * vec;
     const size_t segs = (size_t)(p->N * p->K) * pl.splits;
-    pl.off_best = (segs * sizeof(float2) + 15) / 16 * 16;
-    pl.bytes = pl.off_best + segs * p->n_out * sizeof(u64);
+    // chunks of up to 32 threads, as long as the join has kHeld for each of its threads
+    const int64_t want = kHeld * kJoinThreads;
+    while (pl.lg < 5 && p->K * pl.splits * (kThreads >> (pl.lg + 1)) >= want) ++pl.lg;
+    pl.off_chunks = (segs * sizeof(float2) + 255) / 256 * 256;
+    pl.bytes = pl.off_chunks + segs * (kThreads >> pl.lg) * sizeof(float);
     return pl;
 }
 
 template <typename T>
-void launch_segments(const BeamArgs& A, int packs, unsigned ctas, cudaStream_t st)
+int launch_beam(const BeamArgs& A, unsigned segments, unsigned sequences, cudaStream_t st)
 {
-    if (packs == 8) beam_segment_kernel<T, 8><<<ctas, kThreads, 0, st>>>(A);
-    else if (packs == 4) beam_segment_kernel<T, 4><<<ctas, kThreads, 0, st>>>(A);
-    else beam_segment_kernel<T, 2><<<ctas, kThreads, 0, st>>>(A);
+    if (A.lg_packs == 3) beam_segment_kernel<T, 8><<<segments, kThreads, 0, st>>>(A);
+    else if (A.lg_packs == 2) beam_segment_kernel<T, 4><<<segments, kThreads, 0, st>>>(A);
+    else beam_segment_kernel<T, 2><<<segments, kThreads, 0, st>>>(A);
+    const int e = (int)cudaGetLastError();
+    if (e) return e;
+    // The join starts while the segments run and waits on the device for their end.
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sequences);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return (int)cudaLaunchKernelEx(&cfg, beam_join_kernel<T>, A);
 }
 
 }  // namespace
@@ -520,31 +562,18 @@ extern "C" int beam_select(const beam_params_t* p, const void* logits, const flo
         for (int j = 0; j < i; ++j)
             if (overlap(out[i].ptr, out[i].n, out[j].ptr, out[j].n)) return fail(GDN_ERR_ALIAS, "beam_select: outputs overlap");
     }
-    if (rows * pl.splits > (size_t)INT_MAX || (size_t)p->K * pl.splits * p->n_out > (size_t)INT_MAX)
+    // chunks of a sequence are numbered in 32 bits
+    if (rows * pl.splits > (size_t)INT_MAX || (size_t)p->K * pl.splits * kThreads > (size_t)INT_MAX)
         return fail(GDN_ERR_UNSUPPORTED, "beam_select: too many segments for one launch");
     BeamArgs A{};
     A.logits = logits; A.scores = scores; A.done = done; A.slots = slots;
     A.scores_out = scores_out; A.parent = parent; A.token = token; A.src_slots = src_slots;
-    A.sums = (float2*)workspace; A.best = (u64*)((char*)workspace + pl.off_best);
-    A.row_stride = p->row_stride; A.K = (int)p->K; A.V = (int)p->V; A.splits = pl.splits; A.seg = pl.seg; A.n = p->n_out; A.pad = p->pad_token;
+    A.sums = (float2*)workspace; A.chunks = (float*)((char*)workspace + pl.off_chunks);
+    A.row_stride = p->row_stride; A.K = (int)p->K; A.V = (int)p->V; A.splits = pl.splits; A.seg = pl.seg; A.lg_packs = pl.lg_packs; A.lg = pl.lg; A.n = p->n_out; A.pad = p->pad_token;
     cudaStream_t cs = (cudaStream_t)stream;
     const unsigned ctas = (unsigned)(rows * pl.splits);
-    if (p->dtype == GDN_F32) launch_segments<float>(A, pl.packs, ctas, cs);
-    else if (p->dtype == GDN_BF16) launch_segments<__nv_bfloat16>(A, pl.packs, ctas, cs);
-    else launch_segments<__half>(A, pl.packs, ctas, cs);
-    int e = (int)cudaGetLastError();
-    if (!e) {
-        // The join starts while the segments run and waits on the device for their end.
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)p->N);
-        cfg.blockDim = dim3(kThreads);
-        cfg.stream = cs;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        e = (int)cudaLaunchKernelEx(&cfg, beam_join_kernel, A);
-    }
+    const int e = p->dtype == GDN_F32    ? launch_beam<float>(A, ctas, (unsigned)p->N, cs)
+                  : p->dtype == GDN_BF16 ? launch_beam<__nv_bfloat16>(A, ctas, (unsigned)p->N, cs)
+                                         : launch_beam<__half>(A, ctas, (unsigned)p->N, cs);
     return e ? cuda_fail(e, "beam_select launch") : GDN_OK;
 }

@@ -12,8 +12,7 @@
  *   - a logit of -inf (a masked token), or a row of nothing else, has candidates at -inf; they
  *     fill up, lowest index first, what too few others leave;
  *   - logits of +inf share the probability, the others have none.
- * Equality is that of the fp32 c, but within a beam candidates go by their logits first (two different
- * logits whose c round to the same value keep their order).
+ * Equality is that of the fp32 c.
  *
  * Layouts (device memory): logits [N K][V] in dtype, rows row_stride elements apart, V
  * contiguous; scores fp32 [N][K]; done uint8 [N][K]; slots int32 [N][K]; outputs [N][n_out],
