@@ -10,9 +10,9 @@
 //
 // What bounds it: the states' bytes, 8 S_k S_v a head against 7 S_k S_v flops a token.  So the
 // layout follows the reads: 8 lanes a row, each with float4 blocks 32 columns apart (whole 128-byte
-// lines), 4 rows across the warp, all of a warp's state in flight before its first use.  Warps do
-// not meet: each keeps the token's vectors in fp32 in shared memory of its own, a lane widening
-// (and for KDA exponentiating) its share of the columns once for all rows.
+// lines), 4 rows across the warp, all of a warp's state in flight before its first use.  The warps of
+// a CTA share one head: each widens (and for KDA exponentiates) one of the next W tokens into
+// shared memory for all of them, and one barrier serves W tokens.
 #include <climits>
 #include <cstdio>
 
@@ -36,7 +36,6 @@ struct DecodeArgs {
     long long slot_stride, qs0, qs1, ks0, ks1, vs0, vs1;
     int T, n_tok, n_slots, H_k, H_v, SK, SV;
     int gate_dtype, y_dtype, vec, vec_g;
-    unsigned warps;  // n_seq H_v S_v / rows of a warp
     float scale;
 };
 
@@ -47,24 +46,37 @@ __device__ __forceinline__ float4 ld_gate4(const void* p, long long i, int dtype
     return make_float4(ld_any(p, i, dtype), ld_any(p, i + 1, dtype), ld_any(p, i + 2, dtype), ld_any(p, i + 3, dtype));
 }
 
-// One token's operands as they arrive: a lane's share of q, k (and the KDA gate), one v, beta, g.
-template <typename T, int SHARE, bool KDA>
-struct Token {
-    Pack<T, 4> q[SHARE], k[SHARE];
-    float4 g[SHARE];  // scalar gate: g[0].x
-    float v, beta;
+// A token's row vectors and numbers in fp32, for all warps of a CTA: what the dots take of the state (k, q; times
+// the gate for KDA), for KDA also k and the gate itself, the CTA's rows of v, and {exp g, beta, k . q}.
+template <int NV, int RT, bool KDA>
+struct Staged {
+    float4 vec[KDA ? 4 : 2][8 * NV];
+    float v[16 * RT];
+    float4 num;
 };
 
-template <typename T, int SHARE, bool KDA>
-__device__ __forceinline__ void load_token(Token<T, SHARE, KDA>& x, const DecodeArgs& A, const T* q, const T* k, const T* v, long long row,
-                                           int h, int lane)
+// A lane's share of one token as it arrives.
+template <typename T, int NV, int RT, bool KDA>
+struct Token {
+    static constexpr int SHARE = (32 * NV + 127) / 128, ROWS = (16 * RT + 31) / 32;
+    Pack<T, 4> q[SHARE], k[SHARE];
+    float4 g[SHARE];  // scalar gate: g[0].x
+    T v[ROWS];
+    float beta;
+};
+
+template <typename T, int NV, int RT, bool KDA>
+__device__ __forceinline__ void load_token(Token<T, NV, RT, KDA>& x, const DecodeArgs& A, const T* q, const T* k, const T* v, int rows,
+                                           long long row, int h, int lane)
 {
     const long long gh = row * A.H_v + h;
     x.beta = ld_any(A.beta, gh, A.gate_dtype);
     if (!KDA) x.g[0].x = ld_any(A.g, gh, A.gate_dtype);
-    x.v = to_f32(__ldg(v + row * A.vs0));
 #pragma unroll
-    for (int s = 0; s < SHARE; ++s) {
+    for (int s = 0; s < x.ROWS; ++s)
+        if (32 * s + lane < rows) x.v[s] = __ldg(v + row * A.vs0 + 32 * s + lane);
+#pragma unroll
+    for (int s = 0; s < x.SHARE; ++s) {
         const int c = 128 * s + 4 * lane;
         if (c < A.SK) {
             x.k[s] = ld_pack<T, 4>(k + row * A.ks0 + c, A.vec);
@@ -74,20 +86,49 @@ __device__ __forceinline__ void load_token(Token<T, SHARE, KDA>& x, const Decode
     }
 }
 
-// RT: rows of a lane (4 RT a warp); NV: its float4 blocks of a row.
+// One warp widens (and for KDA exponentiates) a token into shared memory.
 template <typename T, int NV, int RT, bool KDA>
-__global__ void __launch_bounds__(128) gdn_decode_kernel(const DecodeArgs A)
+__device__ __forceinline__ void stage_token(Staged<NV, RT, KDA>& S, const Token<T, NV, RT, KDA>& x, const DecodeArgs& A, int rows, int lane)
 {
-    constexpr int COLS = 32 * NV, SHARE = (COLS + 127) / 128;
-    // The token's row vectors in fp32, for each warp: what the dots take of the state (k, q; times the gate
-    // for KDA), and for KDA also k and the gate itself.
-    __shared__ float4 rows[4][KDA ? 4 : 2][COLS / 4];
-    const unsigned w = blockIdx.x * 4u + (threadIdx.x >> 5);
-    if (w >= A.warps) return;
-    const int lane = threadIdx.x & 31, cl = lane & 7, grp = lane >> 3;
-    const unsigned per_head = A.SV / (4 * RT);
-    const unsigned nh = w / per_head;
-    const int row0 = (int)(w - nh * per_head) * 4 * RT;
+    float kq = 0.f;
+#pragma unroll
+    for (int s = 0; s < x.SHARE; ++s) {
+        const int c = 128 * s + 4 * lane;
+        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), q = k, a = k;
+        if (c < A.SK) {
+            k = make_float4(x.k[s].get(0), x.k[s].get(1), x.k[s].get(2), x.k[s].get(3));
+            q = make_float4(x.q[s].get(0), x.q[s].get(1), x.q[s].get(2), x.q[s].get(3));
+            if (KDA) a = make_float4(expf(x.g[s].x), expf(x.g[s].y), expf(x.g[s].z), expf(x.g[s].w));
+        }
+        kq += (k.x * q.x + k.y * q.y) + (k.z * q.z + k.w * q.w);
+        if (c < 32 * NV) {
+            if (KDA) {
+                S.vec[KDA ? 2 : 0][c / 4] = k;
+                S.vec[KDA ? 3 : 0][c / 4] = a;
+                k = make_float4(k.x * a.x, k.y * a.y, k.z * a.z, k.w * a.w);
+                q = make_float4(q.x * a.x, q.y * a.y, q.z * a.z, q.w * a.w);
+            }
+            S.vec[0][c / 4] = k;
+            S.vec[1][c / 4] = q;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) kq += __shfl_xor_sync(kFull, kq, o);
+#pragma unroll
+    for (int s = 0; s < x.ROWS; ++s)
+        if (32 * s + lane < rows) S.v[32 * s + lane] = to_f32(x.v[s]);
+    if (lane == 0) S.num = make_float4(KDA ? 1.f : expf(x.g[0].x), x.beta, kq, 0.f);
+}
+
+// One CTA of W <= 4 warps: 4 RT W rows of one head's state.  RT: rows of a lane; NV: its float4 blocks of a row.
+template <typename T, int NV, int RT, bool KDA>
+__global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6) gdn_decode_kernel(const DecodeArgs A)
+{
+    __shared__ Staged<NV, RT, KDA> staged[2][4];  // W tokens, while the next W arrive
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, cl = lane & 7, grp = lane >> 3;
+    const int rows = 4 * RT * W;  // of the CTA
+    const unsigned per_head = A.SV / rows, nh = blockIdx.x / per_head;
+    const int first = (int)(blockIdx.x - nh * per_head) * rows, row0 = first + warp * 4 * RT;
     const int n = nh / A.H_v, h = nh - n * A.H_v;
 
     const int s_in = __ldg(A.slot_in + n), s_out = __ldg(A.slot_out + n);
@@ -100,9 +141,13 @@ __global__ void __launch_bounds__(128) gdn_decode_kernel(const DecodeArgs A)
         hi = lo + A.T;
     }
     if (s_in < -1 || s_in >= A.n_slots || s_out < -1 || s_out >= A.n_slots || lo < 0 || hi < lo || hi > A.n_tok) {
-        if (lane == 0) atomicOr(&g_decode_status, 1);
+        if (threadIdx.x == 0) atomicOr(&g_decode_status, 1);
         return;
     }
+    const int hk = h % A.H_k;
+    const T *qh = (const T*)A.q + hk * A.qs1, *kh = (const T*)A.k + hk * A.ks1, *vh = (const T*)A.v + h * A.vs1 + first;
+    Token<T, NV, RT, KDA> x;
+    if (lo + warp < hi) load_token<T, NV, RT, KDA>(x, A, qh, kh, vh, rows, lo + warp, h, lane);
 
     // rows row0 + grp RT + r of the state, r < RT
     const long long at = ((long long)h * A.SV + row0 + grp * RT) * A.SK;
@@ -112,109 +157,94 @@ __global__ void __launch_bounds__(128) gdn_decode_kernel(const DecodeArgs A)
 #pragma unroll
         for (int b = 0; b < NV; ++b) {
             const int c = 32 * b + 4 * cl;
-            ulonglong2 x = make_ulonglong2(0, 0);
+            ulonglong2 v = make_ulonglong2(0, 0);
             if (s_in >= 0 && c < A.SK)
-                x = *reinterpret_cast<const ulonglong2*>(A.pool + s_in * A.slot_stride + at + r * A.SK + c);
-            m[r][b][0] = x.x;
-            m[r][b][1] = x.y;
+                v = *reinterpret_cast<const ulonglong2*>(A.pool + s_in * A.slot_stride + at + r * A.SK + c);
+            m[r][b][0] = v.x;
+            m[r][b][1] = v.y;
         }
 
     // After the exchange between a row's 8 lanes, lanes 0-3 hold u and lanes 4-7 o; row mine of the RT.
     constexpr int kShare = 4 / RT;  // lanes that hold the same sum
     const int mine = (cl & 3) / kShare;
     const int j = row0 + grp * RT + mine;
-    const int hk = h % A.H_k;
-    const T *qh = (const T*)A.q + hk * A.qs1, *kh = (const T*)A.k + hk * A.ks1, *vh = (const T*)A.v + h * A.vs1 + j;
-    float4(*mem)[COLS / 4] = rows[threadIdx.x >> 5];
 
-    Token<T, SHARE, KDA> x;
-    if (lo < hi) load_token<T, SHARE, KDA>(x, A, qh, kh, vh, lo, h, lane);
-    for (long long t = lo; t < hi; ++t) {
-        // this lane's four columns (or twice four): fp32, and the gate
-        float kq = 0.f;
-        const float as = KDA ? 1.f : expf(x.g[0].x), beta = x.beta, vj = x.v;
-#pragma unroll
-        for (int s = 0; s < SHARE; ++s) {
-            const int c = 128 * s + 4 * lane;
-            float4 k = make_float4(0.f, 0.f, 0.f, 0.f), q = k, a = k;
-            if (c < A.SK) {
-                k = make_float4(x.k[s].get(0), x.k[s].get(1), x.k[s].get(2), x.k[s].get(3));
-                q = make_float4(x.q[s].get(0), x.q[s].get(1), x.q[s].get(2), x.q[s].get(3));
-                if (KDA) a = make_float4(expf(x.g[s].x), expf(x.g[s].y), expf(x.g[s].z), expf(x.g[s].w));
-            }
-            kq += (k.x * q.x + k.y * q.y) + (k.z * q.z + k.w * q.w);
-            if (c < COLS) {
-                if (KDA) {
-                    mem[2][c / 4] = k;
-                    mem[3][c / 4] = a;
-                    k = make_float4(k.x * a.x, k.y * a.y, k.z * a.z, k.w * a.w);
-                    q = make_float4(q.x * a.x, q.y * a.y, q.z * a.z, q.w * a.w);
-                }
-                mem[0][c / 4] = k;
-                mem[1][c / 4] = q;
-            }
+    if (lo + warp < hi) stage_token<T, NV, RT, KDA>(staged[0][warp], x, A, rows, lane);
+    if (lo + W + warp < hi) load_token<T, NV, RT, KDA>(x, A, qh, kh, vh, rows, lo + W + warp, h, lane);
+    const bool writes = cl >= 4 && (cl & (kShare - 1)) == 0;
+    const int y_shift = A.y_dtype == GDN_F32 ? 2 : 1;
+    char* y = (char*)A.y + (((lo * A.H_v + h) * A.SV + j) << y_shift);
+    const long long y_step = (long long)A.H_v * A.SV << y_shift;
+    int set = 0;
+    for (long long t0 = lo; t0 < hi; t0 += W, set ^= 1) {
+        __syncthreads();
+        // the tokens after these W, staged by the warps while they are in them
+        if (t0 + W + warp < hi) {
+            stage_token<T, NV, RT, KDA>(staged[set ^ 1][warp], x, A, rows, lane);
+            if (t0 + 2 * W + warp < hi) load_token<T, NV, RT, KDA>(x, A, qh, kh, vh, rows, t0 + 2 * W + warp, h, lane);
         }
-        if (t + 1 < hi) load_token<T, SHARE, KDA>(x, A, qh, kh, vh, t + 1, h, lane);
+        const int now = hi - t0 < W ? (int)(hi - t0) : W;
+        for (int i = 0; i < now; ++i) {
+            const Staged<NV, RT, KDA>& S = staged[set][i];
+            const float4 num = S.num;
+            const float vj = S.v[j - first];
+            float s[2 * RT];
+            {
+                f2 u2[RT], o2[RT];
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) kq += __shfl_xor_sync(kFull, kq, o);
-        __syncwarp();
-        float s[2 * RT];
-        {
-            f2 u2[RT], o2[RT];
+                for (int r = 0; r < RT; ++r) u2[r] = o2[r] = 0;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) u2[r] = o2[r] = 0;
+                for (int b = 0; b < NV; ++b) {
+                    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&S.vec[0][8 * b + cl]);
+                    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&S.vec[1][8 * b + cl]);
 #pragma unroll
-            for (int b = 0; b < NV; ++b) {
-                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&mem[0][8 * b + cl]);
-                const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&mem[1][8 * b + cl]);
+                    for (int r = 0; r < RT; ++r) {
+                        u2[r] = fma2(m[r][b][0], k.x, u2[r]);
+                        o2[r] = fma2(m[r][b][0], q.x, o2[r]);
+                        u2[r] = fma2(m[r][b][1], k.y, u2[r]);
+                        o2[r] = fma2(m[r][b][1], q.y, o2[r]);
+                    }
+                }
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    u2[r] = fma2(m[r][b][0], k.x, u2[r]);
-                    o2[r] = fma2(m[r][b][0], q.x, o2[r]);
-                    u2[r] = fma2(m[r][b][1], k.y, u2[r]);
-                    o2[r] = fma2(m[r][b][1], q.y, o2[r]);
+                    s[r] = sum2(u2[r]);
+                    s[RT + r] = sum2(o2[r]);
+                }
+            }
+            // reduce-scatter of the 2 RT sums over the 8 lanes, then a butterfly over the lanes that share one
+#pragma unroll
+            for (int n2 = RT, bit = 4; n2 >= 1; n2 >>= 1, bit >>= 1) {
+                const bool up = (cl & bit) != 0;
+#pragma unroll
+                for (int e = 0; e < n2; ++e) {
+                    const float send = up ? s[e] : s[n2 + e], keep = up ? s[n2 + e] : s[e];
+                    s[e] = keep + __shfl_xor_sync(kFull, send, bit);
                 }
             }
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                s[r] = sum2(u2[r]);
-                s[RT + r] = sum2(o2[r]);
+            for (int bit = kShare / 2; bit >= 1; bit >>= 1) s[0] += __shfl_xor_sync(kFull, s[0], bit);
+            const float sum = KDA ? s[0] : num.x * s[0];
+            float delta = num.y * (vj - sum);  // on lanes 0-3
+            float d[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) d[r] = __shfl_sync(kFull, delta, (lane & 24) + r * kShare);
+            delta = __shfl_xor_sync(kFull, delta, 4);
+            if (writes) st_any(y, 0, A.y_dtype, A.scale * fmaf(delta, num.z, sum));
+            y += y_step;
+            const f2 as2 = pack2(num.x, num.x);
+#pragma unroll
+            for (int b = 0; b < NV; ++b) {
+                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&S.vec[KDA ? 2 : 0][8 * b + cl]);
+                ulonglong2 a = make_ulonglong2(as2, as2);
+                if (KDA) a = *reinterpret_cast<const ulonglong2*>(&S.vec[KDA ? 3 : 0][8 * b + cl]);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const f2 dd = pack2(d[r], d[r]);
+                    m[r][b][0] = fma2(k.x, dd, mul2(m[r][b][0], a.x));
+                    m[r][b][1] = fma2(k.y, dd, mul2(m[r][b][1], a.y));
+                }
             }
         }
-        // reduce-scatter of the 2 RT sums over the 8 lanes, then a butterfly over the lanes that share one
-#pragma unroll
-        for (int n2 = RT, bit = 4; n2 >= 1; n2 >>= 1, bit >>= 1) {
-            const bool up = (cl & bit) != 0;
-#pragma unroll
-            for (int i = 0; i < n2; ++i) {
-                const float send = up ? s[i] : s[n2 + i], keep = up ? s[n2 + i] : s[i];
-                s[i] = keep + __shfl_xor_sync(kFull, send, bit);
-            }
-        }
-#pragma unroll
-        for (int bit = kShare / 2; bit >= 1; bit >>= 1) s[0] += __shfl_xor_sync(kFull, s[0], bit);
-        const float sum = KDA ? s[0] : as * s[0];
-        float delta = beta * (vj - sum);  // on lanes 0-3
-        float d[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) d[r] = __shfl_sync(kFull, delta, (lane & 24) + r * kShare);
-        delta = __shfl_xor_sync(kFull, delta, 4);
-        if (cl >= 4 && (cl & (kShare - 1)) == 0)
-            st_any(A.y, (t * A.H_v + h) * A.SV + j, A.y_dtype, A.scale * fmaf(delta, kq, sum));
-        const f2 as2 = pack2(as, as);
-#pragma unroll
-        for (int b = 0; b < NV; ++b) {
-            const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&mem[KDA ? 2 : 0][8 * b + cl]);
-            ulonglong2 a = make_ulonglong2(as2, as2);
-            if (KDA) a = *reinterpret_cast<const ulonglong2*>(&mem[KDA ? 3 : 0][8 * b + cl]);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const f2 dd = pack2(d[r], d[r]);
-                m[r][b][0] = fma2(k.x, dd, mul2(m[r][b][0], a.x));
-                m[r][b][1] = fma2(k.y, dd, mul2(m[r][b][1], a.y));
-            }
-        }
-        __syncwarp();
     }
 
     if (s_out < 0) return;
@@ -230,17 +260,19 @@ __global__ void __launch_bounds__(128) gdn_decode_kernel(const DecodeArgs A)
 }
 
 template <typename T, int NV, int RT>
-int launch_decode_g(DecodeArgs& A, long long heads, bool kda, cudaStream_t st)
+int launch_decode_g(const DecodeArgs& A, long long heads, bool kda, cudaStream_t st)
 {
-    A.warps = (unsigned)(heads * (A.SV / (4 * RT)));
-    const unsigned ctas = (A.warps + 3) / 4;
-    if (kda) gdn_decode_kernel<T, NV, RT, true><<<ctas, 128, 0, st>>>(A);
-    else gdn_decode_kernel<T, NV, RT, false><<<ctas, 128, 0, st>>>(A);
+    const int groups = A.SV / (4 * RT);  // warps' rows of a head
+    int W = 4;
+    while (groups % W != 0) --W;
+    const unsigned ctas = (unsigned)(heads * (groups / W));
+    if (kda) gdn_decode_kernel<T, NV, RT, true><<<ctas, 32 * W, 0, st>>>(A);
+    else gdn_decode_kernel<T, NV, RT, false><<<ctas, 32 * W, 0, st>>>(A);
     return (int)cudaGetLastError();
 }
 
 template <typename T>
-int launch_decode_t(DecodeArgs& A, long long heads, bool kda, cudaStream_t st)
+int launch_decode_t(const DecodeArgs& A, long long heads, bool kda, cudaStream_t st)
 {
     // Few heads are spread over more warps of one row a lane; many take more rows a lane, so
     // that a token's q and k serve them all.
@@ -293,7 +325,7 @@ gdn_status_t check_decode(const gdn_decode_params_t* p)
         return fail(GDN_ERR_UNSUPPORTED, "gdn_decode: S_k must be 16, 32, 64, 128 or 256");
     if (p->S_v % 16 != 0 || p->S_v > 256) return fail(GDN_ERR_UNSUPPORTED, "gdn_decode: S_v must be a multiple of 16 up to 256");
     if (p->H_v > 65535 || p->n_tok > INT_MAX || p->T > INT_MAX || p->n_slots > INT_MAX ||
-        p->n_seq > (int64_t)UINT_MAX / (p->H_v * (p->S_v / 4)))
+        p->n_seq > (int64_t)INT_MAX / (p->H_v * (p->S_v / 4)))
         return fail(GDN_ERR_UNSUPPORTED, "gdn_decode: sizes beyond the kernel's index range");
     if (p->slot_stride < p->H_v * p->S_v * p->S_k || p->slot_stride % 4 != 0)
         return fail(GDN_ERR_INVALID_ARG, "gdn_decode: slot_stride must be a multiple of 4 of at least H_v S_v S_k");
