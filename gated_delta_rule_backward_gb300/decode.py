@@ -146,14 +146,17 @@ def gdn_states_move(pool, src, dst, group=1, stream=None):
     """Slot dst[i] = what slot src[i] held (zeros for -1), in every layer, the moves of each
     consecutive `group` simultaneous.  pool: [n_layers, n_slots, ...] of any type, every
     (layer, slot) dense; src, dst: int32 device tensors of one length."""
-    if pool.dim() < 2 or src.numel() != dst.numel():
+    shape, strides, es = pool.shape, pool.stride(), pool.element_size()
+    n = src.numel()
+    if len(shape) < 2 or dst.numel() != n:
         raise ValueError("pool must be [n_layers, n_slots, ...], and src and dst of one length")
-    es, (L, S) = pool.element_size(), pool.shape[:2]
-    if pool.numel() and not pool[0, 0].is_contiguous():
-        raise ValueError("each layer's slots must be dense")
-    state = pool.numel() // (L * S) * es if L * S else 0
-    st = _lib.gdn_states_move(pool.data_ptr(), L, pool.stride(0) * es if L > 1 else 0, S,
-                              pool.stride(1) * es if S > 1 else state, state, _index(src, "src"), _index(dst, "dst"),
-                              src.numel(), group, _stream(stream))
+    state = 1  # a slot's elements, dense from the last dimension on
+    for size, step in zip(shape[:1:-1], strides[:1:-1]):
+        if size != 1 and step != state and pool.numel():
+            raise ValueError("each layer's slots must be dense")
+        state *= size
+    L, S = shape[0], shape[1]
+    st = _lib.gdn_states_move(pool.data_ptr(), L, strides[0] * es if L > 1 else 0, S, strides[1] * es if S > 1 else state * es,
+                              state * es, _index(src, "src"), _index(dst, "dst"), n, group, _stream(stream))
     if st != gdn.GDN_OK:
         raise gdn.GdnError(st, "gdn_states_move")
