@@ -21,7 +21,7 @@
 #include "gdn_elem.cuh"
 #include "gdn_f32x2.cuh"
 #include "gdn_internal.h"
-#include "gdn_tc.cuh"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 namespace {
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamArg
     __shared__ float2 part[kWarps];
     const int row = blockIdx.x / A.splits, split = blockIdx.x - row * A.splits;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    tc::grid_dep_launch();
+    begin_after();
     const T* base = (const T*)A.logits + row * A.row_stride;
     const int first = split * A.seg - lead_of(base);
     if ((A.done && A.done[row]) || !(A.scores[row] > -INFINITY)) return;
@@ -222,6 +222,8 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row0 = (long long)blockIdx.x * A.K;
     const int per = A.splits * (kThreads >> A.lg);  // chunks of a row
+    // The segments' CTAs have all begun, and so have waited for what the stream did before them: the
+    // scores can be read; their own sums and maxima only after the wait below.
     if (tid < A.K) {
         const float score = A.scores[row0 + tid];
         row_score[tid] = score;
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs 
     }
     __syncthreads();
     const int all_chunks = n_on * per;
-    tc::grid_dep_wait();
+    begin_after();
     // A thread's chunks are tid + j kJoinThreads of the going beams' chunks; the first kHeld stay in registers.
     float held[kHeld];
     int held_row[kHeld];
@@ -511,22 +513,9 @@ BeamPlan plan_of(const beam_params_t* p)
 template <typename T>
 int launch_beam(const BeamArgs& A, unsigned segments, unsigned sequences, cudaStream_t st)
 {
-    if (A.lg_packs == 3) beam_segment_kernel<T, 8><<<segments, kThreads, 0, st>>>(A);
-    else if (A.lg_packs == 2) beam_segment_kernel<T, 4><<<segments, kThreads, 0, st>>>(A);
-    else beam_segment_kernel<T, 2><<<segments, kThreads, 0, st>>>(A);
-    const int e = (int)cudaGetLastError();
-    if (e) return e;
-    // The join starts while the segments run and waits on the device for their end.
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sequences);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, beam_join_kernel<T>, A);
+    const auto segment = A.lg_packs == 3 ? beam_segment_kernel<T, 8> : A.lg_packs == 2 ? beam_segment_kernel<T, 4> : beam_segment_kernel<T, 2>;
+    const int e = launch_after(segment, segments, kThreads, 0, st, A);
+    return e ? e : launch_after(beam_join_kernel<T>, sequences, kJoinThreads, 0, st, A);
 }
 
 }  // namespace

@@ -20,6 +20,7 @@
 #include "gdn_device.cuh"
 #include "gdn_elem.cuh"
 #include "gdn_f32x2.cuh"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 namespace {
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
     const int first = (int)(blockIdx.x - nh * per_head) * rows, row0 = first + warp * 4 * RT;
     const int n = nh / A.H_v, h = nh - n * A.H_v;
 
+    begin_after();
     const int s_in = __ldg(A.slot_in + n), s_out = __ldg(A.slot_out + n);
     long long lo, hi;
     if (A.cu) {
@@ -266,9 +268,7 @@ int launch_decode_g(const DecodeArgs& A, long long heads, bool kda, cudaStream_t
     int W = 4;
     while (groups % W != 0) --W;
     const unsigned ctas = (unsigned)(heads * (groups / W));
-    if (kda) gdn_decode_kernel<T, NV, RT, true><<<ctas, 32 * W, 0, st>>>(A);
-    else gdn_decode_kernel<T, NV, RT, false><<<ctas, 32 * W, 0, st>>>(A);
-    return (int)cudaGetLastError();
+    return launch_after(kda ? gdn_decode_kernel<T, NV, RT, true> : gdn_decode_kernel<T, NV, RT, false>, ctas, 32 * W, 0, st, A);
 }
 
 template <typename T>
@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(256) gdn_states_move_kernel(const MoveArgs A)
     const unsigned pc = blockIdx.x % A.pieces, gl = blockIdx.x / A.pieces;
     const unsigned gr = gl % A.groups, layer = gl / A.groups;
     const int nm = min(A.group, A.n_moves - (int)gr * A.group);
+    begin_after();
     if (threadIdx.x < G) {
         long long f = -2, t = 0;
         if ((int)threadIdx.x < nm) {
@@ -479,6 +480,7 @@ __global__ void __launch_bounds__(256) gdn_states_move_large_kernel(const MoveAr
     const int n16 = bytes / 16, per = A.piece / 16;
     const int m0 = gr * A.group, nm = A.n_moves - m0 < A.group ? A.n_moves - m0 : A.group;
     char* base = A.pool + layer * A.layer_stride + at;
+    begin_after();
     for (int i = threadIdx.x; i < nm * n16; i += blockDim.x) {
         const int m = i / n16, e = i - m * n16;
         const int s = __ldg(A.src + m0 + m), d = __ldg(A.dst + m0 + m);
@@ -501,8 +503,7 @@ __global__ void __launch_bounds__(256) gdn_states_move_large_kernel(const MoveAr
 template <int G, int P>
 int launch_move(const MoveArgs& A, unsigned ctas, cudaStream_t st)
 {
-    gdn_states_move_kernel<G, P><<<ctas, 256, 0, st>>>(A);
-    return (int)cudaGetLastError();
+    return launch_after(gdn_states_move_kernel<G, P>, ctas, 256, 0, st, A);
 }
 
 }  // namespace
@@ -560,10 +561,7 @@ extern "C" gdn_status_t gdn_states_move(void* pool, int64_t n_layers, int64_t la
         const size_t smem = (size_t)(piece * group);
         if (smem > 40 * 1024)
             e = (int)cudaFuncSetAttribute(gdn_states_move_large_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (!e) {
-            gdn_states_move_large_kernel<<<(unsigned)ctas, 256, smem, st>>>(A);
-            e = (int)cudaGetLastError();
-        }
+        if (!e) e = launch_after(gdn_states_move_large_kernel, (unsigned)ctas, 256, smem, st, A);
     }
     return e ? cuda_fail(e, "gdn_states_move launch") : GDN_OK;
 }

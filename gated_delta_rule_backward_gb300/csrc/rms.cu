@@ -12,7 +12,7 @@
 #include "gdn_elem.cuh"
 #include "gdn_f32x2.cuh"
 #include "gdn_internal.h"
-#include "gdn_tc.cuh"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 namespace {
@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(VPT > 0 && VPT < (VEC > 1 ? 4 : 16) ? 256 : kM
     __shared__ float2 buf[32];
     const int tid = threadIdx.x, step = blockDim.x * VEC;
     const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    begin_after();
     if (row >= A.rows) return;  // the whole row's threads leave together
     const T* x = (const T*)A.x + row * A.xs;
     const T* r = A.res ? (const T*)A.res + row * A.rs : x;
@@ -390,7 +391,7 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
     const int tid = threadIdx.x, step = blockDim.x * VEC;
     const int threads = blockDim.x * blockDim.y, own = threadIdx.y * blockDim.x + tid;
     const bool vec = VEC > 1 && A.vec;
-    tc::grid_dep_launch();
+    begin_after();
     Nums<VEC> w[VPT], dw[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -488,6 +489,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_backward_long_kernel(const Rm
 {
     __shared__ float2 buf[32];
     const long long row = blockIdx.x;
+    begin_after();
     const T *h = (const T*)A.h + row * A.hs, *dy = (const T*)A.dy + row * A.dys;
     const T* dh = A.dh ? (const T*)A.dh + row * A.D : nullptr;
     const float rstd = __ldg(A.rstd + row);
@@ -506,6 +508,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) rms_dweight_long_kernel(const RmsBwd A)
 {
     const int c = blockIdx.y * 256 + threadIdx.x;
+    begin_after();
     if (c >= A.D) return;
     float t = 0.f;
     for (long long row = blockIdx.x; row < A.rows; row += gridDim.x)
@@ -590,10 +593,10 @@ int launch_fwd_v(const RmsFwd& A, const Shape& s, cudaStream_t st)
 {
     const unsigned grid = (unsigned)((A.rows + s.ry - 1) / s.ry);
     const dim3 block(s.tpr, s.ry);
-    if (A.y_dtype != RMS_E4M3) rms_forward_kernel<T, VEC, VPT, kPlain><<<grid, block, 0, st>>>(A);
-    else if (!A.lg_group) rms_forward_kernel<T, VEC, VPT, kRowCodes><<<grid, block, 0, st>>>(A);
-    else if constexpr (VEC > 1) rms_forward_kernel<T, VEC, VPT, kGroupCodes><<<grid, block, 0, st>>>(A);
-    return (int)cudaGetLastError();
+    if (A.y_dtype != RMS_E4M3) return launch_after(rms_forward_kernel<T, VEC, VPT, kPlain>, grid, block, 0, st, A);
+    else if (!A.lg_group) return launch_after(rms_forward_kernel<T, VEC, VPT, kRowCodes>, grid, block, 0, st, A);
+    else if constexpr (VEC > 1) return launch_after(rms_forward_kernel<T, VEC, VPT, kGroupCodes>, grid, block, 0, st, A);
+    return (int)cudaErrorInvalidValue;  // groups of columns go with whole packs
 }
 
 template <typename T, int VEC>
@@ -623,8 +626,7 @@ int launch_bwd_v(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
         const int e = (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e) return e;
     }
-    kernel<<<ctas, dim3(s.tpr, s.ry), smem, st>>>(A);
-    return (int)cudaGetLastError();
+    return launch_after(kernel, ctas, dim3(s.tpr, s.ry), smem, st, A);
 }
 
 template <typename T, int VEC>
@@ -637,10 +639,11 @@ int launch_bwd(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
         case 4: if constexpr (VEC <= 4) return launch_bwd_v<T, VEC, 4>(A, s, ctas, st); break;
         case 8: if constexpr (VEC == 1) return launch_bwd_v<T, VEC, 8>(A, s, ctas, st); break;
         case 16: if constexpr (VEC == 1) return launch_bwd_v<T, VEC, 16>(A, s, ctas, st); break;
-        default:
-            rms_backward_long_kernel<T><<<(unsigned)A.rows, kMaxThreads, 0, st>>>(A);
-            if (A.part) rms_dweight_long_kernel<T><<<dim3(ctas, (A.D + 255) / 256), 256, 0, st>>>(A);
-            return (int)cudaGetLastError();
+        default: {
+            const int e = launch_after(rms_backward_long_kernel<T>, (unsigned)A.rows, kMaxThreads, 0, st, A);
+            if (e || !A.part) return e;
+            return launch_after(rms_dweight_long_kernel<T>, dim3(ctas, (A.D + 255) / 256), 256, 0, st, A);
+        }
     }
     return (int)cudaErrorInvalidValue;
 }
@@ -785,17 +788,7 @@ extern "C" int rms_backward(const rms_params_t* p, const void* h, const void* we
     else if (p->x_dtype == GDN_BF16) e = s.vec > 1 ? launch_bwd<__nv_bfloat16, 8>(A, s, ctas, cs) : launch_bwd<__nv_bfloat16, 1>(A, s, ctas, cs);
     else e = s.vec > 1 ? launch_bwd<__half, 8>(A, s, ctas, cs) : launch_bwd<__half, 1>(A, s, ctas, cs);
     if (!e && dweight) {
-        // starts while the rows run and waits on the device for their end
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)((p->D + 7) / 8));
-        cfg.blockDim = dim3(128);
-        cfg.stream = cs;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        e = (int)cudaLaunchKernelEx(&cfg, rms_dweight_sum_kernel, (const float*)A.part, ctas, A.D, dweight);
+        e = launch_after(rms_dweight_sum_kernel, (unsigned)((p->D + 7) / 8), 128, 0, cs, (const float*)A.part, ctas, A.D, dweight);
     }
     return e ? cuda_fail(e, "rms_backward launch") : GDN_OK;
 }
