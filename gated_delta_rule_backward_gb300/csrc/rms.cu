@@ -418,8 +418,10 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
         for (int i = 0; i < RING - 1; ++i) fetch(row0 + i * all, i);
     }
     int set = 0, slot = 0;
+    float next_rstd = row0 < A.rows ? __ldg(A.rstd + row0) : 0.f;
     for (long long row = row0; row < A.rows; row += all, set ^= 1, slot = (slot + 1) % RING) {
-        const float rstd = __ldg(A.rstd + row);
+        const float rstd = next_rstd;
+        if (row + all < A.rows) next_rstd = __ldg(A.rstd + row + all);
         if (vec) {
             fetch(row + (RING - 1) * all, (slot + RING - 1) % RING);
             asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
