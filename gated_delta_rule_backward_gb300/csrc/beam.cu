@@ -141,19 +141,21 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamArg
     float m = -INFINITY;
 #pragma unroll
     for (int p = 0; p < PACKS; ++p) m = fmaxf(m, pack_max(x[p]));  // a pack of NaNs: -inf stays
-    // The sum against the thread's own maximum: (x - m) log2 e in two roundings, then the exponential.
+    // The sum against the thread's own maximum, 2^((x - m) L) with L = log2 e, as 2^(x L - r) for r = m L rounded: one
+    // product and sum an element, and what r is off by is taken out of the sum at the end.
     float s = 0.f;
     if (m < INFINITY && m > -INFINITY) {
+        const float r = m * kLog2e;
+        const f2 rr = pack2(-r, -r), ll = pack2(kLog2e, kLog2e);
         f2 s2 = 0;
-        const f2 mm = pack2(-m, -m), ll = pack2(kLog2e, kLog2e);
 #pragma unroll
         for (int p = 0; p < PACKS; ++p)
 #pragma unroll
             for (int i = 0; i < VEC; i += 2) {
-                const float2 v = unpack2(mul2(add2(pack2(x[p].get(i), x[p].get(i + 1)), mm), ll));
+                const float2 v = unpack2(fma2(x[p].pair(i), ll, rr));
                 s2 = add2(s2, pack2(ex2(v.x), ex2(v.y)));
             }
-        s = sum2(s2);
+        s = sum2(s2) * ex2(-fmaf(m, kLog2e, -r));
     }
     if (m == INFINITY || s != s) {  // infinities share the probability; NaNs are left out
         s = 0.f;

@@ -8,12 +8,26 @@
 #include <cuda_runtime.h>
 
 #include "../../include/gdn.h"
+#include "gdn_f32x2.cuh"
 
 namespace gdn {
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+
+// Two neighbours, widened together.
+__device__ __forceinline__ f2 widen2(const float* p) { return pack2(p[0], p[1]); }
+__device__ __forceinline__ f2 widen2(const __nv_bfloat16* p)
+{
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ f2 widen2(const __half* p)
+{
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(p));
+    return pack2(v.x, v.y);
+}
 
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
@@ -41,9 +55,11 @@ __device__ __forceinline__ void st_any(void* p, long long i, int dtype, float x)
 // VEC consecutive elements as one load where `vec` says that they are aligned for it; kept as they are
 // stored until get() widens them, so that a load in flight holds few registers.
 template <typename T, int VEC>
-struct Pack {
+struct alignas(VEC * sizeof(T)) Pack {
     T x[VEC];
     __device__ __forceinline__ float get(int i) const { return to_f32(x[i]); }
+    // Elements i and i + 1 (i even) for the packed fp32 instructions.
+    __device__ __forceinline__ f2 pair(int i) const { return widen2(x + i); }
 };
 
 template <typename T, int VEC>
