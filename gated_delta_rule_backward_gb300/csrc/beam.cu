@@ -14,6 +14,10 @@
 // index first) in one 64-bit number, so ranks do not depend on the lists' order.  Where a list
 // does not hold all that reach the bound (very many equal scores), n rounds of a CTA-wide
 // maximum over the chunks that reach it select instead.
+//
+// The stream is bound by the exponentials' instructions (nine a logit with the maximum) and, for few
+// rows, by latency: 16 x 8 rows of 128257 bf16 logits 10 us of 16.6, 128 x 8 rows of 151937 64 us in all, 4.9 TB/s.
+// Selecting inside every segment instead (a list and its ranks a CTA) took 17 us for the stream.
 #include <climits>
 #include <cstdio>
 

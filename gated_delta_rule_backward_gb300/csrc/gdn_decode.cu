@@ -13,6 +13,11 @@
 // lines), 4 rows across the warp, all of a warp's state in flight before its first use.  The warps of
 // a CTA share one head: each widens (and for KDA exponentiates) one of the next W tokens into
 // shared memory for all of them, and one barrier serves W tokens.
+//
+// Measured at 48 heads of 128 (16 key heads, bf16): 64 sequences' next tokens 63 us, 6.4 TB/s of 6.7 for a copy;
+// 200 sequences of up to 5 tokens, KDA, 204 us, 6.3 TB/s (four CTAs an SM; three 233 us; every warp
+// widening its own tokens 248 us; every lane 643 us); one sequence 3.1 us.  Many tokens on small heads
+// are bound by the fp32 pipe and by the longest sequence: 60 sequences of 16 tokens, 4 heads of 64, 9.6 us.
 #include <climits>
 #include <cstdio>
 
@@ -274,8 +279,9 @@ int launch_decode_g(const DecodeArgs& A, long long heads, bool kda, cudaStream_t
 template <typename T>
 int launch_decode_t(const DecodeArgs& A, long long heads, bool kda, cudaStream_t st)
 {
-    // Few heads are spread over more warps of one row a lane; many take more rows a lane, so
-    // that a token's q and k serve them all.
+    // Few heads are spread over more warps of one row a lane; many take more rows a lane, so that a token's
+    // q and k serve them all.  Both sides, one row against four a lane: 48 heads of 128, 1 sequence 3.1 and
+    // 3.2 us, 4 sequences 6.2 and 5.5, 8 sequences 13.7 and 10.9; 8 x 4 heads of 64, 16 tokens, 6.9 and 8.0.
     const bool wide = heads * A.SV >= 16 * 4 * kNumSMs;
     if (A.SK <= 32) return wide ? launch_decode_g<T, 1, 4>(A, heads, kda, st) : launch_decode_g<T, 1, 1>(A, heads, kda, st);
     if (A.SK == 64) return wide ? launch_decode_g<T, 2, 4>(A, heads, kda, st) : launch_decode_g<T, 2, 1>(A, heads, kda, st);
