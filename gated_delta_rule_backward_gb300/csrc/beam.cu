@@ -20,6 +20,7 @@
 // Selecting inside every segment instead (a list and its ranks a CTA) took 17 us for the stream.
 #include <climits>
 #include <cstdio>
+#include <type_traits>
 
 #include "../../include/beam.h"
 #include "gdn_elem.cuh"
@@ -102,28 +103,33 @@ __device__ __forceinline__ int lead_of(const T* row)
 {
     return (int)(((uintptr_t)row & 15) / sizeof(T));
 }
-// N packs whose first elements are at first + in(p): the whole ones all in flight at once, then the few elements of a
-// pack that the row's ends cut.
+// N packs whose first elements are at first + in(p): the whole ones all in flight at once, then the elements of a
+// pack that the row's first or last 16 bytes cut (in a loop of its own, so that the code that always runs stays short).
 template <typename T, int VEC, int N, typename In>
 __device__ __forceinline__ void ld_chunk_packs(Pack<T, VEC> (&x)[N], const T* row, int first, int seg, int V, const In& in)
 {
     Pack<T, VEC> none;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) none.x[i] = from_f32<T>(-INFINITY);
+    unsigned cut = 0;
 #pragma unroll
     for (int p = 0; p < N; ++p) {
         const int at = first + in(p);
+        const bool inside = in(p) < seg && at + VEC > 0 && at < V, whole = inside && at >= 0 && at + VEC <= V;
         x[p] = none;
-        if (in(p) < seg && at >= 0 && at + VEC <= V) x[p] = ld_pack<T, VEC>(row + at, true);
+        if (whole) x[p] = ld_pack<T, VEC>(row + at, true);
+        cut |= (inside && !whole ? 1u : 0u) << p;
     }
+    while (cut) {
+        const int c = __ffs(cut) - 1, at = first + in(c);
+        cut &= cut - 1;
+        Pack<T, VEC> part = none;
 #pragma unroll
-    for (int p = 0; p < N; ++p) {
-        const int at = first + in(p);
-        if (in(p) < seg && ((at < 0 && at + VEC > 0) || (at < V && at + VEC > V))) {
+        for (int i = 0; i < VEC; ++i)
+            if (at + i >= 0 && at + i < V) part.x[i] = row[at + i];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (at + i >= 0 && at + i < V) x[p].x[i] = row[at + i];
-        }
+        for (int p = 0; p < N; ++p)
+            if (p == c) x[p] = part;
     }
 }
 
@@ -213,6 +219,7 @@ __device__ __forceinline__ unsigned nth_top(const unsigned* top, int n, int lane
     return best > kNegInf ? best : kNegInf + 1;  // an item at -inf is none
 }
 
+constexpr int kMostReads = 8;  // packs of a chunk that a thread has in flight
 constexpr int kHeld = 2;  // chunks whose maxima a thread of the join keeps in registers
 
 template <typename T>
@@ -288,44 +295,61 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs 
     }
     __syncthreads();
 
-    // order(score) of a logit of beam k; 0 for one that is none
-    auto score_of = [&](int k, float x) -> unsigned {
-        if (!(x > -INFINITY)) return 0u;
-        const float m = row_max[k];
-        const float c = row_score[k] + ((x == m ? 0.f : x - m) - row_log[k]) + 0.f;  // + 0: -0 becomes 0
-        return c > -INFINITY ? order(c) : 0u;
+    // order(score) of a beam's logit; 0 for one that is none
+    struct Beam {
+        float score, max, log;
+        __device__ __forceinline__ unsigned of(float x) const
+        {
+            const float c = score + ((x == max ? 0.f : x - max) - log) + 0.f;  // + 0: -0 becomes 0
+            const unsigned o = order(c);
+            return (x > -INFINITY) & (c > -INFINITY) ? o : 0u;
+        }
     };
+    auto beam_of = [&](int k) { return Beam{row_score[k], row_max[k], row_log[k]}; };
     // every chunk of this thread: (its number among the going beams' chunks, order(its maximum's score))
     auto each_chunk = [&](auto&& take) {
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j) take(tid + j * kJoinThreads, score_of(held_row[j], held[j]));
+        for (int j = 0; j < kHeld; ++j) take(tid + j * kJoinThreads, beam_of(held_row[j]).of(held[j]));
         for (int i = tid + kHeld * kJoinThreads; i < all_chunks; i += kJoinThreads) {
             const int r = i / per, k = rows_on[r];
-            take(i, score_of(k, __ldcg(A.chunks + (row0 + k) * per + (i - r * per))));
+            take(i, beam_of(k).of(__ldcg(A.chunks + (row0 + k) * per + (i - r * per))));
         }
     };
-    // every element of the going beams' chunk i that reaches `least`, shared by LC threads: (order(score), index)
-    auto each_element = [&](int i, int LC, unsigned least, auto&& take) {
+    // every element of the going beams' chunk i that reaches `least`, shared by LC threads with `reads` packs in
+    // flight each: (order(score), index)
+    auto elements_of = [&](auto reads, int i, int LC, unsigned least, auto&& take) {
+        constexpr int kReads = decltype(reads)::value;
         const int r = i / per, c = i - r * per, k = rows_on[r];
+        const Beam beam = beam_of(k);
         const T* base = (const T*)A.logits + (row0 + k) * A.row_stride;
         const int split = c / (kThreads >> A.lg), t0 = (c - split * (kThreads >> A.lg)) << A.lg, first = split * A.seg - lead_of(base);
-        for (int q0 = tid & (LC - 1); q0 < 1 << (A.lg_packs + A.lg); q0 += 4 * LC) {
-            Pack<T, VEC> x[4];
+        for (int q0 = tid & (LC - 1); q0 < 1 << (A.lg_packs + A.lg); q0 += kReads * LC) {
+            Pack<T, VEC> x[kReads];
             auto in = [&](int p) {
                 const int q = q0 + LC * p;
                 return q < 1 << (A.lg_packs + A.lg) ? ((q >> A.lg) * kThreads + t0 + (q & ((1 << A.lg) - 1))) * VEC : A.seg;
             };
-            ld_chunk_packs<T, VEC, 4>(x, base, first, A.seg, A.V, in);
+            ld_chunk_packs<T, VEC, kReads>(x, base, first, A.seg, A.V, in);
+            unsigned reach = 0;  // the packs that hold such an element: few, so they are read again one by one
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                if (score_of(k, pack_max(x[p])) < least) continue;
+            for (int p = 0; p < kReads; ++p) reach |= (beam.of(pack_max(x[p])) >= least ? 1u : 0u) << p;
+#pragma unroll 1
+            for (; reach; reach &= reach - 1) {
+                const int one = in(__ffs(reach) - 1);
+                Pack<T, VEC> y[1];
+                ld_chunk_packs<T, VEC, 1>(y, base, first, A.seg, A.V, [&](int) { return one; });
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const unsigned o = score_of(k, x[p].get(e));
-                    if (o >= least) take(o, (unsigned)k * (unsigned)A.V + (unsigned)(first + in(p) + e));
+                    const unsigned o = beam.of(y[0].get(e));
+                    if (o >= least) take(o, (unsigned)k * (unsigned)A.V + (unsigned)(first + one + e));
                 }
             }
         }
+    };
+
+    auto each_element = [&](int i, int LC, unsigned least, auto&& take) {
+        if (1 << (A.lg_packs + A.lg) <= LC) elements_of(std::integral_constant<int, 1>(), i, LC, least, take);
+        else elements_of(std::integral_constant<int, kMostReads>(), i, LC, least, take);
     };
 
     unsigned mine = 0;
@@ -395,12 +419,14 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs 
         fits = listed <= kList;
         if (fits) {
             found = listed < A.n ? listed : A.n;
-            for (int t = tid; t < listed; t += kJoinThreads) {
-                const u64 key = elements[t];
+            for (int t0 = 0; t0 < listed; t0 += kJoinThreads / 8) {  // eight threads a key
+                const int t = t0 + tid / 8;
+                const u64 key = t < listed ? elements[t] : ~0ull;
                 int rank = 0;
-#pragma unroll 4
-                for (int i = 0; i < listed; ++i) rank += elements[i] > key;
-                if (rank < A.n) out[rank] = key;
+                for (int i = tid & 7; i < listed; i += 8) rank += elements[i] > key;
+#pragma unroll
+                for (int o = 4; o >= 1; o >>= 1) rank += __shfl_xor_sync(kAll, rank, o);
+                if (t < listed && (tid & 7) == 0 && rank < A.n) out[rank] = key;
             }
             __syncthreads();
         }
@@ -416,7 +442,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs 
             };
             for (int i = warp; i < all_chunks; i += kJoinWarps) {
                 const int r = i / per, c = i - r * per, k = rows_on[r];
-                if (score_of(k, __ldcg(A.chunks + (row0 + k) * per + c)) >= bound) each_element(i, 32, max(bound, (unsigned)(best >> 32)), better);
+                if (beam_of(k).of(__ldcg(A.chunks + (row0 + k) * per + c)) >= bound) each_element(i, 32, max(bound, (unsigned)(best >> 32)), better);
             }
             if (tid < A.K && kind[tid] > 0) better(order(row_score[tid] + 0.f), (unsigned)tid * (unsigned)A.V + (unsigned)A.pad);
 #pragma unroll
