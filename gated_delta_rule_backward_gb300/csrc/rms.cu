@@ -1,8 +1,12 @@
 // rms.cu -- root-mean-square norm with the residual's addition, forward and backward (include/rms.h).
 //
 // Both directions are one pass over their rows: what is read once is held in registers until the
-// row's sums are known.  TPR threads share a row, each with VPT packs of VEC elements, two to a
-// register pair for the packed fp32 instructions.  Bytes bound both.
+// row's sums are known.  TPR threads share a row, each with VPT packs of VEC elements (16 bytes), two to
+// a register pair for the packed fp32 instructions.  Bytes bound both.
+//
+// Packs lie at multiples of VEC of the flat index row D + column, so that they are aligned for any D: where VEC does
+// not divide D, a row begins `lead` elements into its first pack and may end inside its last.  A cut pack is still
+// read as a whole (its other elements are a neighbouring row's, and set to zero) and stored one by one.
 //
 // Forward: a CTA a row (a warp where rows are short), five CTAs an SM, so that other rows' loads
 // are in flight while one is summed; with y = (h w) rstd the largest |h w| of a row, summed beside
@@ -35,7 +39,7 @@ struct RmsFwd {
     void *h, *y;
     float *scales, *rstd;
     long long xs, rs;
-    int rows, D, w_dtype, y_dtype, lg_group, vec;
+    int rows, D, w_dtype, y_dtype, lg_group, vec, w_vec;
     float eps, inv_D;
 };
 
@@ -45,7 +49,7 @@ struct RmsBwd {
     void* dx;
     float* part;  // [gridDim.x][D] sums of dy n over a CTA's rows; null without dweight
     long long hs, dys;
-    int rows, D, w_dtype, vec;
+    int rows, D, w_dtype, vec, w_vec;
     float inv_D;
 };
 
@@ -103,15 +107,6 @@ struct Nums {
         return m;
     }
 };
-template <>
-struct Nums<1> {
-    float v;
-    __device__ __forceinline__ void fill(float x) { v = x; }
-    __device__ __forceinline__ void set(int, float x, float) { v = x; }
-    __device__ __forceinline__ float2 pair(int) const { return make_float2(v, 0.f); }
-    __device__ __forceinline__ float sum() const { return v; }
-    __device__ __forceinline__ float max_abs() const { return fabsf(v); }
-};
 template <int VEC>
 __device__ __forceinline__ Nums<VEC> add(const Nums<VEC>& a, const Nums<VEC>& b)
 {
@@ -120,7 +115,6 @@ __device__ __forceinline__ Nums<VEC> add(const Nums<VEC>& a, const Nums<VEC>& b)
     for (int i = 0; i < VEC / 2; ++i) r.v[i] = add2(a.v[i], b.v[i]);
     return r;
 }
-__device__ __forceinline__ Nums<1> add(const Nums<1>& a, const Nums<1>& b) { return {a.v + b.v}; }
 template <int VEC>
 __device__ __forceinline__ Nums<VEC> mul(const Nums<VEC>& a, const Nums<VEC>& b)
 {
@@ -129,7 +123,6 @@ __device__ __forceinline__ Nums<VEC> mul(const Nums<VEC>& a, const Nums<VEC>& b)
     for (int i = 0; i < VEC / 2; ++i) r.v[i] = mul2(a.v[i], b.v[i]);
     return r;
 }
-__device__ __forceinline__ Nums<1> mul(const Nums<1>& a, const Nums<1>& b) { return {a.v * b.v}; }
 template <int VEC>
 __device__ __forceinline__ Nums<VEC> mul(const Nums<VEC>& a, float b)
 {
@@ -139,7 +132,6 @@ __device__ __forceinline__ Nums<VEC> mul(const Nums<VEC>& a, float b)
     for (int i = 0; i < VEC / 2; ++i) r.v[i] = mul2(a.v[i], bb);
     return r;
 }
-__device__ __forceinline__ Nums<1> mul(const Nums<1>& a, float b) { return {a.v * b}; }
 template <int VEC>
 __device__ __forceinline__ Nums<VEC> fma(const Nums<VEC>& a, const Nums<VEC>& b, const Nums<VEC>& c)
 {
@@ -148,7 +140,6 @@ __device__ __forceinline__ Nums<VEC> fma(const Nums<VEC>& a, const Nums<VEC>& b,
     for (int i = 0; i < VEC / 2; ++i) r.v[i] = fma2(a.v[i], b.v[i], c.v[i]);
     return r;
 }
-__device__ __forceinline__ Nums<1> fma(const Nums<1>& a, const Nums<1>& b, const Nums<1>& c) { return {fmaf(a.v, b.v, c.v)}; }
 template <int VEC>
 __device__ __forceinline__ Nums<VEC> fma(const Nums<VEC>& a, float b, const Nums<VEC>& c)
 {
@@ -158,7 +149,6 @@ __device__ __forceinline__ Nums<VEC> fma(const Nums<VEC>& a, float b, const Nums
     for (int i = 0; i < VEC / 2; ++i) r.v[i] = fma2(a.v[i], bb, c.v[i]);
     return r;
 }
-__device__ __forceinline__ Nums<1> fma(const Nums<1>& a, float b, const Nums<1>& c) { return {fmaf(a.v, b, c.v)}; }
 
 __device__ __forceinline__ float2 widen2(uint32_t w, __nv_bfloat16) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
 __device__ __forceinline__ float2 widen2(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
@@ -173,20 +163,39 @@ __device__ __forceinline__ uint32_t narrow2(float2 x, __half)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A thread's VEC elements of a row (16 bytes of T, or one element) as they are stored.
-template <typename T, int VEC>
-__device__ __forceinline__ uint4 ld_cols(const T* row, int c, int D, bool vec)
+// Where row `row` begins in its first pack.
+template <int VEC>
+__device__ __forceinline__ int lead_of(long long row, int D)
+{
+    return (int)(((unsigned)row * (unsigned)D) & (VEC - 1));
+}
+
+// The first `from` and the elements past `to` of a pack set to zero.
+template <typename T>
+__device__ __forceinline__ uint4 cut_pack(const uint4& x, int from, int to)
+{
+    constexpr int PER = 4 / (int)sizeof(T);  // elements of a word
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4 * PER; ++i)
+        if (i < from || i >= to) w[i / PER] &= PER == 1 ? 0u : i & 1 ? 0xffffu : 0xffff0000u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The pack at column c of a row of D (zero outside the row), as it is stored.  CUT: packs may be cut by the row's ends;
+// vec: packs are aligned; `more`: what lies around the row in memory may be read, too.
+template <typename T, int VEC, bool CUT>
+__device__ __forceinline__ uint4 ld_cols(const T* row, int c, int D, bool vec, bool more)
 {
     uint4 r = make_uint4(0, 0, 0, 0);
-    if (VEC == 1) {
-        if (c < D) r.x = sizeof(T) == 4 ? reinterpret_cast<const uint32_t*>(row)[c] : reinterpret_cast<const uint16_t*>(row)[c];
-    } else if (vec) {
+    if (vec && (!CUT || more || (c >= 0 && c + VEC <= D))) {
         if (c < D) r = *reinterpret_cast<const uint4*>(row + c);
-    } else {
+        if (CUT && (c < 0 || c + VEC > D)) r = cut_pack<T>(r, -c, D - c);
+    } else if (c < D) {
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-            if (c + i < D) {
+            if (c + i >= 0 && c + i < D) {
                 if (sizeof(T) == 4) w[i & 3] = reinterpret_cast<const uint32_t*>(row)[c + i];
                 else w[(i / 2) & 3] |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[c + i] << (16 * (i & 1));
             }
@@ -205,7 +214,7 @@ __device__ __forceinline__ Nums<VEC> widen(const uint4& x)
         for (int i = 0; i < VEC; i += 2) r.set(i, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
     } else {
 #pragma unroll
-        for (int i = 0; i < (VEC + 1) / 2; ++i) {
+        for (int i = 0; i < VEC / 2; ++i) {
             const float2 v = widen2(w[i], T());
             r.set(2 * i, v.x, v.y);
         }
@@ -213,13 +222,11 @@ __device__ __forceinline__ Nums<VEC> widen(const uint4& x)
     return r;
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool CUT>
 __device__ __forceinline__ void st_cols(T* row, int c, int D, bool vec, const Nums<VEC>& v)
 {
-    if constexpr (VEC == 1) {
-        if (c < D) row[c] = from_f32<T>(v.v);
-    } else if (vec) {
-        if (c >= D) return;
+    if (vec && (!CUT || (c >= 0 && c + VEC <= D))) {
+        if (!CUT && c >= D) return;
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < VEC; i += 4) {
@@ -231,58 +238,59 @@ __device__ __forceinline__ void st_cols(T* row, int c, int D, bool vec, const Nu
         } else {
             *reinterpret_cast<uint2*>(row + c) = make_uint2(narrow2(v.pair(0), T()), narrow2(v.pair(2), T()));
         }
-    } else {
+    } else if (c < D) {
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
             const float2 a = v.pair(i);
-            if (c + i < D) row[c + i] = from_f32<T>(a.x);
-            if (c + i + 1 < D) row[c + i + 1] = from_f32<T>(a.y);
+            if (c + i >= 0 && c + i < D) row[c + i] = from_f32<T>(a.x);
+            if (c + i + 1 >= 0 && c + i + 1 < D) row[c + i + 1] = from_f32<T>(a.y);
         }
     }
 }
 
-template <int VEC>
+template <int VEC, bool CUT>
 __device__ __forceinline__ Nums<VEC> ld_weight(const void* p, int dtype, int c, int D, bool vec)
 {
     Nums<VEC> w;
     if (!p) {
         w.fill(1.f);
-    } else if (VEC >= 4 && vec && dtype == GDN_F32) {
+    } else if (!CUT && vec && dtype == GDN_F32) {
 #pragma unroll
-        for (int b = 0; b + 3 < VEC; b += 4) {
+        for (int b = 0; b < VEC; b += 4) {
             const float4 v = c < D ? __ldg(reinterpret_cast<const float4*>((const float*)p + c + b)) : make_float4(0.f, 0.f, 0.f, 0.f);
             w.set(b, v.x, v.y);
             w.set(b + 2, v.z, v.w);
         }
+    } else if (CUT && dtype == GDN_F32 && c >= 0 && c + VEC <= D) {
+        const float* q = (const float*)p + c;
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) w.set(i, __ldg(q + i), __ldg(q + i + 1));
     } else {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 2) w.set(i, c + i < D ? ld_any(p, c + i, dtype) : 0.f, VEC > 1 && c + i + 1 < D ? ld_any(p, c + i + 1, dtype) : 0.f);
+        for (int i = 0; i < VEC; i += 2)
+            w.set(i, c + i >= 0 && c + i < D ? ld_any(p, c + i, dtype) : 0.f, c + i + 1 >= 0 && c + i + 1 < D ? ld_any(p, c + i + 1, dtype) : 0.f);
     }
     return w;
 }
 
-template <int VEC>
+template <int VEC, bool CUT>
 __device__ __forceinline__ void st_e4m3(uint8_t* row, int c, int D, bool vec, const Nums<VEC>& v)
 {
-    if constexpr (VEC == 1) {
-        if (c < D) row[c] = __nv_cvt_float_to_fp8(v.v, __NV_SATFINITE, __NV_E4M3);
-    } else {
-        uint32_t w[VEC / 4];
+    uint32_t w[VEC / 4];
 #pragma unroll
-        for (int i = 0; i < VEC; i += 4) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(v.pair(i), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(v.pair(i + 2), __NV_SATFINITE, __NV_E4M3);
-            w[i / 4] = lo | hi << 16;
-        }
-        if (vec) {
-            if (c >= D) return;
-            if constexpr (VEC == 8) *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t*>(row + c) = w[0];
-        } else {
+    for (int i = 0; i < VEC; i += 4) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(v.pair(i), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(v.pair(i + 2), __NV_SATFINITE, __NV_E4M3);
+        w[i / 4] = lo | hi << 16;
+    }
+    if (vec && (!CUT || (c >= 0 && c + VEC <= D))) {
+        if (!CUT && c >= D) return;
+        if constexpr (VEC == 8) *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(row + c) = w[0];
+    } else if (c < D) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (c + i < D) row[c + i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
-        }
+        for (int i = 0; i < VEC; ++i)
+            if (c + i >= 0 && c + i < D) row[c + i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
     }
 }
 
@@ -290,13 +298,13 @@ __device__ __forceinline__ void st_e4m3(uint8_t* row, int c, int D, bool vec, co
 enum { kPlain = 0, kRowCodes = 1, kGroupCodes = 2 };
 
 // What follows the sums, for one pack: h and y (or its codes and scale) to memory.
-template <typename T, int VEC, int OUT>
+template <typename T, int VEC, int OUT, bool CUT>
 __device__ __forceinline__ void finish_pack(const RmsFwd& A, const Nums<VEC>& h, long long row, int c, float rstd, float inv)
 {
     const bool vec = A.vec;
     const long long at = row * A.D;
-    if (A.h) st_cols<T, VEC>((T*)A.h + at, c, A.D, vec, h);
-    const Nums<VEC> y = mul(mul(h, ld_weight<VEC>(A.w, A.w_dtype, c, A.D, vec)), rstd);
+    if (A.h) st_cols<T, VEC, CUT>((T*)A.h + at, c, A.D, vec, h);
+    const Nums<VEC> y = mul(mul(h, ld_weight<VEC, CUT>(A.w, A.w_dtype, c, A.D, A.w_vec)), rstd);
     if (OUT == kGroupCodes) {
         float m = y.max_abs();
         // the lanes of a group (a power of two; every lane of the warp is here)
@@ -311,49 +319,52 @@ __device__ __forceinline__ void finish_pack(const RmsFwd& A, const Nums<VEC>& h,
         if (c < A.D && (c & ((1 << A.lg_group) - 1)) == 0) A.scales[row * (A.D >> A.lg_group) + (c >> A.lg_group)] = scale;
     }
     if (OUT != kPlain) {
-        st_e4m3<VEC>((uint8_t*)A.y + at, c, A.D, vec, mul(y, inv));
+        st_e4m3<VEC, CUT>((uint8_t*)A.y + at, c, A.D, vec, mul(y, inv));
     } else if (A.y_dtype == GDN_BF16) {
-        st_cols<__nv_bfloat16, VEC>((__nv_bfloat16*)A.y + at, c, A.D, vec, y);
+        st_cols<__nv_bfloat16, VEC, CUT>((__nv_bfloat16*)A.y + at, c, A.D, vec, y);
     } else if (A.y_dtype == GDN_F32) {
-        st_cols<float, VEC>((float*)A.y + at, c, A.D, vec, y);
+        st_cols<float, VEC, CUT>((float*)A.y + at, c, A.D, vec, y);
     } else {
-        st_cols<__half, VEC>((__half*)A.y + at, c, A.D, vec, y);
+        st_cols<__half, VEC, CUT>((__half*)A.y + at, c, A.D, vec, y);
     }
 }
 
 // VPT packs a thread; VPT = 0: rows that registers do not hold, read again (from L2) after the sums.
 // Rows of fewer than the most packs have 256 threads at most, five CTAs an SM: 4096 rows of 6144
 // to codes take 28 us so, 30 us with the four that the compiler's own choice of registers leaves.
-template <typename T, int VEC, int VPT, int OUT>
-__global__ void __launch_bounds__(VPT > 0 && VPT < (VEC > 1 ? 4 : 16) ? 256 : kMaxThreads, VPT > 0 && VPT < (VEC > 1 ? 4 : 16) ? 5 : 1)
-    rms_forward_kernel(const RmsFwd A)
+template <typename T, int VPT, int OUT, bool CUT>
+__global__ void __launch_bounds__(VPT > 0 && VPT < 4 ? 256 : kMaxThreads, VPT > 0 && VPT < 4 ? 5 : 1) rms_forward_kernel(const RmsFwd A)
 {
+    constexpr int VEC = 16 / (int)sizeof(T);
     __shared__ float2 buf[32];
     const int tid = threadIdx.x, step = blockDim.x * VEC;
     const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     begin_after();
     if (row >= A.rows) return;  // the whole row's threads leave together
+    const int c0 = tid * VEC - (CUT ? lead_of<VEC>(row, A.D) : 0);
     const T* x = (const T*)A.x + row * A.xs;
     const T* r = A.res ? (const T*)A.res + row * A.rs : x;
+    // a sum that replaces an input row may only be read by its own row's threads
+    const bool vec = A.vec, more = CUT && row + 1 < A.rows && A.h != A.x && A.h != A.res;
     Nums<VEC> h[VPT ? VPT : 1], acc;
     acc.fill(0.f);
     float m = 0.f;
     auto sum_at = [&](int c) {
-        const uint4 a = ld_cols<T, VEC>(x, c, A.D, A.vec);
+        const uint4 a = ld_cols<T, VEC, CUT>(x, c, A.D, vec, more);
         if (!A.res) return widen<T, VEC>(a);
-        return add(widen<T, VEC>(a), widen<T, VEC>(ld_cols<T, VEC>(r, c, A.D, A.vec)));
+        return add(widen<T, VEC>(a), widen<T, VEC>(ld_cols<T, VEC, CUT>(r, c, A.D, vec, more)));
     };
     auto take = [&](const Nums<VEC>& hv, int c) {
         acc = fma(hv, hv, acc);
-        if (OUT == kRowCodes) m = fmaxf(m, mul(hv, ld_weight<VEC>(A.w, A.w_dtype, c, A.D, A.vec)).max_abs());
+        if (OUT == kRowCodes) m = fmaxf(m, mul(hv, ld_weight<VEC, CUT>(A.w, A.w_dtype, c, A.D, A.w_vec)).max_abs());
     };
     if (VPT) {
         uint4 px[VPT ? VPT : 1], pr[VPT ? VPT : 1];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) px[v] = ld_cols<T, VEC>(x, tid * VEC + v * step, A.D, A.vec);
+        for (int v = 0; v < VPT; ++v) px[v] = ld_cols<T, VEC, CUT>(x, c0 + v * step, A.D, vec, more);
         if (A.res) {
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) pr[v] = ld_cols<T, VEC>(r, tid * VEC + v * step, A.D, A.vec);
+            for (int v = 0; v < VPT; ++v) pr[v] = ld_cols<T, VEC, CUT>(r, c0 + v * step, A.D, vec, more);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) h[v] = add(widen<T, VEC>(px[v]), widen<T, VEC>(pr[v]));
         } else {
@@ -361,9 +372,9 @@ __global__ void __launch_bounds__(VPT > 0 && VPT < (VEC > 1 ? 4 : 16) ? 256 : kM
             for (int v = 0; v < VPT; ++v) h[v] = widen<T, VEC>(px[v]);
         }
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) take(h[v], tid * VEC + v * step);
+        for (int v = 0; v < VPT; ++v) take(h[v], c0 + v * step);
     } else {
-        for (int c = tid * VEC; c < A.D; c += step) take(sum_at(c), c);
+        for (int c = c0; c < A.D; c += step) take(sum_at(c), c);
     }
     const float2 sm = row_reduce<OUT == kRowCodes, false>(acc.sum(), m, buf);
     const float rstd = rsqrtf(sm.x * A.inv_D + A.eps);
@@ -374,96 +385,130 @@ __global__ void __launch_bounds__(VPT > 0 && VPT < (VEC > 1 ? 4 : 16) ? 256 : kM
     }
     if (VPT) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) finish_pack<T, VEC, OUT>(A, h[v], row, tid * VEC + v * step, rstd, inv);
+        for (int v = 0; v < VPT; ++v) finish_pack<T, VEC, OUT, CUT>(A, h[v], row, c0 + v * step, rstd, inv);
     } else {
         // whole steps, so that the lanes that share a scale stay together
-        for (int c0 = 0; c0 < A.D; c0 += step) finish_pack<T, VEC, OUT>(A, sum_at(c0 + tid * VEC), row, c0 + tid * VEC, rstd, inv);
+        for (int c = c0; c - c0 < A.D + VEC; c += step) finish_pack<T, VEC, OUT, CUT>(A, sum_at(c), row, c, rstd, inv);
     }
 }
 
-__device__ __forceinline__ void copy_async(uint4* to, const void* from, bool there)
+__device__ __forceinline__ void copy_async(uint4* to, const void* from, uint32_t bytes)  // the rest of 16 bytes: zeros
 {
-    const uint32_t bytes = there ? 16 : 0;  // 0: zeros
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(bytes) : "memory");
 }
 
-// Rows blockIdx.x blockDim.y + threadIdx.y, then a whole grid of rows further: a thread keeps its columns,
-// their weights and their part of dweight in registers over all its rows.  Whole packs come through a
-// ring of rows in shared memory, where every thread copies and reads places of its own, so that
-// the rows in flight need neither registers nor barriers.
-template <typename T, int VEC, int VPT, int RING>
+// Rows blockIdx.x blockDim.y + threadIdx.y, then a whole grid of rows further (a multiple of VEC of them, so that
+// a thread's columns stay): a thread keeps its columns, their weights and their part of dweight in registers
+// over all its rows.  Packs come through a ring of rows in shared memory, where every thread copies and
+// reads places of its own, so that the rows in flight need neither registers nor barriers.
+// RING = 0, for tensors off their 16 bytes: every pack is read directly.
+// LEAN, for the longest rows: no more than dweight's part stays in registers; the weights are in shared memory,
+// and the ring is read twice.
+template <typename T, int VPT, int RING, bool CUT>
 __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
 {
-    extern __shared__ uint4 ring[];  // [RING][3 VPT][threads]; at the end, as floats, [blockDim.y][D]
+    constexpr int VEC = 16 / (int)sizeof(T), HELD = VPT * VEC > 16 ? 1 : VPT;
+    constexpr bool LEAN = VPT * VEC > 16;
+    extern __shared__ uint4 ring[];  // [RING][3 VPT][threads], LEAN: weights [VPT][VEC / 4][threads]; at the end, as floats, [blockDim.y][D]
     __shared__ float2 buf[2][kRingThreads / 32];
     const int tid = threadIdx.x, step = blockDim.x * VEC;
     const int threads = blockDim.x * blockDim.y, own = threadIdx.y * blockDim.x + tid;
-    const bool vec = VEC > 1 && A.vec;
     begin_after();
-    Nums<VEC> w[VPT], dw[VPT];
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        w[v] = ld_weight<VEC>(A.w, A.w_dtype, tid * VEC + v * step, A.D, A.vec);
-        dw[v].fill(0.f);
-    }
     const long long all = (long long)gridDim.x * blockDim.y, row0 = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    const int c0 = tid * VEC - (CUT ? lead_of<VEC>(row0, A.D) : 0);
     const T *h = (const T*)A.h, *dy = (const T*)A.dy, *dh = (const T*)A.dh;
     auto fetch = [&](long long row, int slot) {
         if (row < A.rows) {
             uint4* to = ring + (size_t)slot * 3 * VPT * threads + own;
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                const int c = tid * VEC + v * step, cc = c < A.D ? c : 0;
-                copy_async(to + (3 * v) * threads, h + row * A.hs + cc, c < A.D);
-                copy_async(to + (3 * v + 1) * threads, dy + row * A.dys + cc, c < A.D);
-                if (dh) copy_async(to + (3 * v + 2) * threads, dh + row * A.D + cc, c < A.D);
+                const int c = c0 + v * step, at = c < A.D ? c : 0;
+                const uint32_t bytes = c >= A.D ? 0 : !CUT || c + VEC <= A.D ? 16 : (uint32_t)(A.D - c) * sizeof(T);
+                copy_async(to + (3 * v) * threads, h + row * A.hs + at, bytes);
+                copy_async(to + (3 * v + 1) * threads, dy + row * A.dys + at, bytes);
+                if (dh) copy_async(to + (3 * v + 2) * threads, dh + row * A.D + at, bytes);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    if (vec) {
+    constexpr bool vec = RING > 0;
+    if constexpr (vec) {
 #pragma unroll
         for (int i = 0; i < RING - 1; ++i) fetch(row0 + i * all, i);
     }
+    float4* weights = reinterpret_cast<float4*>(ring + (vec ? (size_t)RING * 3 * VPT * threads : 0)) + own;
+    auto weight = [&](int v) {
+        Nums<VEC> r;
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const float4 x = weights[(v * (VEC / 4) + i / 4) * threads];
+            r.set(i, x.x, x.y);
+            r.set(i + 2, x.z, x.w);
+        }
+        return r;
+    };
+    Nums<VEC> w[HELD], dw[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const Nums<VEC> wv = ld_weight<VEC, CUT>(A.w, A.w_dtype, c0 + v * step, A.D, A.w_vec);
+        if (LEAN) {
+#pragma unroll
+            for (int i = 0; i < VEC; i += 4) {
+                const float2 a = wv.pair(i), b = wv.pair(i + 2);
+                weights[(v * (VEC / 4) + i / 4) * threads] = make_float4(a.x, a.y, b.x, b.y);
+            }
+        } else {
+            w[LEAN ? 0 : v] = wv;
+        }
+        dw[v].fill(0.f);
+    }
     int set = 0, slot = 0;
     float next_rstd = row0 < A.rows ? __ldg(A.rstd + row0) : 0.f;
-    for (long long row = row0; row < A.rows; row += all, set ^= 1, slot = (slot + 1) % RING) {
+    for (long long row = row0; row < A.rows; row += all, set ^= 1, slot = vec ? (slot + 1) % (RING ? RING : 1) : 0) {
         const float rstd = next_rstd;
         if (row + all < A.rows) next_rstd = __ldg(A.rstd + row + all);
-        if (vec) {
+        if constexpr (vec) {
             fetch(row + (RING - 1) * all, (slot + RING - 1) % RING);
             asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
         }
-        Nums<VEC> n[VPT], t[VPT], acc;
-        uint4 pg[VPT];
+        const uint4* from = ring + (size_t)slot * 3 * VPT * threads + own;
+        // pack v of h (0), dy (1) or dh (2); in the row's first pack, the neighbouring row's elements are zeros
+        auto pack = [&](int v, int which) -> uint4 {
+            const int c = c0 + v * step;
+            if constexpr (!vec) {
+                const T* src = which == 0 ? h + row * A.hs : which == 1 ? dy + row * A.dys : dh + row * A.D;
+                return ld_cols<T, VEC, CUT>(src, c, A.D, false, false);
+            }
+            uint4 x = from[(3 * v + which) * threads];
+            if (CUT && c < 0) x = cut_pack<T>(x, -c, VEC);
+            return x;
+        };
+        Nums<VEC> n[HELD], t[HELD], acc;
+        uint4 pg[HELD];
         acc.fill(0.f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            uint4 a, b;
-            const int c = tid * VEC + v * step;
-            if (vec) {
-                const uint4* from = ring + ((size_t)slot * 3 * VPT + 3 * v) * threads + own;
-                a = from[0];
-                b = from[threads];
-                if (dh) pg[v] = from[2 * threads];
-            } else {
-                a = ld_cols<T, VEC>(h + row * A.hs, c, A.D, false);
-                b = ld_cols<T, VEC>(dy + row * A.dys, c, A.D, false);
-                if (dh) pg[v] = ld_cols<T, VEC>(dh + row * A.D, c, A.D, false);
-            }
-            n[v] = mul(widen<T, VEC>(a), rstd);
-            t[v] = widen<T, VEC>(b);
-            dw[v] = fma(t[v], n[v], dw[v]);
-            t[v] = mul(t[v], w[v]);
-            acc = fma(t[v], n[v], acc);
+            const int k = LEAN ? 0 : v;
+            n[k] = mul(widen<T, VEC>(pack(v, 0)), rstd);
+            t[k] = widen<T, VEC>(pack(v, 1));
+            if (!LEAN && dh) pg[k] = pack(v, 2);
+            dw[v] = fma(t[k], n[k], dw[v]);
+            t[k] = mul(t[k], LEAN ? weight(v) : w[k]);
+            acc = fma(t[k], n[k], acc);
         }
         const float c = -rstd * (row_reduce<false, true>(acc.sum(), 0.f, buf[set] + threadIdx.y * (blockDim.x >> 5)).x * A.inv_D);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
+            const int k = LEAN ? 0 : v;
+            if (LEAN) {
+                n[k] = mul(widen<T, VEC>(pack(v, 0)), rstd);
+                t[k] = mul(widen<T, VEC>(pack(v, 1)), weight(v));
+                if (dh) pg[k] = pack(v, 2);
+            }
             Nums<VEC> o;
-            if (dh) o = fma(t[v], rstd, widen<T, VEC>(pg[v]));
-            else o = mul(t[v], rstd);
-            st_cols<T, VEC>((T*)A.dx + row * A.D, tid * VEC + v * step, A.D, A.vec, fma(n[v], c, o));
+            if (dh) o = fma(t[k], rstd, widen<T, VEC>(pg[k]));
+            else o = mul(t[k], rstd);
+            st_cols<T, VEC, CUT>((T*)A.dx + row * A.D, c0 + v * step, A.D, vec, fma(n[k], c, o));
         }
     }
     if (!A.part) return;
@@ -473,14 +518,7 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();  // the ring is read
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int i = 0; i < VEC; i += 2) {
-                const int c = tid * VEC + v * step + i;
-                const float2 x = dw[v].pair(i);
-                if (c < A.D) sums[(size_t)threadIdx.y * A.D + c] = x.x;
-                if (VEC > 1 && c + 1 < A.D) sums[(size_t)threadIdx.y * A.D + c + 1] = x.y;
-            }
+        for (int v = 0; v < VPT; ++v) st_cols<float, VEC, CUT>(sums + (size_t)threadIdx.y * A.D, c0 + v * step, A.D, !CUT, dw[v]);
         __syncthreads();
         for (int c = own; c < A.D; c += threads) {
             float t = 0.f;
@@ -489,7 +527,7 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
         }
     } else {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) st_cols<float, VEC>(out, tid * VEC + v * step, A.D, A.vec, dw[v]);
+        for (int v = 0; v < VPT; ++v) st_cols<float, VEC, CUT>(out, c0 + v * step, A.D, !CUT, dw[v]);
     }
 }
 
@@ -548,24 +586,20 @@ __global__ void __launch_bounds__(128) rms_dweight_sum_kernel(const float* part,
     }
 }
 
-// How a row is laid over threads: tpr threads of vpt packs (0: more than registers hold), ry rows a CTA.
+// How a row is laid over threads: tpr threads of vpt packs (0: more than registers hold), ry rows a CTA.  It, and with
+// it the order of every sum, goes by D, the rows and the types alone: the same numbers give the same bits
+// whatever their alignment and strides (packs off their 16 bytes are loaded one by one).
 struct Shape {
-    int vec, vpt, tpr, ry;
+    int vpt, tpr, ry;
 };
 
-// The layout, and with it the order of every sum, goes by D, the rows and the types alone: the same numbers give the
-// same bits whatever their alignment (packs off their 16 bytes are loaded one by one).  `most`: elements
-// of a thread; `threads`: below so many, a thread takes one pack more only when its row has more than that.
+// `most`: packs of a thread; a thread takes one more while the row has more than `threads` times as many.
 Shape shape_of(const rms_params_t* p, int most, int threads, int max_threads)
 {
-    const int vecn = 16 / (int)elem_size(p->x_dtype);
-    Shape s{};
-    s.vec = p->D % vecn == 0 ? vecn : 1;
-    const int64_t packs = (p->D + s.vec - 1) / s.vec;
-    most /= s.vec;
-    s.ry = 1;
-    s.vpt = 1;
-    while (s.vpt < most && packs > threads * (int64_t)s.vpt) s.vpt = s.vec > 1 && s.vpt < 4 ? s.vpt + 1 : 2 * s.vpt;
+    const int vec = 16 / (int)elem_size(p->x_dtype);
+    const int64_t packs = (p->D + (p->D % vec ? vec - 1 : 0) + vec - 1) / vec;
+    Shape s{1, 0, 1};
+    while (s.vpt < most && packs > threads * (int64_t)s.vpt) ++s.vpt;
     const int64_t t = ((packs + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     if (t > max_threads) s.vpt = 0;
     s.tpr = t > max_threads ? max_threads : (int)t;
@@ -576,10 +610,9 @@ Shape shape_of(const rms_params_t* p, int most, int threads, int max_threads)
 // lane) a warp each, several to a CTA where there are many.
 Shape fwd_shape(const rms_params_t* p)
 {
-    const int vecn = 16 / (int)elem_size(p->x_dtype);
     const bool shorter = p->D <= 512;
-    Shape s = shape_of(p, p->D % vecn == 0 ? 4 * vecn : 16, shorter ? 32 : 256, kMaxThreads);
-    if (shorter && s.tpr == 32) {
+    Shape s = shape_of(p, 4, shorter ? 32 : 256, kMaxThreads);
+    if (s.tpr == 32) {
         s.ry = 8;
         while (s.ry > 1 && p->rows < (int64_t)s.ry * 2 * kNumSMs) s.ry /= 2;
     }
@@ -587,10 +620,12 @@ Shape fwd_shape(const rms_params_t* p)
 }
 
 // Backward: a row's exchange between threads costs as much as 16 elements' arithmetic, so 16 elements a
-// thread; one CTA of up to 512 threads an SM.
+// thread, for longer rows three packs of 16-bit elements; one CTA of up to 512 threads an SM.
 Shape bwd_shape(const rms_params_t* p)
 {
-    Shape s = shape_of(p, 16, 32, kRingThreads);
+    const int most = p->x_dtype == GDN_F32 ? 4 : 2;
+    Shape s = shape_of(p, most, 32, kRingThreads);
+    if (s.vpt == 0 && most < 3) s = shape_of(p, 3, 32, kRingThreads);
     if (s.vpt > 0) {
         s.ry = kRingThreads / s.tpr;
         while (s.ry > 1 && p->rows < (int64_t)s.ry * kNumSMs) s.ry /= 2;
@@ -598,40 +633,43 @@ Shape bwd_shape(const rms_params_t* p)
     return s;
 }
 
-template <typename T, int VEC, int VPT>
+template <typename T, int VPT>
 int launch_fwd_v(const RmsFwd& A, const Shape& s, cudaStream_t st)
 {
     const unsigned grid = (unsigned)((A.rows + s.ry - 1) / s.ry);
     const dim3 block(s.tpr, s.ry);
-    if (A.y_dtype != RMS_E4M3) return launch_after(rms_forward_kernel<T, VEC, VPT, kPlain>, grid, block, 0, st, A);
-    else if (!A.lg_group) return launch_after(rms_forward_kernel<T, VEC, VPT, kRowCodes>, grid, block, 0, st, A);
-    else if constexpr (VEC > 1) return launch_after(rms_forward_kernel<T, VEC, VPT, kGroupCodes>, grid, block, 0, st, A);
-    return (int)cudaErrorInvalidValue;  // groups of columns go with whole packs
+    const bool cut = A.D % (16 / (int)sizeof(T)) != 0;  // groups of columns divide D into whole packs
+    const auto kernel = A.y_dtype != RMS_E4M3 ? (cut ? rms_forward_kernel<T, VPT, kPlain, true> : rms_forward_kernel<T, VPT, kPlain, false>)
+                        : !A.lg_group         ? (cut ? rms_forward_kernel<T, VPT, kRowCodes, true> : rms_forward_kernel<T, VPT, kRowCodes, false>)
+                                              : rms_forward_kernel<T, VPT, kGroupCodes, false>;
+    return launch_after(kernel, grid, block, 0, st, A);
 }
 
-template <typename T, int VEC>
+template <typename T>
 int launch_fwd(const RmsFwd& A, const Shape& s, cudaStream_t st)
 {
     switch (s.vpt) {
-        case 1: return launch_fwd_v<T, VEC, 1>(A, s, st);
-        case 2: return launch_fwd_v<T, VEC, 2>(A, s, st);
-        case 3: if constexpr (VEC > 1) return launch_fwd_v<T, VEC, 3>(A, s, st); break;
-        case 4: return launch_fwd_v<T, VEC, 4>(A, s, st);
-        case 8: if constexpr (VEC == 1) return launch_fwd_v<T, VEC, 8>(A, s, st); break;
-        case 16: if constexpr (VEC == 1) return launch_fwd_v<T, VEC, 16>(A, s, st); break;
-        default: return launch_fwd_v<T, VEC, 0>(A, s, st);
+        case 1: return launch_fwd_v<T, 1>(A, s, st);
+        case 2: return launch_fwd_v<T, 2>(A, s, st);
+        case 3: return launch_fwd_v<T, 3>(A, s, st);
+        case 4: return launch_fwd_v<T, 4>(A, s, st);
+        default: return launch_fwd_v<T, 0>(A, s, st);
     }
-    return (int)cudaErrorInvalidValue;
 }
 
-template <typename T, int VEC, int VPT>
+template <typename T, int VPT>
 int launch_bwd_v(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
 {
+    constexpr int VEC = 16 / (int)sizeof(T);
     const size_t row = (size_t)3 * VPT * s.tpr * s.ry * 16;  // of a ring: 96 KB at most
-    const bool deep = 4 * row <= 200 * 1024;
-    size_t smem = VEC > 1 && A.vec ? (deep ? 4 : 2) * row : 0;
+    const size_t weights = VPT * VEC > 16 ? (size_t)VPT * VEC * 4 * s.tpr * s.ry : 0;
+    const bool deep = 4 * row + weights <= 200 * 1024, cut = A.D % VEC != 0;
+    size_t smem = weights + (A.vec ? (deep ? 4 : 2) * row : 0);
+    if (smem > 220 * 1024) return (int)cudaErrorInvalidValue;  // not for the shapes of bwd_shape()
     if (A.part && s.ry > 1 && smem < (size_t)s.ry * A.D * 4) smem = (size_t)s.ry * A.D * 4;
-    const auto kernel = deep ? rms_backward_kernel<T, VEC, VPT, 4> : rms_backward_kernel<T, VEC, VPT, 2>;
+    const auto kernel = !A.vec ? rms_backward_kernel<T, VPT, 0, true>
+                        : deep ? (cut ? rms_backward_kernel<T, VPT, 4, true> : rms_backward_kernel<T, VPT, 4, false>)
+                               : (cut ? rms_backward_kernel<T, VPT, 2, true> : rms_backward_kernel<T, VPT, 2, false>);
     if (smem > 40 * 1024) {
         const int e = (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e) return e;
@@ -639,23 +677,18 @@ int launch_bwd_v(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
     return launch_after(kernel, ctas, dim3(s.tpr, s.ry), smem, st, A);
 }
 
-template <typename T, int VEC>
+template <typename T>
 int launch_bwd(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
 {
     switch (s.vpt) {
-        case 1: return launch_bwd_v<T, VEC, 1>(A, s, ctas, st);
-        case 2: return launch_bwd_v<T, VEC, 2>(A, s, ctas, st);
-        case 3: if constexpr (VEC == 4) return launch_bwd_v<T, VEC, 3>(A, s, ctas, st); break;
-        case 4: if constexpr (VEC <= 4) return launch_bwd_v<T, VEC, 4>(A, s, ctas, st); break;
-        case 8: if constexpr (VEC == 1) return launch_bwd_v<T, VEC, 8>(A, s, ctas, st); break;
-        case 16: if constexpr (VEC == 1) return launch_bwd_v<T, VEC, 16>(A, s, ctas, st); break;
-        default: {
-            const int e = launch_after(rms_backward_long_kernel<T>, (unsigned)A.rows, kMaxThreads, 0, st, A);
-            if (e || !A.part) return e;
-            return launch_after(rms_dweight_long_kernel<T>, dim3(ctas, (A.D + 255) / 256), 256, 0, st, A);
-        }
+        case 1: return launch_bwd_v<T, 1>(A, s, ctas, st);
+        case 2: return launch_bwd_v<T, 2>(A, s, ctas, st);
+        case 3: return launch_bwd_v<T, 3>(A, s, ctas, st);
+        case 4: if constexpr (sizeof(T) == 4) return launch_bwd_v<T, 4>(A, s, ctas, st);
     }
-    return (int)cudaErrorInvalidValue;
+    const int e = launch_after(rms_backward_long_kernel<T>, (unsigned)A.rows, kMaxThreads, 0, st, A);
+    if (e || !A.part) return e;
+    return launch_after(rms_dweight_long_kernel<T>, dim3(ctas, (A.D + 255) / 256), 256, 0, st, A);
 }
 
 // CTAs of the backward, each with its own part of dweight.
@@ -698,12 +731,17 @@ int check(const rms_params_t* p)
     return GDN_OK;
 }
 
-bool wide_ok(const rms_params_t* p, std::initializer_list<const void*> ptrs)
+// Packs of 16 bytes are aligned in every tensor that has rows.
+bool packs_ok(const rms_params_t* p, std::initializer_list<const void*> ptrs)
 {
-    const int vecn = 16 / (int)elem_size(p->x_dtype);
+    const int vec = 16 / (int)elem_size(p->x_dtype);
     for (const void* q : ptrs)
         if ((uintptr_t)q % 16 != 0) return false;
-    return p->D % vecn == 0 && p->x_s % vecn == 0 && p->res_s % vecn == 0;
+    return (p->x_s - p->D) % vec == 0 && (p->res_s - p->D) % vec == 0;
+}
+bool weight_ok(const rms_params_t* p, const void* weight)
+{
+    return (uintptr_t)weight % 16 == 0 && p->D % (16 / (int)elem_size(p->x_dtype)) == 0;
 }
 
 }  // namespace
@@ -746,13 +784,14 @@ extern "C" int rms_forward(const rms_params_t* p, const void* x, const void* res
     A.xs = p->x_s; A.rs = p->res_s; A.rows = (int)p->rows; A.D = (int)p->D;
     A.w_dtype = p->w_dtype; A.y_dtype = p->y_dtype; A.lg_group = e4 && p->group ? (p->group == 16 ? 4 : p->group == 32 ? 5 : p->group == 64 ? 6 : 7) : 0;
     A.eps = p->eps; A.inv_D = 1.f / (float)p->D;
-    A.vec = wide_ok(p, {x, residual, weight, h, y});
+    A.vec = packs_ok(p, {x, residual, h, y});
+    A.w_vec = weight_ok(p, weight);
     const Shape s = fwd_shape(p);
     cudaStream_t cs = (cudaStream_t)stream;
     int e;
-    if (p->x_dtype == GDN_F32) e = s.vec > 1 ? launch_fwd<float, 4>(A, s, cs) : launch_fwd<float, 1>(A, s, cs);
-    else if (p->x_dtype == GDN_BF16) e = s.vec > 1 ? launch_fwd<__nv_bfloat16, 8>(A, s, cs) : launch_fwd<__nv_bfloat16, 1>(A, s, cs);
-    else e = s.vec > 1 ? launch_fwd<__half, 8>(A, s, cs) : launch_fwd<__half, 1>(A, s, cs);
+    if (p->x_dtype == GDN_F32) e = launch_fwd<float>(A, s, cs);
+    else if (p->x_dtype == GDN_BF16) e = launch_fwd<__nv_bfloat16>(A, s, cs);
+    else e = launch_fwd<__half>(A, s, cs);
     return e ? cuda_fail(e, "rms_forward launch") : GDN_OK;
 }
 
@@ -790,13 +829,14 @@ extern "C" int rms_backward(const rms_params_t* p, const void* h, const void* we
     A.h = h; A.w = weight; A.dy = dy; A.dh = dh; A.rstd = rstd; A.dx = dx; A.part = dweight ? (float*)workspace : nullptr;
     A.hs = p->x_s; A.dys = p->res_s; A.rows = (int)p->rows; A.D = (int)p->D; A.w_dtype = p->w_dtype;
     A.inv_D = 1.f / (float)p->D;
-    A.vec = wide_ok(p, {h, weight, dy, dh, dx});
+    A.vec = packs_ok(p, {h, dy, dh, dx});
+    A.w_vec = weight_ok(p, weight);
     const Shape s = bwd_shape(p);
     const int ctas = bwd_ctas(p, s);
     int e;
-    if (p->x_dtype == GDN_F32) e = s.vec > 1 ? launch_bwd<float, 4>(A, s, ctas, cs) : launch_bwd<float, 1>(A, s, ctas, cs);
-    else if (p->x_dtype == GDN_BF16) e = s.vec > 1 ? launch_bwd<__nv_bfloat16, 8>(A, s, ctas, cs) : launch_bwd<__nv_bfloat16, 1>(A, s, ctas, cs);
-    else e = s.vec > 1 ? launch_bwd<__half, 8>(A, s, ctas, cs) : launch_bwd<__half, 1>(A, s, ctas, cs);
+    if (p->x_dtype == GDN_F32) e = launch_bwd<float>(A, s, ctas, cs);
+    else if (p->x_dtype == GDN_BF16) e = launch_bwd<__nv_bfloat16>(A, s, ctas, cs);
+    else e = launch_bwd<__half>(A, s, ctas, cs);
     if (!e && dweight) {
         e = launch_after(rms_dweight_sum_kernel, (unsigned)((p->D + 7) / 8), 128, 0, cs, (const float*)A.part, ctas, A.D, dweight);
     }
