@@ -182,16 +182,26 @@ __device__ __forceinline__ uint4 cut_pack(const uint4& x, int from, int to)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The pack at column c of a row of D (zero outside the row), as it is stored.  CUT: packs may be cut by the row's ends;
-// vec: packs are aligned; `more`: what lies around the row in memory may be read, too.
-template <typename T, int VEC, bool CUT>
-__device__ __forceinline__ uint4 ld_cols(const T* row, int c, int D, bool vec, bool more)
+// How a tensor's packs are reached: whole and aligned, aligned but cut by the rows' ends, or element by element.
+enum { kWhole = 0, kCut = 1, kSingle = 2 };
+
+// The pack at column c of a row of D (zero outside the row), as it is stored.  `more`: what lies around the row in memory
+// may be read, too.
+template <typename T, int VEC, int HOW>
+__device__ __forceinline__ uint4 ld_cols(const T* row, int c, int D, bool more)
 {
     uint4 r = make_uint4(0, 0, 0, 0);
-    if (vec && (!CUT || more || (c >= 0 && c + VEC <= D))) {
+    if (HOW == kWhole) {
         if (c < D) r = *reinterpret_cast<const uint4*>(row + c);
-        if (CUT && (c < 0 || c + VEC > D)) r = cut_pack<T>(r, -c, D - c);
-    } else if (c < D) {
+        return r;
+    }
+    const bool whole = c >= 0 && c + VEC <= D;
+    if (HOW == kCut) {
+        if (c < D && (whole || more)) r = *reinterpret_cast<const uint4*>(row + c);
+        if (whole || c >= D) return r;
+        if (more) return cut_pack<T>(r, -c, D - c);
+    }
+    if (c < D) {
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
@@ -222,11 +232,11 @@ __device__ __forceinline__ Nums<VEC> widen(const uint4& x)
     return r;
 }
 
-template <typename T, int VEC, bool CUT>
-__device__ __forceinline__ void st_cols(T* row, int c, int D, bool vec, const Nums<VEC>& v)
+template <typename T, int VEC, int HOW>
+__device__ __forceinline__ void st_cols(T* row, int c, int D, const Nums<VEC>& v)
 {
-    if (vec && (!CUT || (c >= 0 && c + VEC <= D))) {
-        if (!CUT && c >= D) return;
+    if (HOW == kWhole || (HOW == kCut && c >= 0 && c + VEC <= D)) {
+        if (HOW == kWhole && c >= D) return;
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < VEC; i += 4) {
@@ -248,20 +258,20 @@ __device__ __forceinline__ void st_cols(T* row, int c, int D, bool vec, const Nu
     }
 }
 
-template <int VEC, bool CUT>
+template <int VEC, int HOW>
 __device__ __forceinline__ Nums<VEC> ld_weight(const void* p, int dtype, int c, int D, bool vec)
 {
     Nums<VEC> w;
     if (!p) {
         w.fill(1.f);
-    } else if (!CUT && vec && dtype == GDN_F32) {
+    } else if (HOW == kWhole && vec && dtype == GDN_F32) {
 #pragma unroll
         for (int b = 0; b < VEC; b += 4) {
             const float4 v = c < D ? __ldg(reinterpret_cast<const float4*>((const float*)p + c + b)) : make_float4(0.f, 0.f, 0.f, 0.f);
             w.set(b, v.x, v.y);
             w.set(b + 2, v.z, v.w);
         }
-    } else if (CUT && dtype == GDN_F32 && c >= 0 && c + VEC <= D) {
+    } else if (HOW != kWhole && dtype == GDN_F32 && c >= 0 && c + VEC <= D) {
         const float* q = (const float*)p + c;
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) w.set(i, __ldg(q + i), __ldg(q + i + 1));
@@ -273,8 +283,8 @@ __device__ __forceinline__ Nums<VEC> ld_weight(const void* p, int dtype, int c, 
     return w;
 }
 
-template <int VEC, bool CUT>
-__device__ __forceinline__ void st_e4m3(uint8_t* row, int c, int D, bool vec, const Nums<VEC>& v)
+template <int VEC, int HOW>
+__device__ __forceinline__ void st_e4m3(uint8_t* row, int c, int D, const Nums<VEC>& v)
 {
     uint32_t w[VEC / 4];
 #pragma unroll
@@ -283,8 +293,8 @@ __device__ __forceinline__ void st_e4m3(uint8_t* row, int c, int D, bool vec, co
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(v.pair(i + 2), __NV_SATFINITE, __NV_E4M3);
         w[i / 4] = lo | hi << 16;
     }
-    if (vec && (!CUT || (c >= 0 && c + VEC <= D))) {
-        if (!CUT && c >= D) return;
+    if (HOW == kWhole || (HOW == kCut && c >= 0 && c + VEC <= D)) {
+        if (HOW == kWhole && c >= D) return;
         if constexpr (VEC == 8) *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
         else *reinterpret_cast<uint32_t*>(row + c) = w[0];
     } else if (c < D) {
@@ -298,13 +308,12 @@ __device__ __forceinline__ void st_e4m3(uint8_t* row, int c, int D, bool vec, co
 enum { kPlain = 0, kRowCodes = 1, kGroupCodes = 2 };
 
 // What follows the sums, for one pack: h and y (or its codes and scale) to memory.
-template <typename T, int VEC, int OUT, bool CUT>
+template <typename T, int VEC, int OUT, int HOW>
 __device__ __forceinline__ void finish_pack(const RmsFwd& A, const Nums<VEC>& h, long long row, int c, float rstd, float inv)
 {
-    const bool vec = A.vec;
     const long long at = row * A.D;
-    if (A.h) st_cols<T, VEC, CUT>((T*)A.h + at, c, A.D, vec, h);
-    const Nums<VEC> y = mul(mul(h, ld_weight<VEC, CUT>(A.w, A.w_dtype, c, A.D, A.w_vec)), rstd);
+    if (A.h) st_cols<T, VEC, HOW>((T*)A.h + at, c, A.D, h);
+    const Nums<VEC> y = mul(mul(h, ld_weight<VEC, HOW>(A.w, A.w_dtype, c, A.D, A.w_vec)), rstd);
     if (OUT == kGroupCodes) {
         float m = y.max_abs();
         // the lanes of a group (a power of two; every lane of the warp is here)
@@ -319,21 +328,21 @@ __device__ __forceinline__ void finish_pack(const RmsFwd& A, const Nums<VEC>& h,
         if (c < A.D && (c & ((1 << A.lg_group) - 1)) == 0) A.scales[row * (A.D >> A.lg_group) + (c >> A.lg_group)] = scale;
     }
     if (OUT != kPlain) {
-        st_e4m3<VEC, CUT>((uint8_t*)A.y + at, c, A.D, vec, mul(y, inv));
+        st_e4m3<VEC, HOW>((uint8_t*)A.y + at, c, A.D, mul(y, inv));
     } else if (A.y_dtype == GDN_BF16) {
-        st_cols<__nv_bfloat16, VEC, CUT>((__nv_bfloat16*)A.y + at, c, A.D, vec, y);
+        st_cols<__nv_bfloat16, VEC, HOW>((__nv_bfloat16*)A.y + at, c, A.D, y);
     } else if (A.y_dtype == GDN_F32) {
-        st_cols<float, VEC, CUT>((float*)A.y + at, c, A.D, vec, y);
+        st_cols<float, VEC, HOW>((float*)A.y + at, c, A.D, y);
     } else {
-        st_cols<__half, VEC, CUT>((__half*)A.y + at, c, A.D, vec, y);
+        st_cols<__half, VEC, HOW>((__half*)A.y + at, c, A.D, y);
     }
 }
 
 // VPT packs a thread; VPT = 0: rows that registers do not hold, read again (from L2) after the sums.
 // Rows of fewer than the most packs have 256 threads at most, five CTAs an SM: 4096 rows of 6144
 // to codes take 28 us so, 30 us with the four that the compiler's own choice of registers leaves.
-template <typename T, int VPT, int OUT, bool CUT>
-__global__ void __launch_bounds__(VPT > 0 && VPT < 4 ? 256 : kMaxThreads, VPT > 0 && VPT < 4 ? 5 : 1) rms_forward_kernel(const RmsFwd A)
+template <typename T, int VPT, int OUT, int HOW>
+__global__ void __launch_bounds__(VPT > 0 && VPT < 4 ? 256 : kMaxThreads, VPT > 0 && VPT < 4 ? (HOW == kWhole ? 5 : 4) : 1) rms_forward_kernel(const RmsFwd A)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
     __shared__ float2 buf[32];
@@ -341,30 +350,30 @@ __global__ void __launch_bounds__(VPT > 0 && VPT < 4 ? 256 : kMaxThreads, VPT > 
     const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     begin_after();
     if (row >= A.rows) return;  // the whole row's threads leave together
-    const int c0 = tid * VEC - (CUT ? lead_of<VEC>(row, A.D) : 0);
+    const int c0 = tid * VEC - (HOW != kWhole ? lead_of<VEC>(row, A.D) : 0);
     const T* x = (const T*)A.x + row * A.xs;
     const T* r = A.res ? (const T*)A.res + row * A.rs : x;
     // a sum that replaces an input row may only be read by its own row's threads
-    const bool vec = A.vec, more = CUT && row + 1 < A.rows && A.h != A.x && A.h != A.res;
+    const bool more = HOW == kCut && row + 1 < A.rows && A.h != A.x && A.h != A.res;
     Nums<VEC> h[VPT ? VPT : 1], acc;
     acc.fill(0.f);
     float m = 0.f;
     auto sum_at = [&](int c) {
-        const uint4 a = ld_cols<T, VEC, CUT>(x, c, A.D, vec, more);
+        const uint4 a = ld_cols<T, VEC, HOW>(x, c, A.D, more);
         if (!A.res) return widen<T, VEC>(a);
-        return add(widen<T, VEC>(a), widen<T, VEC>(ld_cols<T, VEC, CUT>(r, c, A.D, vec, more)));
+        return add(widen<T, VEC>(a), widen<T, VEC>(ld_cols<T, VEC, HOW>(r, c, A.D, more)));
     };
     auto take = [&](const Nums<VEC>& hv, int c) {
         acc = fma(hv, hv, acc);
-        if (OUT == kRowCodes) m = fmaxf(m, mul(hv, ld_weight<VEC, CUT>(A.w, A.w_dtype, c, A.D, A.w_vec)).max_abs());
+        if (OUT == kRowCodes) m = fmaxf(m, mul(hv, ld_weight<VEC, HOW>(A.w, A.w_dtype, c, A.D, A.w_vec)).max_abs());
     };
     if (VPT) {
         uint4 px[VPT ? VPT : 1], pr[VPT ? VPT : 1];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) px[v] = ld_cols<T, VEC, CUT>(x, c0 + v * step, A.D, vec, more);
+        for (int v = 0; v < VPT; ++v) px[v] = ld_cols<T, VEC, HOW>(x, c0 + v * step, A.D, more);
         if (A.res) {
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) pr[v] = ld_cols<T, VEC, CUT>(r, c0 + v * step, A.D, vec, more);
+            for (int v = 0; v < VPT; ++v) pr[v] = ld_cols<T, VEC, HOW>(r, c0 + v * step, A.D, more);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) h[v] = add(widen<T, VEC>(px[v]), widen<T, VEC>(pr[v]));
         } else {
@@ -385,10 +394,10 @@ __global__ void __launch_bounds__(VPT > 0 && VPT < 4 ? 256 : kMaxThreads, VPT > 
     }
     if (VPT) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) finish_pack<T, VEC, OUT, CUT>(A, h[v], row, c0 + v * step, rstd, inv);
+        for (int v = 0; v < VPT; ++v) finish_pack<T, VEC, OUT, HOW>(A, h[v], row, c0 + v * step, rstd, inv);
     } else {
         // whole steps, so that the lanes that share a scale stay together
-        for (int c = c0; c - c0 < A.D + VEC; c += step) finish_pack<T, VEC, OUT, CUT>(A, sum_at(c), row, c, rstd, inv);
+        for (int c = c0; c - c0 < A.D + VEC; c += step) finish_pack<T, VEC, OUT, HOW>(A, sum_at(c), row, c, rstd, inv);
     }
 }
 
@@ -404,18 +413,19 @@ __device__ __forceinline__ void copy_async(uint4* to, const void* from, uint32_t
 // RING = 0, for tensors off their 16 bytes: every pack is read directly.
 // LEAN, for the longest rows: no more than dweight's part stays in registers; the weights are in shared memory,
 // and the ring is read twice.
-template <typename T, int VPT, int RING, bool CUT>
+template <typename T, int VPT, int RING, int HOW>
 __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
 {
     constexpr int VEC = 16 / (int)sizeof(T), HELD = VPT * VEC > 16 ? 1 : VPT;
     constexpr bool LEAN = VPT * VEC > 16;
+    constexpr int kPart = HOW == kWhole ? kWhole : kSingle;  // a part's rows begin anywhere
     extern __shared__ uint4 ring[];  // [RING][3 VPT][threads], LEAN: weights [VPT][VEC / 4][threads]; at the end, as floats, [blockDim.y][D]
     __shared__ float2 buf[2][kRingThreads / 32];
     const int tid = threadIdx.x, step = blockDim.x * VEC;
     const int threads = blockDim.x * blockDim.y, own = threadIdx.y * blockDim.x + tid;
     begin_after();
     const long long all = (long long)gridDim.x * blockDim.y, row0 = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-    const int c0 = tid * VEC - (CUT ? lead_of<VEC>(row0, A.D) : 0);
+    const int c0 = tid * VEC - (HOW != kWhole ? lead_of<VEC>(row0, A.D) : 0);
     const T *h = (const T*)A.h, *dy = (const T*)A.dy, *dh = (const T*)A.dh;
     auto fetch = [&](long long row, int slot) {
         if (row < A.rows) {
@@ -423,7 +433,7 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const int c = c0 + v * step, at = c < A.D ? c : 0;
-                const uint32_t bytes = c >= A.D ? 0 : !CUT || c + VEC <= A.D ? 16 : (uint32_t)(A.D - c) * sizeof(T);
+                const uint32_t bytes = c >= A.D ? 0 : HOW == kWhole || c + VEC <= A.D ? 16 : (uint32_t)(A.D - c) * sizeof(T);
                 copy_async(to + (3 * v) * threads, h + row * A.hs + at, bytes);
                 copy_async(to + (3 * v + 1) * threads, dy + row * A.dys + at, bytes);
                 if (dh) copy_async(to + (3 * v + 2) * threads, dh + row * A.D + at, bytes);
@@ -450,7 +460,7 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
     Nums<VEC> w[HELD], dw[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        const Nums<VEC> wv = ld_weight<VEC, CUT>(A.w, A.w_dtype, c0 + v * step, A.D, A.w_vec);
+        const Nums<VEC> wv = ld_weight<VEC, HOW>(A.w, A.w_dtype, c0 + v * step, A.D, A.w_vec);
         if (LEAN) {
 #pragma unroll
             for (int i = 0; i < VEC; i += 4) {
@@ -477,10 +487,10 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
             const int c = c0 + v * step;
             if constexpr (!vec) {
                 const T* src = which == 0 ? h + row * A.hs : which == 1 ? dy + row * A.dys : dh + row * A.D;
-                return ld_cols<T, VEC, CUT>(src, c, A.D, false, false);
+                return ld_cols<T, VEC, HOW>(src, c, A.D, false);
             }
             uint4 x = from[(3 * v + which) * threads];
-            if (CUT && c < 0) x = cut_pack<T>(x, -c, VEC);
+            if (HOW != kWhole && c < 0) x = cut_pack<T>(x, -c, VEC);
             return x;
         };
         Nums<VEC> n[HELD], t[HELD], acc;
@@ -508,7 +518,7 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
             Nums<VEC> o;
             if (dh) o = fma(t[k], rstd, widen<T, VEC>(pg[k]));
             else o = mul(t[k], rstd);
-            st_cols<T, VEC, CUT>((T*)A.dx + row * A.D, c0 + v * step, A.D, vec, fma(n[k], c, o));
+            st_cols<T, VEC, HOW>((T*)A.dx + row * A.D, c0 + v * step, A.D, fma(n[k], c, o));
         }
     }
     if (!A.part) return;
@@ -518,7 +528,7 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();  // the ring is read
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) st_cols<float, VEC, CUT>(sums + (size_t)threadIdx.y * A.D, c0 + v * step, A.D, !CUT, dw[v]);
+        for (int v = 0; v < VPT; ++v) st_cols<float, VEC, kPart>(sums + (size_t)threadIdx.y * A.D, c0 + v * step, A.D, dw[v]);
         __syncthreads();
         for (int c = own; c < A.D; c += threads) {
             float t = 0.f;
@@ -527,7 +537,7 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
         }
     } else {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) st_cols<float, VEC, CUT>(out, c0 + v * step, A.D, !CUT, dw[v]);
+        for (int v = 0; v < VPT; ++v) st_cols<float, VEC, kPart>(out, c0 + v * step, A.D, dw[v]);
     }
 }
 
@@ -638,10 +648,14 @@ int launch_fwd_v(const RmsFwd& A, const Shape& s, cudaStream_t st)
 {
     const unsigned grid = (unsigned)((A.rows + s.ry - 1) / s.ry);
     const dim3 block(s.tpr, s.ry);
-    const bool cut = A.D % (16 / (int)sizeof(T)) != 0;  // groups of columns divide D into whole packs
-    const auto kernel = A.y_dtype != RMS_E4M3 ? (cut ? rms_forward_kernel<T, VPT, kPlain, true> : rms_forward_kernel<T, VPT, kPlain, false>)
-                        : !A.lg_group         ? (cut ? rms_forward_kernel<T, VPT, kRowCodes, true> : rms_forward_kernel<T, VPT, kRowCodes, false>)
-                                              : rms_forward_kernel<T, VPT, kGroupCodes, false>;
+    const int how = !A.vec ? kSingle : A.D % (16 / (int)sizeof(T)) != 0 ? kCut : kWhole;
+    void (*kernel)(RmsFwd);
+    if (A.y_dtype != RMS_E4M3)
+        kernel = how == kWhole ? rms_forward_kernel<T, VPT, kPlain, kWhole> : how == kCut ? rms_forward_kernel<T, VPT, kPlain, kCut> : rms_forward_kernel<T, VPT, kPlain, kSingle>;
+    else if (!A.lg_group)
+        kernel = how == kWhole ? rms_forward_kernel<T, VPT, kRowCodes, kWhole> : how == kCut ? rms_forward_kernel<T, VPT, kRowCodes, kCut> : rms_forward_kernel<T, VPT, kRowCodes, kSingle>;
+    else  // groups of columns divide D into whole packs
+        kernel = how == kWhole ? rms_forward_kernel<T, VPT, kGroupCodes, kWhole> : rms_forward_kernel<T, VPT, kGroupCodes, kSingle>;
     return launch_after(kernel, grid, block, 0, st, A);
 }
 
@@ -667,9 +681,9 @@ int launch_bwd_v(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
     size_t smem = weights + (A.vec ? (deep ? 4 : 2) * row : 0);
     if (smem > 220 * 1024) return (int)cudaErrorInvalidValue;  // not for the shapes of bwd_shape()
     if (A.part && s.ry > 1 && smem < (size_t)s.ry * A.D * 4) smem = (size_t)s.ry * A.D * 4;
-    const auto kernel = !A.vec ? rms_backward_kernel<T, VPT, 0, true>
-                        : deep ? (cut ? rms_backward_kernel<T, VPT, 4, true> : rms_backward_kernel<T, VPT, 4, false>)
-                               : (cut ? rms_backward_kernel<T, VPT, 2, true> : rms_backward_kernel<T, VPT, 2, false>);
+    const auto kernel = !A.vec ? rms_backward_kernel<T, VPT, 0, kSingle>
+                        : deep ? (cut ? rms_backward_kernel<T, VPT, 4, kCut> : rms_backward_kernel<T, VPT, 4, kWhole>)
+                               : (cut ? rms_backward_kernel<T, VPT, 2, kCut> : rms_backward_kernel<T, VPT, 2, kWhole>);
     if (smem > 40 * 1024) {
         const int e = (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e) return e;
