@@ -271,10 +271,23 @@ __device__ __forceinline__ Nums<VEC> ld_weight(const void* p, int dtype, int c, 
             w.set(b, v.x, v.y);
             w.set(b + 2, v.z, v.w);
         }
-    } else if (HOW != kWhole && dtype == GDN_F32 && c >= 0 && c + VEC <= D) {
-        const float* q = (const float*)p + c;
+    } else if (HOW == kCut && vec && dtype == GDN_F32 && c >= 0 && (c & ~3) + VEC + 4 <= D) {
+        // c is not a multiple of 4: the 16-byte loads around it, moved on by c mod 4 (the same for the whole row)
+        const float* q = (const float*)p + (c & ~3);
+        float x[VEC + 4];
 #pragma unroll
-        for (int i = 0; i < VEC; i += 2) w.set(i, __ldg(q + i), __ldg(q + i + 1));
+        for (int b = 0; b < VEC + 4; b += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(q + b));
+            x[b] = v.x;
+            x[b + 1] = v.y;
+            x[b + 2] = v.z;
+            x[b + 3] = v.w;
+        }
+        const bool one = c & 1, two = c & 2;
+#pragma unroll
+        for (int i = 0; i < VEC + 2; ++i) x[i] = one ? x[i + 1] : x[i];
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) w.set(i, two ? x[i + 2] : x[i], two ? x[i + 3] : x[i + 1]);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; i += 2)
@@ -753,11 +766,6 @@ bool packs_ok(const rms_params_t* p, std::initializer_list<const void*> ptrs)
         if ((uintptr_t)q % 16 != 0) return false;
     return (p->x_s - p->D) % vec == 0 && (p->res_s - p->D) % vec == 0;
 }
-bool weight_ok(const rms_params_t* p, const void* weight)
-{
-    return (uintptr_t)weight % 16 == 0 && p->D % (16 / (int)elem_size(p->x_dtype)) == 0;
-}
-
 }  // namespace
 }  // namespace gdn
 
@@ -799,7 +807,7 @@ extern "C" int rms_forward(const rms_params_t* p, const void* x, const void* res
     A.w_dtype = p->w_dtype; A.y_dtype = p->y_dtype; A.lg_group = e4 && p->group ? (p->group == 16 ? 4 : p->group == 32 ? 5 : p->group == 64 ? 6 : 7) : 0;
     A.eps = p->eps; A.inv_D = 1.f / (float)p->D;
     A.vec = packs_ok(p, {x, residual, h, y});
-    A.w_vec = weight_ok(p, weight);
+    A.w_vec = (uintptr_t)weight % 16 == 0;
     const Shape s = fwd_shape(p);
     cudaStream_t cs = (cudaStream_t)stream;
     int e;
@@ -844,7 +852,7 @@ extern "C" int rms_backward(const rms_params_t* p, const void* h, const void* we
     A.hs = p->x_s; A.dys = p->res_s; A.rows = (int)p->rows; A.D = (int)p->D; A.w_dtype = p->w_dtype;
     A.inv_D = 1.f / (float)p->D;
     A.vec = packs_ok(p, {h, dy, dh, dx});
-    A.w_vec = weight_ok(p, weight);
+    A.w_vec = (uintptr_t)weight % 16 == 0;
     const Shape s = bwd_shape(p);
     const int ctas = bwd_ctas(p, s);
     int e;
