@@ -15,9 +15,11 @@
 // does not hold all that reach the bound (very many equal scores), n rounds of a CTA-wide
 // maximum over the chunks that reach it select instead.
 //
-// The stream is bound by the exponentials' instructions (nine a logit with the maximum) and, for few
-// rows, by latency: 16 x 8 rows of 128257 bf16 logits 10 us of 16.6, 128 x 8 rows of 151937 64 us in all, 4.9 TB/s.
-// Selecting inside every segment instead (a list and its ranks a CTA) took 17 us for the stream.
+// The stream is bound by the exponentials' instructions (eight a logit with the maximum) and, for few
+// rows, by latency: 16 x 8 rows of 128257 bf16 logits 13.1 us in a graph, join and all, 128 x 8 rows of 151937 64 us,
+// 4.9 TB/s.  Selecting inside every segment instead (a list and its ranks a CTA) took 17 us for the stream.
+// The join is a chain of loads and barriers: what it runs is kept short and free of branches (the 16 x 8 rows
+// took 15.7 us in a graph before that and the wider stream loads).
 #include <climits>
 #include <cstdio>
 #include <type_traits>
