@@ -48,7 +48,7 @@ struct DecodeArgs {
 // Four consecutive gates as fp32.
 __device__ __forceinline__ float4 ld_gate4(const void* p, long long i, int dtype, bool vec)
 {
-    if (vec && dtype == GDN_F32) return __ldg(reinterpret_cast<const float4*>((const float*)p + i));
+    if (vec && dtype == GDN_F32) return ld_plain(reinterpret_cast<const float4*>((const float*)p + i));
     return make_float4(ld_any(p, i, dtype), ld_any(p, i + 1, dtype), ld_any(p, i + 2, dtype), ld_any(p, i + 3, dtype));
 }
 
@@ -80,7 +80,7 @@ __device__ __forceinline__ void load_token(Token<T, NV, RT, KDA>& x, const Decod
     if (!KDA) x.g[0].x = ld_any(A.g, gh, A.gate_dtype);
 #pragma unroll
     for (int s = 0; s < x.ROWS; ++s)
-        if (32 * s + lane < rows) x.v[s] = __ldg(v + row * A.vs0 + 32 * s + lane);
+        if (32 * s + lane < rows) x.v[s] = ld_plain(v + row * A.vs0 + 32 * s + lane);
 #pragma unroll
     for (int s = 0; s < x.SHARE; ++s) {
         const int c = 128 * s + 4 * lane;
@@ -138,11 +138,11 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
     const int n = nh / A.H_v, h = nh - n * A.H_v;
 
     begin_after();
-    const int s_in = __ldg(A.slot_in + n), s_out = __ldg(A.slot_out + n);
+    const int s_in = ld_plain(A.slot_in + n), s_out = ld_plain(A.slot_out + n);
     long long lo, hi;
     if (A.cu) {
-        lo = __ldg(A.cu + n);
-        hi = __ldg(A.cu + n + 1);
+        lo = ld_plain(A.cu + n);
+        hi = ld_plain(A.cu + n + 1);
     } else {
         lo = (long long)n * A.T;
         hi = lo + A.T;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(256) gdn_states_move_kernel(const MoveArgs A)
     if (threadIdx.x < G) {
         long long f = -2, t = 0;
         if ((int)threadIdx.x < nm) {
-            const int s = __ldg(A.src + gr * A.group + threadIdx.x), d = __ldg(A.dst + gr * A.group + threadIdx.x);
+            const int s = ld_plain(A.src + gr * A.group + threadIdx.x), d = ld_plain(A.dst + gr * A.group + threadIdx.x);
             if (bad_move(A, s, d)) {
                 if (pc == 0 && layer == 0) atomicOr(&g_decode_status, 2);
             } else if (d >= 0 && s != d) {
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(256) gdn_states_move_large_kernel(const MoveAr
     begin_after();
     for (int i = threadIdx.x; i < nm * n16; i += blockDim.x) {
         const int m = i / n16, e = i - m * n16;
-        const int s = __ldg(A.src + m0 + m), d = __ldg(A.dst + m0 + m);
+        const int s = ld_plain(A.src + m0 + m), d = ld_plain(A.dst + m0 + m);
         if (bad_move(A, s, d)) {
             if (e == 0) atomicOr(&g_decode_status, 2);
             continue;
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(256) gdn_states_move_large_kernel(const MoveAr
     __syncthreads();
     for (int i = threadIdx.x; i < nm * n16; i += blockDim.x) {
         const int m = i / n16, e = i - m * n16;
-        const int s = __ldg(A.src + m0 + m), d = __ldg(A.dst + m0 + m);
+        const int s = ld_plain(A.src + m0 + m), d = ld_plain(A.dst + m0 + m);
         if (bad_move(A, s, d) || d < 0 || s == d) continue;
         reinterpret_cast<uint4*>(base + d * A.slot_stride)[e] = buf[m * per + e];
     }

@@ -38,12 +38,18 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
+// A plain load.  A load through the path for constant data (`ld.global.nc`) would be a promise that nobody writes
+// there while this kernel runs, which launch_after() does not keep: the kernel starts beside the one that may still be
+// writing it, and the compiler may lift such a load above the wait.
+template <typename V>
+__device__ __forceinline__ V ld_plain(const V* p) { return *p; }
+
 // One element of a tensor whose type is only known at run time (gdn_dtype_t).
 __device__ __forceinline__ float ld_any(const void* p, long long i, int dtype)
 {
-    if (dtype == GDN_F32) return __ldg((const float*)p + i);
-    if (dtype == GDN_BF16) return __bfloat162float(__ldg((const __nv_bfloat16*)p + i));
-    return __half2float(__ldg((const __half*)p + i));
+    if (dtype == GDN_F32) return ld_plain((const float*)p + i);
+    if (dtype == GDN_BF16) return __bfloat162float(ld_plain((const __nv_bfloat16*)p + i));
+    return __half2float(ld_plain((const __half*)p + i));
 }
 __device__ __forceinline__ void st_any(void* p, long long i, int dtype, float x)
 {
@@ -69,12 +75,12 @@ __device__ __forceinline__ Pack<T, VEC> ld_pack(const T* p, bool vec)
     constexpr int B = (int)sizeof(T) * VEC;
     static_assert(B == 4 || B == 8 || B == 16, "one load of 4, 8 or 16 bytes");
     if (vec) {
-        if (B == 16) *reinterpret_cast<uint4*>(&r) = __ldg(reinterpret_cast<const uint4*>(p));
-        else if (B == 8) *reinterpret_cast<uint2*>(&r) = __ldg(reinterpret_cast<const uint2*>(p));
-        else *reinterpret_cast<uint32_t*>(&r) = __ldg(reinterpret_cast<const uint32_t*>(p));
+        if (B == 16) *reinterpret_cast<uint4*>(&r) = ld_plain(reinterpret_cast<const uint4*>(p));
+        else if (B == 8) *reinterpret_cast<uint2*>(&r) = ld_plain(reinterpret_cast<const uint2*>(p));
+        else *reinterpret_cast<uint32_t*>(&r) = ld_plain(reinterpret_cast<const uint32_t*>(p));
     } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) r.x[i] = __ldg(p + i);
+        for (int i = 0; i < VEC; ++i) r.x[i] = ld_plain(p + i);
     }
     return r;
 }

@@ -268,7 +268,7 @@ __device__ __forceinline__ Nums<VEC> ld_weight(const void* p, int dtype, int c, 
     } else if (HOW == kWhole && vec && dtype == GDN_F32) {
 #pragma unroll
         for (int b = 0; b < VEC; b += 4) {
-            const float4 v = c < D ? __ldg(reinterpret_cast<const float4*>((const float*)p + c + b)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = c < D ? ld_plain(reinterpret_cast<const float4*>((const float*)p + c + b)) : make_float4(0.f, 0.f, 0.f, 0.f);
             w.set(b, v.x, v.y);
             w.set(b + 2, v.z, v.w);
         }
@@ -278,7 +278,7 @@ __device__ __forceinline__ Nums<VEC> ld_weight(const void* p, int dtype, int c, 
         float x[VEC + 4];
 #pragma unroll
         for (int b = 0; b < VEC + 4; b += 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(q + b));
+            const float4 v = ld_plain(reinterpret_cast<const float4*>(q + b));
             x[b] = v.x;
             x[b + 1] = v.y;
             x[b + 2] = v.z;
@@ -487,10 +487,10 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
         dw[v].fill(0.f);
     }
     int set = 0, slot = 0;
-    float next_rstd = row0 < A.rows ? __ldg(A.rstd + row0) : 0.f;
+    float next_rstd = row0 < A.rows ? ld_plain(A.rstd + row0) : 0.f;
     for (long long row = row0; row < A.rows; row += all, set ^= 1, slot = vec ? (slot + 1) % (RING ? RING : 1) : 0) {
         const float rstd = next_rstd;
-        if (row + all < A.rows) next_rstd = __ldg(A.rstd + row + all);
+        if (row + all < A.rows) next_rstd = ld_plain(A.rstd + row + all);
         if constexpr (vec) {
             fetch(row + (RING - 1) * all, (slot + RING - 1) % RING);
             asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_backward_long_kernel(const Rm
     begin_after();
     const T *h = (const T*)A.h + row * A.hs, *dy = (const T*)A.dy + row * A.dys;
     const T* dh = A.dh ? (const T*)A.dh + row * A.D : nullptr;
-    const float rstd = __ldg(A.rstd + row);
+    const float rstd = ld_plain(A.rstd + row);
     float s = 0.f;
     for (int c = threadIdx.x; c < A.D; c += blockDim.x)
         s = fmaf(to_f32(dy[c]) * (A.w ? ld_any(A.w, c, A.w_dtype) : 1.f), to_f32(h[c]) * rstd, s);
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(256) rms_dweight_long_kernel(const RmsBwd A)
     if (c >= A.D) return;
     float t = 0.f;
     for (long long row = blockIdx.x; row < A.rows; row += gridDim.x)
-        t = fmaf(to_f32(((const T*)A.dy)[row * A.dys + c]), to_f32(((const T*)A.h)[row * A.hs + c]) * __ldg(A.rstd + row), t);
+        t = fmaf(to_f32(((const T*)A.dy)[row * A.dys + c]), to_f32(((const T*)A.h)[row * A.hs + c]) * ld_plain(A.rstd + row), t);
     A.part[(size_t)blockIdx.x * A.D + c] = t;
 }
 
