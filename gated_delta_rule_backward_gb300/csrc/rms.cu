@@ -662,7 +662,9 @@ int launch_fwd_v(const RmsFwd& A, const Shape& s, cudaStream_t st)
 {
     const unsigned grid = (unsigned)((A.rows + s.ry - 1) / s.ry);
     const dim3 block(s.tpr, s.ry);
-    const int how = !A.vec ? kSingle : A.D % (16 / (int)sizeof(T)) != 0 ? kCut : kWhole;
+    // a cut pack may reach into the next row, but not past it: rows shorter than a pack are read element by element
+    constexpr int VEC = 16 / (int)sizeof(T);
+    const int how = !A.vec || A.D < VEC ? kSingle : A.D % VEC != 0 ? kCut : kWhole;
     void (*kernel)(RmsFwd);
     if (A.y_dtype != RMS_E4M3)
         kernel = how == kWhole ? rms_forward_kernel<T, VPT, kPlain, kWhole> : how == kCut ? rms_forward_kernel<T, VPT, kPlain, kCut> : rms_forward_kernel<T, VPT, kPlain, kSingle>;

@@ -197,3 +197,42 @@ def test_rows_beyond_32_bit_offsets():
     y, rstd = torch.empty(3, D, device="cuda"), torch.empty(3, device="cuda")
     rms.rms_forward(rms.params_for(x, y_dtype=F32), x, None, None, None, y, None, rstd)
     assert torch.equal(y, rms.forward(dense, y_dtype=F32)[0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("D", [1, 2, 3, 5, 7, 9])
+def test_rows_shorter_than_a_pack(D, dtype):
+    """A pack may hold several rows, and what follows the last one is not theirs (here NaN)."""
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    for rows in (1, 2, 3, 9, 40):
+        bufs = [torch.full((rows * D + 64,), float("nan"), device="cuda", dtype=dtype) for _ in range(2)]
+        x, r = (b[: rows * D].view(rows, D) for b in bufs)
+        for t in (x, r):
+            t.copy_(1 + torch.rand(rows, D, generator=gen, device="cuda"))
+        w = 1 + 0.1 * torch.randn(D, generator=gen, device="cuda")
+        y, h, rstd = check_forward(x, r, w)
+        dx, dw = rms.backward(x, rstd, r, w)
+        assert torch.isfinite(dx.float()).all() and torch.isfinite(dw).all()
+        for b in bufs:
+            assert torch.isnan(b[rows * D:]).all()
+
+
+def test_each_call_sees_what_the_one_before_it_wrote():
+    """Launches overlap the end of the kernel before them; none may read ahead of its writes."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    x, w = torch.randn(600, 2048, generator=gen, device="cuda"), torch.ones(2048, device="cuda")
+
+    def chain(pause):
+        h, g, ws = x.clone(), torch.ones_like(x), w.clone()
+        for _ in range(6):
+            y, h, rstd = rms.forward(h, ws, g, y_dtype=F32)
+            pause()
+            g, dw = rms.backward(h, rstd, y, ws)
+            pause()
+            ws.copy_(1 + 0.01 * torch.tanh(dw))
+            pause()
+        return h, g, ws
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(chain(lambda: None), want))
