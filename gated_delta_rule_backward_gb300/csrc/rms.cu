@@ -26,6 +26,7 @@
 #include "gdn_f32x2.cuh"
 #include "gdn_internal.h"
 #include "gdn_launch.cuh"
+#include "gdn_packs.h"
 
 namespace gdn {
 namespace {
@@ -162,13 +163,6 @@ __device__ __forceinline__ uint32_t narrow2(float2 x, __half)
 {
     const __half2 v = __floats2half2_rn(x.x, x.y);
     return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Where row `row` begins in its first pack.
-template <int VEC>
-__device__ __forceinline__ int lead_of(long long row, int D)
-{
-    return (int)(((unsigned)row * (unsigned)D) & (VEC - 1));
 }
 
 // The first `from` and the elements past `to` of a pack set to zero.
@@ -364,7 +358,7 @@ __global__ void __launch_bounds__(VPT > 0 && VPT < 4 ? 256 : kMaxThreads, VPT > 
     const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     begin_after();
     if (row >= A.rows) return;  // the whole row's threads leave together
-    const int c0 = tid * VEC - (HOW != kWhole ? lead_of<VEC>(row, A.D) : 0);
+    const int c0 = tid * VEC - (HOW != kWhole ? pack_lead(row, A.D, VEC) : 0);
     const T* x = (const T*)A.x + row * A.xs;
     const T* r = A.res ? (const T*)A.res + row * A.rs : x;
     // a sum that replaces an input row may only be read by its own row's threads
@@ -439,18 +433,17 @@ __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
     const int threads = blockDim.x * blockDim.y, own = threadIdx.y * blockDim.x + tid;
     begin_after();
     const long long all = (long long)gridDim.x * blockDim.y, row0 = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-    const int c0 = tid * VEC - (HOW != kWhole ? lead_of<VEC>(row0, A.D) : 0);
+    const int lead = HOW != kWhole ? pack_lead(row0, A.D, VEC) : 0, c0 = tid * VEC - lead;
     const T *h = (const T*)A.h, *dy = (const T*)A.dy, *dh = (const T*)A.dh;
     auto fetch = [&](long long row, int slot) {
         if (row < A.rows) {
             uint4* to = ring + (size_t)slot * 3 * VPT * threads + own;
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                const int c = c0 + v * step, at = c < A.D ? c : 0;
-                const uint32_t bytes = c >= A.D ? 0 : HOW == kWhole || c + VEC <= A.D ? 16 : (uint32_t)(A.D - c) * sizeof(T);
-                copy_async(to + (3 * v) * threads, h + row * A.hs + at, bytes);
-                copy_async(to + (3 * v + 1) * threads, dy + row * A.dys + at, bytes);
-                if (dh) copy_async(to + (3 * v + 2) * threads, dh + row * A.D + at, bytes);
+                const PackCopy p = ring_copy(c0 + v * step, lead, A.D, VEC, (int)sizeof(T));
+                copy_async(to + (3 * v) * threads, h + row * A.hs + p.at, p.bytes);
+                copy_async(to + (3 * v + 1) * threads, dy + row * A.dys + p.at, p.bytes);
+                if (dh) copy_async(to + (3 * v + 2) * threads, dh + row * A.D + p.at, p.bytes);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
