@@ -237,8 +237,9 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row0 = (long long)blockIdx.x * A.K;
     const int per = A.splits * (kThreads >> A.lg);  // chunks of a row
-    // The segments' CTAs have all begun, and so have waited for what the stream did before them: the
-    // scores can be read; their own sums and maxima only after the wait below.
+    // The wait comes before the scores too, although the segments' kernel has waited for whoever wrote those: it made
+    // them visible to itself alone.
+    begin_after();
     if (tid < A.K) {
         const float score = A.scores[row0 + tid];
         row_score[tid] = score;
@@ -262,7 +263,6 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs 
     }
     __syncthreads();
     const int all_chunks = n_on * per;
-    begin_after();
     // A thread's chunks are tid + j kJoinThreads of the going beams' chunks; the first kHeld stay in registers.
     float held[kHeld];
     int held_row[kHeld];
