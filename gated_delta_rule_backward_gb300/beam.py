@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import gdn
-from .decode import DTYPE_CODES, _stream
+from .decode import DTYPE_CODES, _allocating_on, _hand_over, _stream
 
 _lib = gdn._lib
 
@@ -80,7 +80,9 @@ def select(logits, scores, done=None, slots=None, n_out=None, pad_token=0, strea
             raise ValueError("done (uint8 or bool) and slots (int32) must be contiguous [N, K]")
     N, dev = scores.shape[0], logits.device
     i32 = lambda: torch.empty((N, p.n_out), dtype=torch.int32, device=dev)
-    out = [torch.empty((N, p.n_out), dtype=torch.float32, device=dev), i32(), i32()]
-    src = i32() if slots is not None else None
-    beam_select(p, logits, scores, done, slots, *out, src, workspace(p, dev), stream)
+    with _allocating_on(stream):
+        out = [torch.empty((N, p.n_out), dtype=torch.float32, device=dev), i32(), i32()]
+        src = i32() if slots is not None else None
+        beam_select(p, logits, scores, done, slots, *out, src, workspace(p, dev), stream)
+    _hand_over(stream, *out, src)
     return tuple(out) if src is None else (*out, src)

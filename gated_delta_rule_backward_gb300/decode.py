@@ -8,6 +8,7 @@ its shapes and strides stay.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -117,6 +118,22 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _allocating_on(stream):
+    """What an allocating call makes comes from the pool of the stream that uses it: memory of the current stream's may
+    still be in use there, and a workspace that goes back to it could be handed out while `stream` works in it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *tensors):
+    """Outputs made on `stream` are also the current stream's: freed ones are not used again before its work on them
+    is done.  (That the current stream waits for `stream` first is the caller's part.)"""
+    if stream is not None:
+        here = torch.cuda.current_stream()
+        for t in tensors:
+            if t is not None:
+                t.record_stream(here)
+
+
 def _index(t, what):
     if t.dtype != torch.int32 or not t.is_contiguous():
         raise TypeError(f"{what} must be contiguous int32")
@@ -137,8 +154,10 @@ def gdn_decode(p: DecodeParams, q, k, v, g, beta, cu_tokens, pool, slot_in, slot
 def decode(q, k, v, g, beta, pool, slot_in, slot_out=None, cu_tokens=None, scale=None, y_dtype=None, stream=None):
     """Allocate y and run gdn_decode (slot_out None: in place).  Returns y [n_tok,H_v,S_v]."""
     p = params_for(q, k, v, g, beta, pool, slot_in.numel(), y_dtype=y_dtype, scale=scale)
-    y = torch.empty(v.shape, dtype=torch.float32 if y_dtype is None else y_dtype, device=v.device)
-    gdn_decode(p, q, k, v, g, beta, cu_tokens, pool, slot_in, slot_in if slot_out is None else slot_out, y, stream)
+    with _allocating_on(stream):
+        y = torch.empty(v.shape, dtype=torch.float32 if y_dtype is None else y_dtype, device=v.device)
+        gdn_decode(p, q, k, v, g, beta, cu_tokens, pool, slot_in, slot_in if slot_out is None else slot_out, y, stream)
+    _hand_over(stream, y)
     return y
 
 

@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import gdn
-from .decode import DTYPE_CODES, _stream
+from .decode import DTYPE_CODES, _allocating_on, _hand_over, _stream
 
 _lib = gdn._lib
 
@@ -106,20 +106,25 @@ def forward(x, weight=None, residual=None, eps=1e-6, y_dtype=None, group=0, stre
     where y holds e4m3 codes.  Without a residual h is x itself."""
     p = params_for(x, weight, eps, y_dtype, group, residual)
     rows, D, dev = x.shape[0], x.shape[1], x.device
-    h = x if residual is None else torch.empty((rows, D), dtype=x.dtype, device=dev)
-    y = torch.empty((rows, D), dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    scales = torch.empty((rows, D // group) if group else (rows,), dtype=torch.float32, device=dev) if p.y_dtype == E4M3 else None
-    rms_forward(p, x, residual, weight, None if residual is None else h, y, scales, rstd, stream)
+    with _allocating_on(stream):
+        h = None if residual is None else torch.empty((rows, D), dtype=x.dtype, device=dev)
+        y = torch.empty((rows, D), dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        scales = torch.empty((rows, D // group) if group else (rows,), dtype=torch.float32, device=dev) if p.y_dtype == E4M3 else None
+        rms_forward(p, x, residual, weight, h, y, scales, rstd, stream)
+    _hand_over(stream, h, y, rstd, scales)
+    h = x if residual is None else h
     return (y, h, rstd) if scales is None else (y, scales, h, rstd)
 
 
 def backward(h, rstd, dy, weight=None, dh=None, stream=None):
     """Allocate and run rms_backward.  Returns (dx, dweight); dweight is None without a weight."""
     p = params_for(h, weight, residual=dy)
-    dx = torch.empty(tuple(h.shape), dtype=h.dtype, device=h.device)
-    dw = ws = None
-    if weight is not None:
-        dw, ws = torch.empty(h.shape[1], dtype=torch.float32, device=h.device), workspace(p, h.device)
-    rms_backward(p, h, weight, rstd, dy, dh, dx, dw, ws, stream)
+    with _allocating_on(stream):
+        dx = torch.empty(tuple(h.shape), dtype=h.dtype, device=h.device)
+        dw = ws = None
+        if weight is not None:
+            dw, ws = torch.empty(h.shape[1], dtype=torch.float32, device=h.device), workspace(p, h.device)
+        rms_backward(p, h, weight, rstd, dy, dh, dx, dw, ws, stream)
+    _hand_over(stream, dx, dw)
     return dx, dw
