@@ -29,6 +29,7 @@
 #include "gdn_f32x2.cuh"
 #include "gdn_internal.h"
 #include "gdn_launch.cuh"
+#include "gdn_packs.h"
 
 namespace gdn {
 namespace {
@@ -101,14 +102,22 @@ __device__ __forceinline__ float pack_max(const Pack<__half, 8>& v)
 // A row's packs lie on 16-byte boundaries: it starts `lead` elements into the first.  Pack p of thread t of segment
 // `split` begins at element split seg - lead + (256 p + t) VEC; what is outside the row or the segment reads as -inf.
 template <typename T>
-__device__ __forceinline__ int lead_of(const T* row)
+struct Segment {
+    const T* at;  // on 16 bytes
+    unsigned column;  // of its first element, in unsigned arithmetic (the first segment may begin before the row)
+    int lo, end;
+};
+template <typename T>
+__device__ __forceinline__ Segment<T> segment_of(const BeamArgs& A, const T* row, int split)
 {
-    return (int)(((uintptr_t)row & 15) / sizeof(T));
+    const unsigned lead = (unsigned)(((uintptr_t)row & 15) / sizeof(T));
+    const PackSegment s = pack_segment((unsigned)split, A.seg, lead, A.V);
+    return {row - lead + s.first, s.first - lead, s.lo, s.end};
 }
-// N packs whose first elements are at first + in(p): the whole ones all in flight at once, then the elements of a
+// N packs whose first elements are in(p) into a segment: the whole ones all in flight at once, then the elements of a
 // pack that the row's first or last 16 bytes cut (in a loop of its own, so that the code that always runs stays short).
 template <typename T, int VEC, int N, typename In>
-__device__ __forceinline__ void ld_chunk_packs(Pack<T, VEC> (&x)[N], const T* row, int first, int seg, int V, const In& in)
+__device__ __forceinline__ void ld_chunk_packs(Pack<T, VEC> (&x)[N], const Segment<T>& s, const In& in)
 {
     Pack<T, VEC> none;
 #pragma unroll
@@ -116,19 +125,19 @@ __device__ __forceinline__ void ld_chunk_packs(Pack<T, VEC> (&x)[N], const T* ro
     unsigned cut = 0;
 #pragma unroll
     for (int p = 0; p < N; ++p) {
-        const int at = first + in(p);
-        const bool inside = in(p) < seg && at + VEC > 0 && at < V, whole = inside && at >= 0 && at + VEC <= V;
+        const int at = in(p);
+        const bool inside = at < s.end, whole = at >= s.lo && at + VEC <= s.end;
         x[p] = none;
-        if (whole) x[p] = ld_pack<T, VEC>(row + at, true);
+        if (whole) x[p] = ld_pack<T, VEC>(s.at + at, true);
         cut |= (inside && !whole ? 1u : 0u) << p;
     }
     while (cut) {
-        const int c = __ffs(cut) - 1, at = first + in(c);
+        const int c = __ffs(cut) - 1, at = in(c);
         cut &= cut - 1;
         Pack<T, VEC> part = none;
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-            if (at + i >= 0 && at + i < V) part.x[i] = row[at + i];
+            if (at + i >= s.lo && at + i < s.end) part.x[i] = s.at[at + i];
 #pragma unroll
         for (int p = 0; p < N; ++p)
             if (p == c) x[p] = part;
@@ -145,11 +154,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_segment_kernel(const BeamArg
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     begin_after();
     const T* base = (const T*)A.logits + row * A.row_stride;
-    const int first = split * A.seg - lead_of(base);
     if ((A.done && A.done[row]) || !(A.scores[row] > -INFINITY)) return;
 
     Pack<T, VEC> x[PACKS];
-    ld_chunk_packs<T, VEC, PACKS>(x, base, first, A.seg, A.V, [&](int p) { return (p * kThreads + tid) * VEC; });
+    ld_chunk_packs<T, VEC, PACKS>(x, segment_of(A, base, split), [&](int p) { return (p * kThreads + tid) * VEC; });
     float m = -INFINITY;
 #pragma unroll
     for (int p = 0; p < PACKS; ++p) m = fmaxf(m, pack_max(x[p]));  // a pack of NaNs: -inf stays
@@ -323,15 +331,15 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs 
         constexpr int kReads = decltype(reads)::value;
         const int r = i / per, c = i - r * per, k = rows_on[r];
         const Beam beam = beam_of(k);
-        const T* base = (const T*)A.logits + (row0 + k) * A.row_stride;
-        const int split = c / (kThreads >> A.lg), t0 = (c - split * (kThreads >> A.lg)) << A.lg, first = split * A.seg - lead_of(base);
+        const int split = c / (kThreads >> A.lg), t0 = (c - split * (kThreads >> A.lg)) << A.lg;
+        const Segment<T> s = segment_of(A, (const T*)A.logits + (row0 + k) * A.row_stride, split);
         for (int q0 = tid & (LC - 1); q0 < 1 << (A.lg_packs + A.lg); q0 += kReads * LC) {
             Pack<T, VEC> x[kReads];
             auto in = [&](int p) {
                 const int q = q0 + LC * p;
                 return q < 1 << (A.lg_packs + A.lg) ? ((q >> A.lg) * kThreads + t0 + (q & ((1 << A.lg) - 1))) * VEC : A.seg;
             };
-            ld_chunk_packs<T, VEC, kReads>(x, base, first, A.seg, A.V, in);
+            ld_chunk_packs<T, VEC, kReads>(x, s, in);
             unsigned reach = 0;  // the packs that hold such an element: few, so they are read again one by one
 #pragma unroll
             for (int p = 0; p < kReads; ++p) reach |= (beam.of(pack_max(x[p])) >= least ? 1u : 0u) << p;
@@ -339,11 +347,11 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamArgs 
             for (; reach; reach &= reach - 1) {
                 const int one = in(__ffs(reach) - 1);
                 Pack<T, VEC> y[1];
-                ld_chunk_packs<T, VEC, 1>(y, base, first, A.seg, A.V, [&](int) { return one; });
+                ld_chunk_packs<T, VEC, 1>(y, s, [&](int) { return one; });
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const unsigned o = beam.of(y[0].get(e));
-                    if (o >= least) take(o, (unsigned)k * (unsigned)A.V + (unsigned)(first + one + e));
+                    if (o >= least) take(o, (unsigned)k * (unsigned)A.V + (s.column + (unsigned)(one + e)));
                 }
             }
         }

@@ -27,4 +27,17 @@ GDN_PACKS_FN PackCopy ring_copy(int c, int lead, int D, int vec, int elem_bytes)
     return {c, c + vec <= D ? 16u : (unsigned)((D - c) * elem_bytes)};
 }
 
+// Segment `split` of `seg` elements (whole packs) of a row of V whose first element is `lead` past a 16-byte boundary:
+// the segment begins `first` elements after that boundary, and of its elements those from lo to below end are the
+// row's.  Unsigned, since what the last segments reach to passes 2^31 for the longest rows.
+struct PackSegment {
+    unsigned first;
+    int lo, end;
+};
+GDN_PACKS_FN PackSegment pack_segment(unsigned split, int seg, unsigned lead, int V)
+{
+    const unsigned first = split * (unsigned)seg, all = (unsigned)V + lead, left = first < all ? all - first : 0u;
+    return {first, split == 0 ? (int)lead : 0, left < (unsigned)seg ? (int)left : seg};
+}
+
 }  // namespace gdn

@@ -25,7 +25,8 @@
  *   GDN_ERR_INVALID_ARG  NULL pointer, negative N, K or V < 1, row_stride < V, unknown dtype, n_out
  *                        < 1 or above K V, pad_token outside [0, V) with done, a pointer not
  *                        aligned to its element (the workspace to 16 bytes), src_slots without slots
- *   GDN_ERR_UNSUPPORTED  n_out above 64, K above 64, K V or N K beyond 2^31 - 1
+ *   GDN_ERR_UNSUPPORTED  n_out above 64, K above 64, K V or 64 N K above 2^31 - 1, more than 2^31 - 1
+ *                        segments (of 32 KB of a row, or fewer where rows are few) in all
  *   GDN_ERR_ALIAS        an output or the workspace overlaps an input or another output
  *   GDN_ERR_WORKSPACE    workspace smaller than beam_workspace_bytes()
  *   GDN_ERR_CUDA         a launch failed

@@ -32,6 +32,27 @@ extern "C" int norm_ring_row(long long row, int D, long long stride, long long t
         }
     return next >= D ? 0 : 6;
 }
+
+// A row of V elements, the first `lead` past a 16-byte boundary, in `splits` segments of `seg`: 0 where the
+// segments' elements follow each other and are the row's, else 1 + the kind of mistake.  Long rows: the first and
+// last segments.
+extern "C" int selection_row(int V, int lead, int splits, int seg, int vec)
+{
+    for (long long s = 0; s < splits; s = s == 40 && splits > 200 ? splits - 40 : s + 1) {
+        const PackSegment p = pack_segment((unsigned)s, seg, (unsigned)lead, V);
+        long long lo = s * seg - lead, end = lo + seg;  // columns, in more than 32 bits
+        if (lo < 0) lo = 0;
+        if (end > V) end = V;
+        if (end < lo) end = lo;
+        const long long first = (long long)p.first - lead;
+        if (p.first != (unsigned long long)s * seg || p.end < 0 || p.end > seg || p.lo < 0 || p.lo >= vec) return 1;
+        if (lo < end && (first + p.lo != lo || first + p.end != end)) return 2;
+        if (lo == end && p.end > p.lo) return 3;
+        // the column of an element in the kernel's 32-bit arithmetic
+        if (lo < end && (p.first - (unsigned)lead) + (unsigned)(p.end - 1) != (unsigned long long)(end - 1)) return 4;
+    }
+    return (long long)splits * seg - lead >= V ? 0 : 5;
+}
 """
 
 
@@ -58,3 +79,15 @@ def test_norm_ring_copies_are_aligned_and_inside(host, elem_bytes):
                 for row in list(range(17)) + [rows - 1]:
                     got = host.norm_ring_row(i64(row), D, i64(stride), i64(total), vec, elem_bytes, threads, vpt)
                     assert got == 0, (D, vpt, rows, stride, row, got)
+
+
+@pytest.mark.parametrize("vec", [4, 8])
+def test_selection_segments_cover_a_row_of_any_length(host, vec):
+    for V in [1, 2, 7, 8, 9, 63, 1000, 4096, 32000, 50001, 128257, 2**24 + 1, 2**30, 2**31 - 20000, 2**31 - 9, 2**31 - 8, 2**31 - 2, 2**31 - 1]:
+        for lg_packs in (1, 2, 3):   # as the plan of a selection cuts rows: segments of one size, whole packs
+            span, most = V + vec - 1, (vec * 256) << lg_packs
+            splits = -(-span // most)
+            seg = -(-span // (splits * vec)) * vec
+            for lead in range(vec):
+                got = host.selection_row(V, lead, splits, seg, vec)
+                assert got == 0, (V, lg_packs, lead, got)
