@@ -118,8 +118,13 @@ def forward(x, weight=None, residual=None, eps=1e-6, y_dtype=None, group=0, stre
 
 
 def backward(h, rstd, dy, weight=None, dh=None, stream=None):
-    """Allocate and run rms_backward.  Returns (dx, dweight); dweight is None without a weight."""
+    """Allocate and run rms_backward.  h, dy [rows, D] may have any row stride; dh, of h's type, and
+    rstd (fp32, a number a row) are dense.  Returns (dx, dweight); dweight is None without a weight."""
     p = params_for(h, weight, residual=dy)
+    if rstd.dtype != torch.float32 or (dh is not None and dh.dtype != h.dtype):
+        raise TypeError("rstd must be float32, and dh of h's type")
+    if rstd.numel() != h.shape[0] or not rstd.is_contiguous() or (dh is not None and (dh.shape != h.shape or not dh.is_contiguous())):
+        raise ValueError("rstd must be contiguous [rows], and dh contiguous of h's shape")
     with _allocating_on(stream):
         dx = torch.empty(tuple(h.shape), dtype=h.dtype, device=h.device)
         dw = ws = None

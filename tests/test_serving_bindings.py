@@ -63,3 +63,24 @@ def test_memory_comes_from_the_stream_that_uses_it(calls):
 def test_without_a_stream_the_current_one_is_left_alone(calls):
     every_call(None)
     assert len(calls) == 20 and all(stream is None and what != "recorded" for what, stream in calls)
+
+
+def test_norm_gradient_refuses_what_it_would_misread(calls):
+    """dh is read as dense [rows, D] of h's type and rstd as dense fp32 [rows]; h and dy may have any row stride."""
+    wide, w, rstd = torch.zeros(6, 128), torch.ones(64), torch.ones(6)
+    h, dy, dense = wide[:, :64], wide[:, 64:], torch.zeros(6, 64)
+    rms.backward(h, rstd, dy, w, dense)
+    rms.backward(h, rstd[:, None], dy, w, dense)             # [rows, 1] holds the same numbers
+    rms.backward(h[:1], rstd[:1], dy[:1], w, wide[:1, :64])  # one row is dense whatever its stride
+    done = [c for c in calls if c[0] == "call"]
+    assert len(done) == 3
+    for bad, err in ((dict(dh=wide[:, :64]), ValueError), (dict(dh=torch.zeros(6, 1).expand(6, 64)), ValueError),
+                     (dict(dh=torch.zeros(64, 6).t()), ValueError), (dict(dh=dense[:5]), ValueError), (dict(dh=torch.zeros(64, 6)), ValueError),
+                     (dict(dh=dense.bfloat16()), TypeError), (dict(dh=dense.double()), TypeError),
+                     (dict(rstd=torch.ones(5)), ValueError), (dict(rstd=torch.ones(12)[::2]), ValueError), (dict(rstd=torch.ones(1).expand(6)), ValueError),
+                     (dict(rstd=rstd.bfloat16()), TypeError), (dict(rstd=rstd.double()), TypeError)):
+        with pytest.raises(err):
+            rms.backward(**{**dict(h=h, rstd=rstd, dy=dy, weight=w, dh=dense), **bad})
+    with pytest.raises(TypeError):
+        rms.backward(h.bfloat16(), rstd, dy.bfloat16(), w, dense)   # an fp32 dh beside bf16 rows
+    assert [c for c in calls if c[0] == "call"] == done
