@@ -416,6 +416,8 @@ extern "C" gdn_status_t gdn_decode(const gdn_decode_params_t* p, const void* q, 
 namespace gdn {
 namespace {
 
+constexpr int kMostGroup = 1024, kLeastPiece = 128, kMostGroupBytes = kMostGroup * kLeastPiece;  // of larger groups
+
 struct MoveArgs {
     char* pool;
     const int *src, *dst;
@@ -522,7 +524,7 @@ extern "C" gdn_status_t gdn_states_move(void* pool, int64_t n_layers, int64_t la
     if (n_layers < 0 || n_slots < 0 || state_bytes < 0 || n_moves < 0 || layer_stride < 0 || slot_stride < 0 || group < 1)
         return fail(GDN_ERR_INVALID_ARG, "gdn_states_move: negative size or stride, or group < 1");
     if (group > n_moves) group = n_moves > 0 ? n_moves : 1;
-    if (group > 1024) return fail(GDN_ERR_UNSUPPORTED, "gdn_states_move: more than 1024 moves in a group");
+    if (group > kMostGroup) return fail(GDN_ERR_UNSUPPORTED, "gdn_states_move: more than 1024 moves in a group");
     if (n_layers == 0 || n_moves == 0 || state_bytes == 0 || n_slots == 0) return GDN_OK;
     if (!pool || !src || !dst) return fail(GDN_ERR_INVALID_ARG, "gdn_states_move: NULL pointer");
     if ((uintptr_t)pool % 16 || layer_stride % 16 || slot_stride % 16 || state_bytes % 16 || (uintptr_t)src % 4 || (uintptr_t)dst % 4)
@@ -547,7 +549,7 @@ extern "C" gdn_status_t gdn_states_move(void* pool, int64_t n_layers, int64_t la
         piece = 4096 * (G == 1 ? 4 : 1);  // 16 bytes of 256 threads, P times
     } else {
         piece = 32 * 1024 / group / 16 * 16;
-        if (piece < 128) piece = 128;
+        if (piece < kLeastPiece) piece = kLeastPiece;
         if (piece > state_bytes) piece = state_bytes;
     }
     A.piece = (int)piece;
@@ -565,8 +567,9 @@ extern "C" gdn_status_t gdn_states_move(void* pool, int64_t n_layers, int64_t la
     else if (group <= 16) e = launch_move<16, 1>(A, (unsigned)ctas, st);
     else {
         const size_t smem = (size_t)(piece * group);
+        // the limit is the kernel's, not the call's: every call sets the same, so that none lowers another thread's
         if (smem > 40 * 1024)
-            e = (int)cudaFuncSetAttribute(gdn_states_move_large_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            e = (int)cudaFuncSetAttribute(gdn_states_move_large_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostGroupBytes);
         if (!e) e = launch_after(gdn_states_move_large_kernel, (unsigned)ctas, 256, smem, st, A);
     }
     return e ? cuda_fail(e, "gdn_states_move launch") : GDN_OK;

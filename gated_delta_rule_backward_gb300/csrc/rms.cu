@@ -32,6 +32,7 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxThreads = 1024, kRingThreads = 512;
+constexpr int kMostSmem = 220 * 1024;  // of a backward CTA, beside its static arrays
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kE4m3Max = 448.f;
 constexpr float kTinyScale = 1.17549435e-38f;  // 2^-126
@@ -688,13 +689,14 @@ int launch_bwd_v(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
     const size_t weights = VPT * VEC > 16 ? (size_t)VPT * VEC * 4 * s.tpr * s.ry : 0;
     const bool deep = 4 * row + weights <= 200 * 1024, cut = A.D % VEC != 0;
     size_t smem = weights + (A.vec ? (deep ? 4 : 2) * row : 0);
-    if (smem > 220 * 1024) return (int)cudaErrorInvalidValue;  // not for the shapes of bwd_shape()
     if (A.part && s.ry > 1 && smem < (size_t)s.ry * A.D * 4) smem = (size_t)s.ry * A.D * 4;
+    if (smem > kMostSmem) return (int)cudaErrorInvalidValue;  // not for the shapes of bwd_shape()
     const auto kernel = !A.vec ? rms_backward_kernel<T, VPT, 0, kSingle>
                         : deep ? (cut ? rms_backward_kernel<T, VPT, 4, kCut> : rms_backward_kernel<T, VPT, 4, kWhole>)
                                : (cut ? rms_backward_kernel<T, VPT, 2, kCut> : rms_backward_kernel<T, VPT, 2, kWhole>);
+    // the limit is the kernel's, not the call's: every call sets the same, so that none lowers another thread's
     if (smem > 40 * 1024) {
-        const int e = (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const int e = (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (e) return e;
     }
     return launch_after(kernel, ctas, dim3(s.tpr, s.ry), smem, st, A);
