@@ -570,16 +570,17 @@ __global__ void __launch_bounds__(kMaxThreads) rms_backward_long_kernel(const Rm
     }
 }
 
+// CTAs (256 columns, a part of the rows): the columns along x, since a grid's y ends at 65535.
 template <typename T>
 __global__ void __launch_bounds__(256) rms_dweight_long_kernel(const RmsBwd A)
 {
-    const int c = blockIdx.y * 256 + threadIdx.x;
+    const int c = blockIdx.x * 256 + threadIdx.x;
     begin_after();
     if (c >= A.D) return;
     float t = 0.f;
-    for (long long row = blockIdx.x; row < A.rows; row += gridDim.x)
+    for (long long row = blockIdx.y; row < A.rows; row += gridDim.y)
         t = fmaf(to_f32(((const T*)A.dy)[row * A.dys + c]), to_f32(((const T*)A.h)[row * A.hs + c]) * ld_plain(A.rstd + row), t);
-    A.part[(size_t)blockIdx.x * A.D + c] = t;
+    A.part[(size_t)blockIdx.y * A.D + c] = t;
 }
 
 // dweight = the parts' sum, 8 columns a CTA, 16 threads over the parts of each.  Small CTAs: they are
@@ -713,7 +714,7 @@ int launch_bwd(const RmsBwd& A, const Shape& s, int ctas, cudaStream_t st)
     }
     const int e = launch_after(rms_backward_long_kernel<T>, (unsigned)A.rows, kMaxThreads, 0, st, A);
     if (e || !A.part) return e;
-    return launch_after(rms_dweight_long_kernel<T>, dim3(ctas, (A.D + 255) / 256), 256, 0, st, A);
+    return launch_after(rms_dweight_long_kernel<T>, dim3((A.D + 255) / 256, ctas), 256, 0, st, A);
 }
 
 // CTAs of the backward, each with its own part of dweight.
