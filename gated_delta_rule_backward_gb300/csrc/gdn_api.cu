@@ -594,7 +594,8 @@ gdn_status_t gdn_device_status(void* stream)
     int a = 0, b = 0, c = 0;
     int e = gdn::tc_take_status(stream, &a);
     if (!e) e = gdn::tc_grad_take_status(stream, &b);
-    if (!e) e = gdn::decode_take_status(stream, &c);
+    // one code a call: where a wait gave up, what the serving kernels met stays for the next call
+    if (!e && !a && !b) e = gdn::decode_take_status(stream, &c);
     if (e) return cuda_status(e, "device status");
     if (!a && !b && !c) return GDN_OK;
     if (!a && !b)

@@ -253,8 +253,10 @@ def gdn_backward_noalloc(p: GdnParams, q, k, v, g, beta, ckpt, gy, dstate_T, pac
 
 
 def device_status(stream=None) -> int:
-    """Synchronise `stream` and return (and clear) the device status: GDN_OK, or
-    6 (GDN_ERR_TIMEOUT) when a tensor-core kernel's bounded wait gave up."""
+    """Synchronise `stream` and return (and clear) the device status: GDN_OK, 6
+    (GDN_ERR_TIMEOUT) when a tensor-core kernel's bounded wait gave up, or 1
+    (GDN_ERR_INVALID_ARG) when a serving kernel skipped a slot or token range out of bounds.
+    Where both have been met, the first call returns 6 and the next one 1."""
     return int(_lib.gdn_device_status(_stream_handle(stream)))
 
 

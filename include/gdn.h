@@ -224,7 +224,8 @@ int gdn_timing_stages(const gdn_params_t* p, int backward);
  * call synchronises `stream` (a cudaStream_t, NULL = legacy default stream), then reads
  * and clears the status words: GDN_OK, GDN_ERR_TIMEOUT, GDN_ERR_INVALID_ARG when a serving
  * kernel skipped slots or token ranges out of bounds (gdn_decode.h), or GDN_ERR_CUDA if the
- * stream or the read failed (text in gdn_last_error()).  No counterpart on the pages; it exists
+ * stream or the read failed (text in gdn_last_error()).  Where both kinds have been met, this call
+ * returns the timeout and the next one the other.  No counterpart on the pages; it exists
  * because a GPU kernel cannot return an error code by itself. */
 gdn_status_t gdn_device_status(void* stream);
 
