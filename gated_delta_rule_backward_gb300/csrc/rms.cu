@@ -426,6 +426,7 @@ template <typename T, int VPT, int RING, int HOW>
 __global__ void __maxnreg__(112) rms_backward_kernel(const RmsBwd A)
 {
     constexpr int VEC = 16 / (int)sizeof(T), HELD = VPT * VEC > 16 ? 1 : VPT;
+    static_assert(kNumSMs % VEC == 0, "a grid of kNumSMs CTAs is a multiple of VEC rows: a thread's columns stay");
     constexpr bool LEAN = VPT * VEC > 16;
     constexpr int kPart = HOW == kWhole ? kWhole : kSingle;  // a part's rows begin anywhere
     extern __shared__ uint4 ring[];  // [RING][3 VPT][threads], LEAN: weights [VPT][VEC / 4][threads]; at the end, as floats, [blockDim.y][D]
