@@ -11,12 +11,12 @@
 // Forward: a CTA a row (a warp where rows are short), five CTAs an SM, so that other rows' loads
 // are in flight while one is summed; with y = (h w) rstd the largest |h w| of a row, summed beside
 // the squares, gives its scale without a second exchange.  Measured: 4096 rows of 6144, bf16 to codes with a
-// scale for 128 columns, 29.9 us, 5.9 TB/s of 6.7 for a copy; 4096 of 4095 bf16 30.7 us,
+// scale for 128 columns, 30.0 us, 5.9 TB/s of 6.7 for a copy; 4096 of 4095 bf16 30.7 us,
 // 4.4 TB/s; one row of 2048 1.9 us (in a graph).
 // Backward: one persistent CTA of 512 threads an SM, 16 elements a thread (a row's exchange costs
 // about as much as 16 elements' arithmetic), rows through a ring of asynchronous copies, dweight
 // in registers over all rows, then one part a CTA and a second kernel that sums 152 parts.
-// Measured: 8192 rows of 2048, bf16, 28.4 us in all; 4096 of 4095 39 us.
+// Measured: 8192 rows of 2048, bf16, 28.2 us in all; 4096 of 4095 39 us.
 #include <climits>
 #include <cstdio>
 #include <cuda_fp8.h>
@@ -348,8 +348,8 @@ __device__ __forceinline__ void finish_pack(const RmsFwd& A, const Nums<VEC>& h,
 }
 
 // VPT packs a thread; VPT = 0: rows that registers do not hold, read again (from L2) after the sums.
-// Rows of fewer than the most packs have 256 threads at most, five CTAs an SM: 4096 rows of 6144
-// to codes take 28 us so, 30 us with the four that the compiler's own choice of registers leaves.
+// Rows of fewer than the most packs have 256 threads at most, five CTAs an SM: 4096 rows of 6144 to codes take
+// 29.5 us so in a graph (a scale a row: 31.3), 30.5 us (34.0) with the compiler's own choice of registers.
 template <typename T, int VPT, int OUT, int HOW>
 __global__ void __launch_bounds__(VPT > 0 && VPT < 4 ? 256 : kMaxThreads, VPT > 0 && VPT < 4 ? (HOW == kWhole ? 5 : 4) : 1) rms_forward_kernel(const RmsFwd A)
 {

@@ -12,6 +12,8 @@
  *   - a logit of -inf (a masked token), or a row of nothing else, has candidates at -inf; they
  *     fill up, lowest index first, what too few others leave;
  *   - logits of +inf share the probability, the others have none.
+ * Tokens are best masked with -inf: finite masks leave candidates like any others, and where n_out reaches into
+ * thousands of equal ones, choosing among them takes milliseconds.
  * Equality is that of the fp32 c.
  *
  * Layouts (device memory): logits [N K][V] in dtype, rows row_stride elements apart, V
