@@ -591,17 +591,19 @@ int gdn_backward_launches(const gdn_params_t* p)
 
 gdn_status_t gdn_device_status(void* stream)
 {
-    int a = 0, b = 0, c = 0;
+    int a = 0, b = 0, c = 0, t = 0, la = 0;
     int e = gdn::tc_take_status(stream, &a);
     if (!e) e = gdn::tc_grad_take_status(stream, &b);
+    if (!e) e = gdn::la_take_status(stream, true, &t);
     // one code a call: where a wait gave up, what the serving kernels met stays for the next call
-    if (!e && !a && !b) e = gdn::decode_take_status(stream, &c);
+    if (!e && !a && !b && !t) e = gdn::decode_take_status(stream, &c);
+    if (!e && !a && !b && !t) e = gdn::la_take_status(stream, false, &la);
     if (e) return cuda_status(e, "device status");
-    if (!a && !b && !c) return GDN_OK;
-    if (!a && !b)
-        return fail(GDN_ERR_INVALID_ARG, "%s%s%s met a slot outside the pool%s; what it named was skipped",
-                    c & 1 ? "gdn_decode" : "", c == 3 ? " and " : "", c & 2 ? "gdn_states_move" : "",
-                    c & 1 ? " or a bad cu_tokens" : "");
+    if (!a && !b && !t && !c && !la) return GDN_OK;
+    if (!a && !b && !t)
+        return fail(GDN_ERR_INVALID_ARG, "%s%s%s%s%s met a slot outside the pool%s; what it named was skipped",
+                    c & 1 ? "gdn_decode" : "", c == 3 ? " and " : "", c & 2 ? "gdn_states_move" : "", c && la ? " and " : "",
+                    la ? "la_forward or la_backward" : "", (c & 1) || la ? " or a bad cu_tokens" : "");
     // chain status word: 6 | kernel << 4 | wait-site bits << 8 (gdn_tc_chain.cu)
     static const char* const kernels[] = {"?", "state chain", "?", "dM chain", "selftest"};
     const int ker = (a >> 4) & 15;
@@ -610,8 +612,8 @@ gdn_status_t gdn_device_status(void* stream)
     const char* grad = !b ? "ok" : ((b >> 8) & 1) ? "timed out, a product still in flight at exit" : "timed out";
     return fail(GDN_ERR_TIMEOUT,
                 "a kernel's bounded wait gave up; that call's outputs are invalid (chains: %s, "
-                "wait sites 0x%x; gradient kernel: %s)",
-                a ? kernels[ker < 5 ? ker : 0] : "ok", (unsigned)a >> 8, grad);
+                "wait sites 0x%x; gradient kernel: %s; linear attention: %s)",
+                a ? kernels[ker < 5 ? ker : 0] : "ok", (unsigned)a >> 8, grad, t ? "timed out" : "ok");
 }
 
 gdn_status_t gdn_selftest_wait_timeout(void* stream)

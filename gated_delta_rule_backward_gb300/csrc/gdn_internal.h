@@ -293,6 +293,9 @@ int launch_widen(const void* src, int in_dtype, const long long s[3], int N, int
 // device).  Returns a cudaError_t as int.
 int decode_take_status(void* stream, int* status);
 
+// Reads and clears linear attention's status words: waits that gave up, or bad slots and token ranges.
+int la_take_status(void* stream, bool timeouts, int* status);
+
 // Sets the text gdn_last_error() returns on the calling thread.
 void set_last_error(const char* msg);
 

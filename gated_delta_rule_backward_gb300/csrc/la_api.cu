@@ -1,0 +1,435 @@
+// la_api.cu -- linear attention's C ABI (include/la.h): argument checks, the runs of the core that make up a
+// call, and the two kernels behind the backward pass's runs.
+//
+// The backward pass's dq and dk come per value head in fp32; la_join_kernel sums the value heads of a key head, rounds once,
+// and leaves each token's q . dq - k . dk per value head, whose running sum from the last token on is dg
+// (la_gate_kernel): with s_t = <M_t, D_t>,  dg_t = a_t <D_t, M_{t-1}> = s_t - v_t . D_t k_t  and
+// s_t = dg_{t+1} + scale dy_t . M_t q_t, where both products are q . dq and k . dk.  Bytes bound both.
+#include <climits>
+#include <cstdio>
+
+#include "gdn_device.cuh"
+#include "gdn_elem.cuh"
+#include "gdn_launch.cuh"
+#include "la_internal.h"
+
+namespace gdn {
+namespace {
+
+struct JoinArgs {
+    const void *q, *k;
+    const float *dqh, *dkh;  // [n_tok][H_v][S_k]
+    void *dq, *dk;           // [n_tok][H_k][S_k]
+    float* terms;            // [n_tok][H_v]
+    const int* cu;
+    long long qs0, qs1, ks0, ks1;
+    int n_tok, n_seq, H_k, H_v, SK;
+};
+
+// A warp a token and key head.
+template <typename T>
+__global__ void __launch_bounds__(256) la_join_kernel(const JoinArgs A)
+{
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const long long t = w / A.H_k;
+    const int hk = (int)(w - t * A.H_k), r = A.H_v / A.H_k;
+    begin_after();
+    if (t >= A.n_tok || (A.cu && (t < A.cu[0] || t >= A.cu[A.n_seq]))) return;  // rows that no sequence owns
+    for (int c0 = 0; c0 < A.SK; c0 += 128) {
+        const int c = c0 + 4 * lane;
+        const bool in = c < A.SK;
+        float q[4], k[4], dq[4] = {0.f, 0.f, 0.f, 0.f}, dk[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            q[e] = in ? to_f32(((const T*)A.q)[t * A.qs0 + hk * A.qs1 + c + e]) : 0.f;
+            k[e] = in ? to_f32(((const T*)A.k)[t * A.ks0 + hk * A.ks1 + c + e]) : 0.f;
+        }
+        for (int i = 0; i < r; ++i) {
+            const long long th = t * A.H_v + hk + (long long)i * A.H_k;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            if (in) {
+                a = *reinterpret_cast<const float4*>(A.dqh + th * A.SK + c);
+                b = *reinterpret_cast<const float4*>(A.dkh + th * A.SK + c);
+            }
+            dq[0] += a.x; dq[1] += a.y; dq[2] += a.z; dq[3] += a.w;
+            dk[0] += b.x; dk[1] += b.y; dk[2] += b.z; dk[3] += b.w;
+            float s = (q[0] * a.x + q[1] * a.y + q[2] * a.z + q[3] * a.w) - (k[0] * b.x + k[1] * b.y + k[2] * b.z + k[3] * b.w);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+            if (lane == 0) A.terms[th] = c0 == 0 ? s : A.terms[th] + s;
+        }
+        if (in) {
+            const long long at = (t * A.H_k + hk) * A.SK + c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                ((T*)A.dq)[at + e] = from_f32<T>(dq[e]);
+                ((T*)A.dk)[at + e] = from_f32<T>(dk[e]);
+            }
+        }
+    }
+}
+
+struct GateArgs {
+    LaRun run;  // the sequences
+    const float *terms, *m_T, *d_T;  // m_T, d_T: [n_seq][H_v][states], d_T may be null
+    float* dg;
+    int state;  // elements of one
+};
+
+// A CTA a sequence and head: the anchor <M_T, dM_T>, then the running sum from the last token, 256 tokens at a time;
+// what is carried from one to the next is held in 64 bits.
+__global__ void __launch_bounds__(256) la_gate_kernel(const GateArgs A)
+{
+    __shared__ float part[8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = blockIdx.x / A.run.H, h = blockIdx.x - n * A.run.H;
+    begin_after();
+    const LaSequence s = la_sequence(A.run, n);
+    if (!s.ok) return;  // the runs have reported it
+    double carry = 0.0;
+    if (A.d_T && s.hi > s.lo) {
+        const float4 *m = reinterpret_cast<const float4*>(A.m_T + (long long)blockIdx.x * A.state), *d = reinterpret_cast<const float4*>(A.d_T + (long long)blockIdx.x * A.state);
+        float x = 0.f;
+        for (int i = tid; i < A.state / 4; i += 256) {
+            const float4 a = m[i], b = d[i];
+            x += (a.x * b.x + a.y * b.y) + (a.z * b.z + a.w * b.w);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+        if (lane == 0) part[warp] = x;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 8; ++w) carry += part[w];
+        __syncthreads();
+    }
+    for (long long t0 = s.hi - 1; t0 >= s.lo; t0 -= 256) {
+        const long long t = t0 - tid;
+        float x = t >= s.lo ? A.terms[t * A.run.H + h] : 0.f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(kFull, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) part[warp] = x;
+        __syncthreads();
+        double before = carry;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) before += part[w];
+            carry += part[w];
+        }
+        if (t >= s.lo) A.dg[t * A.run.H + h] = (float)(before + x);
+        __syncthreads();
+    }
+}
+
+int fail(int s, const char* msg)
+{
+    set_last_error(msg);
+    return s;
+}
+
+int cuda_fail(int e, const char* what)
+{
+    char msg[256];
+    snprintf(msg, sizeof msg, "%s: %s", what, cudaGetErrorString((cudaError_t)e));
+    return fail(GDN_ERR_CUDA, msg);
+}
+
+struct Buffer {
+    const void* ptr;
+    size_t n;
+};
+
+bool overlap(const Buffer& a, const Buffer& b)
+{
+    const uintptr_t x = (uintptr_t)a.ptr, y = (uintptr_t)b.ptr;
+    return a.ptr && b.ptr && a.n && b.n && x < y + b.n && y < x + a.n;
+}
+
+template <int I, int O>
+bool aliased(const Buffer (&in)[I], const Buffer (&out)[O])
+{
+    for (int i = 0; i < O; ++i) {
+        for (int j = 0; j < I; ++j)
+            if (overlap(out[i], in[j])) return true;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return true;
+    }
+    return false;
+}
+
+// Bytes that rows of H heads of S elements reach over.
+size_t span(int64_t rows, int64_t H, int64_t S, const int64_t s[2], size_t es)
+{
+    return rows < 1 ? 0 : (size_t)((rows - 1) * s[0] + (H - 1) * s[1] + S) * es;
+}
+
+bool head_size(int64_t S) { return S == 16 || S == 32 || S == 64 || S == 128 || S == 256; }
+
+int check(const la_params_t* p, bool backward)
+{
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "la: params is NULL");
+    if (p->n_seq < 0 || p->T < 0 || p->n_tok < 0 || p->n_slots < 0) return fail(GDN_ERR_INVALID_ARG, "la: negative n_seq, T, n_tok or n_slots");
+    if (p->H_k < 1 || p->H_v < 1 || p->S_k < 1 || p->S_v < 1) return fail(GDN_ERR_INVALID_ARG, "la: heads and head sizes must be >= 1");
+    if (p->H_v % p->H_k != 0) return fail(GDN_ERR_INVALID_ARG, "la: H_v is not a multiple of H_k");
+    if (!known_dtype(p->in_dtype) || !known_dtype(p->gate_dtype) || !known_dtype(p->y_dtype)) return fail(GDN_ERR_INVALID_ARG, "la: unknown dtype");
+    for (int i = 0; i < 2; ++i)
+        if (p->q_s[i] < 0 || p->k_s[i] < 0 || p->v_s[i] < 0 || p->g_s[i] < 0) return fail(GDN_ERR_INVALID_ARG, "la: negative stride");
+    if (!head_size(p->S_k)) return fail(GDN_ERR_UNSUPPORTED, "la: S_k must be 16, 32, 64, 128 or 256");
+    if (p->S_v % 16 != 0 || p->S_v > 256) return fail(GDN_ERR_UNSUPPORTED, "la: S_v must be a multiple of 16 up to 256");
+    if (backward && !head_size(p->S_v)) return fail(GDN_ERR_UNSUPPORTED, "la: the backward pass needs S_v of 16, 32, 64, 128 or 256");
+    if (p->H_v > 65535 || p->n_tok > INT_MAX / p->H_v || p->T > INT_MAX || p->n_slots > INT_MAX || p->n_seq > (int64_t)INT_MAX / (p->H_v * 64))
+        return fail(GDN_ERR_UNSUPPORTED, "la: sizes beyond the kernels' index range");
+    if (p->slot_stride < p->H_v * p->S_v * p->S_k || p->slot_stride % 4 != 0)
+        return fail(GDN_ERR_INVALID_ARG, "la: slot_stride must be a multiple of 4 of at least H_v S_v S_k");
+    return GDN_OK;
+}
+
+// What the two entry points check alike: the sequences and the inputs.
+int check_inputs(const la_params_t* p, const void* q, const void* k, const void* v, const void* g, const int32_t* cu, const void* pool,
+                 const int32_t* slot_in)
+{
+    if (!cu && p->n_tok != p->n_seq * p->T) return fail(GDN_ERR_INVALID_ARG, "la: without cu_tokens, n_tok must be n_seq T");
+    if (p->n_seq == 0) return GDN_OK;
+    if (!slot_in || (p->n_slots > 0 && !pool) || (p->n_tok > 0 && (!q || !k || !v || !g))) return fail(GDN_ERR_INVALID_ARG, "la: NULL pointer");
+    if ((uintptr_t)pool % 16) return fail(GDN_ERR_INVALID_ARG, "la: the pool must be 16-byte aligned");
+    const size_t es = elem_size(p->in_dtype);
+    if ((uintptr_t)q % es || (uintptr_t)k % es || (uintptr_t)v % es || (uintptr_t)g % elem_size(p->gate_dtype) || (uintptr_t)slot_in % 4 || (uintptr_t)cu % 4)
+        return fail(GDN_ERR_INVALID_ARG, "la: a pointer is not aligned to its element");
+    return GDN_OK;
+}
+
+LaRun run_of(const la_params_t* p, const void* g, const int32_t* cu)
+{
+    LaRun A{};
+    A.g = g;
+    A.gs0 = p->g_s[0];
+    A.gs1 = p->g_s[1];
+    A.gate_dtype = p->gate_dtype;
+    A.cu = cu;
+    A.T = (int)p->T;
+    A.n_tok = (int)p->n_tok;
+    A.n_seq = (int)p->n_seq;
+    A.H = (int)p->H_v;
+    A.n_slots = (int)p->n_slots;
+    A.co = A.cs = 1.f;
+    return A;
+}
+
+enum { X, Y, Z };
+void operand(LaRun& A, int which, const void* ptr, const int64_t s[2], int64_t heads)
+{
+    (which == X ? A.x : which == Y ? A.y : A.z) = ptr;
+    (which == X ? A.xs0 : which == Y ? A.ys0 : A.zs0) = s[0];
+    (which == X ? A.xs1 : which == Y ? A.ys1 : A.zs1) = s[1];
+    (which == X ? A.xh : which == Y ? A.yh : A.zh) = (int)heads;
+}
+
+int launch_run(const LaRun& A, bool chunked, int dtype, void* workspace, cudaStream_t st)
+{
+    return chunked ? launch_la_chunk(A, workspace, st) : launch_la_token(A, dtype, st);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The chunked form's workspace for these sizes, whatever the roles (S_k = S_v there).
+size_t chunk_bytes(const la_params_t* p)
+{
+    if (!la_chunk_fits(p)) return 0;
+    LaRun A = run_of(p, nullptr, nullptr);
+    A.DK = (int)p->S_k;
+    A.DV = (int)p->S_v;
+    return round256(la_chunk_workspace(A));
+}
+
+struct BackwardPlan {
+    size_t dqh, dkh, terms, m_T, chunk, bytes;  // offsets
+};
+BackwardPlan plan_of(const la_params_t* p)
+{
+    BackwardPlan pl{};
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += round256(n);
+        return here;
+    };
+    const size_t heads = (size_t)p->n_tok * p->H_v;
+    pl.dqh = take(heads * p->S_k * 4);
+    pl.dkh = take(heads * p->S_k * 4);
+    pl.terms = take(heads * 4);
+    pl.m_T = take((size_t)p->n_seq * p->H_v * p->S_v * p->S_k * 4);
+    pl.chunk = take(chunk_bytes(p));
+    pl.bytes = at;
+    return pl;
+}
+
+}  // namespace
+
+int la_take_word(const void* symbol, void* stream, int* status)
+{
+    cudaStream_t s = (cudaStream_t)stream;
+    int v = 0;
+    int e = (int)cudaMemcpyFromSymbolAsync(&v, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (!e) e = (int)cudaStreamSynchronize(s);
+    if (!e && v) {
+        const int zero = 0;
+        e = (int)cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+        if (!e) e = (int)cudaStreamSynchronize(s);
+    }
+    *status = v;
+    return e;
+}
+
+int la_take_status(void* stream, bool timeouts, int* status)
+{
+    int a = 0, b = 0;
+    int e = timeouts ? la_chunk_take_timeout(stream, &a) : la_token_take_bad(stream, &a);
+    if (!e && !timeouts) e = la_chunk_take_bad(stream, &b);
+    *status = a | b;
+    return e;
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" int la_form(const la_params_t* p) { return check(p, false) != GDN_OK ? -1 : la_chunk_fits(p) ? 1 : 0; }
+
+extern "C" size_t la_workspace_bytes(const la_params_t* p) { return check(p, false) == GDN_OK ? chunk_bytes(p) : 0; }
+
+extern "C" size_t la_backward_workspace_bytes(const la_params_t* p) { return check(p, true) == GDN_OK ? plan_of(p).bytes : 0; }
+
+extern "C" int la_forward(const la_params_t* p, const void* q, const void* k, const void* v, const void* g, const int32_t* cu,
+                          float* pool, const int32_t* slot_in, const int32_t* slot_out, void* y, void* workspace,
+                          size_t workspace_bytes, void* stream)
+{
+    int st = check(p, false);
+    if (st == GDN_OK) st = check_inputs(p, q, k, v, g, cu, pool, slot_in);
+    if (st != GDN_OK || p->n_seq == 0) return st;
+    const size_t es = elem_size(p->in_dtype), ys = elem_size(p->y_dtype);
+    if (!slot_out || (p->n_tok > 0 && !y)) return fail(GDN_ERR_INVALID_ARG, "la_forward: NULL pointer");
+    if ((uintptr_t)y % ys || (uintptr_t)slot_out % 4) return fail(GDN_ERR_INVALID_ARG, "la_forward: a pointer is not aligned to its element");
+    const size_t need = chunk_bytes(p);
+    if (need && (!workspace || workspace_bytes < need)) return fail(GDN_ERR_WORKSPACE, "la_forward: workspace smaller than la_workspace_bytes()");
+    if (need && (uintptr_t)workspace % 16) return fail(GDN_ERR_INVALID_ARG, "la_forward: the workspace must be 16-byte aligned");
+    const size_t n_pool = p->n_slots > 0 ? (size_t)((p->n_slots - 1) * p->slot_stride + p->H_v * p->S_v * p->S_k) * 4 : 0;
+    const size_t n_seq = (size_t)p->n_seq;
+    const Buffer in[] = {{q, span(p->n_tok, p->H_k, p->S_k, p->q_s, es)}, {k, span(p->n_tok, p->H_k, p->S_k, p->k_s, es)},
+                         {v, span(p->n_tok, p->H_v, p->S_v, p->v_s, es)}, {g, span(p->n_tok, p->H_v, 1, p->g_s, elem_size(p->gate_dtype))},
+                         {cu, (n_seq + 1) * 4}, {slot_in, n_seq * 4}, {slot_out, n_seq * 4}};
+    const Buffer out[] = {{y, (size_t)(p->n_tok * p->H_v * p->S_v) * ys}, {pool, n_pool}, {workspace, need}};
+    if (aliased(in, out)) return fail(GDN_ERR_ALIAS, "la_forward: y, the pool or the workspace overlaps an input or another of them");
+
+    LaRun A = run_of(p, g, cu);
+    operand(A, X, q, p->q_s, p->H_k);
+    operand(A, Y, k, p->k_s, p->H_k);
+    operand(A, Z, v, p->v_s, p->H_v);
+    A.DK = (int)p->S_k;
+    A.DV = (int)p->S_v;
+    A.s_in = A.s_out = pool;
+    A.slot_in = slot_in;
+    A.slot_out = slot_out;
+    A.in_stride = A.out_stride = p->slot_stride;
+    A.co = p->scale;
+    A.out = y;
+    A.out_dtype = p->y_dtype;
+    const int e = launch_run(A, la_chunk_fits(p), p->in_dtype, workspace, (cudaStream_t)stream);
+    return e ? cuda_fail(e, "la_forward launch") : GDN_OK;
+}
+
+extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, const void* v, const void* g, const int32_t* cu,
+                           const float* pool, const int32_t* slot_in, const void* dy, const float* dstate_T, void* dq, void* dk,
+                           void* dv, float* dg, float* dstate_0, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check(p, true);
+    if (st == GDN_OK) st = check_inputs(p, q, k, v, g, cu, pool, slot_in);
+    if (st != GDN_OK || p->n_seq == 0) return st;
+    const size_t es = elem_size(p->in_dtype);
+    if (p->n_tok > 0 && (!dy || !dq || !dk || !dv || !dg)) return fail(GDN_ERR_INVALID_ARG, "la_backward: NULL pointer");
+    if ((uintptr_t)dy % es || (uintptr_t)dq % es || (uintptr_t)dk % es || (uintptr_t)dv % es || (uintptr_t)dg % 4 || (uintptr_t)dstate_T % 16 ||
+        (uintptr_t)dstate_0 % 16 || (uintptr_t)workspace % 16)
+        return fail(GDN_ERR_INVALID_ARG, "la_backward: a pointer is not aligned to its element (states and the workspace to 16 bytes)");
+    const BackwardPlan pl = plan_of(p);
+    if (!workspace || workspace_bytes < pl.bytes) return fail(GDN_ERR_WORKSPACE, "la_backward: workspace smaller than la_backward_workspace_bytes()");
+    const size_t n_seq = (size_t)p->n_seq, state = (size_t)(p->S_v * p->S_k), states = n_seq * p->H_v * state * 4;
+    const size_t n_pool = p->n_slots > 0 ? (size_t)((p->n_slots - 1) * p->slot_stride + p->H_v * state) * 4 : 0;
+    const size_t n_k = (size_t)(p->n_tok * p->H_k * p->S_k) * es, n_v = (size_t)(p->n_tok * p->H_v * p->S_v) * es;
+    const Buffer in[] = {{q, span(p->n_tok, p->H_k, p->S_k, p->q_s, es)}, {k, span(p->n_tok, p->H_k, p->S_k, p->k_s, es)},
+                         {v, span(p->n_tok, p->H_v, p->S_v, p->v_s, es)}, {g, span(p->n_tok, p->H_v, 1, p->g_s, elem_size(p->gate_dtype))},
+                         {cu, (n_seq + 1) * 4}, {slot_in, n_seq * 4}, {pool, n_pool}, {dy, n_v}, {dstate_T, states}};
+    const Buffer out[] = {{dq, n_k}, {dk, n_k}, {dv, n_v}, {dg, (size_t)(p->n_tok * p->H_v) * 4}, {dstate_0, states}, {workspace, pl.bytes}};
+    if (aliased(in, out)) return fail(GDN_ERR_ALIAS, "la_backward: an output or the workspace overlaps an input or another output");
+
+    char* ws = (char*)workspace;
+    const bool chunked = la_chunk_fits(p);
+    const int64_t dense_v[2] = {p->H_v * p->S_v, p->S_v};
+    cudaStream_t cs = (cudaStream_t)stream;
+    float *dqh = (float*)(ws + pl.dqh), *dkh = (float*)(ws + pl.dkh), *m_T = (float*)(ws + pl.m_T);
+
+    LaRun A = run_of(p, g, cu);
+    operand(A, X, dy, dense_v, p->H_v);
+    operand(A, Y, v, p->v_s, p->H_v);
+    operand(A, Z, k, p->k_s, p->H_k);
+    A.DK = (int)p->S_v;
+    A.DV = (int)p->S_k;
+    A.s_in = pool;
+    A.slot_in = slot_in;
+    A.in_stride = p->slot_stride;
+    A.s_out = dstate_T ? m_T : nullptr;
+    A.out_stride = p->H_v * (int64_t)state;
+    A.transposed_in = A.transposed_out = 1;
+    A.co = p->scale;
+    A.out = dqh;
+    A.out_dtype = GDN_F32;
+    int e = launch_run(A, chunked, p->in_dtype, ws + pl.chunk, cs);
+
+    LaRun B = run_of(p, g, cu);
+    operand(B, X, v, p->v_s, p->H_v);
+    operand(B, Y, dy, dense_v, p->H_v);
+    operand(B, Z, q, p->q_s, p->H_k);
+    B.DK = (int)p->S_v;
+    B.DV = (int)p->S_k;
+    B.s_in = dstate_T;
+    B.in_stride = B.out_stride = p->H_v * (int64_t)state;
+    B.transposed_in = 1;
+    B.reverse = 1;
+    B.cs = p->scale;
+    B.out = dkh;
+    B.out_dtype = GDN_F32;
+    if (!e) e = launch_run(B, chunked, p->in_dtype, ws + pl.chunk, cs);
+
+    LaRun C = run_of(p, g, cu);
+    operand(C, X, k, p->k_s, p->H_k);
+    operand(C, Y, q, p->q_s, p->H_k);
+    operand(C, Z, dy, dense_v, p->H_v);
+    C.DK = (int)p->S_k;
+    C.DV = (int)p->S_v;
+    C.s_in = dstate_T;
+    C.s_out = dstate_0;
+    C.in_stride = C.out_stride = B.in_stride;
+    C.reverse = 1;
+    C.cs = p->scale;
+    C.out = dv;
+    C.out_dtype = p->in_dtype;
+    if (!e) e = launch_run(C, chunked, p->in_dtype, ws + pl.chunk, cs);
+
+    if (!e && p->n_tok > 0) {
+        JoinArgs J{};
+        J.q = q; J.k = k; J.dqh = dqh; J.dkh = dkh; J.dq = dq; J.dk = dk; J.terms = (float*)(ws + pl.terms); J.cu = cu;
+        J.qs0 = p->q_s[0]; J.qs1 = p->q_s[1]; J.ks0 = p->k_s[0]; J.ks1 = p->k_s[1];
+        J.n_tok = (int)p->n_tok; J.n_seq = (int)p->n_seq; J.H_k = (int)p->H_k; J.H_v = (int)p->H_v; J.SK = (int)p->S_k;
+        const unsigned ctas = (unsigned)((p->n_tok * p->H_k + 7) / 8);
+        e = p->in_dtype == GDN_F32    ? launch_after(la_join_kernel<float>, ctas, 256, 0, cs, J)
+            : p->in_dtype == GDN_BF16 ? launch_after(la_join_kernel<__nv_bfloat16>, ctas, 256, 0, cs, J)
+                                      : launch_after(la_join_kernel<__half>, ctas, 256, 0, cs, J);
+        GateArgs G{};
+        G.run = A;
+        G.terms = J.terms; G.m_T = m_T; G.d_T = dstate_T; G.dg = dg; G.state = (int)state;
+        G.run.slot_out = nullptr;
+        if (!e) e = launch_after(la_gate_kernel, (unsigned)(p->n_seq * p->H_v), 256, 0, cs, G);
+    }
+    return e ? cuda_fail(e, "la_backward launch") : GDN_OK;
+}
