@@ -7,23 +7,30 @@
 // A call backwards in time walks its tokens, and with them the tiles' rows, from the last one on, each token decaying by
 // the gate of the one behind it; nothing else changes.
 //
-// One CTA owns a state (D x D, fp32, in registers: thread = row j and half of the columns) and walks the chunks of a
-// sequence's segment.  All tiles are [token][column] in shared memory, in core matrices of 8 tokens x 8 columns; X, Y and Z arrive by
-// asynchronous copies as they are stored.  Products with a contraction over columns read a tile K-major, those over
-// tokens read the same bytes MN-major, so that nothing is transposed:
+// One CTA owns a state (D x D, fp32, in registers) and walks the chunks of a
+// sequence's segment.  X, Y and Z arrive by TMA as they are stored, rows of 64 columns in 128-byte swizzle.  Products with a
+// contraction over columns read a tile K-major, those over tokens read the same bytes MN-major, so that nothing is transposed:
 //     P  = X Y^T          128 x 128, K = D     X, Y as stored: exact
 //     XS = X S^T          128 x D,   K = D     S as bf16 hi + lo in shared memory: 2 passes
 //     O  = P' Z           128 x D,   K = 128   P' as bf16 hi + lo in TMEM (in P's columns): 2 passes
 //     dS = Z^T Y'         D x D,     K = 128   Y' as bf16 hi + lo in shared memory: 2 passes
 // hi + lo carries 16 significant bits (2^-16 relative); the accumulators and the state are fp32.
 //
-// Decays.  G is summed in fp64 and kept as two fp32 numbers, since what is needed are small differences of sums that
-// may be large.  e^(G_t - G_s) of 32 x 32 blocks below the diagonal is the product of a row's and a column's factor
-// against the block's last column (each at most 1 for decays); only the diagonal block takes an exponential an element.
+// Two groups of 8 warps work on a chunk side by side.  The first turns P into P' and writes the output; one of its
+// warps issues P, XS and O.  The second sums the gates, makes Y' and keeps the state, and issues dS.  They meet at mbarriers
+// only, so that the tensor cores run P | XS, dS | O of one chunk while the warps are at the others.  A tile is loaded again as soon as
+// its last product is done; the next ones are prefetched into L2.
+//
+// Decays.  G is summed in 64-bit fixed point (powers of two, 31 fraction bits) and kept as a whole and a fractional fp32 number, since
+// what is needed are small differences of sums that may be large.  e^(G_t - G_s) of 32 x 32 blocks off the diagonal is the product of a
+// row's and a column's factor against the block's last column in walking order (each at most 1 for decays); only the diagonal block takes an
+// exponential an element.
 //
 // Long sequences, few heads: segments, as many a sequence and head as fill the SMs.  A first kernel leaves each segment's
 // own contribution to the state (dS alone, summed in TMEM from the last chunk back, against the segment's end) and its decay; the second
 // starts each segment from the sum of those before it.
+#include <cuda.h>
+
 #include "gdn_device.cuh"
 #include "gdn_elem.cuh"
 #include "gdn_launch.cuh"
@@ -35,17 +42,20 @@ namespace {
 
 __device__ int g_la_chunk_bad, g_la_chunk_timeout;
 
-constexpr int L = 128;                 // tokens of a chunk
-constexpr int kThreads = 256;          // two warps a scheduler, so that a thread can hold half a state's row and a tile's
-constexpr int kIssuer = 128;           // issues the products: its warp has the least to do (columns 64 .. of rows 0 .. 31 of P' are zeros)
+constexpr int L = 128;         // tokens of a chunk
+constexpr int kGroup = 256;    // threads of a group
+constexpr int kThreads = 2 * kGroup;
+constexpr int kScoreIssuer = 4;  // warp of the first group that issues products: forwards it has the least to do (columns 64 .. of rows 0 .. 31 of P' are zeros)
+constexpr int kStateIssuer = 0;  // and of the second
 constexpr int kMostSegments = 16;
 constexpr uint32_t kColP = 0, kColO = 128, kColXS = 256, kColS = 384, kTmemCols = 512;
 
 struct LaChunkArgs {
+    CUtensorMap x, y, z;     // [n_tok][heads][D], boxes of 128 tokens x 1 head x 64 columns
     LaRun run;
     float *states, *decays;  // [n_seq H][segments][D D]: the state before, then each segment's contribution but the last; [n_seq H][segments]
     int segments, per;       // per sequence; chunks of one
-    int vec, vec_out;
+    int tma, vec_out;        // tma: the maps are good (rows on 16 bytes); without, threads copy element by element
 };
 
 // Bytes of shared memory.
@@ -55,89 +65,187 @@ struct Smem {
     static constexpr int x = 0, y = tile, z = 2 * tile, yh = 3 * tile, yl = 4 * tile;
     static constexpr int sh = 5 * tile, sl = sh + D * D * 2;
     static constexpr int g = sl + D * D * 2;  // five arrays of L floats, then barriers
-    static constexpr int bars = g + 5 * L * 4, sums = bars + 64, bytes = sums + 64;
-    static constexpr int z1 = sh;  // the first kernel's second Z
+    static constexpr int bars = g + 5 * L * 4, bytes = bars + 192;
+    // the first kernel's second Y and Z
+    static constexpr int y1 = sh, z1 = x;
+    // Z as operand of a product with M = 128 is read over 128 columns, whatever D
+    static constexpr int z_read = 2 * L * 128;
+    static_assert(z + z_read <= bytes && z1 + z_read <= bytes && y1 + tile <= g, "shared memory");
 };
-static_assert(Smem<128>::bytes <= kSmemPerCtaMax, "shared memory");
+static_assert(Smem<128>::bytes <= kSmemPerCtaMax && Smem<64>::bytes <= kSmemPerCtaMax, "shared memory");
+
+// mbarriers: products done and tiles loaded (one arrival each), then handovers (one arrival a warp of a group)
+enum { kBarP, kBarXS, kBarS, kBarO, kLoadX, kLoadY, kLoadZ, kSingle, kFullXY = kSingle, kFullG, kFullZ, kFullS, kFreeXS, kFreeG, kBars };
 
 struct Gates {
-    float *hi, *lo, *e, *w, *c;  // G; e^G; e^(G_last - G); e^(G of the block's last column - G)
+    float *hi, *lo, *e, *w, *c;  // G in powers of two; e^G; e^(G_last - G); e^(G of the block's last column - G)
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Where the walk's token i lies, and how far the next one.
-struct Walk {
-    long long first;
-    int step;
-    __device__ __forceinline__ long long row(long long i) const { return first + step * i; }
-};
-
-// Rows i0 .. i0 + 127 of the walk, those from n on as zeros.  A warp's 32 units of 16 bytes are 8 rows of 4: 64 bytes
-// of each row from memory, whole core matrices to shared memory (no bank twice).
-template <int D>
-__device__ __forceinline__ void load_tile(char* sm, int tile, const __nv_bfloat16* src, long long stride, const Walk& w, long long i0, int n, bool vec)
-{
-    const int tid = threadIdx.x;
-#pragma unroll
-    for (int u0 = 0; u0 < L * D / 8; u0 += 256) {
-        const int u = u0 + tid, r = (u & 7) + 8 * ((u >> 3) / (D / 8)), kc = (u >> 3) % (D / 8);
-        const bool real = r < n;
-        const __nv_bfloat16* from = src + w.row(real ? i0 + r : i0) * stride + 8 * kc;
-        const int at = tile + (u >> 3) * 128 + (u & 7) * 16;
-        if (vec) cp_async16(tc::smem_addr(sm + at), from, real);
-        else {
-            Pack<__nv_bfloat16, 8> p;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p.x[e] = real ? from[e] : __float2bfloat16(0.f);
-            *reinterpret_cast<uint4*>(sm + at) = *reinterpret_cast<const uint4*>(&p);
+// What a CTA shares beside its tiles.
+struct Shared {
+    uint64_t* bars;
+    long long* sums;  // 4
+    int* nans;        // 4
+    uint32_t* tmem;
+    volatile int* failed;
+    __device__ __forceinline__ explicit Shared(char* at)
+        : bars((uint64_t*)at), sums((long long*)(at + 128)), nans((int*)(at + 160)), tmem((uint32_t*)(at + 176)), failed((volatile int*)(at + 180)) {}
+    // Until the barrier's phase is complete; gives up as tc::mbar_wait does, and at once after another wait has given up:
+    // what follows then works on what it finds, which is nobody's result, and the kernel ends.
+    __device__ __forceinline__ void wait(int bar, uint32_t phase) const
+    {
+        const uint32_t a = tc::smem_addr(bars + bar);
+        uint64_t start = 0;
+        for (uint32_t it = 0;; ++it) {
+            uint32_t done;
+            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                         : "=r"(done)
+                         : "r"(a), "r"(phase & 1)
+                         : "memory");
+            if (done) return;
+            if ((it & 63) == 0) {
+                if (*failed) return;
+                const uint64_t now = tc::global_ns();
+                if (it == 0) start = now;
+                else if (now - start > tc::kWaitLimitNs) {
+                    *failed = 1;
+                    return;
+                }
+            }
         }
+    }
+    // One arrival of this warp, behind all its lanes.
+    __device__ __forceinline__ void arrive(int bar) const
+    {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bars + bar);
+    }
+};
+
+// One lane of a whole warp, chosen so that the compiler knows that it is one: products issued by it take
+// 68 cycles each, the tensor cores' own rate, where operands fetched from any one lane take up to 90.
+__device__ __forceinline__ bool elect()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+// This warp's number, as a number of the whole warp.
+__device__ __forceinline__ int warp_of(int tid) { return __shfl_sync(kFull, tid >> 5, 0); }
+
+template <int ID>
+__device__ __forceinline__ void group_barrier()
+{
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(kGroup) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Two fp32 numbers as bf16 hi and lo words (the first in the low halves).
+__device__ __forceinline__ void split2(f2 x, uint32_t& hi, uint32_t& lo)
+{
+    const float2 v = unpack2(x);
+    hi = tc::pack_bf16x2(v.x, v.y);
+    const float2 r = unpack2(add2(x, pack2(__uint_as_float((hi << 16) ^ 0x80000000u), __uint_as_float((hi & 0xffff0000u) ^ 0x80000000u))));
+    lo = tc::pack_bf16x2(r.x, r.y);
+}
+
+// A tile's rows in 128-byte swizzle: 64 columns a row, the next 64 columns 16 KB further.
+__device__ __forceinline__ int swizzled(int row, int kc) { return (kc >> 3) * (L * 128) + row * 128 + (((kc & 7) ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int column, int head, int token, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(map), "r"(column), "r"(head), "r"(token), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, int column, int head, int token)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map), "r"(column), "r"(head), "r"(token) : "memory");
+}
+// By one thread: 128 tokens from `token` on (rows outside the tensor read as zeros), and later ones into L2.
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int head, long long token, uint64_t* bar)
+{
+    tc::mbar_expect_tx(bar, L * D * 2);
+#pragma unroll
+    for (int c = 0; c < D; c += 64) tma_tile(dst + c * (L * 2), map, c, head, (int)token, tc::smem_addr(bar));
+}
+template <int D>
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int head, long long token)
+{
+    if (token < 0) return;
+#pragma unroll
+    for (int c = 0; c < D; c += 64) tma_prefetch(map, c, head, (int)token);
+}
+
+// The tile's rows [lo, hi) by T threads, element by element, and the others as zeros; or (copy false) the others alone.
+template <int D, int T>
+__device__ __forceinline__ void fill_tile(char* tile, const __nv_bfloat16* src, long long stride, long long token, int lo, int hi, bool copy, int tid)
+{
+#pragma unroll 1
+    for (int u = tid; u < L * D / 8; u += T) {
+        const int r = u / (D / 8), kc = u % (D / 8);
+        const bool real = r >= lo && r < hi;
+        if (real && !copy) continue;
+        Pack<__nv_bfloat16, 8> p;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p.x[e] = real ? src[(token + r) * stride + 8 * kc + e] : __float2bfloat16(0.f);
+        *reinterpret_cast<uint4*>(tile + swizzled(r, kc)) = *reinterpret_cast<const uint4*>(&p);
     }
 }
 
-// The gate before the walk's token i enters (0 where there is none: rows from n on, and backwards the first).
-__device__ __forceinline__ double load_gate(const LaRun& A, const Walk& w, int h, long long i, bool real)
+// Log decays in fixed point: powers of two with 31 fraction bits.
+constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;
+__device__ __forceinline__ long long to_fixed(float gate)
 {
-    if (!real || (A.reverse && i == 0)) return 0.0;
-    const float g = ld_any(A.g, (w.row(i) + A.reverse) * A.gs0 + h * A.gs1, A.gate_dtype);
-    return g < kLaLeastGate ? (double)kLaLeastGate : (double)g;
+    const float hi = gate * kLog2eHi, lo = fmaf(gate, kLog2eHi, -hi) + gate * kLog2eLo;
+    const float whole = rintf(hi);
+    return ((long long)__float2int_rn(whole) << 31) + (long long)__float2int_rn(((hi - whole) + lo) * 2147483648.f);
+}
+__device__ __forceinline__ float whole_of(long long x) { return (float)(int)(x >> 31); }
+__device__ __forceinline__ float fraction_of(long long x) { return (float)(int)(x & 0x7fffffff) * 4.65661287e-10f; }
+__device__ __forceinline__ float from_fixed(long long x) { return whole_of(x) + fraction_of(x); }
+
+// The gate before the token at `row` enters (0 where there is none: rows that are not real, and backwards behind the last).
+__device__ __forceinline__ float load_gate(const LaRun& A, const LaSequence& q, int h, long long row, bool real)
+{
+    if (!real || (A.reverse && row + 1 >= q.hi)) return 0.f;
+    const float g = ld_any(A.g, (row + A.reverse) * A.gs0 + h * A.gs1, A.gate_dtype);
+    return g < kLaLeastGate ? kLaLeastGate : g;
 }
 
-// Inclusive sums over the first 128 threads, by warps; the sums of the warps before come from shared memory behind a barrier.
-__device__ __forceinline__ double scan_warp(double x, int lane)
+// Inclusive sums over a warp, and whether a NaN is among what was summed.
+__device__ __forceinline__ long long scan_warp(float gate, int lane, bool* nan)
 {
+    *nan = (__ballot_sync(kFull, gate != gate) & (0xffffffffu >> (31 - lane))) != 0;
+    long long x = gate == gate ? to_fixed(gate) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(kFull, x, o);
+        const long long y = __shfl_up_sync(kFull, x, o);
         if (lane >= o) x += y;
     }
     return x;
 }
 
-// Y' = w Y as bf16 hi and lo: units of 16 bytes, each lane 8 columns of one token.
-template <int D>
-__device__ __forceinline__ void decayed_keys(char* sm, int y, int yh, int yl, const float* w)
+// Y' = w Y as bf16 hi and lo, by T threads: units of 16 bytes, each lane 8 columns of one token.  Y' lies in core matrices of 8 tokens x 8
+// columns: a warp's 32 units are 8 tokens of 4, whole core matrices (no bank twice on either side).
+template <int D, int T>
+__device__ __forceinline__ void decayed_keys(char* sm, int y, int yh, int yl, const float* w, int tid)
 {
-    const int tid = threadIdx.x;
 #pragma unroll 4
-    for (int u0 = 0; u0 < L * D / 8; u0 += 256) {
-        const int u = u0 + tid, r = (u & 7) + 8 * ((u >> 3) / (D / 8)), at = (u >> 3) * 128 + (u & 7) * 16;
-        const uint4 v = *reinterpret_cast<const uint4*>(sm + y + at);
-        const f2 ww = pack2(w[r], w[r]);
+    for (int u0 = 0; u0 < L * D / 8; u0 += T) {
+        const int u = u0 + tid, kc = (u >> 3) % (D / 8), r = (u & 7) + 8 * ((u >> 3) / (D / 8)), at = (u >> 3) * 128 + (u & 7) * 16;
+        const uint4 v = *reinterpret_cast<const uint4*>(sm + y + swizzled(r, kc));
+        const float wr = w[r];
+        const f2 ww = pack2(wr, wr);
         uint4 hi, lo;
-        auto part = [&](uint32_t x, uint32_t& h, uint32_t& l) {
-            const float2 p = unpack2(mul2(pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), ww));
-            tc::split_bf16x2(p.x, p.y, h, l);
-        };
+        auto part = [&](uint32_t x, uint32_t& h, uint32_t& l) { split2(mul2(pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), ww), h, l); };
         part(v.x, hi.x, lo.x);
         part(v.y, hi.y, lo.y);
         part(v.z, hi.z, lo.z);
@@ -147,51 +255,75 @@ __device__ __forceinline__ void decayed_keys(char* sm, int y, int yh, int yl, co
     }
 }
 
-// Products, by one thread.  K-major: rows of the tile are M or N, columns K; MN-major: columns are M or N, rows K.
+// Operands in shared memory.  Of tiles in 128-byte swizzle: K-major (tokens are M or N; 32 bytes a slice of 16 columns, 16 KB every 64)
+// and MN-major (columns are M or N; 16 rows a slice).  Of Y' and S, in core matrices: MN-major and K-major.
+constexpr uint64_t kSwizzle128 = 2ull << 61;
+__device__ __forceinline__ uint64_t swizzled_k(uint32_t tile) { return tc::make_desc(tile, 16, 1024) | kSwizzle128; }
+__device__ __forceinline__ uint64_t swizzled_mn(uint32_t tile) { return tc::make_desc(tile, L * 128, 1024) | kSwizzle128; }
+__device__ __forceinline__ uint64_t step_k(int s) { return (uint64_t)((s >> 2) * (L * 128) + (s & 3) * 32) >> 4; }
+__device__ __forceinline__ uint64_t step_mn(int s) { return (uint64_t)(s * 2048) >> 4; }
 template <int D>
-__device__ __forceinline__ uint64_t k_major(uint32_t tile, int slice) { return tc::make_desc(tile + slice * 256, 128, D * 16); }
+__device__ __forceinline__ uint64_t cores_k(uint32_t tile) { return tc::make_desc(tile, 128, D * 16); }
 template <int D>
-__device__ __forceinline__ uint64_t mn_major(uint32_t tile, int slice) { return tc::make_desc(tile + slice * D * 32, D * 16, 128); }
+__device__ __forceinline__ uint64_t cores_mn(uint32_t tile) { return tc::make_desc(tile, D * 16, 128); }
 constexpr uint32_t kTransposedA = 1u << 15, kTransposedB = 1u << 16;
 
-// dS (+)= Z^T Y'; slices of 16 tokens
+// dS (+)= Z^T Y'.  M is 128 for D = 64 too: rows 64 .. 127 read what follows Z in shared memory (Smem::z_read) and are nobody's.
 template <int D>
-__device__ __forceinline__ void issue_state(uint32_t tmem, uint32_t z, uint32_t yh, uint32_t yl, int slices, bool accumulate)
+__device__ __forceinline__ void issue_state(uint32_t tmem, uint32_t z, uint32_t yh, uint32_t yl, bool accumulate)
 {
     constexpr uint32_t idesc = tc::idesc_bf16(D) | kTransposedA | kTransposedB;
-    for (int s = 0; s < slices; ++s) {
-        const uint64_t a = mn_major<D>(z, s);
-        tc::mma_ss16(tmem + kColS, a, mn_major<D>(yh, s), idesc, accumulate || s > 0);
-        tc::mma_ss16(tmem + kColS, a, mn_major<D>(yl, s), idesc, 1);
+    const uint64_t a = swizzled_mn(z), bh = cores_mn<D>(yh), bl = cores_mn<D>(yl);
+#pragma unroll
+    for (int s = 0; s < L / 16; ++s) {
+        tc::mma_ss16(tmem + kColS, a + step_mn(s), bh + s * D * 2, idesc, accumulate || s > 0);
+        tc::mma_ss16(tmem + kColS, a + step_mn(s), bl + s * D * 2, idesc, 1);
     }
 }
-
-__device__ __forceinline__ float exp_diff2(float ah, float al, float bh, float bl) { return expf((ah - bh) + (al - bl)); }
-
-template <int N>
-__device__ __forceinline__ void ld_cols(uint32_t at, float (&v)[N])
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t tmem, uint32_t x, uint32_t y)
 {
-    static_assert(N % 32 == 0, "columns");
+    const uint64_t a = swizzled_k(x), b = swizzled_k(y);
 #pragma unroll
-    for (int i = 0; i < N; i += 32) tc::ld32(at + i, *reinterpret_cast<float(*)[32]>(v + i));
+    for (int s = 0; s < D / 16; ++s) tc::mma_ss16(tmem + kColP, a + step_k(s), b + step_k(s), tc::idesc_bf16(L), s > 0);
+}
+template <int D>
+__device__ __forceinline__ void issue_state_output(uint32_t tmem, uint32_t x, uint32_t sh, uint32_t sl)
+{
+    const uint64_t a = swizzled_k(x), bh = cores_k<D>(sh), bl = cores_k<D>(sl);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+        tc::mma_ss16(tmem + kColXS, a + step_k(s), bh + 16 * s, tc::idesc_bf16(D), s > 0);
+        tc::mma_ss16(tmem + kColXS, a + step_k(s), bl + 16 * s, tc::idesc_bf16(D), 1);
+    }
+}
+// O = P' Z; of every 32 columns of P, 16 hold hi words and 16 lo words.
+template <int D>
+__device__ __forceinline__ void issue_output(uint32_t tmem, uint32_t z)
+{
+    constexpr uint32_t idesc = tc::idesc_bf16(D) | kTransposedB;
+    const uint64_t b = swizzled_mn(z);
+#pragma unroll
+    for (int s = 0; s < L / 16; ++s) {
+        const uint32_t a = tmem + kColP + 32 * (s >> 1) + 8 * (s & 1);
+        tc::mma_ts16(tmem + kColO, a, b + step_mn(s), idesc, s > 0);
+        tc::mma_ts16(tmem + kColO, a + 16, b + step_mn(s), idesc, 1);
+    }
 }
 
 // What both kernels begin with: barriers and tensor memory.
-template <int BARS>
-__device__ __forceinline__ uint32_t begin(uint64_t* bars)
+__device__ __forceinline__ uint32_t begin(const Shared& sh)
 {
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 6);
-    int* err = reinterpret_cast<int*>(bars + 7);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < BARS; ++i) tc::mbar_init(bars + i, 1);
+        for (int i = 0; i < kBars; ++i) tc::mbar_init(sh.bars + i, i < kSingle ? 1 : kGroup / 32);
         tc::mbar_fence_init();
-        *err = 0;
+        *sh.failed = 0;
     }
-    if (threadIdx.x < 32) tc::tmem_alloc(holder, kTmemCols);
+    if (threadIdx.x < 32) tc::tmem_alloc(sh.tmem, kTmemCols);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    return *holder;
+    return *sh.tmem;
 }
 
 __device__ __forceinline__ float* state_of(const LaChunkArgs& A, int D, int nh, int segment)
@@ -205,7 +337,13 @@ __device__ __forceinline__ void load_state(float (&m)[N], const float* head, int
 {
     if (!transposed) {
 #pragma unroll
-        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(m + i) = *reinterpret_cast<const float4*>(head + j * D + c0 + i);
+        for (int i = 0; i < N; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(head + j * D + c0 + i);
+            m[i] = v.x;
+            m[i + 1] = v.y;
+            m[i + 2] = v.z;
+            m[i + 3] = v.w;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) m[i] = head[(c0 + i) * D + j];
@@ -216,14 +354,14 @@ __device__ __forceinline__ void store_state(const float (&m)[N], float* head, in
 {
     if (!transposed) {
 #pragma unroll
-        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(head + j * D + c0 + i) = *reinterpret_cast<const float4*>(m + i);
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(head + j * D + c0 + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) head[(c0 + i) * D + j] = m[i];
     }
 }
 
-// The chunks [c0, c1) of segment `segment` of a sequence of `len` tokens; last: no segment follows.
+// The chunks [c0, c1) of segment `segment` of a sequence, in walking order; last: no segment follows.
 struct Part {
     long long c0, c1;
     bool none, last;
@@ -239,102 +377,151 @@ __device__ __forceinline__ Part part_of(const LaChunkArgs& A, long long len, int
     return p;
 }
 
+// What a CTA works on.
+struct Work {
+    LaSequence q;
+    Part part;
+    uint32_t tmem;
+    int h, nh, segment, count;
+    bool reverse;
+    // Of the segment's chunk i: the token of its row 0, and its real rows [lo, hi).  Backwards, chunks are cut from
+    // the sequence's end, rows stay in the tokens' order.
+    __device__ __forceinline__ long long token(int i) const
+    {
+        const long long at = (part.c0 + i) * L;
+        return reverse ? q.hi - L - at : q.lo + at;
+    }
+    __device__ __forceinline__ int lo(int i) const
+    {
+        const long long t = token(i);
+        return t < q.lo ? (int)(q.lo - t) : 0;
+    }
+    __device__ __forceinline__ int hi(int i) const
+    {
+        const long long left = q.hi - token(i);
+        return left < L ? (int)left : L;
+    }
+};
+
+__device__ __forceinline__ const __nv_bfloat16* head_of(const void* p, int h, int heads, long long stride)
+{
+    return (const __nv_bfloat16*)p + (h % heads) * stride;
+}
+
 // Segment contributions: segments - 1 CTAs a sequence and head.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const LaChunkArgs A)
+__global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_constant__ LaChunkArgs A)
 {
     using S = Smem<D>;
-    extern __shared__ __align__(128) char sm[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::bars);
-    double* sums = reinterpret_cast<double*>(sm + S::sums);
+    extern __shared__ __align__(1024) char sm[];
+    const Shared sh(sm + S::bars);
     float* sw = reinterpret_cast<float*>(sm + S::g);
-    volatile int& s_err = *reinterpret_cast<int*>(bars + 7);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per_seq = A.segments - 1, nh = blockIdx.x / per_seq, segment = blockIdx.x - nh * per_seq;
-    const int n = nh / A.run.H, h = nh - n * A.run.H;
+    const int tid = threadIdx.x, lane = tid & 31, warp = warp_of(tid);
+    const int per_seq = A.segments - 1;
+    Work W;
+    W.nh = blockIdx.x / per_seq;
+    W.segment = blockIdx.x - W.nh * per_seq;
+    const int n = W.nh / A.run.H;
+    W.h = W.nh - n * A.run.H;
+    W.reverse = A.run.reverse;
     begin_after();
-    const LaSequence q = la_sequence(A.run, n);
-    if (!q.ok) return;  // the second kernel reports it
-    const long long len = q.hi - q.lo;
-    const Part part = part_of(A, len, segment);
-    if (part.none || part.last) return;
-    const Walk w = {A.run.reverse ? q.hi - 1 : q.lo, A.run.reverse ? -1 : 1};
-    const uint32_t tmem = begin<1>(bars);
-    const __nv_bfloat16* y = (const __nv_bfloat16*)A.run.y + (h % A.run.yh) * A.run.ys1;
-    const __nv_bfloat16* z = (const __nv_bfloat16*)A.run.z + (h % A.run.zh) * A.run.zs1;
-    const uint32_t base = tc::smem_addr(sm);
-    const int zt[2] = {S::z, S::z1};
-    double carry = 0.0;
-    const long long count = part.c1 - part.c0;
-    bool fine = true;
-    load_tile<D>(sm, S::y, y, A.run.ys0, w, (part.c1 - 1) * L, L, A.vec);
-    load_tile<D>(sm, zt[0], z, A.run.zs0, w, (part.c1 - 1) * L, L, A.vec);
-    cp_commit();
-    for (long long it = 0; it < count; ++it) {
-        const long long c = part.c1 - 1 - it;  // whole chunks: the sequence's last one is the last segment's
-        double G = 0.0;
-        if (tid < L) {
-            G = scan_warp(load_gate(A.run, w, h, c * L + tid, true), lane);
-            if (lane == 31) sums[warp] = G;
-        }
-        cp_wait<0>();
-        __syncthreads();
-        if (tid < L) {
-            double all = 0.0;
-            for (int i = 0; i < 4; ++i) {
-                if (i < warp) G += sums[i];
-                all += sums[i];
+    W.q = la_sequence(A.run, n);
+    if (!W.q.ok) return;  // the second kernel reports it
+    W.part = part_of(A, W.q.hi - W.q.lo, W.segment);
+    if (W.part.none || W.part.last) return;
+    const uint32_t tmem = begin(sh), base = tc::smem_addr(sm);
+    const int count = (int)(W.part.c1 - W.part.c0), yh = W.h % A.run.yh, zh = W.h % A.run.zh;
+    auto y_tile = [](int it) { return it & 1 ? S::y1 : S::y; };
+    auto z_tile = [](int it) { return it & 1 ? S::z1 : S::z; };
+    // a barrier a buffer, since a load is under way while the one before it may not have arrived
+    auto y_bar = [](int it) { return it & 1 ? kLoadX : kLoadY; };
+    auto z_bar = [](int it) { return it & 1 ? kBarP : kLoadZ; };
+    // whole chunks, from the last one back: the sequence's last one is the last segment's
+    auto load = [&](int it) {
+        const int i = count - 1 - it;
+        if (!A.tma) {
+            fill_tile<D, kThreads>(sm + y_tile(it), head_of(A.run.y, W.h, A.run.yh, A.run.ys1), A.run.ys0, W.token(i), 0, L, true, tid);
+            fill_tile<D, kThreads>(sm + z_tile(it), head_of(A.run.z, W.h, A.run.zh, A.run.zs1), A.run.zs0, W.token(i), 0, L, true, tid);
+        } else if (warp == 0 && elect()) {
+            load_tile<D>(base + y_tile(it), &A.y, yh, W.token(i), sh.bars + y_bar(it));
+            load_tile<D>(base + z_tile(it), &A.z, zh, W.token(i), sh.bars + z_bar(it));
+            if (i > 0) {
+                prefetch_tile<D>(&A.y, yh, W.token(i - 1));
+                prefetch_tile<D>(&A.z, zh, W.token(i - 1));
             }
-            sw[tid] = expf((float)(carry + (all - G)));
         }
-        for (int i = 0; i < 4; ++i) carry += sums[i];
-        if (it > 0 && !tc::mbar_wait(bars, (uint32_t)(it - 1) & 1)) s_err = 1;  // the product before has read Y'
+    };
+    const int r = W.reverse ? L - 1 - tid : tid;  // threads in walking order
+    auto gate = [&](int it) { return tid < L && it < count ? load_gate(A.run, W.q, W.h, W.token(count - 1 - it) + r, true) : 0.f; };
+    long long carry = 0;
+    bool nan = false;  // among the gates behind
+    load(0);
+    float next = gate(0);
+    for (int it = 0; it < count; ++it) {
+        long long G = 0;
+        bool bad = false;
+        if (tid < L) {
+            G = scan_warp(next, lane, &bad);
+            if (lane == 31) {
+                sh.sums[warp] = G;
+                sh.nans[warp] = bad;
+            }
+        }
+        next = gate(it + 1);
+        if (it > 0) sh.wait(kBarS, it - 1);  // the product before has read Y' and the other buffers
         __syncthreads();
-        if (s_err) {
-            fine = false;
-            break;
+        if (it + 1 < count) load(it + 1);
+        long long all = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            if (b < warp) G += sh.sums[b];
+            all += sh.sums[b];
+            nan |= sh.nans[b] != 0;
         }
-        decayed_keys<D>(sm, S::y, S::yh, S::yl, sw);
+        if (tid < L) sw[r] = nan ? NAN : ex2(from_fixed(carry + (all - G)));
+        carry += all;
+        if (A.tma) {
+            sh.wait(y_bar(it), it >> 1);
+            sh.wait(z_bar(it), it >> 1);
+        }
+        __syncthreads();
+        decayed_keys<D, kThreads>(sm, y_tile(it), S::yh, S::yl, sw, tid);
         tc::fence_async_smem();
         __syncthreads();
-        if (it + 1 < count) {
-            load_tile<D>(sm, S::y, y, A.run.ys0, w, (c - 1) * L, L, A.vec);
-            load_tile<D>(sm, zt[(it + 1) & 1], z, A.run.zs0, w, (c - 1) * L, L, A.vec);
-            cp_commit();
-        }
-        if (tid == kIssuer) {
+        if (warp == 0 && elect()) {
             tc::fence_after();
-            issue_state<D>(tmem, base + zt[it & 1], base + S::yh, base + S::yl, L / 16, it > 0);
-            tc::commit(bars);
+            issue_state<D>(tmem, base + z_tile(it), base + S::yh, base + S::yl, it > 0);
+            tc::commit(sh.bars + kBarS);
         }
     }
-    cp_wait<0>();
-    if (fine && !tc::mbar_wait(bars, (uint32_t)(count - 1) & 1)) s_err = 1;
+    sh.wait(kBarS, count - 1);
     __syncthreads();
-    if (s_err) {
+    if (*sh.failed) {
         if (tid == 0) atomicOr(&g_la_chunk_timeout, 1);
     } else {
         tc::fence_after();
-        const int j = 32 * (warp & 3) + lane, half = warp >> 2;
-        float d[D / 2];
-        ld_cols(tc::taddr(tmem, warp, kColS) + half * (D / 2), d);
+        constexpr int C = D / 4;  // columns of a thread
+        const int j = 32 * (warp & 3) + lane, c0 = (warp >> 2) * C;
+        float d[C];
+        if constexpr (C == 32) tc::ld32(tc::taddr(tmem, warp, kColS) + c0, d);
+        else tc::ld16(tc::taddr(tmem, warp, kColS) + c0, d);
         tc::wait_ld();
         if (j < D) {
+            const float all = nan ? NAN : ex2(from_fixed(carry));
 #pragma unroll
-            for (int i = 0; i < D / 2; ++i) d[i] *= A.run.cs;
-            const float all = expf((float)carry);
-            if (segment == 0) {
+            for (int i = 0; i < C; ++i) d[i] *= A.run.cs;
+            if (W.segment == 0) {
                 // the state before it, kept for the segment's own start too (the last segment may replace it in place)
-                float m[D / 2];
+                float m[C];
 #pragma unroll
-                for (int i = 0; i < D / 2; ++i) m[i] = 0.f;
-                if (q.in >= 0) load_state<D>(m, A.run.s_in + q.in * A.run.in_stride + (long long)h * D * D, j, half * (D / 2), A.run.transposed_in);
-                store_state<D>(m, state_of(A, D, nh, 0), j, half * (D / 2), false);
+                for (int i = 0; i < C; ++i) m[i] = 0.f;
+                if (W.q.in >= 0) load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, j, c0, A.run.transposed_in);
+                store_state<D>(m, state_of(A, D, W.nh, 0), j, c0, false);
 #pragma unroll
-                for (int i = 0; i < D / 2; ++i) d[i] = fmaf(all, m[i], d[i]);
+                for (int i = 0; i < C; ++i) d[i] = fmaf(all, m[i], d[i]);
             }
-            store_state<D>(d, state_of(A, D, nh, segment + 1), j, half * (D / 2), false);
-            if (tid == 0) A.decays[nh * A.segments + segment + 1] = all;
+            store_state<D>(d, state_of(A, D, W.nh, W.segment + 1), j, c0, false);
+            if (tid == 0) A.decays[W.nh * A.segments + W.segment + 1] = all;
         }
     }
     tc::fence_before();
@@ -342,244 +529,363 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const LaChunkAr
     if (warp == 0) tc::tmem_free(tmem, kTmemCols);
 }
 
+// 32 consecutive bytes.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                 "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// The first group: P' and the output.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const LaChunkArgs A)
+__device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char* sm, const Shared& sh, const Gates& g)
 {
     using S = Smem<D>;
-    constexpr int H = D / 2;  // columns of a thread
-    extern __shared__ __align__(128) char sm[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::bars);
-    uint64_t *bar_p = bars, *bar_xs = bars + 1, *bar_s = bars + 2, *bar_o = bars + 3;
-    double* sums = reinterpret_cast<double*>(sm + S::sums);
-    float* g0 = reinterpret_cast<float*>(sm + S::g);
-    const Gates g = {g0, g0 + L, g0 + 2 * L, g0 + 3 * L, g0 + 4 * L};
-    volatile int& s_err = *reinterpret_cast<int*>(bars + 7);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nh = blockIdx.x / A.segments, segment = blockIdx.x - nh * A.segments;
-    const int n = nh / A.run.H, h = nh - n * A.run.H;
-    begin_after();
-    const LaSequence q = la_sequence(A.run, n);
-    if (!q.ok) {
-        if (tid == 0) atomicOr(&g_la_chunk_bad, 1);
-        return;
-    }
-    const long long len = q.hi - q.lo;
-    const Part part = part_of(A, len, segment);
-    if (part.none) return;
-    const Walk w = {A.run.reverse ? q.hi - 1 : q.lo, A.run.reverse ? -1 : 1};
-    const uint32_t tmem = begin<4>(bars);
-    const __nv_bfloat16* x = (const __nv_bfloat16*)A.run.x + (h % A.run.xh) * A.run.xs1;
-    const __nv_bfloat16* y = (const __nv_bfloat16*)A.run.y + (h % A.run.yh) * A.run.ys1;
-    const __nv_bfloat16* z = (const __nv_bfloat16*)A.run.z + (h % A.run.zh) * A.run.zs1;
-    const uint32_t base = tc::smem_addr(sm);
-    const bool vec = A.vec;
-    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;  // of TMEM: a chunk's token, or a state's row
-    const bool has_state = row < D;
-    auto tokens = [&](long long c) { return (int)(len - c * L < L ? len - c * L : L); };
+    constexpr int H = D / 2;  // columns of a thread's output
+    const int tid = threadIdx.x, lane = tid & 31, warp = warp_of(tid), quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+    const uint32_t base = tc::smem_addr(sm), lanes = tc::taddr(W.tmem, warp, 0);
+    const int xh = W.h % A.run.xh, zh = W.h % A.run.zh;
+    float c2 = 0.f;  // co e^G of this row, of the chunk whose output is next
+    const float c1 = A.run.co * A.run.cs;
 
-    if (part.c0 < part.c1) {
-        const int nt = tokens(part.c0);
-        load_tile<D>(sm, S::x, x, A.run.xs0, w, part.c0 * L, nt, vec);
-        load_tile<D>(sm, S::y, y, A.run.ys0, w, part.c0 * L, nt, vec);
-        cp_commit();
-        load_tile<D>(sm, S::z, z, A.run.zs0, w, part.c0 * L, nt, vec);
-        cp_commit();
+    auto output = [&](int i) {
+        sh.wait(kBarO, i);
+        sh.wait(kBarXS, i);
+        tc::fence_after();
+        const bool real = row >= W.lo(i) && row < W.hi(i);
+        const long long at = ((W.token(i) + row) * A.run.H + W.h) * D + half * H;
+#pragma unroll 1
+        for (int c = 0; c < H; c += 32) {
+            float o[32], xs[32];
+            tc::ld32(lanes + kColO + half * H + c, o);
+            tc::ld32(lanes + kColXS + half * H + c, xs);
+            tc::wait_ld();
+            if (real) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = fmaf(c2, xs[e], c1 * o[e]);
+                if (A.vec_out && A.run.out_dtype == GDN_BF16) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = tc::pack_bf16x2(o[e + 2 * k], o[e + 2 * k + 1]);
+                        st_global32((__nv_bfloat16*)A.run.out + at + c + e, v);
+                    }
+                } else if (A.vec_out && A.run.out_dtype == GDN_F32) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[e + k]);
+                        st_global32((float*)A.run.out + at + c + e, v);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) st_any(A.run.out, at + c + e, A.run.out_dtype, o[e]);
+                }
+            }
+        }
+        tc::fence_before();
+        sh.arrive(kFreeXS);
+    };
+    auto load_x = [&](int i) {
+        load_tile<D>(base + S::x, &A.x, xh, W.token(i), sh.bars + kLoadX);
+        if (i + 1 < W.count) prefetch_tile<D>(&A.x, xh, W.token(i + 1));
+    };
+    auto load_z = [&](int i) {
+        load_tile<D>(base + S::z, &A.z, zh, W.token(i), sh.bars + kLoadZ);
+        if (i + 1 < W.count) prefetch_tile<D>(&A.z, zh, W.token(i + 1));
+    };
+    if (warp == kScoreIssuer && A.tma && W.count > 0 && elect()) {
+        load_x(0);
+        load_z(0);
     }
+
+    for (int i = 0; i < W.count; ++i) {
+        if (warp == kScoreIssuer) {
+            if (i > 0) {  // P' and Z have been read
+                sh.wait(kBarO, i - 1);
+                if (A.tma) {
+                    sh.wait(kBarS, i - 1);
+                    if (elect()) load_z(i);
+                }
+            }
+            sh.wait(kFullXY, i);
+            tc::fence_after();
+            if (elect()) {
+                issue_scores<D>(W.tmem, base + S::x, base + S::y);
+                tc::commit(sh.bars + kBarP);
+            }
+        }
+        if (i > 0) output(i - 1);
+        if (warp == kScoreIssuer) {
+            if (i > 0) sh.wait(kFreeXS, i - 1);
+            sh.wait(kFullS, i);
+            tc::fence_after();
+            if (elect()) {
+                issue_state_output<D>(W.tmem, base + S::x, base + S::sh, base + S::sl);
+                tc::commit(sh.bars + kBarXS);
+            }
+        }
+        sh.wait(kFullG, i);
+        const float gh = g.hi[row], gl = g.lo[row];
+        c2 = A.run.co * g.e[row];
+        sh.wait(kBarP, i);
+        tc::fence_after();
+        // P' in the place of P: every 32 columns become 16 of hi words and 16 of lo words
+#pragma unroll 1
+        for (int b = 2 * half; b < 2 * half + 2; ++b) {
+            uint32_t ph[16], pl[16];
+            if (W.reverse ? b < quarter : b > quarter) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ph[e] = pl[e] = 0u;
+            } else {
+                float p[32];
+                tc::ld32(lanes + kColP + 32 * b, p);
+                if (b != quarter) {
+                    const int last = W.reverse ? 32 * b : 32 * b + 31;
+                    const float rf = ex2((gh - g.hi[last]) + (gl - g.lo[last]));
+                    const f2 rr = pack2(rf, rf);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(g.c + 32 * b + e);
+                        split2(mul2(pack2(p[e], p[e + 1]), mul2(rr, c.x)), ph[e / 2], pl[e / 2]);
+                        split2(mul2(pack2(p[e + 2], p[e + 3]), mul2(rr, c.y)), ph[e / 2 + 1], pl[e / 2 + 1]);
+                    }
+                } else {
+                    // columns that the walk has met: the lanes below and this one, or this one and those above
+                    const uint32_t met = W.reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 uh = *reinterpret_cast<const float2*>(g.hi + 32 * b + e), ul = *reinterpret_cast<const float2*>(g.lo + 32 * b + e);
+                        const float x0 = met >> e & 1 ? p[e] * ex2((gh - uh.x) + (gl - ul.x)) : 0.f;
+                        const float x1 = met >> (e + 1) & 1 ? p[e + 1] * ex2((gh - uh.y) + (gl - ul.y)) : 0.f;
+                        split2(pack2(x0, x1), ph[e / 2], pl[e / 2]);
+                    }
+                }
+            }
+            tc::st16(lanes + kColP + 32 * b, ph);
+            tc::st16(lanes + kColP + 32 * b + 16, pl);
+        }
+        tc::wait_st();
+        tc::fence_before();
+        sh.arrive(kFreeG);
+        group_barrier<1>();
+        if (warp == kScoreIssuer) {
+            sh.wait(kFullZ, i);
+            tc::fence_after();
+            if (elect()) {
+                issue_output<D>(W.tmem, base + S::z);
+                tc::commit(sh.bars + kBarO);
+            }
+            if (A.tma && i + 1 < W.count) {
+                sh.wait(kBarXS, i);
+                sh.wait(kBarP, i);
+                if (elect()) load_x(i + 1);
+            }
+        }
+    }
+    if (W.count > 0) output(W.count - 1);
+}
+
+// The second group: gates, Y' and the state.
+template <int D>
+__device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char* sm, const Shared& sh, const Gates& g)
+{
+    using S = Smem<D>;
+    constexpr int H = D / 2;  // columns of a thread's state row
+    const int tid = threadIdx.x - kGroup, lane = tid & 31, warp = warp_of(tid), quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+    const uint32_t base = tc::smem_addr(sm), lanes = tc::taddr(W.tmem, warp, 0);
+    const bool has_state = row < D;
+    const int yh = W.h % A.run.yh;
+    auto load_y = [&](int i) {
+        load_tile<D>(base + S::y, &A.y, yh, W.token(i), sh.bars + kLoadY);
+        if (i + 1 < W.count) prefetch_tile<D>(&A.y, yh, W.token(i + 1));
+    };
+    if (warp == kStateIssuer && A.tma && W.count > 0 && elect()) load_y(0);
+
+    // the gates of chunk i: threads in walking order
+    const int r = W.reverse ? L - 1 - tid : tid;
+    auto gate = [&](int i) { return tid < L && i < W.count ? load_gate(A.run, W.q, W.h, W.token(i) + r, r >= W.lo(i) && r < W.hi(i)) : 0.f; };
+    float next = gate(0);
+    auto sum_gates = [&](int i) {
+        long long G = 0;
+        bool nan = false;
+        if (tid < L) {
+            G = scan_warp(next, lane, &nan);
+            if (lane == 31) {
+                sh.sums[warp] = G;
+                sh.nans[warp] = nan;
+            }
+        }
+        next = gate(i + 1);
+        if (i > 0) sh.wait(kFreeG, i - 1);
+        group_barrier<2>();
+        if (tid < L) {
+            long long all = 0, before = 0;
+            bool any = false;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (b < warp) {
+                    before += sh.sums[b];
+                    nan |= sh.nans[b] != 0;
+                }
+                all += sh.sums[b];
+                any |= sh.nans[b] != 0;
+            }
+            const long long end = before + sh.sums[warp];  // of this block of 32
+            G += before;
+            g.hi[r] = nan ? NAN : whole_of(G);
+            g.lo[r] = fraction_of(G);
+            g.e[r] = nan ? NAN : ex2(from_fixed(G));
+            g.w[r] = any ? NAN : ex2(from_fixed(all - G));
+            g.c[r] = sh.nans[warp] ? NAN : ex2(from_fixed(end - G));
+        }
+        group_barrier<2>();
+        sh.arrive(kFullG);
+    };
+
     float m[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) m[i] = 0.f;
     if (has_state) {
-        if (segment > 0) {
-            for (int s = 1; s <= segment; ++s) {
-                float d[H];
-                const float a = s > 1 ? A.decays[nh * A.segments + s] : 0.f;
-                load_state<D>(d, state_of(A, D, nh, s), row, half * H, false);
+        if (W.segment > 0) {
+            for (int s = 1; s <= W.segment; ++s) {
+                const float a = s > 1 ? A.decays[W.nh * A.segments + s] : 0.f;
+                const float4* from = reinterpret_cast<const float4*>(state_of(A, D, W.nh, s) + row * D + half * H);
 #pragma unroll
-                for (int i = 0; i < H; ++i) m[i] = s > 1 ? fmaf(a, m[i], d[i]) : d[i];
+                for (int i = 0; i < H; i += 4) {
+                    const float4 d = from[i / 4];
+                    m[i] = s > 1 ? fmaf(a, m[i], d.x) : d.x;
+                    m[i + 1] = s > 1 ? fmaf(a, m[i + 1], d.y) : d.y;
+                    m[i + 2] = s > 1 ? fmaf(a, m[i + 2], d.z) : d.z;
+                    m[i + 3] = s > 1 ? fmaf(a, m[i + 3], d.w) : d.w;
+                }
             }
-        } else if (!part.last) {
-            load_state<D>(m, state_of(A, D, nh, 0), row, half * H, false);
-        } else if (q.in >= 0) {
-            load_state<D>(m, A.run.s_in + q.in * A.run.in_stride + (long long)h * D * D, row, half * H, A.run.transposed_in);
+        } else if (!W.part.last) {
+            load_state<D>(m, state_of(A, D, W.nh, 0), row, half * H, false);
+        } else if (W.q.in >= 0) {
+            load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, row, half * H, A.run.transposed_in);
         }
     }
     auto put_state = [&]() {
+        if (has_state) {
 #pragma unroll
-        for (int i = 0; i < H; i += 8) {
-            uint4 hi, lo;
-            tc::split_bf16x2(m[i], m[i + 1], hi.x, lo.x);
-            tc::split_bf16x2(m[i + 2], m[i + 3], hi.y, lo.y);
-            tc::split_bf16x2(m[i + 4], m[i + 5], hi.z, lo.z);
-            tc::split_bf16x2(m[i + 6], m[i + 7], hi.w, lo.w);
-            const int at = ((row >> 3) * (D / 8) + (half * H + i) / 8) * 128 + (row & 7) * 16;
-            *reinterpret_cast<uint4*>(sm + S::sh + at) = hi;
-            *reinterpret_cast<uint4*>(sm + S::sl + at) = lo;
+            for (int i = 0; i < H; i += 8) {
+                uint4 hi, lo;
+                split2(pack2(m[i], m[i + 1]), hi.x, lo.x);
+                split2(pack2(m[i + 2], m[i + 3]), hi.y, lo.y);
+                split2(pack2(m[i + 4], m[i + 5]), hi.z, lo.z);
+                split2(pack2(m[i + 6], m[i + 7]), hi.w, lo.w);
+                const int at = ((row >> 3) * (D / 8) + (half * H + i) / 8) * 128 + (row & 7) * 16;
+                *reinterpret_cast<uint4*>(sm + S::sh + at) = hi;
+                *reinterpret_cast<uint4*>(sm + S::sl + at) = lo;
+            }
         }
+        tc::fence_async_smem();
+        sh.arrive(kFullS);
     };
-    if (has_state) put_state();
+    if (W.count > 0) {
+        put_state();
+        sum_gates(0);
+    }
 
-    bool fine = true;
-    for (long long c = part.c0; c < part.c1; ++c) {
-        const uint32_t phase = (uint32_t)(c - part.c0) & 1;
-        const int nt = tokens(c), slices = (nt + 15) / 16, ahead = c + 1 < part.c1 ? tokens(c + 1) : 0;
-        double G = 0.0;
-        cp_wait<1>();  // X and Y
+    for (int i = 0; i < W.count; ++i) {
+        const bool more = i + 1 < W.count;
+        const int lo = W.lo(i), hi = W.hi(i);
+        const bool cut = lo > 0 || hi < L;  // rows of Y and Z that are another sequence's: zeros, since theirs may hold anything
+        if (A.tma) {
+            sh.wait(kLoadX, i);
+            sh.wait(kLoadY, i);
+        } else {
+            fill_tile<D, kGroup>(sm + S::x, head_of(A.run.x, W.h, A.run.xh, A.run.xs1), A.run.xs0, W.token(i), lo, hi, true, tid);
+        }
+        if (cut || !A.tma) {
+            fill_tile<D, kGroup>(sm + S::y, head_of(A.run.y, W.h, A.run.yh, A.run.ys1), A.run.ys0, W.token(i), lo, hi, !A.tma, tid);
+            tc::fence_async_smem();
+            group_barrier<2>();
+        }
+        sh.arrive(kFullXY);
+        decayed_keys<D, kGroup>(sm, S::y, S::yh, S::yl, g.w, tid);
+        const float a = g.e[W.reverse ? 0 : L - 1];
+        if (A.tma) sh.wait(kLoadZ, i);
+        else if (i > 0) sh.wait(kBarO, i - 1);
+        if (cut || !A.tma) fill_tile<D, kGroup>(sm + S::z, head_of(A.run.z, W.h, A.run.zh, A.run.zs1), A.run.zs0, W.token(i), lo, hi, !A.tma, tid);
         tc::fence_async_smem();
         tc::fence_before();
-        __syncthreads();
-        if (tid == kIssuer) {
+        sh.arrive(kFullZ);
+        group_barrier<2>();
+        if (warp == kStateIssuer) {
             tc::fence_after();
-            for (int s = 0; s < D / 16; ++s) tc::mma_ss16(tmem + kColP, k_major<D>(base + S::x, s), k_major<D>(base + S::y, s), tc::idesc_bf16(L), s > 0);
-            tc::commit(bar_p);
-            for (int s = 0; s < D / 16; ++s) {
-                const uint64_t a = k_major<D>(base + S::x, s);
-                tc::mma_ss16(tmem + kColXS, a, k_major<D>(base + S::sh, s), tc::idesc_bf16(D), s > 0);
-                tc::mma_ss16(tmem + kColXS, a, k_major<D>(base + S::sl, s), tc::idesc_bf16(D), 1);
+            if (elect()) {
+                issue_state<D>(W.tmem, base + S::z, base + S::yh, base + S::yl, false);
+                tc::commit(sh.bars + kBarS);
             }
-            tc::commit(bar_xs);
-        }
-        if (tid < L) {
-            G = scan_warp(load_gate(A.run, w, h, c * L + tid, tid < nt), lane);
-            if (lane == 31) sums[warp] = G;
-        }
-        __syncthreads();
-        if (tid < L) {
-            double all = 0.0, before = 0.0;
-            for (int i = 0; i < 4; ++i) {
-                if (i < warp) before += sums[i];
-                all += sums[i];
+            if (more && A.tma) {
+                sh.wait(kBarP, i);
+                if (elect()) load_y(i + 1);
             }
-            const double end = before + sums[warp];  // of this block of 32
-            G += before;
-            g.hi[tid] = (float)G;
-            g.lo[tid] = (float)(G - (double)g.hi[tid]);
-            g.e[tid] = expf((float)G);
-            g.w[tid] = expf((float)(all - G));
-            g.c[tid] = expf((float)(end - G));
         }
-        __syncthreads();
-        decayed_keys<D>(sm, S::y, S::yh, S::yl, g.w);
-        cp_wait<0>();  // Z
-        tc::fence_async_smem();
-        __syncthreads();
-        if (tid == kIssuer) {
-            tc::fence_after();
-            issue_state<D>(tmem, base + S::z, base + S::yh, base + S::yl, slices, false);
-            tc::commit(bar_s);
-        }
-        {
-            if (!tc::mbar_wait(bar_p, phase)) s_err = 1;
-            tc::fence_after();
-            if (ahead) load_tile<D>(sm, S::y, y, A.run.ys0, w, (c + 1) * L, ahead, vec);
-            // P' in the place of P: 32 columns at a time, hi and lo
-            uint32_t ph[32], pl[32];
-            const float gh = g.hi[row], gl = g.lo[row];
-            const uint32_t from = tc::taddr(tmem, warp, kColP) + half * 64;
+        if (more) sum_gates(i + 1);
+        sh.wait(kBarS, i);
+        tc::fence_after();
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int block = 2 * half + b;
-                if (block > quarter) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) ph[16 * b + i] = pl[16 * b + i] = 0u;
-                } else {
-                    float p[32];
-                    tc::ld32(from + 32 * b, p);
-                    const float rf = block < quarter ? exp_diff2(gh, gl, g.hi[32 * block + 31], g.lo[32 * block + 31]) : 0.f;
-                    tc::wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const int s = 32 * block + i;
-                        if (block < quarter) {
-                            p[i] = p[i] * (rf * g.c[s]);
-                            p[i + 1] = p[i + 1] * (rf * g.c[s + 1]);
-                        } else {
-                            p[i] = i <= lane ? p[i] * exp_diff2(gh, gl, g.hi[s], g.lo[s]) : 0.f;
-                            p[i + 1] = i + 1 <= lane ? p[i + 1] * exp_diff2(gh, gl, g.hi[s + 1], g.lo[s + 1]) : 0.f;
-                        }
-                        tc::split_bf16x2(p[i], p[i + 1], ph[16 * b + i / 2], pl[16 * b + i / 2]);
-                    }
-                }
-            }
-            // both halves of these 32 rows have been read
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-            tc::st32(tc::taddr(tmem, warp, kColP) + half * 32, ph);
-            tc::st32(tc::taddr(tmem, warp, kColP) + 64 + half * 32, pl);
-            tc::wait_st();
-        }
-        tc::fence_before();
-        __syncthreads();
-        if (s_err) {
-            fine = false;
-            break;
-        }
-        if (tid == kIssuer) {
-            tc::fence_after();
-            constexpr uint32_t idesc = tc::idesc_bf16(D) | kTransposedB;
-            for (int s = 0; s < slices; ++s) {
-                const uint64_t b = mn_major<D>(base + S::z, s);
-                tc::mma_ts16(tmem + kColO, tmem + kColP + 8 * s, b, idesc, s > 0);
-                tc::mma_ts16(tmem + kColO, tmem + kColP + 64 + 8 * s, b, idesc, 1);
-            }
-            tc::commit(bar_o);
-        }
-        {
-            if (!tc::mbar_wait(bar_xs, phase)) s_err = 1;
-            if (ahead) load_tile<D>(sm, S::x, x, A.run.xs0, w, (c + 1) * L, ahead, vec);
-            cp_commit();
-            if (!tc::mbar_wait(bar_s, phase)) s_err = 1;
-            tc::fence_after();
-            {
-                float d[H];
-                ld_cols(tc::taddr(tmem, warp, kColS) + half * H, d);
-                const float a = g.e[L - 1];
-                tc::wait_ld();
-#pragma unroll
-                for (int i = 0; i < H; ++i) m[i] = fmaf(A.run.cs, d[i], a * m[i]);
-            }
-            if (has_state) put_state();
-            if (!tc::mbar_wait(bar_o, phase)) s_err = 1;
-            tc::fence_after();
-            if (ahead) load_tile<D>(sm, S::z, z, A.run.zs0, w, (c + 1) * L, ahead, vec);
-            cp_commit();
-            float o[H], xs[H];
-            ld_cols(tc::taddr(tmem, warp, kColO) + half * H, o);
-            ld_cols(tc::taddr(tmem, warp, kColXS) + half * H, xs);
-            const float c1 = A.run.co * A.run.cs, c2 = A.run.co * g.e[row];
+        for (int c = 0; c < H; c += 32) {
+            float d[32];
+            tc::ld32(lanes + kColS + half * H + c, d);
             tc::wait_ld();
-            if (row < nt) {
-                const long long at = (w.row(c * L + row) * A.run.H + h) * D + half * H;
 #pragma unroll
-                for (int i = 0; i < H; ++i) o[i] = fmaf(c2, xs[i], c1 * o[i]);
-                if (A.vec_out && A.run.out_dtype == GDN_BF16) {
-#pragma unroll
-                    for (int i = 0; i < H; i += 8)
-                        *reinterpret_cast<uint4*>((__nv_bfloat16*)A.run.out + at + i) =
-                            make_uint4(tc::pack_bf16x2(o[i], o[i + 1]), tc::pack_bf16x2(o[i + 2], o[i + 3]), tc::pack_bf16x2(o[i + 4], o[i + 5]), tc::pack_bf16x2(o[i + 6], o[i + 7]));
-                } else if (A.vec_out && A.run.out_dtype == GDN_F32) {
-#pragma unroll
-                    for (int i = 0; i < H; i += 4) *reinterpret_cast<float4*>((float*)A.run.out + at + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < H; ++i) st_any(A.run.out, at + i, A.run.out_dtype, o[i]);
-                }
-            }
+            for (int e = 0; e < 32; ++e) m[c + e] = fmaf(A.run.cs, d[e], a * m[c + e]);
+        }
+        if (more) {
+            sh.wait(kBarP, i);
+            sh.wait(kBarXS, i);
+            put_state();
         }
     }
-    cp_wait<0>();
-    tc::fence_before();
-    __syncthreads();
-    if (s_err) fine = false;
-    if (!fine) {
-        if (tid == 0) atomicOr(&g_la_chunk_timeout, 1);
-    } else if (has_state && part.last && q.out >= 0) {
-        if (A.run.reverse && len > 0) {
-            const float a = expf(ld_any(A.run.g, q.lo * A.run.gs0 + h * A.run.gs1, A.run.gate_dtype));
+    if (has_state && W.part.last && W.q.out >= 0 && !*sh.failed) {
+        if (W.reverse && W.q.hi > W.q.lo) {
+            const float a = expf(ld_any(A.run.g, W.q.lo * A.run.gs0 + W.h * A.run.gs1, A.run.gate_dtype));
 #pragma unroll
             for (int i = 0; i < H; ++i) m[i] *= a;
         }
-        store_state<D>(m, A.run.s_out + q.out * A.run.out_stride + (long long)h * D * D, row, half * H, A.run.transposed_out);
+        store_state<D>(m, A.run.s_out + W.q.out * A.run.out_stride + (long long)W.h * D * D, row, half * H, A.run.transposed_out);
     }
-    if (warp == 0) tc::tmem_free(tmem, kTmemCols);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_constant__ LaChunkArgs A)
+{
+    using S = Smem<D>;
+    extern __shared__ __align__(1024) char sm[];
+    const Shared sh(sm + S::bars);
+    float* g0 = reinterpret_cast<float*>(sm + S::g);
+    const Gates g = {g0, g0 + L, g0 + 2 * L, g0 + 3 * L, g0 + 4 * L};
+    Work W;
+    W.nh = blockIdx.x / A.segments;
+    W.segment = blockIdx.x - W.nh * A.segments;
+    const int n = W.nh / A.run.H;
+    W.h = W.nh - n * A.run.H;
+    W.reverse = A.run.reverse;
+    begin_after();
+    W.q = la_sequence(A.run, n);
+    if (!W.q.ok) {
+        if (threadIdx.x == 0) atomicOr(&g_la_chunk_bad, 1);
+        return;
+    }
+    W.part = part_of(A, W.q.hi - W.q.lo, W.segment);
+    if (W.part.none) return;
+    W.count = W.part.c1 > W.part.c0 ? (int)(W.part.c1 - W.part.c0) : 0;
+    W.tmem = begin(sh);
+    if (threadIdx.x < kGroup) scores<D>(A, W, sm, sh, g);
+    else states<D>(A, W, sm, sh, g);
+    tc::fence_before();
+    __syncthreads();
+    if (*sh.failed && threadIdx.x == 0) atomicOr(&g_la_chunk_timeout, 1);
+    if (threadIdx.x < 32) tc::tmem_free(W.tmem, kTmemCols);
 }
 
 // Segments a sequence and head: as many as leave every SM one, each of several chunks.
@@ -596,7 +902,25 @@ void plan(const LaRun& A, int* segments, int* per)
     *segments = (int)(chunks > 0 ? (chunks + p - 1) / p : 1);
 }
 
-bool vec16(const void* ptr, long long s0, long long s1) { return (uintptr_t)ptr % 16 == 0 && s0 % 8 == 0 && s1 % 8 == 0; }
+// A map of [n_tok][heads][D]: false where its rows do not lie on 16 bytes, or are otherwise nothing for TMA.
+bool make_map(CUtensorMap* map, const void* ptr, long long s0, long long s1, int heads, int n_tok, int D)
+{
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r);
+        return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? (Encode)f : (Encode) nullptr;
+    }();
+    if (heads == 1) s1 = D;
+    if (n_tok == 1) s0 = (long long)heads * D;
+    if (!encode || n_tok < 1 || (uintptr_t)ptr % 16 || s0 % 8 || s1 % 8 || s0 < 1 || s1 < 1 || s0 >= (1ll << 38) || s1 >= (1ll << 38)) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)n_tok}, strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s0 * 2};
+    const cuuint32_t box[3] = {64, 1, L}, ones[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int D>
 int launch(const LaChunkArgs& A, cudaStream_t st)
@@ -631,8 +955,9 @@ int launch_la_chunk(const LaRun& run, void* workspace, cudaStream_t st)
     plan(run, &A.segments, &A.per);
     A.states = (float*)workspace;
     A.decays = A.states + (long long)run.n_seq * run.H * A.segments * run.DK * run.DV;
-    A.vec = vec16(run.x, run.xs0, run.xs1) && vec16(run.y, run.ys0, run.ys1) && vec16(run.z, run.zs0, run.zs1);
-    A.vec_out = (uintptr_t)run.out % 16 == 0;
+    A.tma = make_map(&A.x, run.x, run.xs0, run.xs1, run.xh, run.n_tok, run.DK) && make_map(&A.y, run.y, run.ys0, run.ys1, run.yh, run.n_tok, run.DK) &&
+            make_map(&A.z, run.z, run.zs0, run.zs1, run.zh, run.n_tok, run.DV);
+    A.vec_out = (uintptr_t)run.out % 32 == 0;
     return run.DK == 128 ? launch<128>(A, st) : launch<64>(A, st);
 }
 

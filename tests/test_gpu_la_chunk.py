@@ -37,7 +37,7 @@ def backward(x, counts, slot_in, **kw):
 
 @pytest.mark.parametrize("S", [64, 128])
 @pytest.mark.parametrize("counts,H_k,H_v", [([32], 1, 1), ([128], 1, 2), ([129], 2, 2), ([127, 1, 0, 300], 2, 6), ([1000], 1, 1), ([40] * 7, 3, 3), ([260, 0, 511, 33], 5, 10),
-                                            ([2100], 1, 1), ([700, 3, 1500], 1, 3), ([33] * 90, 2, 4), ([256, 256], 1, 4)])
+                                            ([2100], 1, 1), ([700, 3, 1500], 1, 3), ([33] * 90, 2, 4), ([256, 256], 1, 4), ([1400], 16, 48), ([900, 1000], 8, 40)])
 def test_forward(counts, H_k, H_v, S):
     N = len(counts)
     x = P.problem(counts, H_k, H_v, S, dtype=BF16, slots=2 * N, seed=S + sum(counts))
@@ -50,7 +50,7 @@ def test_forward(counts, H_k, H_v, S):
 
 
 @pytest.mark.parametrize("S", [64, 128])
-@pytest.mark.parametrize("counts,H_k,H_v", [([32], 1, 1), ([129], 2, 2), ([127, 1, 0, 300], 2, 6), ([1000], 1, 1), ([40] * 7, 3, 3), ([700, 3, 900], 1, 3)])
+@pytest.mark.parametrize("counts,H_k,H_v", [([32], 1, 1), ([129], 2, 2), ([127, 1, 0, 300], 2, 6), ([1000], 1, 1), ([40] * 7, 3, 3), ([700, 3, 900], 1, 3), ([800], 16, 48)])
 def test_backward(counts, H_k, H_v, S):
     N = len(counts)
     x = P.problem(counts, H_k, H_v, S, dtype=BF16, seed=S + sum(counts))
