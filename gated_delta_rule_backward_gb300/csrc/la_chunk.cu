@@ -9,17 +9,18 @@
 //
 // One CTA owns a state (D x D, fp32, in registers) and walks the chunks of a
 // sequence's segment.  X, Y and Z arrive by TMA as they are stored, rows of 64 columns in 128-byte swizzle.  Products with a
-// contraction over columns read a tile K-major, those over tokens read the same bytes MN-major, so that nothing is transposed:
-//     P  = X Y^T          128 x 128, K = D     X, Y as stored: exact
-//     XS = X S^T          128 x D,   K = D     S as bf16 hi + lo in shared memory: 2 passes
-//     O  = P' Z           128 x D,   K = 128   P' as bf16 hi + lo in TMEM (in P's columns): 2 passes
-//     dS = Z^T Y'         D x D,     K = 128   Y' as bf16 hi + lo in shared memory: 2 passes
-// hi + lo carries 16 significant bits (2^-16 relative); the accumulators and the state are fp32.
+// contraction over columns read a tile K-major, those over tokens read the same bytes MN-major:
+//     P   = X Y^T          128 x 128, K = D     X, Y as stored: exact
+//     O   = X S^T          128 x D,   K = D     S as bf16 hi + lo in shared memory: 2 passes
+//     O   <- e^G O + P' Z  128 x D,   K = 128   P' (with cs) as bf16 hi + lo in TMEM, in P's columns: 2 passes
+//     dS^T = Y'^T Z        D x D,     K = 128   Y'^T as bf16 hi + lo in TMEM: 2 passes
+// hi + lo carries 16 significant bits (2^-16 relative); the accumulators and the state are fp32.  What bounds the products, beside the tensor
+// cores' own rate, is shared memory, which hands 128 bytes a cycle to all of them and the threads; so the operands that are made here are made in
+// tensor memory, Y'^T by way of transposing loads.
 //
-// Two groups of 8 warps work on a chunk side by side.  The first turns P into P' and writes the output; one of its
-// warps issues P, XS and O.  The second sums the gates, makes Y' and keeps the state, and issues dS.  They meet at mbarriers
-// only, so that the tensor cores run P | XS, dS | O of one chunk while the warps are at the others.  A tile is loaded again as soon as
-// its last product is done; the next ones are prefetched into L2.
+// Two groups of 8 warps work on a chunk side by side.  The first turns P into P', scales O's rows by e^G and writes the output; one of its
+// warps issues P and both parts of O.  The second sums the gates, makes Y' and keeps the state, and issues dS.  They meet at mbarriers
+// only, so that the tensor cores run P | X S^T, dS | P' Z of one chunk while the warps are at the others.
 //
 // Decays.  G is summed in 64-bit fixed point (powers of two, 31 fraction bits) and kept as a whole and a fractional fp32 number, since
 // what is needed are small differences of sums that may be large.  e^(G_t - G_s) of 32 x 32 blocks off the diagonal is the product of a
@@ -48,7 +49,8 @@ constexpr int kThreads = 2 * kGroup;
 constexpr int kScoreIssuer = 4;  // warp of the first group that issues products: forwards it has the least to do (columns 64 .. of rows 0 .. 31 of P' are zeros)
 constexpr int kStateIssuer = 0;  // and of the second
 constexpr int kMostSegments = 16;
-constexpr uint32_t kColP = 0, kColO = 128, kColXS = 256, kColS = 384, kTmemCols = 512;
+constexpr uint32_t kColP = 0, kColO = 128, kColS = 256, kColY = 384, kTmemCols = 512;  // Y': 64 columns of hi words, 64 of lo
+constexpr float kMostSpan = 60.f;  // powers of two that a block's factors may reach over
 
 struct LaChunkArgs {
     CUtensorMap x, y, z;     // [n_tok][heads][D], boxes of 128 tokens x 1 head x 64 columns
@@ -62,20 +64,27 @@ struct LaChunkArgs {
 template <int D>
 struct Smem {
     static constexpr int tile = L * D * 2;
-    static constexpr int x = 0, y = tile, z = 2 * tile, yh = 3 * tile, yl = 4 * tile;
-    static constexpr int sh = 5 * tile, sl = sh + D * D * 2;
-    static constexpr int g = sl + D * D * 2;  // five arrays of L floats, then barriers
-    static constexpr int bars = g + 5 * L * 4, bytes = bars + 192;
-    // the first kernel's second Y and Z
-    static constexpr int y1 = sh, z1 = x;
-    // Z as operand of a product with M = 128 is read over 128 columns, whatever D
-    static constexpr int z_read = 2 * L * 128;
-    static_assert(z + z_read <= bytes && z1 + z_read <= bytes && y1 + tile <= g, "shared memory");
+    static constexpr int x = 0, sh = 5 * tile, sl = sh + D * D * 2;
+    static constexpr int y(int i) { return i & 1 ? 2 * tile : tile; }
+    static constexpr int z(int i) { return i & 1 ? 4 * tile : 3 * tile; }
+    static constexpr int g = 6 * tile + (D == 128 ? tile : 0);  // five arrays of L floats, then barriers
+    static constexpr int bars = g + 5 * L * 4, bytes = bars + 224;
+    static_assert(sl + D * D * 2 <= g, "shared memory");
+    // the first kernel: three stages of Y and Z
+    static constexpr int stage(int i) { return i % 3 * 2 * tile; }
 };
 static_assert(Smem<128>::bytes <= kSmemPerCtaMax && Smem<64>::bytes <= kSmemPerCtaMax, "shared memory");
 
-// mbarriers: products done and tiles loaded (one arrival each), then handovers (one arrival a warp of a group)
-enum { kBarP, kBarXS, kBarS, kBarO, kLoadX, kLoadY, kLoadZ, kSingle, kFullXY = kSingle, kFullG, kFullZ, kFullS, kFreeXS, kFreeG, kBars };
+// mbarriers: products done, tiles loaded, and Y read by P (one arrival each; a barrier a buffer, since a load may be under way while the one
+// before it has not arrived); handovers (one arrival a warp of a group); Z read by both its products (two).  A wait tells a phase from the
+// one before it and the one behind it, no more: whoever waits for a phase has waited for the one before it, and the phase behind it comes
+// only by way of something that this waiter does afterwards.
+enum {
+    kBarP, kBarXS, kBarS, kBarO, kLoadX, kLoadY, kLoadZ = kLoadY + 2, kFreeY = kLoadZ + 2, kSingle = kFreeY + 2,
+    kFullXY = kSingle, kFullG, kFullZ, kFullS, kFreeO, kFreeG, kFreeZ, kBars = kFreeZ + 2
+};
+// of the first kernel
+enum { kProduct = kBarP, kStage = kLoadX };
 
 struct Gates {
     float *hi, *lo, *e, *w, *c;  // G in powers of two; e^G; e^(G_last - G); e^(G of the block's last column - G)
@@ -89,7 +98,10 @@ struct Shared {
     uint32_t* tmem;
     volatile int* failed;
     __device__ __forceinline__ explicit Shared(char* at)
-        : bars((uint64_t*)at), sums((long long*)(at + 128)), nans((int*)(at + 160)), tmem((uint32_t*)(at + 176)), failed((volatile int*)(at + 180)) {}
+        : bars((uint64_t*)at), sums((long long*)(at + 160)), nans((int*)(at + 192)), tmem((uint32_t*)(at + 208)), failed((volatile int*)(at + 212))
+    {
+        static_assert(kBars * 8 <= 160, "barriers");
+    }
     // Until the barrier's phase is complete; gives up as tc::mbar_wait does, and at once after another wait has given up:
     // what follows then works on what it finds, which is nobody's result, and the kernel ends.
     __device__ __forceinline__ void wait(int bar, uint32_t phase) const
@@ -133,6 +145,13 @@ __device__ __forceinline__ bool elect()
 // This warp's number, as a number of the whole warp.
 __device__ __forceinline__ int warp_of(int tid) { return __shfl_sync(kFull, tid >> 5, 0); }
 
+// 16 lanes x 16 columns: registers 2 i and 2 i + 1 are columns 4 i .. of lanes 0 .. 7 and 8 .. 15, thread = 4 lane + column.
+__device__ __forceinline__ void st_16x128b(uint32_t at, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+}
+
 template <int ID>
 __device__ __forceinline__ void group_barrier()
 {
@@ -168,11 +187,10 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map, int column,
 {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map), "r"(column), "r"(head), "r"(token) : "memory");
 }
-// By one thread: 128 tokens from `token` on (rows outside the tensor read as zeros), and later ones into L2.
+// By one thread: 128 tokens from `token` on (rows outside the tensor read as zeros), whose bytes the barrier expects; and later ones into L2.
 template <int D>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int head, long long token, uint64_t* bar)
 {
-    tc::mbar_expect_tx(bar, L * D * 2);
 #pragma unroll
     for (int c = 0; c < D; c += 64) tma_tile(dst + c * (L * 2), map, c, head, (int)token, tc::smem_addr(bar));
 }
@@ -233,51 +251,60 @@ __device__ __forceinline__ long long scan_warp(float gate, int lane, bool* nan)
     return x;
 }
 
-// Y' = w Y as bf16 hi and lo, by T threads: units of 16 bytes, each lane 8 columns of one token.  Y' lies in core matrices of 8 tokens x 8
-// columns: a warp's 32 units are 8 tokens of 4, whole core matrices (no bank twice on either side).
-template <int D, int T>
-__device__ __forceinline__ void decayed_keys(char* sm, int y, int yh, int yl, const float* w, int tid)
+// Y'^T = (w Y)^T as bf16 hi and lo into TMEM, by PARTS x 4 warps: a warp's 32 lanes of TMEM are columns of Y, and it takes 128 / PARTS
+// tokens.  A transposing load of 8 tokens x 8 columns leaves a lane two tokens of one column, which is where TMEM's 16 x 128-bit shape wants them.
+template <int D, int PARTS>
+__device__ __forceinline__ void decayed_keys(uint32_t tile, uint32_t tmem, const float* w, int quarter, int part, int lane)
 {
-#pragma unroll 4
-    for (int u0 = 0; u0 < L * D / 8; u0 += T) {
-        const int u = u0 + tid, kc = (u >> 3) % (D / 8), r = (u & 7) + 8 * ((u >> 3) / (D / 8)), at = (u >> 3) * 128 + (u & 7) * 16;
-        const uint4 v = *reinterpret_cast<const uint4*>(sm + y + swizzled(r, kc));
-        const float wr = w[r];
-        const f2 ww = pack2(wr, wr);
-        uint4 hi, lo;
-        auto part = [&](uint32_t x, uint32_t& h, uint32_t& l) { split2(mul2(pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), ww), h, l); };
-        part(v.x, hi.x, lo.x);
-        part(v.y, hi.y, lo.y);
-        part(v.z, hi.z, lo.z);
-        part(v.w, hi.w, lo.w);
-        *reinterpret_cast<uint4*>(sm + yh + at) = hi;
-        *reinterpret_cast<uint4*>(sm + yl + at) = lo;
+    if (32 * quarter < D) {
+#pragma unroll 1
+        for (int t0 = part * (L / PARTS); t0 < (part + 1) * (L / PARTS); t0 += 32) {
+            f2 ww[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) ww[b] = *reinterpret_cast<const f2*>(w + t0 + 8 * b + 2 * (lane & 3));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t at = tile + swizzled(t0 + lane, 4 * quarter + 2 * h + c);
+                    uint32_t v[4];
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                 : "r"(at)
+                                 : "memory");
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        split2(mul2(pack2(__uint_as_float(v[b] << 16), __uint_as_float(v[b] & 0xffff0000u)), ww[b]), hi[2 * b + c], lo[2 * b + c]);
+                }
+                const uint32_t to = tmem + ((uint32_t)(32 * quarter + 16 * h) << 16) + t0 / 2;
+                st_16x128b(to, hi);
+                st_16x128b(to + 64, lo);
+            }
+        }
+        tc::wait_st();
     }
 }
 
 // Operands in shared memory.  Of tiles in 128-byte swizzle: K-major (tokens are M or N; 32 bytes a slice of 16 columns, 16 KB every 64)
-// and MN-major (columns are M or N; 16 rows a slice).  Of Y' and S, in core matrices: MN-major and K-major.
+// and MN-major (columns are N; 16 rows a slice).  Of S^T, rows i, in core matrices of 8 x 8: MN-major.
 constexpr uint64_t kSwizzle128 = 2ull << 61;
 __device__ __forceinline__ uint64_t swizzled_k(uint32_t tile) { return tc::make_desc(tile, 16, 1024) | kSwizzle128; }
 __device__ __forceinline__ uint64_t swizzled_mn(uint32_t tile) { return tc::make_desc(tile, L * 128, 1024) | kSwizzle128; }
 __device__ __forceinline__ uint64_t step_k(int s) { return (uint64_t)((s >> 2) * (L * 128) + (s & 3) * 32) >> 4; }
 __device__ __forceinline__ uint64_t step_mn(int s) { return (uint64_t)(s * 2048) >> 4; }
-template <int D>
-__device__ __forceinline__ uint64_t cores_k(uint32_t tile) { return tc::make_desc(tile, 128, D * 16); }
-template <int D>
-__device__ __forceinline__ uint64_t cores_mn(uint32_t tile) { return tc::make_desc(tile, D * 16, 128); }
-constexpr uint32_t kTransposedA = 1u << 15, kTransposedB = 1u << 16;
+constexpr uint32_t kTransposedB = 1u << 16;
 
-// dS (+)= Z^T Y'.  M is 128 for D = 64 too: rows 64 .. 127 read what follows Z in shared memory (Smem::z_read) and are nobody's.
+// dS^T (+)= Y'^T Z.  M is 128 for D = 64 too: lanes 64 .. 127 are nobody's.
 template <int D>
-__device__ __forceinline__ void issue_state(uint32_t tmem, uint32_t z, uint32_t yh, uint32_t yl, bool accumulate)
+__device__ __forceinline__ void issue_state(uint32_t to, uint32_t y, uint32_t z, bool accumulate)
 {
-    constexpr uint32_t idesc = tc::idesc_bf16(D) | kTransposedA | kTransposedB;
-    const uint64_t a = swizzled_mn(z), bh = cores_mn<D>(yh), bl = cores_mn<D>(yl);
+    constexpr uint32_t idesc = tc::idesc_bf16(D) | kTransposedB;
+    const uint64_t b = swizzled_mn(z);
 #pragma unroll
     for (int s = 0; s < L / 16; ++s) {
-        tc::mma_ss16(tmem + kColS, a + step_mn(s), bh + s * D * 2, idesc, accumulate || s > 0);
-        tc::mma_ss16(tmem + kColS, a + step_mn(s), bl + s * D * 2, idesc, 1);
+        tc::mma_ts16(to, y + 8 * s, b + step_mn(s), idesc, accumulate || s > 0);
+        tc::mma_ts16(to, y + 64 + 8 * s, b + step_mn(s), idesc, 1);
     }
 }
 template <int D>
@@ -290,14 +317,15 @@ __device__ __forceinline__ void issue_scores(uint32_t tmem, uint32_t x, uint32_t
 template <int D>
 __device__ __forceinline__ void issue_state_output(uint32_t tmem, uint32_t x, uint32_t sh, uint32_t sl)
 {
-    const uint64_t a = swizzled_k(x), bh = cores_k<D>(sh), bl = cores_k<D>(sl);
+    constexpr uint32_t idesc = tc::idesc_bf16(D) | kTransposedB;
+    const uint64_t a = swizzled_k(x), bh = tc::make_desc(sh, D * 16, 128), bl = tc::make_desc(sl, D * 16, 128);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-        tc::mma_ss16(tmem + kColXS, a + step_k(s), bh + 16 * s, tc::idesc_bf16(D), s > 0);
-        tc::mma_ss16(tmem + kColXS, a + step_k(s), bl + 16 * s, tc::idesc_bf16(D), 1);
+        tc::mma_ss16(tmem + kColO, a + step_k(s), bh + s * D * 2, idesc, s > 0);
+        tc::mma_ss16(tmem + kColO, a + step_k(s), bl + s * D * 2, idesc, 1);
     }
 }
-// O = P' Z; of every 32 columns of P, 16 hold hi words and 16 lo words.
+// Of every 32 columns of P, 16 hold hi words and 16 lo words.
 template <int D>
 __device__ __forceinline__ void issue_output(uint32_t tmem, uint32_t z)
 {
@@ -306,7 +334,7 @@ __device__ __forceinline__ void issue_output(uint32_t tmem, uint32_t z)
 #pragma unroll
     for (int s = 0; s < L / 16; ++s) {
         const uint32_t a = tmem + kColP + 32 * (s >> 1) + 8 * (s & 1);
-        tc::mma_ts16(tmem + kColO, a, b + step_mn(s), idesc, s > 0);
+        tc::mma_ts16(tmem + kColO, a, b + step_mn(s), idesc, 1);
         tc::mma_ts16(tmem + kColO, a + 16, b + step_mn(s), idesc, 1);
     }
 }
@@ -315,7 +343,7 @@ __device__ __forceinline__ void issue_output(uint32_t tmem, uint32_t z)
 __device__ __forceinline__ uint32_t begin(const Shared& sh)
 {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kBars; ++i) tc::mbar_init(sh.bars + i, i < kSingle ? 1 : kGroup / 32);
+        for (int i = 0; i < kBars; ++i) tc::mbar_init(sh.bars + i, i < kSingle ? 1 : i < kFreeZ ? kGroup / 32 : 2);
         tc::mbar_fence_init();
         *sh.failed = 0;
     }
@@ -331,33 +359,33 @@ __device__ __forceinline__ float* state_of(const LaChunkArgs& A, int D, int nh, 
     return A.states + ((long long)nh * A.segments + segment) * D * D;
 }
 
-// A row's columns [c0, c0 + N) of a state in memory.
+// Columns j in [c0, c0 + N) of row i of S^T; in memory rows follow each other in S^T's order (`rows`) or in S's.
 template <int D, int N>
-__device__ __forceinline__ void load_state(float (&m)[N], const float* head, int j, int c0, bool transposed)
+__device__ __forceinline__ void load_state(float (&m)[N], const float* head, int i, int c0, bool rows)
 {
-    if (!transposed) {
+    if (rows) {
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(head + j * D + c0 + i);
-            m[i] = v.x;
-            m[i + 1] = v.y;
-            m[i + 2] = v.z;
-            m[i + 3] = v.w;
+        for (int c = 0; c < N; c += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(head + i * D + c0 + c);
+            m[c] = v.x;
+            m[c + 1] = v.y;
+            m[c + 2] = v.z;
+            m[c + 3] = v.w;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) m[i] = head[(c0 + i) * D + j];
+        for (int c = 0; c < N; ++c) m[c] = head[(c0 + c) * D + i];
     }
 }
 template <int D, int N>
-__device__ __forceinline__ void store_state(const float (&m)[N], float* head, int j, int c0, bool transposed)
+__device__ __forceinline__ void store_state(const float (&m)[N], float* head, int i, int c0, bool rows)
 {
-    if (!transposed) {
+    if (rows) {
 #pragma unroll
-        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(head + j * D + c0 + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+        for (int c = 0; c < N; c += 4) *reinterpret_cast<float4*>(head + i * D + c0 + c) = make_float4(m[c], m[c + 1], m[c + 2], m[c + 3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) head[(c0 + i) * D + j] = m[i];
+        for (int c = 0; c < N; ++c) head[(c0 + c) * D + i] = m[c];
     }
 }
 
@@ -401,6 +429,8 @@ struct Work {
         const long long left = q.hi - token(i);
         return left < L ? (int)left : L;
     }
+    // Whether threads write its tiles: without TMA, and where rows are another sequence's (of TMA's, one chunk of a segment at most).
+    __device__ __forceinline__ bool made(const LaChunkArgs& A, int i) const { return !A.tma || lo(i) > 0 || hi(i) < L; }
 };
 
 __device__ __forceinline__ const __nv_bfloat16* head_of(const void* p, int h, int heads, long long stride)
@@ -431,32 +461,30 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     if (W.part.none || W.part.last) return;
     const uint32_t tmem = begin(sh), base = tc::smem_addr(sm);
     const int count = (int)(W.part.c1 - W.part.c0), yh = W.h % A.run.yh, zh = W.h % A.run.zh;
-    auto y_tile = [](int it) { return it & 1 ? S::y1 : S::y; };
-    auto z_tile = [](int it) { return it & 1 ? S::z1 : S::z; };
-    // a barrier a buffer, since a load is under way while the one before it may not have arrived
-    auto y_bar = [](int it) { return it & 1 ? kLoadX : kLoadY; };
-    auto z_bar = [](int it) { return it & 1 ? kBarP : kLoadZ; };
     // whole chunks, from the last one back: the sequence's last one is the last segment's
+    auto token = [&](int it) { return W.token(count - 1 - it); };
     auto load = [&](int it) {
-        const int i = count - 1 - it;
         if (!A.tma) {
-            fill_tile<D, kThreads>(sm + y_tile(it), head_of(A.run.y, W.h, A.run.yh, A.run.ys1), A.run.ys0, W.token(i), 0, L, true, tid);
-            fill_tile<D, kThreads>(sm + z_tile(it), head_of(A.run.z, W.h, A.run.zh, A.run.zs1), A.run.zs0, W.token(i), 0, L, true, tid);
+            fill_tile<D, kThreads>(sm + S::stage(it), head_of(A.run.y, W.h, A.run.yh, A.run.ys1), A.run.ys0, token(it), 0, L, true, tid);
+            fill_tile<D, kThreads>(sm + S::stage(it) + S::tile, head_of(A.run.z, W.h, A.run.zh, A.run.zs1), A.run.zs0, token(it), 0, L, true, tid);
         } else if (warp == 0 && elect()) {
-            load_tile<D>(base + y_tile(it), &A.y, yh, W.token(i), sh.bars + y_bar(it));
-            load_tile<D>(base + z_tile(it), &A.z, zh, W.token(i), sh.bars + z_bar(it));
-            if (i > 0) {
-                prefetch_tile<D>(&A.y, yh, W.token(i - 1));
-                prefetch_tile<D>(&A.z, zh, W.token(i - 1));
+            uint64_t* bar = sh.bars + kStage + it % 3;
+            tc::mbar_expect_tx(bar, 2 * S::tile);
+            load_tile<D>(base + S::stage(it), &A.y, yh, token(it), bar);
+            load_tile<D>(base + S::stage(it) + S::tile, &A.z, zh, token(it), bar);
+            if (it + 1 < count) {
+                prefetch_tile<D>(&A.y, yh, token(it + 1));
+                prefetch_tile<D>(&A.z, zh, token(it + 1));
             }
         }
     };
     const int r = W.reverse ? L - 1 - tid : tid;  // threads in walking order
-    auto gate = [&](int it) { return tid < L && it < count ? load_gate(A.run, W.q, W.h, W.token(count - 1 - it) + r, true) : 0.f; };
+    auto gate = [&](int it) { return tid < L && it < count ? load_gate(A.run, W.q, W.h, token(it) + r, true) : 0.f; };
     long long carry = 0;
     bool nan = false;  // among the gates behind
     load(0);
     float next = gate(0);
+    // Y' in two buffers, as are the barriers of the products that read them
     for (int it = 0; it < count; ++it) {
         long long G = 0;
         bool bad = false;
@@ -468,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
             }
         }
         next = gate(it + 1);
-        if (it > 0) sh.wait(kBarS, it - 1);  // the product before has read Y' and the other buffers
+        if (it > 1) sh.wait(kProduct + (it & 1), (it >> 1) - 1);  // the product before the last has read Y' and its stage
         __syncthreads();
         if (it + 1 < count) load(it + 1);
         long long all = 0;
@@ -480,33 +508,34 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
         }
         if (tid < L) sw[r] = nan ? NAN : ex2(from_fixed(carry + (all - G)));
         carry += all;
-        if (A.tma) {
-            sh.wait(y_bar(it), it >> 1);
-            sh.wait(z_bar(it), it >> 1);
-        }
+        if (A.tma) sh.wait(kStage + it % 3, it / 3);
         __syncthreads();
-        decayed_keys<D, kThreads>(sm, y_tile(it), S::yh, S::yl, sw, tid);
+        tc::fence_after();
+        const uint32_t y = tmem + kColY - 128 * (it & 1);  // the columns of Y' and, of the other kernel, dS
+        decayed_keys<D, 4>(base + S::stage(it), y, sw, warp & 3, warp >> 2, lane);
         tc::fence_async_smem();
+        tc::fence_before();
         __syncthreads();
         if (warp == 0 && elect()) {
             tc::fence_after();
-            issue_state<D>(tmem, base + z_tile(it), base + S::yh, base + S::yl, it > 0);
-            tc::commit(sh.bars + kBarS);
+            issue_state<D>(tmem, y, base + S::stage(it) + S::tile, it > 0);
+            tc::commit(sh.bars + kProduct + (it & 1));
         }
     }
-    sh.wait(kBarS, count - 1);
+    if (count > 1) sh.wait(kProduct + (count & 1), ((count - 2) >> 1));
+    sh.wait(kProduct + ((count - 1) & 1), (count - 1) >> 1);
     __syncthreads();
     if (*sh.failed) {
         if (tid == 0) atomicOr(&g_la_chunk_timeout, 1);
     } else {
         tc::fence_after();
         constexpr int C = D / 4;  // columns of a thread
-        const int j = 32 * (warp & 3) + lane, c0 = (warp >> 2) * C;
+        const int row = 32 * (warp & 3) + lane, c0 = (warp >> 2) * C;
         float d[C];
-        if constexpr (C == 32) tc::ld32(tc::taddr(tmem, warp, kColS) + c0, d);
-        else tc::ld16(tc::taddr(tmem, warp, kColS) + c0, d);
+        if constexpr (C == 32) tc::ld32(tc::taddr(tmem, warp, 0) + c0, d);
+        else tc::ld16(tc::taddr(tmem, warp, 0) + c0, d);
         tc::wait_ld();
-        if (j < D) {
+        if (row < D) {
             const float all = nan ? NAN : ex2(from_fixed(carry));
 #pragma unroll
             for (int i = 0; i < C; ++i) d[i] *= A.run.cs;
@@ -515,12 +544,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
                 float m[C];
 #pragma unroll
                 for (int i = 0; i < C; ++i) m[i] = 0.f;
-                if (W.q.in >= 0) load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, j, c0, A.run.transposed_in);
-                store_state<D>(m, state_of(A, D, W.nh, 0), j, c0, false);
+                if (W.q.in >= 0) load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, row, c0, A.run.transposed_in);
+                store_state<D>(m, state_of(A, D, W.nh, 0), row, c0, true);
 #pragma unroll
                 for (int i = 0; i < C; ++i) d[i] = fmaf(all, m[i], d[i]);
             }
-            store_state<D>(d, state_of(A, D, W.nh, W.segment + 1), j, c0, false);
+            store_state<D>(d, state_of(A, D, W.nh, W.segment + 1), row, c0, true);
             if (tid == 0) A.decays[W.nh * A.segments + W.segment + 1] = all;
         }
     }
@@ -546,55 +575,52 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_of(tid), quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
     const uint32_t base = tc::smem_addr(sm), lanes = tc::taddr(W.tmem, warp, 0);
     const int xh = W.h % A.run.xh, zh = W.h % A.run.zh;
-    float c2 = 0.f;  // co e^G of this row, of the chunk whose output is next
-    const float c1 = A.run.co * A.run.cs;
 
     auto output = [&](int i) {
         sh.wait(kBarO, i);
-        sh.wait(kBarXS, i);
         tc::fence_after();
-        const bool real = row >= W.lo(i) && row < W.hi(i);
-        const long long at = ((W.token(i) + row) * A.run.H + W.h) * D + half * H;
-#pragma unroll 1
-        for (int c = 0; c < H; c += 32) {
-            float o[32], xs[32];
-            tc::ld32(lanes + kColO + half * H + c, o);
-            tc::ld32(lanes + kColXS + half * H + c, xs);
-            tc::wait_ld();
-            if (real) {
+        float o[H];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = fmaf(c2, xs[e], c1 * o[e]);
-                if (A.vec_out && A.run.out_dtype == GDN_BF16) {
+        for (int c = 0; c < H; c += 32) tc::ld32(lanes + kColO + half * H + c, *reinterpret_cast<float(*)[32]>(o + c));
+        tc::wait_ld();
+        tc::fence_before();
+        sh.arrive(kFreeO);
+        if (row >= W.lo(i) && row < W.hi(i)) {
+            const long long at = ((W.token(i) + row) * A.run.H + W.h) * D + half * H;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 16) {
-                        uint32_t v[8];
+            for (int e = 0; e < H; ++e) o[e] *= A.run.co;
+            if (A.vec_out && A.run.out_dtype == GDN_BF16) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = tc::pack_bf16x2(o[e + 2 * k], o[e + 2 * k + 1]);
-                        st_global32((__nv_bfloat16*)A.run.out + at + c + e, v);
-                    }
-                } else if (A.vec_out && A.run.out_dtype == GDN_F32) {
+                for (int e = 0; e < H; e += 16) {
+                    uint32_t v[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[e + k]);
-                        st_global32((float*)A.run.out + at + c + e, v);
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) st_any(A.run.out, at + c + e, A.run.out_dtype, o[e]);
+                    for (int k = 0; k < 8; ++k) v[k] = tc::pack_bf16x2(o[e + 2 * k], o[e + 2 * k + 1]);
+                    st_global32((__nv_bfloat16*)A.run.out + at + e, v);
                 }
+            } else if (A.vec_out && A.run.out_dtype == GDN_F32) {
+#pragma unroll
+                for (int e = 0; e < H; e += 8) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[e + k]);
+                    st_global32((float*)A.run.out + at + e, v);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < H; ++e) st_any(A.run.out, at + e, A.run.out_dtype, o[e]);
             }
         }
-        tc::fence_before();
-        sh.arrive(kFreeXS);
+        __syncwarp();
     };
     auto load_x = [&](int i) {
+        tc::mbar_expect_tx(sh.bars + kLoadX, S::tile);
         load_tile<D>(base + S::x, &A.x, xh, W.token(i), sh.bars + kLoadX);
         if (i + 1 < W.count) prefetch_tile<D>(&A.x, xh, W.token(i + 1));
     };
     auto load_z = [&](int i) {
-        load_tile<D>(base + S::z, &A.z, zh, W.token(i), sh.bars + kLoadZ);
+        uint64_t* bar = sh.bars + kLoadZ + (i & 1);
+        tc::mbar_expect_tx(bar, S::tile);
+        load_tile<D>(base + S::z(i), &A.z, zh, W.token(i), bar);
         if (i + 1 < W.count) prefetch_tile<D>(&A.z, zh, W.token(i + 1));
     };
     if (warp == kScoreIssuer && A.tma && W.count > 0 && elect()) {
@@ -603,24 +629,26 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
     }
 
     for (int i = 0; i < W.count; ++i) {
+        const bool more = i + 1 < W.count, made = W.made(A, i);
         if (warp == kScoreIssuer) {
-            if (i > 0) {  // P' and Z have been read
-                sh.wait(kBarO, i - 1);
-                if (A.tma) {
-                    sh.wait(kBarS, i - 1);
-                    if (elect()) load_z(i);
-                }
+            if (i > 0) sh.wait(kBarO, i - 1);  // P' has been read
+            if (A.tma) {
+                if (i > 0 && more) sh.wait(kFreeZ + ((i + 1) & 1), (i - 1) >> 1);
+                if (more && elect()) load_z(i + 1);
+                sh.wait(kLoadX, i);
+                sh.wait(kLoadY + (i & 1), i >> 1);
             }
-            sh.wait(kFullXY, i);
+            if (made) sh.wait(kFullXY, A.tma ? 0 : i);
             tc::fence_after();
             if (elect()) {
-                issue_scores<D>(W.tmem, base + S::x, base + S::y);
+                issue_scores<D>(W.tmem, base + S::x, base + S::y(i));
                 tc::commit(sh.bars + kBarP);
+                tc::commit(sh.bars + kFreeY + (i & 1));
             }
         }
         if (i > 0) output(i - 1);
         if (warp == kScoreIssuer) {
-            if (i > 0) sh.wait(kFreeXS, i - 1);
+            if (i > 0) sh.wait(kFreeO, i - 1);
             sh.wait(kFullS, i);
             tc::fence_after();
             if (elect()) {
@@ -629,8 +657,7 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
             }
         }
         sh.wait(kFullG, i);
-        const float gh = g.hi[row], gl = g.lo[row];
-        c2 = A.run.co * g.e[row];
+        const float gh = g.hi[row], gl = g.lo[row], eg = g.e[row];
         sh.wait(kBarP, i);
         tc::fence_after();
         // P' in the place of P: every 32 columns become 16 of hi words and 16 of lo words
@@ -643,11 +670,18 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
             } else {
                 float p[32];
                 tc::ld32(lanes + kColP + 32 * b, p);
-                if (b != quarter) {
-                    const int last = W.reverse ? 32 * b : 32 * b + 31;
-                    const float rf = ex2((gh - g.hi[last]) + (gl - g.lo[last]));
+                const int last = W.reverse ? 32 * b : 32 * b + 31, first = W.reverse ? 32 * b + 31 : 32 * b;
+                // columns that the walk has met: all of them, or of the diagonal block those of the lanes below and this one (backwards, above)
+                const uint32_t met = b != quarter ? 0xffffffffu : W.reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+                // a factor of the row and one of the column, where both are far from fp32's limits
+                if (b != quarter || fabsf(g.hi[first] - g.hi[last]) < kMostSpan) {
+                    const float rf = ex2((gh - g.hi[last]) + (gl - g.lo[last])) * A.run.cs;
                     const f2 rr = pack2(rf, rf);
                     tc::wait_ld();
+                    if (b == quarter) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) p[e] = met >> e & 1 ? p[e] : 0.f;
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(g.c + 32 * b + e);
@@ -655,14 +689,12 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
                         split2(mul2(pack2(p[e + 2], p[e + 3]), mul2(rr, c.y)), ph[e / 2 + 1], pl[e / 2 + 1]);
                     }
                 } else {
-                    // columns that the walk has met: the lanes below and this one, or this one and those above
-                    const uint32_t met = W.reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
                     tc::wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float2 uh = *reinterpret_cast<const float2*>(g.hi + 32 * b + e), ul = *reinterpret_cast<const float2*>(g.lo + 32 * b + e);
-                        const float x0 = met >> e & 1 ? p[e] * ex2((gh - uh.x) + (gl - ul.x)) : 0.f;
-                        const float x1 = met >> (e + 1) & 1 ? p[e + 1] * ex2((gh - uh.y) + (gl - ul.y)) : 0.f;
+                        const float x0 = met >> e & 1 ? p[e] * (ex2((gh - uh.x) + (gl - ul.x)) * A.run.cs) : 0.f;
+                        const float x1 = met >> (e + 1) & 1 ? p[e + 1] * (ex2((gh - uh.y) + (gl - ul.y)) * A.run.cs) : 0.f;
                         split2(pack2(x0, x1), ph[e / 2], pl[e / 2]);
                     }
                 }
@@ -670,21 +702,32 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
             tc::st16(lanes + kColP + 32 * b, ph);
             tc::st16(lanes + kColP + 32 * b + 16, pl);
         }
+        sh.arrive(kFreeG);
+        // e^G X S^T
+        sh.wait(kBarXS, i);
+        tc::fence_after();
+#pragma unroll 1
+        for (int c = 0; c < H; c += 32) {
+            float o[32];
+            uint32_t u[32];
+            tc::ld32(lanes + kColO + half * H + c, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * eg);
+            tc::st32(lanes + kColO + half * H + c, u);
+        }
         tc::wait_st();
         tc::fence_before();
-        sh.arrive(kFreeG);
         group_barrier<1>();
         if (warp == kScoreIssuer) {
-            sh.wait(kFullZ, i);
+            if (A.tma) sh.wait(kLoadZ + (i & 1), i >> 1);
+            if (made) sh.wait(kFullZ, A.tma ? 0 : i);
             tc::fence_after();
             if (elect()) {
-                issue_output<D>(W.tmem, base + S::z);
+                issue_output<D>(W.tmem, base + S::z(i));
                 tc::commit(sh.bars + kBarO);
-            }
-            if (A.tma && i + 1 < W.count) {
-                sh.wait(kBarXS, i);
-                sh.wait(kBarP, i);
-                if (elect()) load_x(i + 1);
+                tc::commit(sh.bars + kFreeZ + (i & 1));
+                if (A.tma && more) load_x(i + 1);  // P and X S^T are done
             }
         }
     }
@@ -702,10 +745,15 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
     const bool has_state = row < D;
     const int yh = W.h % A.run.yh;
     auto load_y = [&](int i) {
-        load_tile<D>(base + S::y, &A.y, yh, W.token(i), sh.bars + kLoadY);
+        uint64_t* bar = sh.bars + kLoadY + (i & 1);
+        tc::mbar_expect_tx(bar, S::tile);
+        load_tile<D>(base + S::y(i), &A.y, yh, W.token(i), bar);
         if (i + 1 < W.count) prefetch_tile<D>(&A.y, yh, W.token(i + 1));
     };
-    if (warp == kStateIssuer && A.tma && W.count > 0 && elect()) load_y(0);
+    if (warp == kStateIssuer && A.tma && elect()) {
+        if (W.count > 0) load_y(0);
+        if (W.count > 1) load_y(1);
+    }
 
     // the gates of chunk i: threads in walking order
     const int r = W.reverse ? L - 1 - tid : tid;
@@ -766,7 +814,7 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
                 }
             }
         } else if (!W.part.last) {
-            load_state<D>(m, state_of(A, D, W.nh, 0), row, half * H, false);
+            load_state<D>(m, state_of(A, D, W.nh, 0), row, half * H, true);
         } else if (W.q.in >= 0) {
             load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, row, half * H, A.run.transposed_in);
         }
@@ -794,39 +842,38 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
     }
 
     for (int i = 0; i < W.count; ++i) {
-        const bool more = i + 1 < W.count;
+        const bool more = i + 1 < W.count, made = W.made(A, i);
         const int lo = W.lo(i), hi = W.hi(i);
-        const bool cut = lo > 0 || hi < L;  // rows of Y and Z that are another sequence's: zeros, since theirs may hold anything
-        if (A.tma) {
-            sh.wait(kLoadX, i);
-            sh.wait(kLoadY, i);
-        } else {
-            fill_tile<D, kGroup>(sm + S::x, head_of(A.run.x, W.h, A.run.xh, A.run.xs1), A.run.xs0, W.token(i), lo, hi, true, tid);
-        }
-        if (cut || !A.tma) {
-            fill_tile<D, kGroup>(sm + S::y, head_of(A.run.y, W.h, A.run.yh, A.run.ys1), A.run.ys0, W.token(i), lo, hi, !A.tma, tid);
+        if (A.tma) sh.wait(kLoadY + (i & 1), i >> 1);
+        if (made) {  // rows of Y and Z that are another sequence's become zeros: theirs may hold anything
+            if (!A.tma) fill_tile<D, kGroup>(sm + S::x, head_of(A.run.x, W.h, A.run.xh, A.run.xs1), A.run.xs0, W.token(i), lo, hi, true, tid);
+            fill_tile<D, kGroup>(sm + S::y(i), head_of(A.run.y, W.h, A.run.yh, A.run.ys1), A.run.ys0, W.token(i), lo, hi, !A.tma, tid);
             tc::fence_async_smem();
             group_barrier<2>();
+            sh.arrive(kFullXY);
         }
-        sh.arrive(kFullXY);
-        decayed_keys<D, kGroup>(sm, S::y, S::yh, S::yl, g.w, tid);
+        decayed_keys<D, 2>(base + S::y(i), W.tmem + kColY, g.w, quarter, half, lane);
         const float a = g.e[W.reverse ? 0 : L - 1];
-        if (A.tma) sh.wait(kLoadZ, i);
-        else if (i > 0) sh.wait(kBarO, i - 1);
-        if (cut || !A.tma) fill_tile<D, kGroup>(sm + S::z, head_of(A.run.z, W.h, A.run.zh, A.run.zs1), A.run.zs0, W.token(i), lo, hi, !A.tma, tid);
-        tc::fence_async_smem();
+        if (made) {
+            if (A.tma) sh.wait(kLoadZ + (i & 1), i >> 1);
+            else if (i > 0) sh.wait(kBarO, i - 1);
+            fill_tile<D, kGroup>(sm + S::z(i), head_of(A.run.z, W.h, A.run.zh, A.run.zs1), A.run.zs0, W.token(i), lo, hi, !A.tma, tid);
+            tc::fence_async_smem();
+            sh.arrive(kFullZ);
+        }
         tc::fence_before();
-        sh.arrive(kFullZ);
         group_barrier<2>();
         if (warp == kStateIssuer) {
+            if (A.tma) sh.wait(kLoadZ + (i & 1), i >> 1);
             tc::fence_after();
             if (elect()) {
-                issue_state<D>(W.tmem, base + S::z, base + S::yh, base + S::yl, false);
+                issue_state<D>(W.tmem + kColS, W.tmem + kColY, base + S::z(i), false);
                 tc::commit(sh.bars + kBarS);
+                tc::commit(sh.bars + kFreeZ + (i & 1));
             }
-            if (more && A.tma) {
-                sh.wait(kBarP, i);
-                if (elect()) load_y(i + 1);
+            if (A.tma && i + 2 < W.count) {
+                sh.wait(kFreeY + (i & 1), i >> 1);
+                if (elect()) load_y(i + 2);
             }
         }
         if (more) sum_gates(i + 1);
@@ -841,7 +888,7 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
             for (int e = 0; e < 32; ++e) m[c + e] = fmaf(A.run.cs, d[e], a * m[c + e]);
         }
         if (more) {
-            sh.wait(kBarP, i);
+            if (!A.tma) sh.wait(kBarP, i);  // X is filled anew
             sh.wait(kBarXS, i);
             put_state();
         }
