@@ -18,9 +18,10 @@
 // cores' own rate, is shared memory, which hands 128 bytes a cycle to all of them and the threads; so the operands that are made here are made in
 // tensor memory, Y'^T by way of transposing loads.
 //
-// Two groups of 8 warps work on a chunk side by side.  The first turns P into P', scales O's rows by e^G and writes the output; one of its
-// warps issues P and both parts of O.  The second sums the gates, makes Y' and keeps the state, and issues dS.  They meet at mbarriers
-// only, so that the tensor cores run P | X S^T, dS | P' Z of one chunk while the warps are at the others.
+// Two groups of 8 warps work on a chunk side by side.  The first turns P into P', scales O's rows by e^G and writes the output.  The second
+// makes Y' and keeps the state.  Three more warps serve them: one issues all products, in the order P, dS, X S^T, P' Z, so that no warp
+// with work of its own stands in the products' queue; one issues all loads, one the stores of whole chunks; one sums the gates.  They meet at mbarriers only.  The second
+// group makes the next chunk's Y' before it hands over the state, since dS waits for the one and only X S^T for the other.
 //
 // Decays.  G is summed in 64-bit fixed point (powers of two, 31 fraction bits) and kept as a whole and a fractional fp32 number, since
 // what is needed are small differences of sums that may be large.  e^(G_t - G_s) of 32 x 32 blocks off the diagonal is the product of a
@@ -45,19 +46,21 @@ __device__ int g_la_chunk_bad, g_la_chunk_timeout;
 
 constexpr int L = 128;         // tokens of a chunk
 constexpr int kGroup = 256;    // threads of a group
-constexpr int kThreads = 2 * kGroup;
-constexpr int kScoreIssuer = 4;  // warp of the first group that issues products: forwards it has the least to do (columns 64 .. of rows 0 .. 31 of P' are zeros)
-constexpr int kStateIssuer = 0;  // and of the second
+constexpr int kThreads = 2 * kGroup + 128;  // registers move between groups of four warps
+constexpr int kIssuer = 16, kLoader = 17, kSummer = 18, kStorer = 19;  // warps
+// Registers a thread: 96 at launch (65536 / 640); those of the serving warps go to the others: 128 x 64 + 512 x 104 = 640 x 96.
+constexpr int kFewRegisters = 64, kManyRegisters = 104;
 constexpr int kMostSegments = 16;
 constexpr uint32_t kColP = 0, kColO = 128, kColS = 256, kColY = 384, kTmemCols = 512;  // Y': 64 columns of hi words, 64 of lo
+constexpr long long kWaitClocks = 400000000;
 constexpr float kMostSpan = 60.f;  // powers of two that a block's factors may reach over
 
 struct LaChunkArgs {
-    CUtensorMap x, y, z;     // [n_tok][heads][D], boxes of 128 tokens x 1 head x 64 columns
+    CUtensorMap x, y, z, out;  // [n_tok][heads][D], boxes of 128 tokens x 1 head x 64 columns
     LaRun run;
     float *states, *decays;  // [n_seq H][segments][D D]: the state before, then each segment's contribution but the last; [n_seq H][segments]
     int segments, per;       // per sequence; chunks of one
-    int tma, vec_out;        // tma: the maps are good (rows on 16 bytes); without, threads copy element by element
+    int tma, tma_out, vec_out;  // tma: the maps are good (rows on 16 bytes); without, threads copy element by element
 };
 
 // Bytes of shared memory.
@@ -67,48 +70,52 @@ struct Smem {
     static constexpr int x = 0, sh = 5 * tile, sl = sh + D * D * 2;
     static constexpr int y(int i) { return i & 1 ? 2 * tile : tile; }
     static constexpr int z(int i) { return i & 1 ? 4 * tile : 3 * tile; }
-    static constexpr int g = 6 * tile + (D == 128 ? tile : 0);  // five arrays of L floats, then barriers
-    static constexpr int bars = g + 5 * L * 4, bytes = bars + 224;
+    static constexpr int g = 6 * tile + (D == 128 ? tile : 0);  // five arrays of L floats (Gates), then barriers
+    static constexpr int bars = g + 5 * L * 4, bytes = bars + 288;
     static_assert(sl + D * D * 2 <= g, "shared memory");
     // the first kernel: three stages of Y and Z
     static constexpr int stage(int i) { return i % 3 * 2 * tile; }
 };
 static_assert(Smem<128>::bytes <= kSmemPerCtaMax && Smem<64>::bytes <= kSmemPerCtaMax, "shared memory");
 
-// mbarriers: products done, tiles loaded, and Y read by P (one arrival each; a barrier a buffer, since a load may be under way while the one
-// before it has not arrived); handovers (one arrival a warp of a group); Z read by both its products (two).  A wait tells a phase from the
-// one before it and the one behind it, no more: whoever waits for a phase has waited for the one before it, and the phase behind it comes
-// only by way of something that this waiter does afterwards.
+// mbarriers: products done, tiles loaded, buffers that may be loaded again (one arrival each; a barrier a buffer, since a load may be under
+// way while the one before it has not arrived), then handovers (one arrival a warp).  A wait tells a phase from the one before it and the one
+// behind it, no more: whoever waits for a phase has waited for the one before it, and the phase behind it comes only by way of
+// something that this waiter does afterwards.
 enum {
-    kBarP, kBarXS, kBarS, kBarO, kLoadX, kLoadY, kLoadZ = kLoadY + 2, kFreeY = kLoadZ + 2, kSingle = kFreeY + 2,
-    kFullXY = kSingle, kFullG, kFullZ, kFullS, kFreeO, kFreeG, kFreeZ, kBars = kFreeZ + 2
+    kBarP, kBarXS, kBarS, kBarO, kLoadX, kLoadY, kLoadZ = kLoadY + 2, kFreeY = kLoadZ + 2, kFreeZ = kFreeY + 2, kSingle = kFreeZ + 2,
+    kFullXY = kSingle, kFullZ, kFullS, kFullK, kFullP, kFreeO, kFullG, kFreeG, kFullW, kFreeW = kFullW + 2, kFullOut = kFreeW + 2, kBars = kFullOut + 2
 };
-// of the first kernel
-enum { kProduct = kBarP, kStage = kLoadX };
+// of the first kernel: products and stages read, stages loaded, Y' and gates made (these two by parity)
+enum { kProduct = kBarP, kRead = kProduct + 2, kStage = kRead + 3, kMade = kSingle, kGates = kMade + 2, kTotal = kGates + 2 };
 
 struct Gates {
-    float *hi, *lo, *e, *w, *c;  // G in powers of two; e^G; e^(G_last - G); e^(G of the block's last column - G)
+    float *hi, *lo, *c;  // G in powers of two; e^(G of the block's last column - G)
+    float* w;            // two buffers of e^(G_last - G)
+    float* a;            // two of e^(G_last)
 };
 
 // What a CTA shares beside its tiles.
 struct Shared {
     uint64_t* bars;
-    long long* sums;  // 4
-    int* nans;        // 4
+    float* decay;      // two
+    long long* total;  // of a segment's gates, and whether a NaN was among them
+    int* nan;
     uint32_t* tmem;
     volatile int* failed;
     __device__ __forceinline__ explicit Shared(char* at)
-        : bars((uint64_t*)at), sums((long long*)(at + 160)), nans((int*)(at + 192)), tmem((uint32_t*)(at + 208)), failed((volatile int*)(at + 212))
+        : bars((uint64_t*)at), decay((float*)(at + 216)), total((long long*)(at + 224)), nan((int*)(at + 232)), tmem((uint32_t*)(at + 236)), failed((volatile int*)(at + 240))
     {
-        static_assert(kBars * 8 <= 160, "barriers");
+        static_assert(kBars * 8 <= 216, "barriers");
     }
-    // Until the barrier's phase is complete; gives up as tc::mbar_wait does, and at once after another wait has given up:
-    // what follows then works on what it finds, which is nobody's result, and the kernel ends.
+    // Until the barrier's phase is complete; gives up after about 0.2 s (of SM clocks: reading the wall clock takes longer than most
+    // waits here), and at once after another wait has given up: what follows then works on what it finds, which is nobody's
+    // result, and the kernel ends.
     __device__ __forceinline__ void wait(int bar, uint32_t phase) const
     {
         const uint32_t a = tc::smem_addr(bars + bar);
-        uint64_t start = 0;
-        for (uint32_t it = 0;; ++it) {
+        long long start = 0;
+        for (uint32_t it = 1;; ++it) {
             uint32_t done;
             asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
                          : "=r"(done)
@@ -117,9 +124,9 @@ struct Shared {
             if (done) return;
             if ((it & 63) == 0) {
                 if (*failed) return;
-                const uint64_t now = tc::global_ns();
-                if (it == 0) start = now;
-                else if (now - start > tc::kWaitLimitNs) {
+                const long long now = clock64();
+                if (it == 64) start = now;
+                else if (now - start > kWaitClocks) {
                     *failed = 1;
                     return;
                 }
@@ -152,10 +159,20 @@ __device__ __forceinline__ void st_16x128b(uint32_t at, const uint32_t (&r)[8])
                  "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 
-template <int ID>
+template <int ID, int T>
 __device__ __forceinline__ void group_barrier()
 {
-    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(kGroup) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(T) : "memory");
+}
+template <int R>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -193,6 +210,16 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 {
 #pragma unroll
     for (int c = 0; c < D; c += 64) tma_tile(dst + c * (L * 2), map, c, head, (int)token, tc::smem_addr(bar));
+}
+template <int D>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, int head, long long token, uint32_t from)
+{
+#pragma unroll
+    for (int c = 0; c < D; c += 64)
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c), "r"(head), "r"((int)token),
+                     "r"(from + c * (L * 2))
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 template <int D>
 __device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int head, long long token)
@@ -238,17 +265,42 @@ __device__ __forceinline__ float load_gate(const LaRun& A, const LaSequence& q, 
     return g < kLaLeastGate ? kLaLeastGate : g;
 }
 
-// Inclusive sums over a warp, and whether a NaN is among what was summed.
-__device__ __forceinline__ long long scan_warp(float gate, int lane, bool* nan)
-{
-    *nan = (__ballot_sync(kFull, gate != gate) & (0xffffffffu >> (31 - lane))) != 0;
-    long long x = gate == gate ? to_fixed(gate) : 0;
+// The running sums of a chunk's 128 gates by one warp: lane l has the walk's tokens 4 l .. 4 l + 3.
+struct GateSums {
+    long long at[4], end, all;  // after each token, after the lane's block of 32, after all
+    uint32_t nan;               // bit k: a NaN up to token k; bit 4: in the block; bit 5: anywhere
+    __device__ __forceinline__ GateSums(const float (&gate)[4], int lane)
+    {
+        bool bad = false;
+        nan = 0;
+        long long x = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(kFull, x, o);
-        if (lane >= o) x += y;
+        for (int k = 0; k < 4; ++k) {
+            bad |= gate[k] != gate[k];
+            nan |= (bad ? 1u : 0u) << k;
+            x += gate[k] == gate[k] ? to_fixed(gate[k]) : 0;
+            at[k] = x;
+        }
+        const long long own = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(kFull, x, o);
+            if (lane >= o) x += y;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) at[k] += x - own;
+        all = __shfl_sync(kFull, x, 31);
+        end = __shfl_sync(kFull, x, lane | 7);
+        const uint32_t lanes = __ballot_sync(kFull, bad);
+        if (lanes & ((1u << lane) - 1)) nan |= 15;
+        if (lanes >> (lane & 24) & 255) nan |= 16;
+        if (lanes) nan |= 32;
     }
-    return x;
+};
+// Four numbers of a lane, in walking order, to an array in the rows' order.
+__device__ __forceinline__ void put4(float* array, bool reverse, int lane, const float (&v)[4])
+{
+    *reinterpret_cast<float4*>(array + (reverse ? L - 4 - 4 * lane : 4 * lane)) = reverse ? make_float4(v[3], v[2], v[1], v[0]) : make_float4(v[0], v[1], v[2], v[3]);
 }
 
 // Y'^T = (w Y)^T as bf16 hi and lo into TMEM, by PARTS x 4 warps: a warp's 32 lanes of TMEM are columns of Y, and it takes 128 / PARTS
@@ -262,7 +314,7 @@ __device__ __forceinline__ void decayed_keys(uint32_t tile, uint32_t tmem, const
             f2 ww[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) ww[b] = *reinterpret_cast<const f2*>(w + t0 + 8 * b + 2 * (lane & 3));
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 uint32_t hi[8], lo[8];
 #pragma unroll
@@ -339,11 +391,12 @@ __device__ __forceinline__ void issue_output(uint32_t tmem, uint32_t z)
     }
 }
 
-// What both kernels begin with: barriers and tensor memory.
-__device__ __forceinline__ uint32_t begin(const Shared& sh)
+// What both kernels begin with: barriers (arrivals(i) of barrier i) and tensor memory.
+template <typename F>
+__device__ __forceinline__ uint32_t begin(const Shared& sh, F&& arrivals)
 {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kBars; ++i) tc::mbar_init(sh.bars + i, i < kSingle ? 1 : i < kFreeZ ? kGroup / 32 : 2);
+        for (int i = 0; i < kBars; ++i) tc::mbar_init(sh.bars + i, arrivals(i));
         tc::mbar_fence_init();
         *sh.failed = 0;
     }
@@ -429,8 +482,9 @@ struct Work {
         const long long left = q.hi - token(i);
         return left < L ? (int)left : L;
     }
+    __device__ __forceinline__ bool whole(int i) const { return lo(i) == 0 && hi(i) == L; }
     // Whether threads write its tiles: without TMA, and where rows are another sequence's (of TMA's, one chunk of a segment at most).
-    __device__ __forceinline__ bool made(const LaChunkArgs& A, int i) const { return !A.tma || lo(i) > 0 || hi(i) < L; }
+    __device__ __forceinline__ bool made(const LaChunkArgs& A, int i) const { return !A.tma || !whole(i); }
 };
 
 __device__ __forceinline__ const __nv_bfloat16* head_of(const void* p, int h, int heads, long long stride)
@@ -459,75 +513,91 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     if (!W.q.ok) return;  // the second kernel reports it
     W.part = part_of(A, W.q.hi - W.q.lo, W.segment);
     if (W.part.none || W.part.last) return;
-    const uint32_t tmem = begin(sh), base = tc::smem_addr(sm);
+    const uint32_t tmem = begin(sh, [](int i) { return i == kMade || i == kMade + 1 ? 16 : 1; }), base = tc::smem_addr(sm);
     const int count = (int)(W.part.c1 - W.part.c0), yh = W.h % A.run.yh, zh = W.h % A.run.zh;
     // whole chunks, from the last one back: the sequence's last one is the last segment's
     auto token = [&](int it) { return W.token(count - 1 - it); };
-    auto load = [&](int it) {
-        if (!A.tma) {
-            fill_tile<D, kThreads>(sm + S::stage(it), head_of(A.run.y, W.h, A.run.yh, A.run.ys1), A.run.ys0, token(it), 0, L, true, tid);
-            fill_tile<D, kThreads>(sm + S::stage(it) + S::tile, head_of(A.run.z, W.h, A.run.zh, A.run.zs1), A.run.zs0, token(it), 0, L, true, tid);
-        } else if (warp == 0 && elect()) {
-            uint64_t* bar = sh.bars + kStage + it % 3;
-            tc::mbar_expect_tx(bar, 2 * S::tile);
-            load_tile<D>(base + S::stage(it), &A.y, yh, token(it), bar);
-            load_tile<D>(base + S::stage(it) + S::tile, &A.z, zh, token(it), bar);
-            if (it + 1 < count) {
-                prefetch_tile<D>(&A.y, yh, token(it + 1));
-                prefetch_tile<D>(&A.z, zh, token(it + 1));
+    // two buffers of Y' and of its weights, three stages of Y and Z
+    auto keys = [&](int it) { return tmem + kColY - 128 * (it & 1); };
+    if (warp == kLoader) {
+        if (A.tma && elect()) {
+            for (int it = 0; it < count; ++it) {
+                if (it >= 3) sh.wait(kRead + it % 3, it / 3 - 1);
+                uint64_t* bar = sh.bars + kStage + it % 3;
+                tc::mbar_expect_tx(bar, 2 * S::tile);
+                load_tile<D>(base + S::stage(it), &A.y, yh, token(it), bar);
+                load_tile<D>(base + S::stage(it) + S::tile, &A.z, zh, token(it), bar);
+                if (it + 2 < count) {
+                    prefetch_tile<D>(&A.y, yh, token(it + 2));
+                    prefetch_tile<D>(&A.z, zh, token(it + 2));
+                }
             }
         }
-    };
-    const int r = W.reverse ? L - 1 - tid : tid;  // threads in walking order
-    auto gate = [&](int it) { return tid < L && it < count ? load_gate(A.run, W.q, W.h, token(it) + r, true) : 0.f; };
-    long long carry = 0;
-    bool nan = false;  // among the gates behind
-    load(0);
-    float next = gate(0);
-    // Y' in two buffers, as are the barriers of the products that read them
-    for (int it = 0; it < count; ++it) {
-        long long G = 0;
-        bool bad = false;
-        if (tid < L) {
-            G = scan_warp(next, lane, &bad);
-            if (lane == 31) {
-                sh.sums[warp] = G;
-                sh.nans[warp] = bad;
-            }
-        }
-        next = gate(it + 1);
-        if (it > 1) sh.wait(kProduct + (it & 1), (it >> 1) - 1);  // the product before the last has read Y' and its stage
-        __syncthreads();
-        if (it + 1 < count) load(it + 1);
-        long long all = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            if (b < warp) G += sh.sums[b];
-            all += sh.sums[b];
-            nan |= sh.nans[b] != 0;
-        }
-        if (tid < L) sw[r] = nan ? NAN : ex2(from_fixed(carry + (all - G)));
-        carry += all;
-        if (A.tma) sh.wait(kStage + it % 3, it / 3);
-        __syncthreads();
-        tc::fence_after();
-        const uint32_t y = tmem + kColY - 128 * (it & 1);  // the columns of Y' and, of the other kernel, dS
-        decayed_keys<D, 4>(base + S::stage(it), y, sw, warp & 3, warp >> 2, lane);
-        tc::fence_async_smem();
-        tc::fence_before();
-        __syncthreads();
-        if (warp == 0 && elect()) {
+        __syncwarp();
+    } else if (warp == kIssuer) {
+        for (int it = 0; it < count; ++it) {
+            if (A.tma) sh.wait(kStage + it % 3, it / 3);
+            sh.wait(kMade + (it & 1), it >> 1);
             tc::fence_after();
-            issue_state<D>(tmem, y, base + S::stage(it) + S::tile, it > 0);
-            tc::commit(sh.bars + kProduct + (it & 1));
+            if (elect()) {
+                issue_state<D>(tmem, keys(it), base + S::stage(it) + S::tile, it > 0);
+                tc::commit(sh.bars + kProduct + (it & 1));
+                tc::commit(sh.bars + kRead + it % 3);
+            }
+            __syncwarp();
         }
-    }
-    if (count > 1) sh.wait(kProduct + (count & 1), ((count - 2) >> 1));
-    sh.wait(kProduct + ((count - 1) & 1), (count - 1) >> 1);
-    __syncthreads();
-    if (*sh.failed) {
-        if (tid == 0) atomicOr(&g_la_chunk_timeout, 1);
-    } else {
+    } else if (warp == kSummer) {
+        long long carry = 0;
+        bool nan = false;  // among the gates behind
+        float next[4];
+        auto gates = [&](int it) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int pos = 4 * lane + k;
+                next[k] = it < count ? load_gate(A.run, W.q, W.h, token(it) + (W.reverse ? L - 1 - pos : pos), true) : 0.f;
+            }
+        };
+        gates(0);
+        for (int it = 0; it < count; ++it) {
+            const GateSums s(next, lane);
+            gates(it + 1);
+            nan |= s.nan != 0 && (s.nan & 32);
+            float w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = nan ? NAN : ex2(from_fixed(carry + (s.all - s.at[k])));
+            if (it > 1) sh.wait(kProduct + (it & 1), (it >> 1) - 1);  // its Y' has been made of the weights before these
+            put4(sw + L * (it & 1), W.reverse, lane, w);
+            carry += s.all;
+            sh.arrive(kGates + (it & 1));
+        }
+        if (lane == 0) {
+            *sh.total = carry;
+            *sh.nan = nan;
+        }
+        sh.arrive(kTotal);
+    } else if (warp < 16) {
+        for (int it = 0; it < count; ++it) {
+            const float* w = sw + L * (it & 1);
+            if (it > 1) sh.wait(kProduct + (it & 1), (it >> 1) - 1);  // the product before the last has read Y', which all warps had made
+            if (A.tma) sh.wait(kStage + it % 3, it / 3);
+            else {
+                if (it > 2) sh.wait(kRead + it % 3, it / 3 - 1);
+                fill_tile<D, 512>(sm + S::stage(it), head_of(A.run.y, W.h, A.run.yh, A.run.ys1), A.run.ys0, token(it), 0, L, true, tid);
+                fill_tile<D, 512>(sm + S::stage(it) + S::tile, head_of(A.run.z, W.h, A.run.zh, A.run.zs1), A.run.zs0, token(it), 0, L, true, tid);
+                tc::fence_async_smem();
+                group_barrier<2, 512>();
+            }
+            sh.wait(kGates + (it & 1), it >> 1);
+            tc::fence_after();
+            decayed_keys<D, 4>(base + S::stage(it), keys(it), w, warp & 3, warp >> 2, lane);
+            tc::fence_before();
+            sh.arrive(kMade + (it & 1));
+        }
+        if (count > 1) sh.wait(kProduct + (count & 1), (count - 2) >> 1);
+        sh.wait(kProduct + ((count - 1) & 1), (count - 1) >> 1);
+        sh.wait(kTotal, 0);
+        const long long carry = *sh.total;
+        const bool nan = *sh.nan != 0;
         tc::fence_after();
         constexpr int C = D / 4;  // columns of a thread
         const int row = 32 * (warp & 3) + lane, c0 = (warp >> 2) * C;
@@ -535,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
         if constexpr (C == 32) tc::ld32(tc::taddr(tmem, warp, 0) + c0, d);
         else tc::ld16(tc::taddr(tmem, warp, 0) + c0, d);
         tc::wait_ld();
-        if (row < D) {
+        if (row < D && !*sh.failed) {
             const float all = nan ? NAN : ex2(from_fixed(carry));
 #pragma unroll
             for (int i = 0; i < C; ++i) d[i] *= A.run.cs;
@@ -555,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     }
     tc::fence_before();
     __syncthreads();
+    if (tid == 0 && *sh.failed) atomicOr(&g_la_chunk_timeout, 1);
     if (warp == 0) tc::tmem_free(tmem, kTmemCols);
 }
 
@@ -573,8 +644,7 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
     using S = Smem<D>;
     constexpr int H = D / 2;  // columns of a thread's output
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_of(tid), quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
-    const uint32_t base = tc::smem_addr(sm), lanes = tc::taddr(W.tmem, warp, 0);
-    const int xh = W.h % A.run.xh, zh = W.h % A.run.zh;
+    const uint32_t lanes = tc::taddr(W.tmem, warp, 0);
 
     auto output = [&](int i) {
         sh.wait(kBarO, i);
@@ -585,7 +655,15 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
         tc::wait_ld();
         tc::fence_before();
         sh.arrive(kFreeO);
-        if (row >= W.lo(i) && row < W.hi(i)) {
+        if (A.tma_out && W.whole(i)) {
+            // through Z's buffer, which is free until the second chunk behind this one
+#pragma unroll
+            for (int e = 0; e < H; e += 8)
+                *reinterpret_cast<uint4*>(sm + S::z(i) + swizzled(row, (half * H + e) / 8)) =
+                    make_uint4(tc::pack_bf16x2(A.run.co * o[e], A.run.co * o[e + 1]), tc::pack_bf16x2(A.run.co * o[e + 2], A.run.co * o[e + 3]),
+                               tc::pack_bf16x2(A.run.co * o[e + 4], A.run.co * o[e + 5]), tc::pack_bf16x2(A.run.co * o[e + 6], A.run.co * o[e + 7]));
+            tc::fence_async_smem();
+        } else if (row >= W.lo(i) && row < W.hi(i)) {
             const long long at = ((W.token(i) + row) * A.run.H + W.h) * D + half * H;
 #pragma unroll
             for (int e = 0; e < H; ++e) o[e] *= A.run.co;
@@ -610,54 +688,12 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
                 for (int e = 0; e < H; ++e) st_any(A.run.out, at + e, A.run.out_dtype, o[e]);
             }
         }
-        __syncwarp();
+        sh.arrive(kFullOut + (i & 1));
     };
-    auto load_x = [&](int i) {
-        tc::mbar_expect_tx(sh.bars + kLoadX, S::tile);
-        load_tile<D>(base + S::x, &A.x, xh, W.token(i), sh.bars + kLoadX);
-        if (i + 1 < W.count) prefetch_tile<D>(&A.x, xh, W.token(i + 1));
-    };
-    auto load_z = [&](int i) {
-        uint64_t* bar = sh.bars + kLoadZ + (i & 1);
-        tc::mbar_expect_tx(bar, S::tile);
-        load_tile<D>(base + S::z(i), &A.z, zh, W.token(i), bar);
-        if (i + 1 < W.count) prefetch_tile<D>(&A.z, zh, W.token(i + 1));
-    };
-    if (warp == kScoreIssuer && A.tma && W.count > 0 && elect()) {
-        load_x(0);
-        load_z(0);
-    }
-
     for (int i = 0; i < W.count; ++i) {
-        const bool more = i + 1 < W.count, made = W.made(A, i);
-        if (warp == kScoreIssuer) {
-            if (i > 0) sh.wait(kBarO, i - 1);  // P' has been read
-            if (A.tma) {
-                if (i > 0 && more) sh.wait(kFreeZ + ((i + 1) & 1), (i - 1) >> 1);
-                if (more && elect()) load_z(i + 1);
-                sh.wait(kLoadX, i);
-                sh.wait(kLoadY + (i & 1), i >> 1);
-            }
-            if (made) sh.wait(kFullXY, A.tma ? 0 : i);
-            tc::fence_after();
-            if (elect()) {
-                issue_scores<D>(W.tmem, base + S::x, base + S::y(i));
-                tc::commit(sh.bars + kBarP);
-                tc::commit(sh.bars + kFreeY + (i & 1));
-            }
-        }
         if (i > 0) output(i - 1);
-        if (warp == kScoreIssuer) {
-            if (i > 0) sh.wait(kFreeO, i - 1);
-            sh.wait(kFullS, i);
-            tc::fence_after();
-            if (elect()) {
-                issue_state_output<D>(W.tmem, base + S::x, base + S::sh, base + S::sl);
-                tc::commit(sh.bars + kBarXS);
-            }
-        }
         sh.wait(kFullG, i);
-        const float gh = g.hi[row], gl = g.lo[row], eg = g.e[row];
+        const float gh = g.hi[row], gl = g.lo[row], eg = ex2(gh + gl);
         sh.wait(kBarP, i);
         tc::fence_after();
         // P' in the place of P: every 32 columns become 16 of hi words and 16 of lo words
@@ -718,18 +754,7 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
         }
         tc::wait_st();
         tc::fence_before();
-        group_barrier<1>();
-        if (warp == kScoreIssuer) {
-            if (A.tma) sh.wait(kLoadZ + (i & 1), i >> 1);
-            if (made) sh.wait(kFullZ, A.tma ? 0 : i);
-            tc::fence_after();
-            if (elect()) {
-                issue_output<D>(W.tmem, base + S::z(i));
-                tc::commit(sh.bars + kBarO);
-                tc::commit(sh.bars + kFreeZ + (i & 1));
-                if (A.tma && more) load_x(i + 1);  // P and X S^T are done
-            }
-        }
+        sh.arrive(kFullP);
     }
     if (W.count > 0) output(W.count - 1);
 }
@@ -743,58 +768,6 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
     const int tid = threadIdx.x - kGroup, lane = tid & 31, warp = warp_of(tid), quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
     const uint32_t base = tc::smem_addr(sm), lanes = tc::taddr(W.tmem, warp, 0);
     const bool has_state = row < D;
-    const int yh = W.h % A.run.yh;
-    auto load_y = [&](int i) {
-        uint64_t* bar = sh.bars + kLoadY + (i & 1);
-        tc::mbar_expect_tx(bar, S::tile);
-        load_tile<D>(base + S::y(i), &A.y, yh, W.token(i), bar);
-        if (i + 1 < W.count) prefetch_tile<D>(&A.y, yh, W.token(i + 1));
-    };
-    if (warp == kStateIssuer && A.tma && elect()) {
-        if (W.count > 0) load_y(0);
-        if (W.count > 1) load_y(1);
-    }
-
-    // the gates of chunk i: threads in walking order
-    const int r = W.reverse ? L - 1 - tid : tid;
-    auto gate = [&](int i) { return tid < L && i < W.count ? load_gate(A.run, W.q, W.h, W.token(i) + r, r >= W.lo(i) && r < W.hi(i)) : 0.f; };
-    float next = gate(0);
-    auto sum_gates = [&](int i) {
-        long long G = 0;
-        bool nan = false;
-        if (tid < L) {
-            G = scan_warp(next, lane, &nan);
-            if (lane == 31) {
-                sh.sums[warp] = G;
-                sh.nans[warp] = nan;
-            }
-        }
-        next = gate(i + 1);
-        if (i > 0) sh.wait(kFreeG, i - 1);
-        group_barrier<2>();
-        if (tid < L) {
-            long long all = 0, before = 0;
-            bool any = false;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b < warp) {
-                    before += sh.sums[b];
-                    nan |= sh.nans[b] != 0;
-                }
-                all += sh.sums[b];
-                any |= sh.nans[b] != 0;
-            }
-            const long long end = before + sh.sums[warp];  // of this block of 32
-            G += before;
-            g.hi[r] = nan ? NAN : whole_of(G);
-            g.lo[r] = fraction_of(G);
-            g.e[r] = nan ? NAN : ex2(from_fixed(G));
-            g.w[r] = any ? NAN : ex2(from_fixed(all - G));
-            g.c[r] = sh.nans[warp] ? NAN : ex2(from_fixed(end - G));
-        }
-        group_barrier<2>();
-        sh.arrive(kFullG);
-    };
 
     float m[H];
 #pragma unroll
@@ -836,24 +809,24 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
         tc::fence_async_smem();
         sh.arrive(kFullS);
     };
-    if (W.count > 0) {
-        put_state();
-        sum_gates(0);
-    }
-
     for (int i = 0; i < W.count; ++i) {
-        const bool more = i + 1 < W.count, made = W.made(A, i);
+        const bool made = W.made(A, i);
         const int lo = W.lo(i), hi = W.hi(i);
         if (A.tma) sh.wait(kLoadY + (i & 1), i >> 1);
         if (made) {  // rows of Y and Z that are another sequence's become zeros: theirs may hold anything
+            if (!A.tma && i > 0) sh.wait(kBarXS, i - 1);
             if (!A.tma) fill_tile<D, kGroup>(sm + S::x, head_of(A.run.x, W.h, A.run.xh, A.run.xs1), A.run.xs0, W.token(i), lo, hi, true, tid);
             fill_tile<D, kGroup>(sm + S::y(i), head_of(A.run.y, W.h, A.run.yh, A.run.ys1), A.run.ys0, W.token(i), lo, hi, !A.tma, tid);
             tc::fence_async_smem();
-            group_barrier<2>();
+            group_barrier<2, kGroup>();
             sh.arrive(kFullXY);
         }
-        decayed_keys<D, 2>(base + S::y(i), W.tmem + kColY, g.w, quarter, half, lane);
-        const float a = g.e[W.reverse ? 0 : L - 1];
+        sh.wait(kFullW + (i & 1), i >> 1);
+        decayed_keys<D, 2>(base + S::y(i), W.tmem + kColY, g.w + L * (i & 1), quarter, half, lane);
+        const float a = g.a[i & 1];
+        tc::fence_before();
+        sh.arrive(kFullK);
+        sh.arrive(kFreeW + (i & 1));
         if (made) {
             if (A.tma) sh.wait(kLoadZ + (i & 1), i >> 1);
             else if (i > 0) sh.wait(kBarO, i - 1);
@@ -861,36 +834,17 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
             tc::fence_async_smem();
             sh.arrive(kFullZ);
         }
-        tc::fence_before();
-        group_barrier<2>();
-        if (warp == kStateIssuer) {
-            if (A.tma) sh.wait(kLoadZ + (i & 1), i >> 1);
-            tc::fence_after();
-            if (elect()) {
-                issue_state<D>(W.tmem + kColS, W.tmem + kColY, base + S::z(i), false);
-                tc::commit(sh.bars + kBarS);
-                tc::commit(sh.bars + kFreeZ + (i & 1));
-            }
-            if (A.tma && i + 2 < W.count) {
-                sh.wait(kFreeY + (i & 1), i >> 1);
-                if (elect()) load_y(i + 2);
-            }
-        }
-        if (more) sum_gates(i + 1);
+        if (A.tma && i > 0) sh.wait(kBarXS, i - 1);
+        put_state();
         sh.wait(kBarS, i);
         tc::fence_after();
 #pragma unroll
-        for (int c = 0; c < H; c += 32) {
-            float d[32];
-            tc::ld32(lanes + kColS + half * H + c, d);
+        for (int c = 0; c < H; c += 16) {
+            float d[16];
+            tc::ld16(lanes + kColS + half * H + c, d);
             tc::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) m[c + e] = fmaf(A.run.cs, d[e], a * m[c + e]);
-        }
-        if (more) {
-            if (!A.tma) sh.wait(kBarP, i);  // X is filled anew
-            sh.wait(kBarXS, i);
-            put_state();
+            for (int e = 0; e < 16; ++e) m[c + e] = fmaf(A.run.cs, d[e], a * m[c + e]);
         }
     }
     if (has_state && W.part.last && W.q.out >= 0 && !*sh.failed) {
@@ -903,6 +857,125 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
     }
 }
 
+// The warp that issues all products of the segment, in order.
+template <int D>
+__device__ __forceinline__ void products(const LaChunkArgs& A, const Work& W, uint32_t base, const Shared& sh)
+{
+    using S = Smem<D>;
+    for (int i = 0; i < W.count; ++i) {
+        const bool made = W.made(A, i);
+        if (i > 0) sh.wait(kBarO, i - 1);  // P' has been read
+        if (A.tma) {
+            sh.wait(kLoadX, i);
+            sh.wait(kLoadY + (i & 1), i >> 1);
+        }
+        if (made) sh.wait(kFullXY, A.tma ? 0 : i);
+        tc::fence_after();
+        if (elect()) {
+            issue_scores<D>(W.tmem, base + S::x, base + S::y(i));
+            tc::commit(sh.bars + kBarP);
+        }
+        __syncwarp();
+        if (A.tma) sh.wait(kLoadZ + (i & 1), i >> 1);
+        if (made) sh.wait(kFullZ, A.tma ? 0 : i);
+        sh.wait(kFullK, i);
+        tc::fence_after();
+        if (elect()) {
+            issue_state<D>(W.tmem + kColS, W.tmem + kColY, base + S::z(i), false);
+            tc::commit(sh.bars + kBarS);
+            tc::commit(sh.bars + kFreeY + (i & 1));
+        }
+        __syncwarp();
+        if (i > 0) sh.wait(kFreeO, i - 1);
+        sh.wait(kFullS, i);
+        tc::fence_after();
+        if (elect()) {
+            issue_state_output<D>(W.tmem, base + S::x, base + S::sh, base + S::sl);
+            tc::commit(sh.bars + kBarXS);
+        }
+        __syncwarp();
+        sh.wait(kFullP, i);
+        tc::fence_after();
+        if (elect()) {
+            issue_output<D>(W.tmem, base + S::z(i));
+            tc::commit(sh.bars + kBarO);
+        }
+        __syncwarp();
+    }
+}
+
+// The thread that stores whole chunks, and frees Z's buffers.
+template <int D>
+__device__ __forceinline__ void stores(const LaChunkArgs& A, const Work& W, uint32_t base, const Shared& sh)
+{
+    for (int i = 0; i < W.count; ++i) {
+        sh.wait(kFullOut + (i & 1), i >> 1);
+        if (A.tma_out && W.whole(i)) {
+            store_tile<D>(&A.out, W.h, W.token(i), base + Smem<D>::z(i));
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        tc::mbar_arrive(sh.bars + kFreeZ + (i & 1));
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// The warp that sums the gates.
+__device__ __forceinline__ void sum_gates(const LaChunkArgs& A, const Work& W, const Shared& sh, const Gates& g)
+{
+    const int lane = threadIdx.x & 31;
+    float next[4];
+    auto gates = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int pos = 4 * lane + k, r = W.reverse ? L - 1 - pos : pos;
+            next[k] = i < W.count ? load_gate(A.run, W.q, W.h, W.token(i) + r, r >= W.lo(i) && r < W.hi(i)) : 0.f;
+        }
+    };
+    gates(0);
+    for (int i = 0; i < W.count; ++i) {
+        const GateSums s(next, lane);
+        gates(i + 1);
+        float hi[4], lo[4], w[4], c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            hi[k] = s.nan >> k & 1 ? NAN : whole_of(s.at[k]);
+            lo[k] = fraction_of(s.at[k]);
+            w[k] = s.nan & 32 ? NAN : ex2(from_fixed(s.all - s.at[k]));
+            c[k] = s.nan & 16 ? NAN : ex2(from_fixed(s.end - s.at[k]));
+        }
+        if (i > 1) sh.wait(kFreeW + (i & 1), (i >> 1) - 1);
+        put4(g.w + L * (i & 1), W.reverse, lane, w);
+        if (lane == 0) g.a[i & 1] = s.nan & 32 ? NAN : ex2(from_fixed(s.all));
+        sh.arrive(kFullW + (i & 1));
+        if (i > 0) sh.wait(kFreeG, i - 1);
+        put4(g.hi, W.reverse, lane, hi);
+        put4(g.lo, W.reverse, lane, lo);
+        put4(g.c, W.reverse, lane, c);
+        sh.arrive(kFullG);
+    }
+}
+
+// The thread that issues all loads.
+template <int D>
+__device__ __forceinline__ void loads(const LaChunkArgs& A, const Work& W, uint32_t base, const Shared& sh)
+{
+    using S = Smem<D>;
+    const int xh = W.h % A.run.xh, yh = W.h % A.run.yh, zh = W.h % A.run.zh;
+    auto load = [&](uint32_t to, const CUtensorMap* map, int head, int i, int bar) {
+        tc::mbar_expect_tx(sh.bars + bar, S::tile);
+        load_tile<D>(to, map, head, W.token(i), sh.bars + bar);
+        if (i + 1 < W.count) prefetch_tile<D>(map, head, W.token(i + 1));
+    };
+    for (int i = 0; i < W.count; ++i) {
+        if (i > 1) sh.wait(kFreeY + (i & 1), (i >> 1) - 1);
+        load(base + S::y(i), &A.y, yh, i, kLoadY + (i & 1));
+        if (i > 0) sh.wait(kBarXS, i - 1);
+        load(base + S::x, &A.x, xh, i, kLoadX);
+        if (i > 1) sh.wait(kFreeZ + (i & 1), (i >> 1) - 1);
+        load(base + S::z(i), &A.z, zh, i, kLoadZ + (i & 1));
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_constant__ LaChunkArgs A)
 {
@@ -910,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_cons
     extern __shared__ __align__(1024) char sm[];
     const Shared sh(sm + S::bars);
     float* g0 = reinterpret_cast<float*>(sm + S::g);
-    const Gates g = {g0, g0 + L, g0 + 2 * L, g0 + 3 * L, g0 + 4 * L};
+    const Gates g = {g0, g0 + L, g0 + 2 * L, g0 + 3 * L, sh.decay};
     Work W;
     W.nh = blockIdx.x / A.segments;
     W.segment = blockIdx.x - W.nh * A.segments;
@@ -926,9 +999,22 @@ __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_cons
     W.part = part_of(A, W.q.hi - W.q.lo, W.segment);
     if (W.part.none) return;
     W.count = W.part.c1 > W.part.c0 ? (int)(W.part.c1 - W.part.c0) : 0;
-    W.tmem = begin(sh);
-    if (threadIdx.x < kGroup) scores<D>(A, W, sm, sh, g);
-    else states<D>(A, W, sm, sh, g);
+    W.tmem = begin(sh, [](int i) { return i < kSingle || i == kFullG || i == kFullW || i == kFullW + 1 ? 1 : 8; });
+    const int warp = warp_of(threadIdx.x);
+    if (warp < 8) {
+        more_registers<kManyRegisters>();
+        scores<D>(A, W, sm, sh, g);
+    } else if (warp < 16) {
+        more_registers<kManyRegisters>();
+        states<D>(A, W, sm, sh, g);
+    } else {
+        fewer_registers<kFewRegisters>();
+        if (warp == kIssuer) products<D>(A, W, tc::smem_addr(sm), sh);
+        if (warp == kSummer) sum_gates(A, W, sh, g);
+        if (warp == kLoader && A.tma && elect()) loads<D>(A, W, tc::smem_addr(sm), sh);
+        if (warp == kStorer && elect()) stores<D>(A, W, tc::smem_addr(sm), sh);
+        __syncwarp();
+    }
     tc::fence_before();
     __syncthreads();
     if (*sh.failed && threadIdx.x == 0) atomicOr(&g_la_chunk_timeout, 1);
@@ -1004,6 +1090,7 @@ int launch_la_chunk(const LaRun& run, void* workspace, cudaStream_t st)
     A.decays = A.states + (long long)run.n_seq * run.H * A.segments * run.DK * run.DV;
     A.tma = make_map(&A.x, run.x, run.xs0, run.xs1, run.xh, run.n_tok, run.DK) && make_map(&A.y, run.y, run.ys0, run.ys1, run.yh, run.n_tok, run.DK) &&
             make_map(&A.z, run.z, run.zs0, run.zs1, run.zh, run.n_tok, run.DV);
+    A.tma_out = A.tma && run.out_dtype == GDN_BF16 && make_map(&A.out, run.out, (long long)run.H * run.DV, run.DV, run.H, run.n_tok, run.DV);
     A.vec_out = (uintptr_t)run.out % 32 == 0;
     return run.DK == 128 ? launch<128>(A, st) : launch<64>(A, st);
 }
