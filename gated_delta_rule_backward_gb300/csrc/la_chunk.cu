@@ -7,21 +7,21 @@
 // A call backwards in time walks its tokens, and with them the tiles' rows, from the last one on, each token decaying by
 // the gate of the one behind it; nothing else changes.
 //
-// One CTA owns a state (D x D, fp32, in registers) and walks the chunks of a
+// One CTA owns a state (D x D, fp32, transposed in TMEM) and walks the chunks of a
 // sequence's segment.  X, Y and Z arrive by TMA as they are stored, rows of 64 columns in 128-byte swizzle.  Products with a
 // contraction over columns read a tile K-major, those over tokens read the same bytes MN-major:
 //     P   = X Y^T          128 x 128, K = D     X, Y as stored: exact
 //     O   = X S^T          128 x D,   K = D     S as bf16 hi + lo in shared memory: 2 passes
 //     O   <- e^G O + P' Z  128 x D,   K = 128   P' (with cs) as bf16 hi + lo in TMEM, in P's columns: 2 passes
-//     dS^T = Y'^T Z        D x D,     K = 128   Y'^T as bf16 hi + lo in TMEM: 2 passes
+//     S^T <- a S^T + Y'^T Z  D x D,   K = 128   Y'^T (with cs) as bf16 hi + lo in TMEM: 2 passes
 // hi + lo carries 16 significant bits (2^-16 relative); the accumulators and the state are fp32.  What bounds the products, beside the tensor
 // cores' own rate, is shared memory, which hands 128 bytes a cycle to all of them and the threads; so the operands that are made here are made in
 // tensor memory, Y'^T by way of transposing loads.
 //
 // Two groups of 8 warps work on a chunk side by side.  The first turns P into P', scales O's rows by e^G and writes the output.  The second
-// makes Y' and keeps the state.  Three more warps serve them: one issues all products, in the order P, dS, X S^T, P' Z, so that no warp
-// with work of its own stands in the products' queue; one issues all loads, one the stores of whole chunks; one sums the gates.  They meet at mbarriers only.  The second
-// group makes the next chunk's Y' before it hands over the state, since dS waits for the one and only X S^T for the other.
+// makes Y' and keeps the state.  Three more warps serve them: one issues all products, in the order P, X S^T, dS, P' Z, so that no warp
+// with work of its own stands in the products' queue; one issues all loads, one the stores of whole chunks; one sums the gates.  They meet at mbarriers only.  Loops over
+// columns are rolled where registers allow: what the warps lacked most with all of it unrolled was instructions.
 //
 // Decays.  G is summed in 64-bit fixed point (powers of two, 31 fraction bits) and kept as a whole and a fractional fp32 number, since
 // what is needed are small differences of sums that may be large.  e^(G_t - G_s) of 32 x 32 blocks off the diagonal is the product of a
@@ -48,11 +48,9 @@ constexpr int L = 128;         // tokens of a chunk
 constexpr int kGroup = 256;    // threads of a group
 constexpr int kThreads = 2 * kGroup + 128;  // registers move between groups of four warps
 constexpr int kIssuer = 16, kLoader = 17, kSummer = 18, kStorer = 19;  // warps
-// Registers a thread: 96 at launch (65536 / 640); those of the serving warps go to the others: 128 x 64 + 512 x 104 = 640 x 96.
-constexpr int kFewRegisters = 64, kManyRegisters = 104;
 constexpr int kMostSegments = 16;
 constexpr uint32_t kColP = 0, kColO = 128, kColS = 256, kColY = 384, kTmemCols = 512;  // Y': 64 columns of hi words, 64 of lo
-constexpr long long kWaitClocks = 400000000;
+constexpr uint32_t kWaitClocks = 400000000, kLookClocks = 20000;
 constexpr float kMostSpan = 60.f;  // powers of two that a block's factors may reach over
 
 struct LaChunkArgs {
@@ -91,7 +89,7 @@ enum { kProduct = kBarP, kRead = kProduct + 2, kStage = kRead + 3, kMade = kSing
 
 struct Gates {
     float *hi, *lo, *c;  // G in powers of two; e^(G of the block's last column - G)
-    float* w;            // two buffers of e^(G_last - G)
+    float* w;            // two buffers of cs e^(G_last - G)
     float* a;            // two of e^(G_last)
 };
 
@@ -109,24 +107,23 @@ struct Shared {
         static_assert(kBars * 8 <= 216, "barriers");
     }
     // Until the barrier's phase is complete; gives up after about 0.2 s (of SM clocks: reading the wall clock takes longer than most
-    // waits here), and at once after another wait has given up: what follows then works on what it finds, which is nobody's
+    // waits here), and soon after another wait has given up: what follows then works on what it finds, which is nobody's
     // result, and the kernel ends.
     __device__ __forceinline__ void wait(int bar, uint32_t phase) const
     {
         const uint32_t a = tc::smem_addr(bars + bar);
-        long long start = 0;
-        for (uint32_t it = 1;; ++it) {
+        const uint32_t start = clock();
+        for (;;) {
             uint32_t done;
             asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
                          : "=r"(done)
                          : "r"(a), "r"(phase & 1)
                          : "memory");
             if (done) return;
-            if ((it & 63) == 0) {
+            const uint32_t now = (uint32_t)clock() - start;
+            if (now > kLookClocks) {
                 if (*failed) return;
-                const long long now = clock64();
-                if (it == 64) start = now;
-                else if (now - start > kWaitClocks) {
+                if (now > kWaitClocks) {
                     *failed = 1;
                     return;
                 }
@@ -164,17 +161,6 @@ __device__ __forceinline__ void group_barrier()
 {
     asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(T) : "memory");
 }
-template <int R>
-__device__ __forceinline__ void more_registers()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void fewer_registers()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-
 __device__ __forceinline__ float ex2(float x)
 {
     float r;
@@ -257,20 +243,40 @@ __device__ __forceinline__ float whole_of(long long x) { return (float)(int)(x >
 __device__ __forceinline__ float fraction_of(long long x) { return (float)(int)(x & 0x7fffffff) * 4.65661287e-10f; }
 __device__ __forceinline__ float from_fixed(long long x) { return whole_of(x) + fraction_of(x); }
 
-// The gate before the token at `row` enters (0 where there is none: rows that are not real, and backwards behind the last).
-__device__ __forceinline__ float load_gate(const LaRun& A, const LaSequence& q, int h, long long row, bool real)
-{
-    if (!real || (A.reverse && row + 1 >= q.hi)) return 0.f;
-    const float g = ld_any(A.g, (row + A.reverse) * A.gs0 + h * A.gs1, A.gate_dtype);
-    return g < kLaLeastGate ? kLaLeastGate : g;
-}
+// A lane's four gates of a chunk whose row 0 is the token `first`: those that enter before the walk's tokens 4 l .. 4 l + 3, for rows in [lo, hi)
+// (0 elsewhere, and backwards behind the sequence's last token).  They are kept as stored until they are summed, so that loads are under way together.
+struct RawGates {
+    uint32_t v[4];
+    __device__ __forceinline__ void load(const LaRun& A, const LaSequence& q, int h, long long first, int lo, int hi, int lane)
+    {
+        const char* p = (const char*)A.g;
+        const long long at = (first + A.reverse) * A.gs0 + h * A.gs1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int pos = 4 * lane + k, r = A.reverse ? L - 1 - pos : pos;
+            const bool real = r >= lo && r < hi && !(A.reverse && first + r + 1 >= q.hi);
+            v[k] = 0;
+            if (real) v[k] = A.gate_dtype == GDN_F32 ? ((const uint32_t*)p)[at + r * A.gs0] : ((const uint16_t*)p)[at + r * A.gs0];
+        }
+    }
+    __device__ __forceinline__ float get(int k, int dtype) const
+    {
+        float g = __uint_as_float(v[k]);
+        if (dtype == GDN_BF16) g = __uint_as_float(v[k] << 16);
+        if (dtype == GDN_F16) g = __half2float(__ushort_as_half((unsigned short)v[k]));
+        return g < kLaLeastGate ? kLaLeastGate : g;
+    }
+};
 
 // The running sums of a chunk's 128 gates by one warp: lane l has the walk's tokens 4 l .. 4 l + 3.
 struct GateSums {
     long long at[4], end, all;  // after each token, after the lane's block of 32, after all
     uint32_t nan;               // bit k: a NaN up to token k; bit 4: in the block; bit 5: anywhere
-    __device__ __forceinline__ GateSums(const float (&gate)[4], int lane)
+    __device__ __forceinline__ GateSums(const RawGates& raw, int dtype, int lane)
     {
+        float gate[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gate[k] = raw.get(k, dtype);
         bool bad = false;
         nan = 0;
         long long x = 0;
@@ -353,7 +359,7 @@ __device__ __forceinline__ void issue_state(uint32_t to, uint32_t y, uint32_t z,
 {
     constexpr uint32_t idesc = tc::idesc_bf16(D) | kTransposedB;
     const uint64_t b = swizzled_mn(z);
-#pragma unroll
+#pragma unroll 4
     for (int s = 0; s < L / 16; ++s) {
         tc::mma_ts16(to, y + 8 * s, b + step_mn(s), idesc, accumulate || s > 0);
         tc::mma_ts16(to, y + 64 + 8 * s, b + step_mn(s), idesc, 1);
@@ -383,7 +389,7 @@ __device__ __forceinline__ void issue_output(uint32_t tmem, uint32_t z)
 {
     constexpr uint32_t idesc = tc::idesc_bf16(D) | kTransposedB;
     const uint64_t b = swizzled_mn(z);
-#pragma unroll
+#pragma unroll 4
     for (int s = 0; s < L / 16; ++s) {
         const uint32_t a = tmem + kColP + 32 * (s >> 1) + 8 * (s & 1);
         tc::mma_ts16(tmem + kColO, a, b + step_mn(s), idesc, 1);
@@ -549,18 +555,16 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     } else if (warp == kSummer) {
         long long carry = 0;
         bool nan = false;  // among the gates behind
-        float next[4];
-        auto gates = [&](int it) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int pos = 4 * lane + k;
-                next[k] = it < count ? load_gate(A.run, W.q, W.h, token(it) + (W.reverse ? L - 1 - pos : pos), true) : 0.f;
-            }
+        RawGates next[2];  // of this chunk and the one behind it
+        auto gates = [&](RawGates& to, int it) {
+            if (it < count) to.load(A.run, W.q, W.h, token(it), 0, L, lane);
         };
-        gates(0);
+        gates(next[0], 0);
+        gates(next[1], 1);
         for (int it = 0; it < count; ++it) {
-            const GateSums s(next, lane);
-            gates(it + 1);
+            const GateSums s(next[0], A.run.gate_dtype, lane);
+            next[0] = next[1];
+            gates(next[1], it + 2);
             nan |= s.nan != 0 && (s.nan & 32);
             float w[4];
 #pragma unroll
@@ -655,39 +659,41 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
         tc::wait_ld();
         tc::fence_before();
         sh.arrive(kFreeO);
-        if (A.tma_out && W.whole(i)) {
+        const bool staged = A.tma_out && W.whole(i);
+        if (staged) {
             // through Z's buffer, which is free until the second chunk behind this one
 #pragma unroll
-            for (int e = 0; e < H; e += 8)
-                *reinterpret_cast<uint4*>(sm + S::z(i) + swizzled(row, (half * H + e) / 8)) =
-                    make_uint4(tc::pack_bf16x2(A.run.co * o[e], A.run.co * o[e + 1]), tc::pack_bf16x2(A.run.co * o[e + 2], A.run.co * o[e + 3]),
-                               tc::pack_bf16x2(A.run.co * o[e + 4], A.run.co * o[e + 5]), tc::pack_bf16x2(A.run.co * o[e + 6], A.run.co * o[e + 7]));
-            tc::fence_async_smem();
+            for (int e = 0; e < H; e += 8) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = tc::pack_bf16x2(A.run.co * o[e + 2 * k], A.run.co * o[e + 2 * k + 1]);
+                *reinterpret_cast<uint4*>(sm + S::z(i) + swizzled(row, (half * H + e) / 8)) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
         } else if (row >= W.lo(i) && row < W.hi(i)) {
             const long long at = ((W.token(i) + row) * A.run.H + W.h) * D + half * H;
-#pragma unroll
-            for (int e = 0; e < H; ++e) o[e] *= A.run.co;
-            if (A.vec_out && A.run.out_dtype == GDN_BF16) {
-#pragma unroll
-                for (int e = 0; e < H; e += 16) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = tc::pack_bf16x2(o[e + 2 * k], o[e + 2 * k + 1]);
-                    st_global32((__nv_bfloat16*)A.run.out + at + e, v);
-                }
-            } else if (A.vec_out && A.run.out_dtype == GDN_F32) {
+            if (A.vec_out && A.run.out_dtype == GDN_F32) {
 #pragma unroll
                 for (int e = 0; e < H; e += 8) {
                     uint32_t v[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[e + k]);
+                    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(A.run.co * o[e + k]);
                     st_global32((float*)A.run.out + at + e, v);
+                }
+            } else if (A.vec_out && A.run.out_dtype == GDN_BF16) {
+#pragma unroll
+                for (int e = 0; e < H; e += 16) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = tc::pack_bf16x2(A.run.co * o[e + 2 * k], A.run.co * o[e + 2 * k + 1]);
+                    st_global32((__nv_bfloat16*)A.run.out + at + e, v);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < H; ++e) st_any(A.run.out, at + e, A.run.out_dtype, o[e]);
+                for (int e = 0; e < H; ++e) st_any(A.run.out, at + e, A.run.out_dtype, A.run.co * o[e]);
             }
         }
+        __syncwarp();
+        if (staged) tc::fence_async_smem();
         sh.arrive(kFullOut + (i & 1));
     };
     for (int i = 0; i < W.count; ++i) {
@@ -769,46 +775,35 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
     const uint32_t base = tc::smem_addr(sm), lanes = tc::taddr(W.tmem, warp, 0);
     const bool has_state = row < D;
 
-    float m[H];
+    // the state before the segment
+#pragma unroll 1
+    for (int c = half * H; c < half * H + H; c += 16) {
+        float m[16];
 #pragma unroll
-    for (int i = 0; i < H; ++i) m[i] = 0.f;
-    if (has_state) {
-        if (W.segment > 0) {
-            for (int s = 1; s <= W.segment; ++s) {
-                const float a = s > 1 ? A.decays[W.nh * A.segments + s] : 0.f;
-                const float4* from = reinterpret_cast<const float4*>(state_of(A, D, W.nh, s) + row * D + half * H);
-#pragma unroll
-                for (int i = 0; i < H; i += 4) {
-                    const float4 d = from[i / 4];
-                    m[i] = s > 1 ? fmaf(a, m[i], d.x) : d.x;
-                    m[i + 1] = s > 1 ? fmaf(a, m[i + 1], d.y) : d.y;
-                    m[i + 2] = s > 1 ? fmaf(a, m[i + 2], d.z) : d.z;
-                    m[i + 3] = s > 1 ? fmaf(a, m[i + 3], d.w) : d.w;
-                }
-            }
-        } else if (!W.part.last) {
-            load_state<D>(m, state_of(A, D, W.nh, 0), row, half * H, true);
-        } else if (W.q.in >= 0) {
-            load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, row, half * H, A.run.transposed_in);
-        }
-    }
-    auto put_state = [&]() {
+        for (int e = 0; e < 16; ++e) m[e] = 0.f;
         if (has_state) {
+            if (W.segment > 0) {
+#pragma unroll 1
+                for (int s = 1; s <= W.segment; ++s) {
+                    float d[16];
+                    load_state<D>(d, state_of(A, D, W.nh, s), row, c, true);
+                    const float a = s > 1 ? A.decays[W.nh * A.segments + s] : 0.f;
 #pragma unroll
-            for (int i = 0; i < H; i += 8) {
-                uint4 hi, lo;
-                split2(pack2(m[i], m[i + 1]), hi.x, lo.x);
-                split2(pack2(m[i + 2], m[i + 3]), hi.y, lo.y);
-                split2(pack2(m[i + 4], m[i + 5]), hi.z, lo.z);
-                split2(pack2(m[i + 6], m[i + 7]), hi.w, lo.w);
-                const int at = ((row >> 3) * (D / 8) + (half * H + i) / 8) * 128 + (row & 7) * 16;
-                *reinterpret_cast<uint4*>(sm + S::sh + at) = hi;
-                *reinterpret_cast<uint4*>(sm + S::sl + at) = lo;
+                    for (int e = 0; e < 16; ++e) m[e] = s > 1 ? fmaf(a, m[e], d[e]) : d[e];
+                }
+            } else if (!W.part.last) {
+                load_state<D>(m, state_of(A, D, W.nh, 0), row, c, true);
+            } else if (W.q.in >= 0) {
+                load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, row, c, A.run.transposed_in);
             }
         }
-        tc::fence_async_smem();
-        sh.arrive(kFullS);
-    };
+        uint32_t u[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(m[e]);
+        tc::st16(lanes + kColS + c, u);
+    }
+    tc::wait_st();
+
     for (int i = 0; i < W.count; ++i) {
         const bool made = W.made(A, i);
         const int lo = W.lo(i), hi = W.hi(i);
@@ -822,8 +817,41 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
             sh.arrive(kFullXY);
         }
         sh.wait(kFullW + (i & 1), i >> 1);
-        decayed_keys<D, 2>(base + S::y(i), W.tmem + kColY, g.w + L * (i & 1), quarter, half, lane);
         const float a = g.a[i & 1];
+        const f2 aa = pack2(a, a);
+        // S as it enters the chunk, for X S^T; a S, for dS to be added to
+        if (A.tma && i > 0) sh.wait(kBarXS, i - 1);
+        if (32 * quarter < D) {
+#pragma unroll 1
+            for (int c = half * H; c < half * H + H; c += 16) {
+                float m[16];
+                uint32_t u[16];
+                tc::ld16(lanes + kColS + c, m);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    uint4 h, l;
+                    split2(pack2(m[e], m[e + 1]), h.x, l.x);
+                    split2(pack2(m[e + 2], m[e + 3]), h.y, l.y);
+                    split2(pack2(m[e + 4], m[e + 5]), h.z, l.z);
+                    split2(pack2(m[e + 6], m[e + 7]), h.w, l.w);
+                    const int at = ((row >> 3) * (D / 8) + (c + e) / 8) * 128 + (row & 7) * 16;
+                    *reinterpret_cast<uint4*>(sm + S::sh + at) = h;
+                    *reinterpret_cast<uint4*>(sm + S::sl + at) = l;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 v = unpack2(mul2(pack2(m[e], m[e + 1]), aa));
+                    u[e] = __float_as_uint(v.x);
+                    u[e + 1] = __float_as_uint(v.y);
+                }
+                tc::st16(lanes + kColS + c, u);
+            }
+            tc::fence_async_smem();
+        }
+        sh.arrive(kFullS);
+        decayed_keys<D, 2>(base + S::y(i), W.tmem + kColY, g.w + L * (i & 1), quarter, half, lane);
+        tc::wait_st();
         tc::fence_before();
         sh.arrive(kFullK);
         sh.arrive(kFreeW + (i & 1));
@@ -834,73 +862,57 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
             tc::fence_async_smem();
             sh.arrive(kFullZ);
         }
-        if (A.tma && i > 0) sh.wait(kBarXS, i - 1);
-        put_state();
         sh.wait(kBarS, i);
         tc::fence_after();
-#pragma unroll
-        for (int c = 0; c < H; c += 16) {
-            float d[16];
-            tc::ld16(lanes + kColS + half * H + c, d);
+    }
+    if (has_state && W.part.last && W.q.out >= 0 && !__any_sync(kFull, *sh.failed)) {
+        float a = 1.f;  // backwards, the state before the first token
+        if (W.reverse && W.q.hi > W.q.lo) a = expf(ld_any(A.run.g, W.q.lo * A.run.gs0 + W.h * A.run.gs1, A.run.gate_dtype));
+        float* to = A.run.s_out + W.q.out * A.run.out_stride + (long long)W.h * D * D;
+#pragma unroll 1
+        for (int c = half * H; c < half * H + H; c += 16) {
+            float m[16];
+            tc::ld16(lanes + kColS + c, m);
             tc::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) m[c + e] = fmaf(A.run.cs, d[e], a * m[c + e]);
+            for (int e = 0; e < 16; ++e) m[e] *= a;
+            store_state<D>(m, to, row, c, A.run.transposed_out);
         }
-    }
-    if (has_state && W.part.last && W.q.out >= 0 && !*sh.failed) {
-        if (W.reverse && W.q.hi > W.q.lo) {
-            const float a = expf(ld_any(A.run.g, W.q.lo * A.run.gs0 + W.h * A.run.gs1, A.run.gate_dtype));
-#pragma unroll
-            for (int i = 0; i < H; ++i) m[i] *= a;
-        }
-        store_state<D>(m, A.run.s_out + W.q.out * A.run.out_stride + (long long)W.h * D * D, row, half * H, A.run.transposed_out);
     }
 }
 
-// The warp that issues all products of the segment, in order.
+// The thread that issues all products of the segment, in order.
 template <int D>
 __device__ __forceinline__ void products(const LaChunkArgs& A, const Work& W, uint32_t base, const Shared& sh)
 {
     using S = Smem<D>;
     for (int i = 0; i < W.count; ++i) {
         const bool made = W.made(A, i);
-        if (i > 0) sh.wait(kBarO, i - 1);  // P' has been read
         if (A.tma) {
             sh.wait(kLoadX, i);
             sh.wait(kLoadY + (i & 1), i >> 1);
         }
         if (made) sh.wait(kFullXY, A.tma ? 0 : i);
+        if (i > 0) sh.wait(kBarO, i - 1);  // P' has been read
         tc::fence_after();
-        if (elect()) {
-            issue_scores<D>(W.tmem, base + S::x, base + S::y(i));
-            tc::commit(sh.bars + kBarP);
-        }
-        __syncwarp();
+        issue_scores<D>(W.tmem, base + S::x, base + S::y(i));
+        tc::commit(sh.bars + kBarP);
+        sh.wait(kFullS, i);
+        if (i > 0) sh.wait(kFreeO, i - 1);
+        tc::fence_after();
+        issue_state_output<D>(W.tmem, base + S::x, base + S::sh, base + S::sl);
+        tc::commit(sh.bars + kBarXS);
         if (A.tma) sh.wait(kLoadZ + (i & 1), i >> 1);
         if (made) sh.wait(kFullZ, A.tma ? 0 : i);
         sh.wait(kFullK, i);
         tc::fence_after();
-        if (elect()) {
-            issue_state<D>(W.tmem + kColS, W.tmem + kColY, base + S::z(i), false);
-            tc::commit(sh.bars + kBarS);
-            tc::commit(sh.bars + kFreeY + (i & 1));
-        }
-        __syncwarp();
-        if (i > 0) sh.wait(kFreeO, i - 1);
-        sh.wait(kFullS, i);
-        tc::fence_after();
-        if (elect()) {
-            issue_state_output<D>(W.tmem, base + S::x, base + S::sh, base + S::sl);
-            tc::commit(sh.bars + kBarXS);
-        }
-        __syncwarp();
+        issue_state<D>(W.tmem + kColS, W.tmem + kColY, base + S::z(i), true);
+        tc::commit(sh.bars + kBarS);
+        tc::commit(sh.bars + kFreeY + (i & 1));
         sh.wait(kFullP, i);
         tc::fence_after();
-        if (elect()) {
-            issue_output<D>(W.tmem, base + S::z(i));
-            tc::commit(sh.bars + kBarO);
-        }
-        __syncwarp();
+        issue_output<D>(W.tmem, base + S::z(i));
+        tc::commit(sh.bars + kBarO);
     }
 }
 
@@ -923,24 +935,22 @@ __device__ __forceinline__ void stores(const LaChunkArgs& A, const Work& W, uint
 __device__ __forceinline__ void sum_gates(const LaChunkArgs& A, const Work& W, const Shared& sh, const Gates& g)
 {
     const int lane = threadIdx.x & 31;
-    float next[4];
-    auto gates = [&](int i) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int pos = 4 * lane + k, r = W.reverse ? L - 1 - pos : pos;
-            next[k] = i < W.count ? load_gate(A.run, W.q, W.h, W.token(i) + r, r >= W.lo(i) && r < W.hi(i)) : 0.f;
-        }
+    RawGates next[2];  // of this chunk and the one behind it
+    auto gates = [&](RawGates& to, int i) {
+        if (i < W.count) to.load(A.run, W.q, W.h, W.token(i), W.lo(i), W.hi(i), lane);
     };
-    gates(0);
+    gates(next[0], 0);
+    gates(next[1], 1);
     for (int i = 0; i < W.count; ++i) {
-        const GateSums s(next, lane);
-        gates(i + 1);
+        const GateSums s(next[0], A.run.gate_dtype, lane);
+        next[0] = next[1];
+        gates(next[1], i + 2);
         float hi[4], lo[4], w[4], c[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             hi[k] = s.nan >> k & 1 ? NAN : whole_of(s.at[k]);
             lo[k] = fraction_of(s.at[k]);
-            w[k] = s.nan & 32 ? NAN : ex2(from_fixed(s.all - s.at[k]));
+            w[k] = s.nan & 32 ? NAN : A.run.cs * ex2(from_fixed(s.all - s.at[k]));
             c[k] = s.nan & 16 ? NAN : ex2(from_fixed(s.end - s.at[k]));
         }
         if (i > 1) sh.wait(kFreeW + (i & 1), (i >> 1) - 1);
@@ -964,7 +974,7 @@ __device__ __forceinline__ void loads(const LaChunkArgs& A, const Work& W, uint3
     auto load = [&](uint32_t to, const CUtensorMap* map, int head, int i, int bar) {
         tc::mbar_expect_tx(sh.bars + bar, S::tile);
         load_tile<D>(to, map, head, W.token(i), sh.bars + bar);
-        if (i + 1 < W.count) prefetch_tile<D>(map, head, W.token(i + 1));
+
     };
     for (int i = 0; i < W.count; ++i) {
         if (i > 1) sh.wait(kFreeY + (i & 1), (i >> 1) - 1);
@@ -1002,14 +1012,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_cons
     W.tmem = begin(sh, [](int i) { return i < kSingle || i == kFullG || i == kFullW || i == kFullW + 1 ? 1 : 8; });
     const int warp = warp_of(threadIdx.x);
     if (warp < 8) {
-        more_registers<kManyRegisters>();
         scores<D>(A, W, sm, sh, g);
     } else if (warp < 16) {
-        more_registers<kManyRegisters>();
         states<D>(A, W, sm, sh, g);
     } else {
-        fewer_registers<kFewRegisters>();
-        if (warp == kIssuer) products<D>(A, W, tc::smem_addr(sm), sh);
+        if (warp == kIssuer && elect()) products<D>(A, W, tc::smem_addr(sm), sh);
         if (warp == kSummer) sum_gates(A, W, sh, g);
         if (warp == kLoader && A.tma && elect()) loads<D>(A, W, tc::smem_addr(sm), sh);
         if (warp == kStorer && elect()) stores<D>(A, W, tc::smem_addr(sm), sh);
