@@ -18,9 +18,9 @@
 // cores' own rate, is shared memory, which hands 128 bytes a cycle to all of them and the threads; so the operands that are made here are made in
 // tensor memory, Y'^T by way of transposing loads.
 //
-// Two groups of 8 warps work on a chunk side by side.  The first turns P into P', scales O's rows by e^G and writes the output.  The second
-// makes Y' and keeps the state.  Three more warps serve them: one issues all products, in the order P, X S^T, dS, P' Z, so that no warp
-// with work of its own stands in the products' queue; one issues all loads, one the stores of whole chunks; one sums the gates.  They meet at mbarriers only.  Loops over
+// Groups of warps work on chunks side by side: eight turn P into P' and scale O's rows by e^G; eight make Y' and keep the state; four write the output.
+// Four more serve them: one issues all products, in the order P, X S^T, dS, P' Z, so that no warp with work of its own stands in the
+// products' queue; one issues all loads, one the stores of whole chunks; one sums the gates.  They meet at mbarriers only.  Loops over
 // columns are rolled where registers allow: what the warps lacked most with all of it unrolled was instructions.
 //
 // Decays.  G is summed in 64-bit fixed point (powers of two, 31 fraction bits) and kept as a whole and a fractional fp32 number, since
@@ -46,8 +46,8 @@ __device__ int g_la_chunk_bad, g_la_chunk_timeout;
 
 constexpr int L = 128;         // tokens of a chunk
 constexpr int kGroup = 256;    // threads of a group
-constexpr int kThreads = 2 * kGroup + 128;  // registers move between groups of four warps
-constexpr int kIssuer = 16, kLoader = 17, kSummer = 18, kStorer = 19;  // warps
+constexpr int kThreads = 2 * kGroup + 256;
+constexpr int kWriters = 16, kIssuer = 20, kLoader = 21, kSummer = 22, kStorer = 23;  // warps
 constexpr int kMostSegments = 16;
 constexpr uint32_t kColP = 0, kColO = 128, kColS = 256, kColY = 384, kTmemCols = 512;  // Y': 64 columns of hi words, 64 of lo
 constexpr uint32_t kWaitClocks = 400000000, kLookClocks = 20000;
@@ -84,8 +84,9 @@ enum {
     kBarP, kBarXS, kBarS, kBarO, kLoadX, kLoadY, kLoadZ = kLoadY + 2, kFreeY = kLoadZ + 2, kFreeZ = kFreeY + 2, kSingle = kFreeZ + 2,
     kFullXY = kSingle, kFullZ, kFullS, kFullK, kFullP, kFreeO, kFullG, kFreeG, kFullW, kFreeW = kFullW + 2, kFullOut = kFreeW + 2, kBars = kFullOut + 2
 };
-// of the first kernel: products and stages read, stages loaded, Y' and gates made (these two by parity)
-enum { kProduct = kBarP, kRead = kProduct + 2, kStage = kRead + 3, kMade = kSingle, kGates = kMade + 2, kTotal = kGates + 2 };
+// of the first kernel: products and stages read, stages loaded; of four chunks, Y' and gates made and the gates' sums so far
+enum { kProduct = 0, kRead = kProduct + 2, kStage = kRead + 3, kMade = kStage + 3, kGates = kMade + 4, kCarry = kGates + 4, kTotal = kCarry + 4 };
+static_assert(kTotal < kBars, "barriers");
 
 struct Gates {
     float *hi, *lo, *c;  // G in powers of two; e^(G of the block's last column - G)
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     if (!W.q.ok) return;  // the second kernel reports it
     W.part = part_of(A, W.q.hi - W.q.lo, W.segment);
     if (W.part.none || W.part.last) return;
-    const uint32_t tmem = begin(sh, [](int i) { return i == kMade || i == kMade + 1 ? 16 : 1; }), base = tc::smem_addr(sm);
+    const uint32_t tmem = begin(sh, [](int i) { return i >= kMade && i < kGates ? 16 : 1; }), base = tc::smem_addr(sm);
     const int count = (int)(W.part.c1 - W.part.c0), yh = W.h % A.run.yh, zh = W.h % A.run.zh;
     // whole chunks, from the last one back: the sequence's last one is the last segment's
     auto token = [&](int it) { return W.token(count - 1 - it); };
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     } else if (warp == kIssuer) {
         for (int it = 0; it < count; ++it) {
             if (A.tma) sh.wait(kStage + it % 3, it / 3);
-            sh.wait(kMade + (it & 1), it >> 1);
+            sh.wait(kMade + (it & 3), it >> 2);
             tc::fence_after();
             if (elect()) {
                 issue_state<D>(tmem, keys(it), base + S::stage(it) + S::tile, it > 0);
@@ -552,36 +553,48 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
             }
             __syncwarp();
         }
-    } else if (warp == kSummer) {
-        long long carry = 0;
-        bool nan = false;  // among the gates behind
-        RawGates next[2];  // of this chunk and the one behind it
-        auto gates = [&](RawGates& to, int it) {
-            if (it < count) to.load(A.run, W.q, W.h, token(it), 0, L, lane);
+    } else if (warp >= kWriters && warp < kWriters + 4) {
+        // the gates: a warp sums every fourth chunk, and gets the sum of those behind it from the warp before
+        long long* sums = reinterpret_cast<long long*>(sw + 4 * L);
+        int* nans = reinterpret_cast<int*>(sums + 4);
+        RawGates next;
+        auto gates = [&](int it) {
+            if (it < count) next.load(A.run, W.q, W.h, token(it), 0, L, lane);
         };
-        gates(next[0], 0);
-        gates(next[1], 1);
-        for (int it = 0; it < count; ++it) {
-            const GateSums s(next[0], A.run.gate_dtype, lane);
-            next[0] = next[1];
-            gates(next[1], it + 2);
-            nan |= s.nan != 0 && (s.nan & 32);
+        gates(warp - kWriters);
+        for (int it = warp - kWriters; it < count; it += 4) {
+            const GateSums s(next, A.run.gate_dtype, lane);
+            gates(it + 4);
+            long long carry = 0;
+            bool nan = false;  // among the gates behind
+            if (it > 0) {
+                sh.wait(kCarry + ((it - 1) & 3), (it - 1) >> 2);
+                carry = sums[(it - 1) & 3];
+                nan = nans[(it - 1) & 3] != 0;
+            }
+            nan |= (s.nan & 32) != 0;
+            if (lane == 0) {
+                sums[it & 3] = carry + s.all;
+                nans[it & 3] = nan;
+            }
+            sh.arrive(kCarry + (it & 3));
             float w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = nan ? NAN : ex2(from_fixed(carry + (s.all - s.at[k])));
-            if (it > 1) sh.wait(kProduct + (it & 1), (it >> 1) - 1);  // its Y' has been made of the weights before these
-            put4(sw + L * (it & 1), W.reverse, lane, w);
-            carry += s.all;
-            sh.arrive(kGates + (it & 1));
+            if (it > 3) sh.wait(kMade + (it & 3), (it >> 2) - 1);  // the weights before these have been read
+            put4(sw + L * (it & 3), W.reverse, lane, w);
+            sh.arrive(kGates + (it & 3));
+            if (it == count - 1) {
+                if (lane == 0) {
+                    *sh.total = carry + s.all;
+                    *sh.nan = nan;
+                }
+                sh.arrive(kTotal);
+            }
         }
-        if (lane == 0) {
-            *sh.total = carry;
-            *sh.nan = nan;
-        }
-        sh.arrive(kTotal);
     } else if (warp < 16) {
         for (int it = 0; it < count; ++it) {
-            const float* w = sw + L * (it & 1);
+            const float* w = sw + L * (it & 3);
             if (it > 1) sh.wait(kProduct + (it & 1), (it >> 1) - 1);  // the product before the last has read Y', which all warps had made
             if (A.tma) sh.wait(kStage + it % 3, it / 3);
             else {
@@ -591,11 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
                 tc::fence_async_smem();
                 group_barrier<2, 512>();
             }
-            sh.wait(kGates + (it & 1), it >> 1);
+            sh.wait(kGates + (it & 3), it >> 2);
             tc::fence_after();
             decayed_keys<D, 4>(base + S::stage(it), keys(it), w, warp & 3, warp >> 2, lane);
             tc::fence_before();
-            sh.arrive(kMade + (it & 1));
+            sh.arrive(kMade + (it & 3));
         }
         if (count > 1) sh.wait(kProduct + (count & 1), (count - 2) >> 1);
         sh.wait(kProduct + ((count - 1) & 1), (count - 1) >> 1);
@@ -641,63 +654,15 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8])
                  : "memory");
 }
 
-// The first group: P' and the output.
+// The first group: P', and the state's part of the output scaled.
 template <int D>
-__device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char* sm, const Shared& sh, const Gates& g)
+__device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, const Shared& sh, const Gates& g)
 {
-    using S = Smem<D>;
     constexpr int H = D / 2;  // columns of a thread's output
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_of(tid), quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
     const uint32_t lanes = tc::taddr(W.tmem, warp, 0);
 
-    auto output = [&](int i) {
-        sh.wait(kBarO, i);
-        tc::fence_after();
-        float o[H];
-#pragma unroll
-        for (int c = 0; c < H; c += 32) tc::ld32(lanes + kColO + half * H + c, *reinterpret_cast<float(*)[32]>(o + c));
-        tc::wait_ld();
-        tc::fence_before();
-        sh.arrive(kFreeO);
-        const bool staged = A.tma_out && W.whole(i);
-        if (staged) {
-            // through Z's buffer, which is free until the second chunk behind this one
-#pragma unroll
-            for (int e = 0; e < H; e += 8) {
-                uint32_t v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = tc::pack_bf16x2(A.run.co * o[e + 2 * k], A.run.co * o[e + 2 * k + 1]);
-                *reinterpret_cast<uint4*>(sm + S::z(i) + swizzled(row, (half * H + e) / 8)) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-        } else if (row >= W.lo(i) && row < W.hi(i)) {
-            const long long at = ((W.token(i) + row) * A.run.H + W.h) * D + half * H;
-            if (A.vec_out && A.run.out_dtype == GDN_F32) {
-#pragma unroll
-                for (int e = 0; e < H; e += 8) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(A.run.co * o[e + k]);
-                    st_global32((float*)A.run.out + at + e, v);
-                }
-            } else if (A.vec_out && A.run.out_dtype == GDN_BF16) {
-#pragma unroll
-                for (int e = 0; e < H; e += 16) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = tc::pack_bf16x2(A.run.co * o[e + 2 * k], A.run.co * o[e + 2 * k + 1]);
-                    st_global32((__nv_bfloat16*)A.run.out + at + e, v);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < H; ++e) st_any(A.run.out, at + e, A.run.out_dtype, A.run.co * o[e]);
-            }
-        }
-        __syncwarp();
-        if (staged) tc::fence_async_smem();
-        sh.arrive(kFullOut + (i & 1));
-    };
     for (int i = 0; i < W.count; ++i) {
-        if (i > 0) output(i - 1);
         sh.wait(kFullG, i);
         const float gh = g.hi[row], gl = g.lo[row], eg = ex2(gh + gl);
         sh.wait(kBarP, i);
@@ -762,7 +727,59 @@ __device__ __forceinline__ void scores(const LaChunkArgs& A, const Work& W, char
         tc::fence_before();
         sh.arrive(kFullP);
     }
-    if (W.count > 0) output(W.count - 1);
+}
+
+// The third group: the output, a row a thread.
+template <int D>
+__device__ __forceinline__ void writes(const LaChunkArgs& A, const Work& W, char* sm, const Shared& sh)
+{
+    using S = Smem<D>;
+    const int lane = threadIdx.x & 31, warp = warp_of(threadIdx.x) - kWriters, row = 32 * warp + lane;
+    const uint32_t lanes = tc::taddr(W.tmem, warp, kColO);
+    for (int i = 0; i < W.count; ++i) {
+        // a whole chunk through Z's buffer, which is free until the second chunk behind this one
+        const bool staged = A.tma_out && W.whole(i), real = row >= W.lo(i) && row < W.hi(i);
+        const long long at = ((W.token(i) + row) * A.run.H + W.h) * D;
+        sh.wait(kBarO, i);
+        tc::fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tc::ld32(lanes + c, o);
+            tc::wait_ld();
+            if (c + 32 == D) {
+                tc::fence_before();
+                sh.arrive(kFreeO);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= A.run.co;
+            if (staged || (real && A.vec_out && A.run.out_dtype == GDN_BF16)) {
+                uint32_t v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = tc::pack_bf16x2(o[2 * k], o[2 * k + 1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 u = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    if (staged) *reinterpret_cast<uint4*>(sm + S::z(i) + swizzled(row, c / 8 + k)) = u;
+                    else *reinterpret_cast<uint4*>((__nv_bfloat16*)A.run.out + at + c + 8 * k) = u;
+                }
+            } else if (real && A.vec_out && A.run.out_dtype == GDN_F32) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[e + k]);
+                    st_global32((float*)A.run.out + at + c + e, v);
+                }
+            } else if (real) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) st_any(A.run.out, at + c + e, A.run.out_dtype, o[e]);
+            }
+            __syncwarp();
+        }
+        if (staged) tc::fence_async_smem();
+        sh.arrive(kFullOut + (i & 1));
+    }
 }
 
 // The second group: gates, Y' and the state.
@@ -1009,19 +1026,17 @@ __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_cons
     W.part = part_of(A, W.q.hi - W.q.lo, W.segment);
     if (W.part.none) return;
     W.count = W.part.c1 > W.part.c0 ? (int)(W.part.c1 - W.part.c0) : 0;
-    W.tmem = begin(sh, [](int i) { return i < kSingle || i == kFullG || i == kFullW || i == kFullW + 1 ? 1 : 8; });
+    W.tmem = begin(sh, [](int i) { return i < kSingle || i == kFullG || i == kFullW || i == kFullW + 1 ? 1 : i == kFreeO || i >= kFullOut ? 4 : 8; });
     const int warp = warp_of(threadIdx.x);
-    if (warp < 8) {
-        scores<D>(A, W, sm, sh, g);
-    } else if (warp < 16) {
-        states<D>(A, W, sm, sh, g);
-    } else {
-        if (warp == kIssuer && elect()) products<D>(A, W, tc::smem_addr(sm), sh);
-        if (warp == kSummer) sum_gates(A, W, sh, g);
-        if (warp == kLoader && A.tma && elect()) loads<D>(A, W, tc::smem_addr(sm), sh);
-        if (warp == kStorer && elect()) stores<D>(A, W, tc::smem_addr(sm), sh);
-        __syncwarp();
-    }
+    const uint32_t base = tc::smem_addr(sm);
+    if (warp < 8) scores<D>(A, W, sh, g);
+    else if (warp < kWriters) states<D>(A, W, sm, sh, g);
+    else if (warp < kIssuer) writes<D>(A, W, sm, sh);
+    else if (warp == kSummer) sum_gates(A, W, sh, g);
+    else if (warp == kIssuer && elect()) products<D>(A, W, base, sh);
+    else if (warp == kLoader && A.tma && elect()) loads<D>(A, W, base, sh);
+    else if (warp == kStorer && elect()) stores<D>(A, W, base, sh);
+    __syncwarp();
     tc::fence_before();
     __syncthreads();
     if (*sh.failed && threadIdx.x == 0) atomicOr(&g_la_chunk_timeout, 1);
