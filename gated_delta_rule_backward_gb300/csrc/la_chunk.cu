@@ -86,7 +86,7 @@ enum {
 };
 // of the first kernel: products and stages read, stages loaded; of four chunks, Y' and gates made and the gates' sums so far
 enum { kProduct = 0, kRead = kProduct + 2, kStage = kRead + 3, kMade = kStage + 3, kGates = kMade + 4, kCarry = kGates + 4, kTotal = kCarry + 4 };
-static_assert(kTotal < kBars, "barriers");
+static_assert((int)kTotal < (int)kBars, "barriers");
 
 struct Gates {
     float *hi, *lo, *c;  // G in powers of two; e^(G of the block's last column - G)
