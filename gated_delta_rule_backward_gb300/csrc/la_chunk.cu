@@ -803,13 +803,13 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
 #pragma unroll 1
                 for (int s = 1; s <= W.segment; ++s) {
                     float d[16];
-                    load_state<D>(d, state_of(A, D, W.nh, s), row, c, true);
+                    load_state<D>(d, state_of(A, D, W.nh, s), row, c, !A.run.again);
                     const float a = s > 1 ? A.decays[W.nh * A.segments + s] : 0.f;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) m[e] = s > 1 ? fmaf(a, m[e], d[e]) : d[e];
                 }
             } else if (!W.part.last) {
-                load_state<D>(m, state_of(A, D, W.nh, 0), row, c, true);
+                load_state<D>(m, state_of(A, D, W.nh, 0), row, c, !A.run.again);
             } else if (W.q.in >= 0) {
                 load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, row, c, A.run.transposed_in);
             }
@@ -1081,7 +1081,7 @@ template <int D>
 int launch(const LaChunkArgs& A, cudaStream_t st)
 {
     int e = (int)cudaFuncSetAttribute(la_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
-    if (!e && A.segments > 1) {
+    if (!e && A.segments > 1 && !A.run.again) {
         e = (int)cudaFuncSetAttribute(la_segment_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
         if (!e) e = launch_after(la_segment_kernel<D>, (unsigned)(A.run.n_seq * A.run.H * (A.segments - 1)), kThreads, Smem<D>::bytes, st, A);
     }

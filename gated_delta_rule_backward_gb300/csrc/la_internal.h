@@ -34,6 +34,7 @@ struct LaRun {
     int reverse;
     float co, cs;
     void* out;  // [n_tok][H][DV]
+    int again;  // chunked form: the workspace holds the segments of a run over the same sequences with y and z in each other's places
 };
 
 // The token rows of sequence n, and the states that it starts from and leaves (-1: none).
