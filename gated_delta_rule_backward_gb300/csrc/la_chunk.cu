@@ -742,40 +742,53 @@ __device__ __forceinline__ void writes(const LaChunkArgs& A, const Work& W, char
         const long long at = ((W.token(i) + row) * A.run.H + W.h) * D;
         sh.wait(kBarO, i);
         tc::fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tc::ld32(lanes + c, o);
-            tc::wait_ld();
-            if (c + 32 == D) {
-                tc::fence_before();
-                sh.arrive(kFreeO);
+        if (staged || (A.vec_out && A.run.out_dtype == GDN_BF16)) {
+            // all columns first, so that the next chunk's product may have their place
+            uint32_t v[D / 2];
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tc::ld32(lanes + c, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[c / 2 + k] = tc::pack_bf16x2(A.run.co * o[2 * k], A.run.co * o[2 * k + 1]);
             }
+            tc::fence_before();
+            sh.arrive(kFreeO);
+            if (staged) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= A.run.co;
-            if (staged || (real && A.vec_out && A.run.out_dtype == GDN_BF16)) {
-                uint32_t v[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = tc::pack_bf16x2(o[2 * k], o[2 * k + 1]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint4 u = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                    if (staged) *reinterpret_cast<uint4*>(sm + S::z(i) + swizzled(row, c / 8 + k)) = u;
-                    else *reinterpret_cast<uint4*>((__nv_bfloat16*)A.run.out + at + c + 8 * k) = u;
-                }
-            } else if (real && A.vec_out && A.run.out_dtype == GDN_F32) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[e + k]);
-                    st_global32((float*)A.run.out + at + c + e, v);
-                }
+                for (int k = 0; k < D / 8; ++k)
+                    *reinterpret_cast<uint4*>(sm + S::z(i) + swizzled(row, k)) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             } else if (real) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) st_any(A.run.out, at + c + e, A.run.out_dtype, o[e]);
+                for (int k = 0; k < D / 8; ++k)
+                    *reinterpret_cast<uint4*>((__nv_bfloat16*)A.run.out + at + 8 * k) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
             __syncwarp();
+        } else {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tc::ld32(lanes + c, o);
+                tc::wait_ld();
+                if (c + 32 == D) {
+                    tc::fence_before();
+                    sh.arrive(kFreeO);
+                }
+                if (real && A.vec_out && A.run.out_dtype == GDN_F32) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(A.run.co * o[e + k]);
+                        st_global32((float*)A.run.out + at + c + e, v);
+                    }
+                } else if (real) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) st_any(A.run.out, at + c + e, A.run.out_dtype, A.run.co * o[e]);
+                }
+                __syncwarp();
+            }
         }
         if (staged) tc::fence_async_smem();
         sh.arrive(kFullOut + (i & 1));
