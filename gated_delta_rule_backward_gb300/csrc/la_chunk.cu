@@ -1056,18 +1056,27 @@ __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_cons
     if (threadIdx.x < 32) tc::tmem_free(W.tmem, kTmemCols);
 }
 
-// Segments a sequence and head: as many as leave every SM one, each of several chunks.
+// Segments a sequence and head, s of p chunks each: at most as many as leave every SM one, and those of the least p + s, since
+// a segment more costs about what a chunk more does (the states that the last one starts from).  Against one segment of c chunks, 3 us a chunk,
+// the first kernel costs a launch and 1.6 times the rest: 8 heads of 128, a prompt of 1024 tokens 36 us in one segment and 36 in 3, of 2048
+// 60 and 47, of 4096 106 and 56 (6 segments; 70 with 16), of 16384 388 and 98 (12); 32 heads, 2048 tokens 60 us and 52 (4), 512 tokens 25 and
+// 36; 64 heads, 2048 tokens 62 and 64 (2), 4096 tokens 109 and 98.
 void plan(const LaRun& A, int* segments, int* per)
 {
     const long long heads = (long long)A.n_seq * A.H;
     const long long chunks = ((long long)A.T + L - 1) / L;
-    long long s = heads > 0 ? kNumSMs / heads : 1;
-    if (s > kMostSegments) s = kMostSegments;
-    if (s > chunks) s = chunks;
-    if (s < 1) s = 1;
-    const long long p = chunks > 0 ? (chunks + s - 1) / s : 1;
-    *per = (int)p;
-    *segments = (int)(chunks > 0 ? (chunks + p - 1) / p : 1);
+    long long most = heads > 0 ? kNumSMs / heads : 1;
+    if (most > kMostSegments) most = kMostSegments;
+    *segments = 1;
+    *per = (int)chunks;
+    long long best = (5 * chunks - 5) / 8;
+    for (long long s = 2; s <= most && s <= chunks; ++s) {
+        const long long p = (chunks + s - 1) / s, real = (chunks + p - 1) / p;
+        if (p + real >= best) continue;
+        best = p + real;
+        *segments = (int)real;
+        *per = (int)p;
+    }
 }
 
 // A map of [n_tok][heads][D]: false where its rows do not lie on 16 bytes, or are otherwise nothing for TMA.
@@ -1104,9 +1113,13 @@ int launch(const LaChunkArgs& A, cudaStream_t st)
 
 }  // namespace
 
+// From 32 tokens on, a chunk's fixed cost is less than that many steps: 32 heads of 128, 31 tokens 21 us token by token and 17 in a chunk (24 tokens 19
+// and 17), 2048 heads 189 and 177 (24 tokens 152 and 177).  Of many heads of 64, half as wide a step, only from 48 on: 1024 heads, 40 tokens 56 us and
+// 60, 48 tokens 65 and 60; 384 heads, 32 tokens 27 and 29, 40 tokens 31 and 29; 256 heads, 32 tokens 25 and 21; 32 heads, 19 and 13.
 bool la_chunk_fits(const la_params_t* p)
 {
-    return p->in_dtype == GDN_BF16 && p->S_k == p->S_v && (p->S_k == 64 || p->S_k == 128) && p->T >= 32;
+    const int least = p->S_k == 64 && p->n_seq * p->H_v > 4 * kNumSMs ? 48 : 32;
+    return p->in_dtype == GDN_BF16 && p->S_k == p->S_v && (p->S_k == 64 || p->S_k == 128) && p->T >= least;
 }
 
 size_t la_chunk_workspace(const LaRun& A)

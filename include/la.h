@@ -14,7 +14,7 @@
  *
  * Two forms compute this (la_form() says which runs):
  *   - the token form walks token by token, states in registers: every type and size;
- *   - the chunked form (bf16, S_k = S_v = 64 or 128, T of 32 or more) takes 128 tokens at a time as dense products on the tensor
+ *   - the chunked form (bf16, S_k = S_v = 64 or 128, T of 32 or more; of many heads of 64, 48) takes 128 tokens at a time as dense products on the tensor
  *     cores, and long sequences in segments whose states are joined, so that a single prompt fills the GPU.
  *
  * Layouts (device memory)
@@ -28,9 +28,10 @@
  *              NULL: every sequence has T tokens, n_tok = n_seq T
  *   pool   [n_slots][H_v][S_v][S_k] fp32, slots slot_stride elements apart
  *   slot_in, slot_out  int32 [n_seq]
- * Arithmetic: states, sums and decays are fp32 whatever the types (accurate expf).  The chunked form's products take bf16
- * inputs as they are and fp32 operands (states, weighted scores, decayed keys) as the sum of two bf16 numbers, 2^-17 relative,
- * with fp32 accumulation; its running sums of log decays are held in two fp32 numbers.  Outputs are rounded once.
+ * Arithmetic: states and sums are fp32 whatever the types.  The token form takes CUDA's expf.  The chunked form's products take bf16
+ * inputs as they are and fp32 operands (states, weighted scores, decayed keys) as the sum of two bf16 numbers, 2^-16 relative,
+ * with fp32 accumulation; its sums of log decays are exact in 64-bit fixed point (2^-31 powers of two), each exponential of a difference the
+ * hardware's 2^x (2^-22 relative).  Outputs are rounded once.
  * dg is a running sum over the tokens that follow, anchored by <M_T, dM_T>: its error is that of the sum, not of
  * the element.  Log decays below -104 (exp = 0 in fp32) count as a = 0.  The same call gives the same bits; in the chunked form
  * they depend on n_seq, T and H_v through the segments.
@@ -40,7 +41,7 @@
  *
  * A slot outside [-1, n_slots), a cu_tokens that falls, leaves [0, n_tok] or gives a sequence more than T tokens is only seen
  * on the device: that sequence is skipped (its outputs keep what they held; in the backward pass, its gradients are unspecified)
- * and the next gdn_device_status returns GDN_ERR_INVALID_ARG.
+ * and the next gdn_device_status returns GDN_ERR_INVALID_ARG; GDN_ERR_TIMEOUT where one of the chunked form's bounded waits gave up.
  *
  * Ownership, streams and errors are those of gdn.h: work is only enqueued on `stream`, nothing is allocated or kept, no
  * output is written when a call returns an error; workspaces are scratch that no call needs zeroed.

@@ -92,14 +92,15 @@ def test_row_strides_places_and_gradients_elsewhere():
 
 
 def test_both_kernels_agree_and_a_weight_of_nothing():
-    """300 rows go to clusters, 310 to the walking kernel."""
+    """A list of more than 256 entries, here padding, sends rows to clusters."""
     x, idx, t = make(310, 6000, 40, BF16)
     dloss = torch.randn(310, device="cuda")
     dloss[::7] = 0.0
-    a, b = distill.forward(x, idx, t, dloss=dloss), distill.forward(x[:300], idx[:300], t[:300], dloss=dloss[:300])
-    assert ((a[0][:300] - b[0]).abs() <= 4e-5).all() and ((a[1][:300] - b[1]).abs() <= 1e-5).all()
-    assert ((a[2][:300].float() - b[2].float()).abs() <= 2.0 ** -7 * b[2].float().abs() + 1e-7).all()
-    assert (a[2][::7] == 0).all()
+    padded = torch.cat([idx, torch.full((310, 260), -1, dtype=torch.int32, device="cuda")], 1), torch.cat([t, torch.zeros(310, 260, device="cuda")], 1)
+    a, b = distill.forward(x, idx, t, dloss=dloss), distill.forward(x, *padded, dloss=dloss)
+    assert ((a[0] - b[0]).abs() <= 4e-5).all() and ((a[1] - b[1]).abs() <= 1e-5).all()
+    assert ((a[2].float() - b[2].float()).abs() <= 2.0 ** -7 * b[2].float().abs() + 1e-7).all()
+    assert (a[2][::7] == 0).all() and (b[2][::7] == 0).all()
 
 
 def test_another_stream_and_a_graph():
