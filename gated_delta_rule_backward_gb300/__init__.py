@@ -6,6 +6,8 @@ Submodules:
   ``decode`` -- the rule's serving form over a pool of states, and the moves of its states
   ``beam``   -- a beam search's selection over beams and vocabulary
   ``rms``    -- the root-mean-square norm with the residual's addition, forward and backward
+  ``la``     -- linear attention with a decay for each head: prompts, single tokens, backward
+  ``distill`` -- distillation from a teacher's top logits: loss, gradient, or both
   ``build``  -- compiles ``libgdn.so`` in-tree with nvcc for sm_103a
   ``synth``  -- seeded synthetic inputs (no recurrence arithmetic)
 """

@@ -242,7 +242,12 @@ __device__ __forceinline__ long long to_fixed(float gate)
 }
 __device__ __forceinline__ float whole_of(long long x) { return (float)(int)(x >> 31); }
 __device__ __forceinline__ float fraction_of(long long x) { return (float)(int)(x & 0x7fffffff) * 4.65661287e-10f; }
-__device__ __forceinline__ float from_fixed(long long x) { return whole_of(x) + fraction_of(x); }
+// The exponent of a sum, however long: 2^-1024 is 0 in fp32.
+__device__ __forceinline__ float from_fixed(long long x)
+{
+    x = x < -(1ll << 41) ? -(1ll << 41) : x;
+    return whole_of(x) + fraction_of(x);
+}
 
 // A lane's four gates of a chunk whose row 0 is the token `first`: those that enter before the walk's tokens 4 l .. 4 l + 3, for rows in [lo, hi)
 // (0 elsewhere, and backwards behind the sequence's last token).  They are kept as stored until they are summed, so that loads are under way together.
@@ -265,7 +270,7 @@ struct RawGates {
         float g = __uint_as_float(v[k]);
         if (dtype == GDN_BF16) g = __uint_as_float(v[k] << 16);
         if (dtype == GDN_F16) g = __half2float(__ushort_as_half((unsigned short)v[k]));
-        return g < kLaLeastGate ? kLaLeastGate : g;
+        return g < kLaLeastGate ? kLaLeastGate : g > kLaMostGate ? kLaMostGate : g;
     }
 };
 

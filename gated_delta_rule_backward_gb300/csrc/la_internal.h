@@ -45,6 +45,7 @@ struct LaSequence {
 };
 
 constexpr float kLaLeastGate = -104.f;  // exp of it is 0 in fp32
+constexpr float kLaMostGate = 1000.f;    // exp of it is infinite
 
 #if defined(__CUDACC__)
 __device__ __forceinline__ LaSequence la_sequence(const LaRun& A, int n)

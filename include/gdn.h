@@ -217,13 +217,13 @@ int gdn_backward_launches(const gdn_params_t* p);
 int gdn_timing_stages(const gdn_params_t* p, int backward);
 
 /* Device-side status of the work enqueued so far on the current device.  The
- * tensor-core kernels (head size 128) wait on hardware barriers for their operand copies
+ * tensor-core kernels (head size 128; linear attention's chunked form, la.h) wait on hardware barriers for their operand copies
  * and products; every such wait is bounded (0.2 s of wall clock, far beyond any
  * legitimate wait), and a wait that gives up makes its kernel return early and record
  * GDN_ERR_TIMEOUT in a device status word, leaving that call's outputs invalid.  This
  * call synchronises `stream` (a cudaStream_t, NULL = legacy default stream), then reads
  * and clears the status words: GDN_OK, GDN_ERR_TIMEOUT, GDN_ERR_INVALID_ARG when a serving
- * kernel skipped slots or token ranges out of bounds (gdn_decode.h), or GDN_ERR_CUDA if the
+ * kernel skipped slots or token ranges out of bounds (gdn_decode.h, la.h), or GDN_ERR_CUDA if the
  * stream or the read failed (text in gdn_last_error()).  Where both kinds have been met, this call
  * returns the timeout and the next one the other.  No counterpart on the pages; it exists
  * because a GPU kernel cannot return an error code by itself. */
