@@ -160,3 +160,59 @@ def test_rows_and_slots_that_are_not_the_calls_own_are_left_alone():
     assert gdn.device_status() == 1 and b"la_forward" in gdn.library().gdn_last_error()
     assert (y[120:] == 7).all() and torch.equal(x["pool"][3], before[3]) and not torch.equal(x["pool"][2], before[2])
     assert gdn.device_status() == 0
+
+
+def test_lengths_that_change_between_replays():
+    """A captured step serves whatever lengths its cu_tokens hold at replay, no sequence above T: several segments, one chunk, nothing."""
+    x = P.problem([1500], 2, 4, 128, dtype=BF16, slots=6, seed=12)
+    s_in, s_out, cu = i32([0, 1, 2]), i32([3, 4, 5]), i32([0, 1500, 1500, 1500])
+    step = lambda: (la.forward(x["q"], x["k"], x["v"], x["g"], x["pool"], s_in, s_out, cu, T=1500), x["pool"][3:].clone(),
+                    *la.backward(x["q"], x["k"], x["v"], x["g"], x["pool"], s_in, x["dy"], x["pool"][:3].contiguous(), cu, T=1500))
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for lengths in ([1500, 0, 0], [1, 1499, 0], [0, 0, 0], [100, 700, 690], [0, 33, 1400]):
+        cu.copy_(cu_of(lengths))
+        n = sum(lengths)
+        graph.replay()
+        again = step()
+        part = {k: v[:n] if k in ("q", "k", "v", "g", "dy") else v for k, v in x.items()}
+        for k, (a, b) in enumerate(zip(captured, again)):
+            rows = slice(None) if k in (1, 6) else slice(0, n)
+            assert torch.equal(a[rows], b[rows]), (lengths, k)
+        y0, after, _ = P.forward(part, lengths, [0, 1, 2], 128 ** -0.5)
+        A_y, A_s, _ = P.forward(part, lengths, [0, 1, 2], 128 ** -0.5, absolute=True)
+        P.within(captured[0][:n], y0, A_y, eps_of(lengths), "y")
+        P.within(captured[1], after, A_s, eps_of(lengths), "state")
+    assert gdn.device_status() == 0
+
+
+def test_nothing_at_all():
+    """Sequences without tokens copy their states, and hand dstate_T back, whatever T allows."""
+    x = P.problem([0, 0], 1, 2, 64, dtype=BF16, slots=4, seed=2)
+    cu = i32([0, 0, 0])
+    y = la.forward(x["q"], x["k"], x["v"], x["g"], x["pool"], i32([1, -1]), i32([2, 3]), cu, T=500)
+    assert y.shape == (0, 2, 64) and torch.equal(x["pool"][2], x["pool"][1]) and (x["pool"][3] == 0).all()
+    out = la.backward(x["q"], x["k"], x["v"], x["g"], x["pool"], i32([1, -1]), x["dy"], x["dstate"], cu, T=500)
+    assert torch.equal(out[4], x["dstate"]) and gdn.device_status() == 0
+
+
+def test_heads_that_share_one_place():
+    """Heads of q, k and v that lie at one address (strides of 0), and keys that are the queries."""
+    x = P.problem([300], 2, 4, 128, dtype=BF16, slots=2, seed=3)
+    x["q"], x["v"] = x["q"][:, :1].expand(300, 2, 128), x["v"][:, :1].expand(300, 4, 128)
+    x["k"] = x["q"]
+    forward(x, [300], [0], [1])
+    backward(x, [300], [0])
+
+
+def test_an_infinity_stays_with_its_chunk_and_sequence():
+    counts = [300, 200]
+    x = P.problem(counts, 1, 2, 64, dtype=BF16, slots=4, seed=4)
+    want = la.forward(x["q"], x["k"], x["v"], x["g"], x["pool"], i32([0, 1]), i32([2, 3]), cu_of(counts), T=300)
+    state = x["pool"][3].clone()
+    x["v"][200, 0, 3] = float("inf")      # the first sequence's second chunk
+    got = la.forward(x["q"], x["k"], x["v"], x["g"], x["pool"], i32([0, 1]), i32([2, 3]), cu_of(counts), T=300)
+    assert torch.equal(got[:128], want[:128]) and torch.equal(got[300:], want[300:]) and torch.equal(x["pool"][3], state)
+    assert not torch.isfinite(got[201:300, 0, 3]).any()
