@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
 
 // ---- many rows ----
 
-constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32, kRowMostPacks = 16;
+constexpr int kRowThreads = 256, kWideThreads = 512, kRowMostPacks = 16;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) { asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory"); }
 
@@ -301,18 +301,18 @@ __device__ __forceinline__ void put2(__nv_bfloat16* y, float a, float b) { *rein
 __device__ __forceinline__ void put2(__half* y, float a, float b) { *reinterpret_cast<__half2*>(y) = __floats2half2_rn(a, b); }
 
 // CTAs an SM, by the registers that a row's packs take.
-constexpr int rows_resident(int packs) { return packs == 16 ? 2 : packs == 8 ? 3 : 4; }
+constexpr int rows_resident(int threads, int packs) { return threads == kWideThreads ? 1 : packs == 16 ? 2 : packs == 8 ? 3 : 4; }
 
-template <typename T, int PACKS, int MODE>
-__global__ void __launch_bounds__(kRowThreads, rows_resident(PACKS)) distill_rows_kernel(const DistillArgs A, int rows)
+template <typename T, int THREADS, int PACKS, int MODE>
+__global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distill_rows_kernel(const DistillArgs A, int rows)
 {
-    constexpr int VEC = 16 / (int)sizeof(T);
-    extern __shared__ __align__(16) char ring[];  // PACKS x kRowThreads packs: the next row's
-    __shared__ __align__(16) int s_idx[kRowThreads];
-    __shared__ __align__(16) float s_p[kRowThreads];
-    __shared__ float s_max[2][kRowWarps], s_sum[2][kRowWarps], s_loss[kRowWarps];
+    constexpr int VEC = 16 / (int)sizeof(T), WARPS = THREADS / 32;
+    extern __shared__ __align__(16) char ring[];  // PACKS x THREADS packs: the next row's
+    __shared__ __align__(16) int s_idx[THREADS];
+    __shared__ __align__(16) float s_p[THREADS];
+    __shared__ float s_max[2][WARPS], s_sum[2][WARPS], s_loss[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t place = tc::smem_addr(ring) + 16 * tid;  // + 16 kRowThreads p
+    const uint32_t place = tc::smem_addr(ring) + 16 * tid;  // + 16 THREADS p
     begin_after();
 
     auto row_of = [&](long long r) { return segment_of((const T*)A.logits + r * A.row_stride, 0, A.seg, A.V); };
@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(kRowThreads, rows_resident(PACKS)) distill_row
             const Segment<T> s = row_of(r);
 #pragma unroll
             for (int p = 0; p < PACKS; ++p) {
-                const int at = (p * kRowThreads + tid) * VEC;
-                if (at >= s.lo && at + VEC <= s.end) cp_async16(place + p * (16 * kRowThreads), s.at + at);
+                const int at = (p * THREADS + tid) * VEC;
+                if (at >= s.lo && at + VEC <= s.end) cp_async16(place + p * (16 * THREADS), s.at + at);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -359,14 +359,14 @@ __global__ void __launch_bounds__(kRowThreads, rows_resident(PACKS)) distill_row
             unsigned cut = 0;
 #pragma unroll
             for (int p = 0; p < PACKS; ++p) {
-                const int at = (p * kRowThreads + tid) * VEC;
+                const int at = (p * THREADS + tid) * VEC;
                 const bool whole = at >= s.lo && at + VEC <= s.end;
                 x[p] = none;
-                if (whole) x[p] = *reinterpret_cast<const Pack<T, VEC>*>(ring + 16 * (tid + p * kRowThreads));
+                if (whole) x[p] = *reinterpret_cast<const Pack<T, VEC>*>(ring + 16 * (tid + p * THREADS));
                 cut |= (at < s.end && !whole ? 1u : 0u) << p;
             }
             while (cut) {
-                const int c = __ffs(cut) - 1, at = (c * kRowThreads + tid) * VEC;
+                const int c = __ffs(cut) - 1, at = (c * THREADS + tid) * VEC;
                 cut &= cut - 1;
                 Pack<T, VEC> part = none;
 #pragma unroll
@@ -390,8 +390,8 @@ __global__ void __launch_bounds__(kRowThreads, rows_resident(PACKS)) distill_row
         }
         const bool any = __syncthreads_or(entry);  // the last row's list and gradients are done with too
         fetch(r + gridDim.x);
-        m = warp_max(s_max[0][lane & (kRowWarps - 1)]);
-        const float top = warp_max(s_max[1][lane & (kRowWarps - 1)]);
+        m = warp_max(s_max[0][lane & (WARPS - 1)]);
+        const float top = warp_max(s_max[1][lane & (WARPS - 1)]);
         const float tj = (t - top) * A.inv_tau, ej = entry ? expf(tj) : 0.f;
         const Exponent at_max(m, A.L);
         float sum = 0.f;
@@ -422,10 +422,10 @@ __global__ void __launch_bounds__(kRowThreads, rows_resident(PACKS)) distill_row
         }
         s_idx[tid] = idx;
         __syncthreads();
-        sum = s_sum[0][lane & (kRowWarps - 1)];
-        float esum = s_sum[1][lane & (kRowWarps - 1)];
+        sum = s_sum[0][lane & (WARPS - 1)];
+        float esum = s_sum[1][lane & (WARPS - 1)];
 #pragma unroll
-        for (int o = kRowWarps / 2; o >= 1; o >>= 1) {
+        for (int o = WARPS / 2; o >= 1; o >>= 1) {
             sum += __shfl_xor_sync(kFull, sum, o);
             esum += __shfl_xor_sync(kFull, esum, o);
         }
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kRowThreads, rows_resident(PACKS)) distill_row
             auto dense = [&](auto&& exponents) {
 #pragma unroll
                 for (int p = 0; p < PACKS; ++p) {
-                    const int at = (p * kRowThreads + tid) * VEC;
+                    const int at = (p * THREADS + tid) * VEC;
                     Pack<T, VEC> y;
 #pragma unroll
                     for (int i = 0; i < VEC; i += 2) {
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kRowThreads, rows_resident(PACKS)) distill_row
         __syncthreads();
         if (MODE != kGradient && tid == 0) {
             float l = 0.f;
-            for (int w = 0; w < kRowWarps && (w == 0 || w * 32 < A.K); ++w) l += s_loss[w];
+            for (int w = 0; w < WARPS && (w == 0 || w * 32 < A.K); ++w) l += s_loss[w];
             A.loss[r] = any ? l : 0.f;
         }
         if (MODE != kLoss && entry) {
@@ -581,33 +581,39 @@ int launch(DistillArgs A, const Plan& pl, int64_t N, cudaStream_t st)
     return (int)cudaLaunchKernelEx(&cfg, kernel, A);
 }
 
-// Rows that a CTA of the rows' kernel walks: up to 64 KB, with a list of no more entries than it has threads.  Loss and gradient of bf16 rows of
-// 32000, against clusters (with the call's 6 us of an idle GPU): 1 row 11 us and 11, 64 rows 11 and 13, 200 rows 15 and 21, 1216 rows 39 and 48, 4096 rows
-// 107 and 147; rows of 8000: 1 row 9 and 11, 200 rows 9 and 13, 4096 rows 42 and 57.
+// Rows that a CTA of the rows' kernel walks: up to 64 KB, or of many rows 128 KB, with a list of no more entries than it has threads.  Loss and gradient of
+// bf16 rows of 32000, against clusters (with the call's 6 us of an idle GPU): 1 row 11 us and 11, 64 rows 11 and 13, 200 rows 15 and 21, 1216 rows 39 and 48,
+// 4096 rows 107 and 147; rows of 8000: 1 row 9 and 11, 200 rows 9 and 13, 4096 rows 42 and 57.  fp32 rows of 32000, one CTA an SM: 1 row 12 and 11, 64 rows 13
+// and 15 (the gradient alone 12 and 11), 100 rows 13 and 21, 300 rows 21 and 29, 4096 rows 178 and 294.
+constexpr int kLeastWide = kNumSMs / 2;
 bool walks_rows(const distill_params_t* p)
 {
     const int vec = 16 / (int)elem_size(p->dtype);
-    return p->K <= kRowThreads && p->V >= vec && (p->V + 2 * vec - 2) / vec <= kRowThreads * kRowMostPacks;
+    const int64_t packs = (p->V + 2 * vec - 2) / vec;
+    return p->K <= kRowThreads && p->V >= vec && (packs <= kRowThreads * kRowMostPacks || (packs <= kWideThreads * kRowMostPacks && p->N >= kLeastWide));
 }
 
-template <typename T, int PACKS, int MODE>
+template <typename T, int THREADS, int PACKS, int MODE>
 int launch_rows(DistillArgs A, int64_t N, cudaStream_t st)
 {
-    constexpr int bytes = PACKS * kRowThreads * 16;
-    A.seg = PACKS * kRowThreads * (16 / (int)sizeof(T));
+    constexpr int bytes = PACKS * THREADS * 16;
+    A.seg = PACKS * THREADS * (16 / (int)sizeof(T));
     if (bytes > 40 * 1024) {
-        const int e = (int)cudaFuncSetAttribute(distill_rows_kernel<T, PACKS, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const int e = (int)cudaFuncSetAttribute(distill_rows_kernel<T, THREADS, PACKS, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e) return e;
     }
-    const int64_t most = rows_resident(PACKS) * kNumSMs;
-    return launch_after(distill_rows_kernel<T, PACKS, MODE>, (unsigned)(N < most ? N : most), kRowThreads, bytes, st, A, (int)N);
+    const int64_t most = rows_resident(THREADS, PACKS) * kNumSMs;
+    return launch_after(distill_rows_kernel<T, THREADS, PACKS, MODE>, (unsigned)(N < most ? N : most), THREADS, bytes, st, A, (int)N);
 }
 template <typename T, int MODE>
 int launch_rows(const distill_params_t* p, const DistillArgs& A, cudaStream_t st)
 {
     const int vec = 16 / (int)sizeof(T);
     const int64_t packs = (p->V + 2 * vec - 2) / vec;
-    return packs <= 4 * kRowThreads ? launch_rows<T, 4, MODE>(A, p->N, st) : packs <= 8 * kRowThreads ? launch_rows<T, 8, MODE>(A, p->N, st) : launch_rows<T, 16, MODE>(A, p->N, st);
+    return packs <= 4 * kRowThreads    ? launch_rows<T, kRowThreads, 4, MODE>(A, p->N, st)
+           : packs <= 8 * kRowThreads  ? launch_rows<T, kRowThreads, 8, MODE>(A, p->N, st)
+           : packs <= 16 * kRowThreads ? launch_rows<T, kRowThreads, 16, MODE>(A, p->N, st)
+                                       : launch_rows<T, kWideThreads, 16, MODE>(A, p->N, st);
 }
 
 template <int MODE>

@@ -4,8 +4,9 @@
 // The backward pass's dq and dk come per value head in fp32; la_join_kernel, behind each of their runs (while part of it is in L2), sums the value
 // heads of a key head, rounds once, and leaves each token's q . dq - k . dk per value head, whose running sum from the last token on is dg
 // (la_gate_kernel): with s_t = <M_t, D_t>,  dg_t = a_t <D_t, M_{t-1}> = s_t - v_t . D_t k_t  and
-// s_t = dg_{t+1} + scale dy_t . M_t q_t, where both products are q . dq and k . dk.  Bytes bound the first, latency the second: 4096 tokens
-// of 48 heads of 128 over 16 key heads, 23 us for each of dq and dk and 7 us.
+// s_t = dg_{t+1} + scale dy_t . M_t q_t, where both products are q . dq and k . dk.  Of 4096 tokens of 48 heads of 128 over 16
+// key heads, each call's first reading from DRAM: the joins 39 us each, 117 MB (half its time waits for them; in a call of la_backward
+// most of it is in L2), the gates 14 us, the latency of one CTA a head.
 #include <climits>
 #include <cstdio>
 
@@ -121,40 +122,48 @@ struct GateArgs {
     int state;  // elements of one
 };
 
-// A CTA a sequence and head: the anchor <M_T, dM_T>, then the running sum from the last token, 4096 tokens at a time, 16 of them a
-// thread; what is carried over a warp's tokens is held in 64 bits.
-__global__ void __launch_bounds__(256) la_gate_kernel(const GateArgs A)
+// A CTA a sequence and head: the anchor <M_T, dM_T>, then the running sum from the last token, 4096 tokens at a time, 8 of them a
+// thread.  What is carried over warps and turns is summed in 64 bits, by a lane a warp (64-bit sums are slow here), and reaches the
+// threads as two fp32 numbers.
+__global__ void __launch_bounds__(512) la_gate_kernel(const GateArgs A)
 {
-    constexpr int E = 16;
-    __shared__ float part[8];
+    constexpr int E = 8, W = 16;
+    __shared__ float part[W];
+    __shared__ float2 before[W];
+    __shared__ double carried;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.x / A.run.H, h = blockIdx.x - n * A.run.H;
     begin_after();
     const LaSequence s = la_sequence(A.run, n);
     if (!s.ok) return;  // the runs have reported it
     const float* terms = A.terms + (long long)h * A.run.n_tok;
-    double carry = 0.0;
-    if (A.d_T && s.hi > s.lo) {
-        const float4 *m = reinterpret_cast<const float4*>(A.m_T + (long long)blockIdx.x * A.state), *d = reinterpret_cast<const float4*>(A.d_T + (long long)blockIdx.x * A.state);
-        float x = 0.f;
-#pragma unroll 4
-        for (int i = tid; i < A.state / 4; i += 256) {
-            const float4 a = m[i], b = d[i];
-            x += (a.x * b.x + a.y * b.y) + (a.z * b.z + a.w * b.w);
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-        if (lane == 0) part[warp] = x;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < 8; ++w) carry += part[w];
-        __syncthreads();
-    }
-    for (long long t0 = s.hi - 1; t0 >= s.lo; t0 -= 256 * E) {
-        const long long t = t0 - (long long)tid * E;  // and the 15 before it
-        float x[E];
+    float x[E];
+    auto load = [&](long long t) {
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = t - e >= s.lo ? terms[t - e] : 0.f;
+    };
+    long long t = s.hi - 1 - (long long)tid * E;  // and the 7 before it
+    load(t);
+    float anchor = 0.f;
+    if (A.d_T && s.hi > s.lo) {
+        const float4 *m = reinterpret_cast<const float4*>(A.m_T + (long long)blockIdx.x * A.state), *d = reinterpret_cast<const float4*>(A.d_T + (long long)blockIdx.x * A.state);
+#pragma unroll 8
+        for (int i = tid; i < A.state / 4; i += 512) {
+            const float4 a = m[i], b = d[i];
+            anchor += (a.x * b.x + a.y * b.y) + (a.z * b.z + a.w * b.w);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) anchor += __shfl_xor_sync(kFull, anchor, o);
+    }
+    if (lane == 0) part[warp] = anchor;
+    __syncthreads();
+    if (tid == 0) {
+        double c = 0.0;
+        for (int w = 0; w < W; ++w) c += part[w];
+        carried = c;
+    }
+    __syncthreads();
+    for (; s.hi - 1 - (t + (long long)tid * E) < s.hi - s.lo; t -= 512 * E) {
 #pragma unroll
         for (int e = 1; e < E; ++e) x[e] += x[e - 1];
         float all = x[E - 1];
@@ -164,19 +173,25 @@ __global__ void __launch_bounds__(256) la_gate_kernel(const GateArgs A)
             if (lane >= o) all += y;
         }
         if (lane == 31) part[warp] = all;
-        const float lanes = __shfl_up_sync(kFull, all, 1);
+        float lanes = __shfl_up_sync(kFull, all, 1);
+        if (lane == 0) lanes = 0.f;
         __syncthreads();
-        double before = carry;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            if (w < warp) before += part[w];
-            carry += part[w];
+        double c = 0.0;
+        if (tid <= W) {
+            c = carried;
+            for (int w = 0; w < tid; ++w) c += part[w];
+            if (tid < W) {
+                const float hi = (float)c;
+                before[tid] = make_float2(hi, isfinite(hi) ? (float)(c - hi) : 0.f);
+            }
         }
-        if (lane > 0) before += lanes;
+        __syncthreads();
+        if (tid == W) carried = c;
+        const float2 b = before[warp];
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (t - e >= s.lo) A.dg[(t - e) * A.run.H + h] = (float)(before + x[e]);
-        __syncthreads();
+            if (t - e >= s.lo) A.dg[(t - e) * A.run.H + h] = b.x + (b.y + (lanes + x[e]));
+        load(t - 512 * E);
     }
 }
 
@@ -491,7 +506,7 @@ extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, c
         G.run = A;
         G.terms = J.terms; G.m_T = m_T; G.d_T = dstate_T; G.dg = dg; G.state = (int)state;
         G.run.slot_out = nullptr;
-        e = launch_after(la_gate_kernel, (unsigned)(p->n_seq * p->H_v), 256, 0, cs, G);
+        e = launch_after(la_gate_kernel, (unsigned)(p->n_seq * p->H_v), 512, 0, cs, G);
     }
     return e ? cuda_fail(e, "la_backward launch") : GDN_OK;
 }

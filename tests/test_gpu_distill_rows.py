@@ -13,7 +13,8 @@ from test_gpu_distill import BF16, F16, F32, INF, check, make, plain  # noqa: E4
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("N,V,K", [(304, 8, 3), (305, 9, 9), (2000, 100, 17), (1000, 1023, 256), (700, 8191, 33), (640, 16380, 100), (1300, 32000, 64),
-                                   (400, 32761, 1), (330, 32768, 5), (310, 4097, 257)])
+                                   (400, 32761, 1), (330, 32768, 5), (310, 4097, 257), (200, 50001, 100), (160, 65522, 256),
+                                   (170, 32760, 64)])
 def test_sizes(N, V, K, dtype):
     check(*make(N, V, K, dtype, seed=V), tau=1.0 if N % 2 else 1.5)
 
@@ -40,7 +41,7 @@ def special(dtype, V=5000, K=12, times=120):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
-@pytest.mark.parametrize("V", [5000, 4999, 1003])
+@pytest.mark.parametrize("V", [5000, 4999, 1003, 32000, 40001])
 def test_special_rows_among_others(dtype, V):
     x, idx, t, order = special(dtype, V)
     loss, lse, d = check(x, idx, t, tau=1.5, in_place=False)
