@@ -5,8 +5,8 @@
 // heads of a key head, rounds once, and leaves each token's q . dq - k . dk per value head, whose running sum from the last token on is dg
 // (la_gate_kernel): with s_t = <M_t, D_t>,  dg_t = a_t <D_t, M_{t-1}> = s_t - v_t . D_t k_t  and
 // s_t = dg_{t+1} + scale dy_t . M_t q_t, where both products are q . dq and k . dk.  Of 4096 tokens of 48 heads of 128 over 16
-// key heads, each call's first reading from DRAM: the joins 39 us each, 117 MB (half its time waits for them; in a call of la_backward
-// most of it is in L2), the gates 14 us, the latency of one CTA a head.
+// key heads, each kernel alone and cold: the joins 37 us each (117 MB from DRAM, at a fifth of whose rate loads wait for loads), the gates 13 us (the
+// latency of a CTA a head).
 #include <climits>
 #include <cstdio>
 
@@ -28,11 +28,12 @@ struct JoinArgs {
     int n_tok, n_seq, H_k, H_v, SK, lower, vec, vec_out;
 };
 
-// LANES lanes a token of one key head (the grid's y), two tokens each; four value heads' rows of both are under way at once.
+// LANES lanes a token of one key head (the grid's y), U tokens each; four value heads' rows of them are under way at once.  Two tokens each: 331 us for all
+// gradients of those 4096 tokens against 326, and with the registers of six CTAs an SM 340.
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) la_join_kernel(const JoinArgs A)
 {
-    constexpr int G = 4, U = 2, per_warp = 32 / LANES;
+    constexpr int G = 4, U = 1, per_warp = 32 / LANES;
     const int lane = threadIdx.x & 31, in_row = lane & (LANES - 1), hk = blockIdx.y, r = A.H_v / A.H_k;
     const long long first = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * (U * per_warp) + lane / LANES;
     begin_after();
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(256) la_join_kernel(const JoinArgs A)
 template <typename T>
 int launch_join(const JoinArgs& A, cudaStream_t st)
 {
-    const int lanes = A.SK >= 128 ? 32 : A.SK / 4, per_cta = 8 * 2 * (32 / lanes);
+    const int lanes = A.SK >= 128 ? 32 : A.SK / 4, per_cta = 8 * 1 * (32 / lanes);
     const dim3 grid((unsigned)((A.n_tok + per_cta - 1) / per_cta), (unsigned)A.H_k);
     return launch_after(lanes == 32 ? la_join_kernel<T, 32> : lanes == 16 ? la_join_kernel<T, 16> : lanes == 8 ? la_join_kernel<T, 8> : la_join_kernel<T, 4>, grid,
                         256, 0, st, A);

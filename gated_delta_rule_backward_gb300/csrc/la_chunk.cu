@@ -31,6 +31,11 @@
 // Long sequences, few heads: segments, as many a sequence and head as fill the SMs.  A first kernel leaves each segment's
 // own contribution to the state (dS alone, summed in TMEM from the last chunk back, against the segment's end) and its decay; the second
 // starts each segment from the sum of those before it.
+//
+// Measured: a prompt of 4096 tokens, 48 heads of 128 (3 segments a head), 70 us; of 32768 tokens, 16 heads (9 segments), 174 us; 23
+// prompts of up to 701 tokens, 16 heads, 60 us.  A chunk of 128 x 128 takes a CTA 3.0 us.  What bounds it is the chain of handovers from one chunk's state to the
+// next and the shared memory that products and threads share: alone and cold, the first kernel 26 us and the second 52 for the 4096 tokens, tensor pipe
+// 44 % of the second's time, issue slots 41 %, DRAM 27 %.
 #include <cuda.h>
 
 #include "gdn_device.cuh"
