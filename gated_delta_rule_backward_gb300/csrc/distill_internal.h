@@ -1,0 +1,28 @@
+// distill_internal.h -- what distillation's two kernels share (include/distill.h).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/distill.h"
+
+namespace gdn {
+
+enum { kLoss = 0, kBoth = 1, kGradient = 2 };
+
+struct DistillArgs {
+    const void* logits;
+    const int* indices;
+    const void* teacher;
+    float *loss, *lse;
+    const float *lse_in, *dloss;
+    void* dlogits;
+    long long row_stride, d_stride;
+    int V, K, seg, chunks, ctas, teacher_dtype;
+    float tau, inv_tau, L;
+};
+
+// Rows that CTAs walk (distill_rows.cu); a cudaError_t as int.
+bool distill_walks_rows(const distill_params_t* p);
+int launch_distill_rows(const distill_params_t* p, const DistillArgs& A, int mode, cudaStream_t st);
+
+}  // namespace gdn
