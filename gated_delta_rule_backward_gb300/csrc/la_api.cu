@@ -455,7 +455,7 @@ extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, c
     A.co = p->scale;
     A.out = per_head;
     A.out_dtype = GDN_F32;
-    int e = launch_run(A, chunked, p->in_dtype, ws + pl.chunk, cs);
+    int e = launch_run(A, false, p->in_dtype, ws + pl.chunk, cs);
 
     JoinArgs J{};
     J.terms = (float*)(ws + pl.terms);
@@ -483,7 +483,7 @@ extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, c
     B.cs = p->scale;
     B.out = per_head;
     B.out_dtype = GDN_F32;
-    if (!e) e = launch_run(B, chunked, p->in_dtype, ws + pl.chunk, cs);
+    if (!e) e = launch_run(B, false, p->in_dtype, ws + pl.chunk, cs);
     if (!e) e = join(k, p->k_s, per_head, dk, 1);
 
     LaRun C = run_of(p, g, cu);
@@ -497,7 +497,6 @@ extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, c
     C.in_stride = C.out_stride = B.in_stride;
     C.reverse = 1;
     C.cs = p->scale;
-    C.again = 1;  // the gradient's states by segments are the run's before, transposed
     C.out = dv;
     C.out_dtype = p->in_dtype;
     if (!e) e = launch_run(C, chunked, p->in_dtype, ws + pl.chunk, cs);
