@@ -306,14 +306,15 @@ int launch_run(const LaRun& A, bool chunked, int dtype, void* workspace, cudaStr
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The chunked form's workspace for these sizes, whatever the roles (S_k = S_v there).
-size_t chunk_bytes(const la_params_t* p)
+// The workspace of the chunked form for these sizes, whatever the roles (S_k = S_v there), and of the backward pass's token form by segments.
+size_t chunk_bytes(const la_params_t* p, bool backward)
 {
     if (!la_chunk_fits(p)) return 0;
     LaRun A = run_of(p, nullptr, nullptr);
     A.DK = (int)p->S_k;
     A.DV = (int)p->S_v;
-    return round256(la_chunk_workspace(A));
+    const size_t a = round256(la_chunk_workspace(A)), b = backward ? round256(la_tokens_workspace(A)) : 0;
+    return a > b ? a : b;
 }
 
 struct BackwardPlan {
@@ -332,7 +333,7 @@ BackwardPlan plan_of(const la_params_t* p)
     pl.heads = take(heads * p->S_k * 4);  // of dq, then of dk
     pl.terms = take(heads * 4);
     pl.m_T = take((size_t)p->n_seq * p->H_v * p->S_v * p->S_k * 4);
-    pl.chunk = take(chunk_bytes(p));
+    pl.chunk = take(chunk_bytes(p, true));
     pl.bytes = at;
     return pl;
 }
@@ -369,7 +370,7 @@ using namespace gdn;
 
 extern "C" int la_form(const la_params_t* p) { return check(p, false) != GDN_OK ? -1 : la_chunk_fits(p) ? 1 : 0; }
 
-extern "C" size_t la_workspace_bytes(const la_params_t* p) { return check(p, false) == GDN_OK ? chunk_bytes(p) : 0; }
+extern "C" size_t la_workspace_bytes(const la_params_t* p) { return check(p, false) == GDN_OK ? chunk_bytes(p, false) : 0; }
 
 extern "C" size_t la_backward_workspace_bytes(const la_params_t* p) { return check(p, true) == GDN_OK ? plan_of(p).bytes : 0; }
 
@@ -383,7 +384,7 @@ extern "C" int la_forward(const la_params_t* p, const void* q, const void* k, co
     const size_t es = elem_size(p->in_dtype), ys = elem_size(p->y_dtype);
     if (!slot_out || (p->n_tok > 0 && !y)) return fail(GDN_ERR_INVALID_ARG, "la_forward: NULL pointer");
     if ((uintptr_t)y % ys || (uintptr_t)slot_out % 4) return fail(GDN_ERR_INVALID_ARG, "la_forward: a pointer is not aligned to its element");
-    const size_t need = chunk_bytes(p);
+    const size_t need = chunk_bytes(p, false);
     if (need && (!workspace || workspace_bytes < need)) return fail(GDN_ERR_WORKSPACE, "la_forward: workspace smaller than la_workspace_bytes()");
     if (need && (uintptr_t)workspace % 16) return fail(GDN_ERR_INVALID_ARG, "la_forward: the workspace must be 16-byte aligned");
     const size_t n_pool = p->n_slots > 0 ? (size_t)((p->n_slots - 1) * p->slot_stride + p->H_v * p->S_v * p->S_k) * 4 : 0;
@@ -455,7 +456,10 @@ extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, c
     A.co = p->scale;
     A.out = per_head;
     A.out_dtype = GDN_F32;
-    int e = launch_run(A, false, p->in_dtype, ws + pl.chunk, cs);
+    // dq and dk token by token, by segments where the chunked form makes their states: dg is a running sum of small differences of both, in which
+    // the chunked form's splits leave 3e-5 of dg's norm (4096 tokens) and this 4e-6
+    auto precise = [&](const LaRun& R) { return chunked ? launch_la_tokens(R, p->in_dtype, ws + pl.chunk, cs) : launch_la_token(R, p->in_dtype, cs); };
+    int e = precise(A);
 
     JoinArgs J{};
     J.terms = (float*)(ws + pl.terms);
@@ -483,7 +487,7 @@ extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, c
     B.cs = p->scale;
     B.out = per_head;
     B.out_dtype = GDN_F32;
-    if (!e) e = launch_run(B, false, p->in_dtype, ws + pl.chunk, cs);
+    if (!e) e = precise(B);
     if (!e) e = join(k, p->k_s, per_head, dk, 1);
 
     LaRun C = run_of(p, g, cu);

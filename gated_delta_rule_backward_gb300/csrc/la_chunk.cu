@@ -826,13 +826,13 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
 #pragma unroll 1
                 for (int s = 1; s <= W.segment; ++s) {
                     float d[16];
-                    load_state<D>(d, state_of(A, D, W.nh, s), row, c, !A.run.again);
+                    load_state<D>(d, state_of(A, D, W.nh, s), row, c, true);
                     const float a = s > 1 ? A.decays[W.nh * A.segments + s] : 0.f;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) m[e] = s > 1 ? fmaf(a, m[e], d[e]) : d[e];
                 }
             } else if (!W.part.last) {
-                load_state<D>(m, state_of(A, D, W.nh, 0), row, c, !A.run.again);
+                load_state<D>(m, state_of(A, D, W.nh, 0), row, c, true);
             } else if (W.q.in >= 0) {
                 load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, row, c, A.run.transposed_in);
             }
@@ -1109,14 +1109,19 @@ bool make_map(CUtensorMap* map, const void* ptr, long long s0, long long s1, int
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What the segments leave, but the last.
+template <int D>
+int launch_segments(const LaChunkArgs& A, cudaStream_t st)
+{
+    if (A.segments < 2) return 0;
+    const int e = (int)cudaFuncSetAttribute(la_segment_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
+    return e ? e : launch_after(la_segment_kernel<D>, (unsigned)(A.run.n_seq * A.run.H * (A.segments - 1)), kThreads, Smem<D>::bytes, st, A);
+}
 template <int D>
 int launch(const LaChunkArgs& A, cudaStream_t st)
 {
     int e = (int)cudaFuncSetAttribute(la_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
-    if (!e && A.segments > 1 && !A.run.again) {
-        e = (int)cudaFuncSetAttribute(la_segment_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
-        if (!e) e = launch_after(la_segment_kernel<D>, (unsigned)(A.run.n_seq * A.run.H * (A.segments - 1)), kThreads, Smem<D>::bytes, st, A);
-    }
+    if (!e) e = launch_segments<D>(A, st);
     if (!e) e = launch_after(la_chunk_kernel<D>, (unsigned)(A.run.n_seq * A.run.H * A.segments), kThreads, Smem<D>::bytes, st, A);
     return e;
 }
@@ -1139,18 +1144,65 @@ size_t la_chunk_workspace(const LaRun& A)
     return segments > 1 ? (size_t)A.n_seq * A.H * segments * ((size_t)A.DK * A.DV + 1) * sizeof(float) : 0;
 }
 
-int launch_la_chunk(const LaRun& run, void* workspace, cudaStream_t st)
+static LaChunkArgs args_of(const LaRun& run, void* workspace, int segments, int per)
 {
     LaChunkArgs A{};
     A.run = run;
-    plan(run, &A.segments, &A.per);
+    A.segments = segments;
+    A.per = per;
     A.states = (float*)workspace;
     A.decays = A.states + (long long)run.n_seq * run.H * A.segments * run.DK * run.DV;
     A.tma = make_map(&A.x, run.x, run.xs0, run.xs1, run.xh, run.n_tok, run.DK) && make_map(&A.y, run.y, run.ys0, run.ys1, run.yh, run.n_tok, run.DK) &&
             make_map(&A.z, run.z, run.zs0, run.zs1, run.zh, run.n_tok, run.DV);
     A.tma_out = A.tma && run.out_dtype == GDN_BF16 && make_map(&A.out, run.out, (long long)run.H * run.DV, run.DV, run.H, run.n_tok, run.DV);
     A.vec_out = (uintptr_t)run.out % 32 == 0;
+    return A;
+}
+
+int launch_la_chunk(const LaRun& run, void* workspace, cudaStream_t st)
+{
+    int segments, per;
+    plan(run, &segments, &per);
+    const LaChunkArgs A = args_of(run, workspace, segments, per);
     return run.DK == 128 ? launch<128>(A, st) : launch<64>(A, st);
+}
+
+// Segments for the token form: as many as fill the places that its CTAs of 64 rows have, of whole chunks, but eight at most: each start
+// from a state of the chunked form's adds to what dg is off by (6 segments 5.9e-6 of its norm, 16 8.6e-6; one 4e-6).  48 heads of 128, gradients of 4096
+// tokens: one segment 4634 us, 6 segments 1547.
+static void plan_tokens(const LaRun& A, int* segments, int* per)
+{
+    const long long ctas = (long long)A.n_seq * A.H * (A.DV / 64), chunks = ((long long)A.T + L - 1) / L;
+    long long s = ctas > 0 ? 4 * kNumSMs / ctas : 1;
+    if (s > 8) s = 8;
+    if (s > chunks) s = chunks;
+    if (s < 1) s = 1;
+    *per = (int)((chunks + s - 1) / s);
+    *segments = *per > 0 ? (int)((chunks + *per - 1) / *per) : 1;
+}
+
+size_t la_tokens_workspace(const LaRun& A)
+{
+    int segments, per;
+    plan_tokens(A, &segments, &per);
+    return segments > 1 ? (size_t)A.n_seq * A.H * segments * ((size_t)A.DK * A.DV + 1) * sizeof(float) : 0;
+}
+
+int launch_la_tokens(const LaRun& run, int dtype, void* workspace, cudaStream_t st)
+{
+    LaRun B = run;
+    int segments, per;
+    plan_tokens(run, &segments, &per);
+    if (segments > 1) {
+        const LaChunkArgs A = args_of(run, workspace, segments, per);
+        const int e = run.DK == 128 ? launch_segments<128>(A, st) : launch_segments<64>(A, st);
+        if (e) return e;
+        B.segments = segments;
+        B.per = per * L;
+        B.states = A.states;
+        B.decays = A.decays;
+    }
+    return launch_la_token(B, dtype, st);
 }
 
 int la_chunk_take_bad(void* stream, int* status) { return la_take_word(&g_la_chunk_bad, stream, status); }

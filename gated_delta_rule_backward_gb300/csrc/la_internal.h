@@ -34,7 +34,10 @@ struct LaRun {
     int reverse;
     float co, cs;
     void* out;  // [n_tok][H][DV]
-    int again;  // chunked form: the workspace holds the segments of a run over the same sequences with y and z in each other's places
+    // Token form: 0, or segments of `per` tokens of each sequence's walk that start from what those before left (transposed, the
+    // first's with the state before it) and their decays; states[.][0] is the state before the first.
+    int segments, per;
+    const float *states, *decays;  // [n_seq H][segments][DK][DV], [n_seq H][segments]
 };
 
 // The token rows of sequence n, and the states that it starts from and leaves (-1: none).
@@ -69,6 +72,8 @@ int launch_la_token(const LaRun& A, int dtype, cudaStream_t stream);
 // The chunked form (la_chunk.cu).
 bool la_chunk_fits(const la_params_t* p);
 size_t la_chunk_workspace(const LaRun& A);  // bytes
+size_t la_tokens_workspace(const LaRun& A);
+int launch_la_tokens(const LaRun& run, int dtype, void* workspace, cudaStream_t st);  // the token form by segments, of the chunked form's sizes
 int launch_la_chunk(const LaRun& A, void* workspace, cudaStream_t stream);
 
 // Read and clear the status words: bad slots and token ranges of either form, and the chunked form's waits that gave up.

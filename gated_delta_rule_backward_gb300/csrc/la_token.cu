@@ -36,14 +36,14 @@ struct LaToken {
 };
 
 // One CTA of W <= 4 warps: 4 RT W rows of one head's state.  RT: rows of a lane; NV: its float4 blocks of a row.
-template <typename T, int NV, int RT>
+template <typename T, int NV, int RT, bool SEGMENTS>
 __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6) la_token_kernel(const LaRun A, int vec)
 {
     __shared__ LaStaged<NV, RT> staged[2][4];  // W tokens, while the next W arrive
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, cl = lane & 7, grp = lane >> 3;
     const int rows = 4 * RT * W;  // of the CTA
-    const unsigned per_head = A.DV / rows, nh = blockIdx.x / per_head;
-    const int first = (int)(blockIdx.x - nh * per_head) * rows;
+    const unsigned per_head = A.DV / rows, of_all = blockIdx.x / per_head, nh = SEGMENTS ? of_all / A.segments : of_all;
+    const int first = (int)(blockIdx.x - of_all * per_head) * rows, segment = SEGMENTS ? (int)(of_all - nh * A.segments) : 0;
     const int n = nh / A.H, h = nh - n * A.H;
 
     begin_after();
@@ -52,15 +52,26 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
         if (threadIdx.x == 0) atomicOr(&g_la_token_status, 1);
         return;
     }
-    const long long len = s.hi - s.lo;
+    // the walk's tokens of this CTA, and whether they are the last
+    long long start = 0, end = s.hi - s.lo;
+    bool is_last = true;
+    if (SEGMENTS) {
+        start = (long long)segment * A.per;
+        if (segment > 0 && start >= end) return;
+        if (start + A.per < end) {
+            end = start + A.per;
+            is_last = false;
+        }
+    }
+    const long long len = end - start;
     const T *xh = (const T*)A.x + (h % A.xh) * A.xs1, *yh = (const T*)A.y + (h % A.yh) * A.ys1, *zh = (const T*)A.z + (h % A.zh) * A.zs1 + first;
 
     // token i of the walk
     LaToken<T, NV, RT> in;
     auto load = [&](long long i) {
-        const long long row = A.reverse ? s.hi - 1 - i : s.lo + i;
+        const long long row = A.reverse ? s.hi - 1 - start - i : s.lo + start + i;
         in.g = 0.f;
-        if (!A.reverse || i > 0) in.g = ld_any(A.g, (row + A.reverse) * A.gs0 + h * A.gs1, A.gate_dtype);
+        if (!A.reverse || start + i > 0) in.g = ld_any(A.g, (row + A.reverse) * A.gs0 + h * A.gs1, A.gate_dtype);
 #pragma unroll
         for (int b = 0; b < in.ROWS; ++b)
             if (32 * b + lane < rows) in.z[b] = ld_plain(zh + row * A.zs0 + 32 * b + lane);
@@ -106,7 +117,19 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
             for (int b = 0; b < NV; ++b) {
                 const int c = 32 * b + 4 * cl, j = first + row_in + r;
                 ulonglong2 v = make_ulonglong2(0, 0);
-                if (s.in >= 0 && c < A.DK) {
+                if (SEGMENTS && (segment > 0 || !is_last)) {
+                    const float* left = A.states + (long long)nh * A.segments * A.DK * A.DV;
+                    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = segment > 0; k <= segment && c < A.DK; ++k) {
+                        const float* d = left + (long long)k * A.DK * A.DV + c * A.DV + j;
+                        const float a = k > 1 ? A.decays[nh * A.segments + k] : 0.f;
+                        w.x = k > 1 ? fmaf(a, w.x, d[0]) : d[0];
+                        w.y = k > 1 ? fmaf(a, w.y, d[A.DV]) : d[A.DV];
+                        w.z = k > 1 ? fmaf(a, w.z, d[2 * A.DV]) : d[2 * A.DV];
+                        w.w = k > 1 ? fmaf(a, w.w, d[3 * A.DV]) : d[3 * A.DV];
+                    }
+                    v = make_ulonglong2(pack2(w.x, w.y), pack2(w.z, w.w));
+                } else if (s.in >= 0 && c < A.DK) {
                     if (!A.transposed_in) v = *reinterpret_cast<const ulonglong2*>(from + j * A.DK + c);
                     else
                         v = make_ulonglong2(pack2(from[c * A.DV + j], from[(c + 1) * A.DV + j]),
@@ -126,7 +149,7 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
     if (W + warp < len) load(W + warp);
     const int shift = A.out_dtype == GDN_F32 ? 2 : 1;
     const long long step = (A.reverse ? -1ll : 1ll) * (((long long)A.H * A.DV) << shift);
-    char* out = (char*)A.out + ((((A.reverse ? s.hi - 1 : s.lo) * A.H + h) * A.DV + first + row_in + mine) << shift);
+    char* out = (char*)A.out + ((((A.reverse ? s.hi - 1 - start : s.lo + start) * A.H + h) * A.DV + first + row_in + mine) << shift);
     int set = 0;
     for (long long t0 = 0; t0 < len; t0 += W, set ^= 1) {
         __syncthreads();
@@ -179,9 +202,9 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
         }
     }
 
-    if (s.out < 0) return;
+    if (s.out < 0 || !is_last) return;
     float last = 1.f;  // backwards, the state before token 0
-    if (A.reverse && len > 0) last = expf(ld_any(A.g, s.lo * A.gs0 + h * A.gs1, A.gate_dtype));
+    if (A.reverse && s.hi > s.lo) last = expf(ld_any(A.g, s.lo * A.gs0 + h * A.gs1, A.gate_dtype));
     const f2 ll = pack2(last, last);
     float* to = A.s_out + s.out * A.out_stride + head;
 #pragma unroll
@@ -212,7 +235,11 @@ int launch_g(const LaRun& A, int vec, cudaStream_t st)
     const int groups = A.DV / (4 * RT);  // warps' rows of a head
     int W = 4;
     while (groups % W != 0) --W;
-    return launch_after(la_token_kernel<T, NV, RT>, (unsigned)((long long)A.n_seq * A.H * (groups / W)), 32 * W, 0, st, A, vec);
+    const long long ctas = (long long)A.n_seq * A.H * (groups / W);
+    if constexpr (sizeof(T) == 2 && (NV == 2 || NV == 4)) {  // the chunked form's sizes
+        if (A.segments) return launch_after(la_token_kernel<T, NV, RT, true>, (unsigned)(ctas * A.segments), 32 * W, 0, st, A, vec);
+    }
+    return launch_after(la_token_kernel<T, NV, RT, false>, (unsigned)ctas, 32 * W, 0, st, A, vec);
 }
 
 bool vec4(const void* ptr, long long s0, long long s1, size_t es) { return (uintptr_t)ptr % (4 * es) == 0 && s0 % 4 == 0 && s1 % 4 == 0; }
@@ -224,7 +251,7 @@ int launch_t(const LaRun& A, cudaStream_t st)
     // Few heads are spread over more warps of one row a lane; many take more rows a lane, so that a token's x and y
     // serve them all.  Rows of 128 columns in all, 24 tokens, 4 rows a lane against 1: 4096 rows 21 us and 19, 8192 21 and 21, 12288 23 and 25, 32768 33 and
     // 54; of 64 columns 8192 rows 19 and 19, 16384 21 and 29; of 256 (2 rows a lane) 4096 rows 23 and 23, 16384 38 and 56.
-    const bool wide = (long long)A.n_seq * A.H * A.DV >= 16 * 4 * kNumSMs;
+    const bool wide = (long long)A.n_seq * A.H * (A.segments ? A.segments : 1) * A.DV >= 16 * 4 * kNumSMs;
     if (A.DK <= 32) return wide ? launch_g<T, 1, 4>(A, vec, st) : launch_g<T, 1, 1>(A, vec, st);
     if (A.DK == 64) return wide ? launch_g<T, 2, 4>(A, vec, st) : launch_g<T, 2, 1>(A, vec, st);
     if (A.DK == 128) return wide ? launch_g<T, 4, 4>(A, vec, st) : launch_g<T, 4, 1>(A, vec, st);
