@@ -28,8 +28,8 @@ struct JoinArgs {
     int n_tok, n_seq, H_k, H_v, SK, lower, vec, vec_out;
 };
 
-// LANES lanes a token of one key head (the grid's y), U tokens each; four value heads' rows of them are under way at once.  Two tokens each: 331 us for all
-// gradients of those 4096 tokens against 326, and with the registers of six CTAs an SM 340.
+// LANES lanes a token of one key head (the grid's y), U tokens each; four value heads' rows of them are under way at once.  Two tokens each: 5 us more for both
+// joins of those 4096 tokens, and with the registers of six CTAs an SM 14.
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) la_join_kernel(const JoinArgs A)
 {

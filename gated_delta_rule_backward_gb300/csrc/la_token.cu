@@ -5,6 +5,8 @@
 // lines), and reads and writes a state once.  The warps of a CTA share one head: each widens one of the next W tokens
 // into shared memory for all of them, and one barrier serves W tokens.
 //
+// Of the backward pass's dq and dk, CTAs of a head may share a sequence by segments (launch_la_tokens).
+//
 // What bounds it: for a token or a few the states' bytes, 8 S_k S_v a head against 4 S_k S_v flops a token (64 sequences of 48 heads
 // of 128, one token: 64 us, 6.3 TB/s, 94 % of the copy rate); for many tokens the chain of tokens, 0.5 us each (32 heads of 128, 32 tokens: 23 us); for
 // the smallest calls latency (one sequence: 7 us alone and cold, two dependent loads, a barrier and cold instructions).
