@@ -216,3 +216,16 @@ def test_an_infinity_stays_with_its_chunk_and_sequence():
     got = la.forward(x["q"], x["k"], x["v"], x["g"], x["pool"], i32([0, 1]), i32([2, 3]), cu_of(counts), T=300)
     assert torch.equal(got[:128], want[:128]) and torch.equal(got[300:], want[300:]) and torch.equal(x["pool"][3], state)
     assert not torch.isfinite(got[201:300, 0, 3]).any()
+
+
+@pytest.mark.parametrize("S,counts", [(128, [640]), (64, [300, 130]), (128, [1100, 90])])
+def test_decays_gradient_is_as_exact_as_fp32(S, counts):
+    """dg is a running sum of small differences of q . dq and k . dk, which are therefore taken in fp32.  A segment's first state is the
+    chunked form's, off by up to 3 2^-18 of its norm at random (two splits' halves and its own): at eight segments the sum jumps by sqrt(8) 1.1e-5 / 4
+    of its own; the token form's roundings are below that.  1e-5 of dg's norm."""
+    x = P.problem(counts, 1, 2, S, dtype=BF16, slots=2, seed=21)
+    slots = list(range(len(counts)))
+    got = la.backward(x["q"], x["k"], x["v"], x["g"], x["pool"], i32(slots), x["dy"], x["dstate"], cu_of(counts), T=max(counts))[3]
+    want = P.backward(x, counts, slots, S ** -0.5)[3]
+    assert float((got.double() - want).norm() / want.norm()) <= 1e-5
+    assert gdn.device_status() == 0
