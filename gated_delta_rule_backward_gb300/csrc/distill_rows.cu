@@ -154,23 +154,15 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
         const Exponent at_max(m, A.L);
         float sum = 0.f;
         if (MODE != kGradient) {
-            const f2 ll = pack2(A.L, A.L), rr = pack2(-at_max.off, -at_max.off);
+            const f2 ll = pack2(A.L, A.L), mm = negative_base(m);
             f2 s2 = 0;
-            if (at_max.base == 0.f) {
 #pragma unroll
-                for (int p = 0; p < PACKS; ++p)
+            for (int p = 0; p < PACKS; ++p)
 #pragma unroll
-                    for (int i = 0; i < VEC; i += 2) {
-                        const float2 v = unpack2(fma2(x[p].pair(i), ll, rr));
-                        s2 = add2(s2, pack2(ex2(v.x), ex2(v.y)));
-                    }
-            } else {
-#pragma unroll
-                for (int p = 0; p < PACKS; ++p)
-#pragma unroll
-                    for (int i = 0; i < VEC; i += 2) s2 = add2(s2, pack2(ex2((x[p].get(i) - m) * A.L), ex2((x[p].get(i + 1) - m) * A.L)));
-            }
-            // what off = m L is off by, out of the sum
+                for (int i = 0; i < VEC; i += 2) {
+                    const float2 v = unpack2(mul2(add2(x[p].pair(i), mm), ll));
+                    s2 = add2(s2, pack2(ex2(v.x), ex2(v.y)));
+                }
             sum = warp_sum(sum2(s2));
         }
         const float es = warp_sum(ej);
@@ -190,7 +182,6 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
         const float pj = ej / esum;
         float base, off;
         if (MODE != kGradient) {
-            if (at_max.base == 0.f && m != -INFINITY) sum *= ex2(-fmaf(m, A.L, -at_max.off));
             const float log_s = logf(sum);
             if (warp * 32 < A.K || warp == 0) {
                 float l = 0.f;
@@ -215,6 +206,14 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
         }
         const float scale = dloss * A.inv_tau;
         if (MODE != kLoss) {
+            // kept as stored: what the sum made of them would take twice the registers
+            if (MODE == kBoth) {
+#pragma unroll
+                for (int p = 0; p < PACKS; ++p) {
+                    uint4& w = reinterpret_cast<uint4&>(x[p]);
+                    asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w));
+                }
+            }
             // scale q, the scale's magnitude in the exponent
             T* out = (T*)A.dlogits + r * A.d_stride;
             T* to = out + (s.at - in);

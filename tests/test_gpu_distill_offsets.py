@@ -1,0 +1,102 @@
+"""Distillation (include/distill.h) of logits that lie far from zero: a softmax does not change when all logits of a row are shifted, however far.
+
+Tolerance.  With D = (m - x) / tau >= 0 (m the row's largest logit), a student's exponential is exp(-D): x - m is rounded once, log2(e) / tau once and their product
+once, 3 2^-24 D, and 2^x is off by 2^-22; the sum over the row adds what test_gpu_distill.py derives.  So q is within 1.2e-5 + 2^-22 D relative, and the teacher's
+p within 1.2e-5 + 2^-22 D_t with its own distances.  None of it depends on where the row lies.  lse is one fp32 number: 4e-6 + 2e-7 |lse|.
+The loss is the sum of p (log p - log q): p's error times what it weighs, and 2^-22 of the terms D, D_t and log V that make up the logarithms, and 1e-5 for the two sums'."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from gated_delta_rule_backward_gb300 import distill  # noqa: E402
+from test_gpu_distill import BF16, F16, F32, make, plain  # noqa: E402
+from test_gpu_distill_clusters import padded  # noqa: E402
+
+
+def far_rows(dtype, V, K, N=None):
+    """Rows of normal logits a long way off, rows of one value, and rows spread over a wide range: those of fp32, as far as the type holds them."""
+    most = torch.finfo(dtype).max
+    offsets = [0.0] + [s * o for o in (40.0, 1e3, 1e4, 6e4, 1e6, 1e9, 1e30) for s in (1, -1) if o < most]
+    flat = [-most, most] + [s * o for o in (300.0, 1e4, 1e9, 5.1e9, 1e10, 1e12, 1e30) for s in (1, -1) if o < most]
+    n = len(offsets) + len(flat) + 2
+    x, idx, t = make(n, V, K, F32, seed=V + K)
+    x[: len(offsets)] += torch.tensor(offsets, device="cuda")[:, None]
+    x[len(offsets): -2] = torch.tensor(flat, device="cuda")[:, None]
+    x[-2] *= 1e4 if dtype != F16 else 1e3
+    x[-1, V // 2:] = -most                       # a masked half
+    x = x.to(dtype)
+    if N is not None:                            # the same rows over and over
+        order = torch.arange(N, device="cuda") % n
+        x, idx, t = x[order].contiguous(), idx[order].contiguous(), t[order].contiguous()
+    return x, idx, t
+
+
+FORMS = {"rows": dict(V=1003, K=20), "wide rows": dict(V=33001, K=12, N=80), "clusters": dict(V=1003, K=20, pad=True), "larger clusters": dict(V=70000, K=12, pad=True),
+         "clusters that read again": dict(V=140001, K=12, dtypes=[F32])}
+CASES = [(form, dtype) for form, kw in FORMS.items() for dtype in kw.get("dtypes", [F32, BF16, F16])]
+
+
+def problem(form, dtype):
+    kw = dict(FORMS[form])
+    kw.pop("dtypes", None)
+    pad = kw.pop("pad", False)
+    x = far_rows(dtype, **kw)
+    return padded(*x) if pad else x
+
+
+def bounds(x, idx, t, dloss, tau):
+    """(loss, its bound, lse, dlogits, their bound) in 64 bits, which at 1e30 hold no log of a sum beside the largest logit: so from the distances to it."""
+    V = x.shape[1]
+    m = x.double().amax(1, keepdim=True)
+    X, T = (x.double() - m) / tau, t.double() / tau
+    loss, lse, d, q, p = plain(x.double() - m, idx, t, dloss, tau)
+    entry = idx >= 0
+    at = idx.long().clamp(0, V - 1)
+    D = -X
+    T = T.masked_fill(~entry, -math.inf)
+    Dt = (T.amax(1, keepdim=True) - T).masked_fill(~entry, 0.0)
+    P = torch.softmax(T, 1).masked_fill(~entry, 0.0)
+    logs = (torch.log_softmax(T, 1).masked_fill(~entry, 0.0) - (X.gather(1, at) - lse[:, None])).abs()
+    off = (P * ((1.2e-5 + 2.0 ** -22 * Dt) * logs + 2.0 ** -22 * (D.gather(1, at) + Dt + math.log(V)))).sum(1) + 1e-5
+    # p of an unlisted token is 0; of one listed twice, each entry's error
+    err = q * (1.2e-5 + 2.0 ** -22 * D) + p * (1.2e-5 + 2.0 ** -22 * Dt.amax(1, keepdim=True))
+    half = 0.0 if x.dtype == F32 else torch.finfo(x.dtype).eps / 2
+    return loss, off, lse + m[:, 0] / tau, d, err * (1 + half) + half * d.abs() + (2.0 ** -24 if x.dtype == F16 else 1e-37)
+
+
+def within(got, want, bound, what):
+    over = ~((got.double() - want).abs() <= bound)
+    assert not over.any(), f"{what}: {int(over.sum())} of {over.numel()} off, in rows {sorted(set(over.nonzero()[:, 0].tolist()))[:20]}, by up to {float((got.double() - want).abs()[over].max()):.3e}"
+
+
+@pytest.mark.parametrize("tau", [1.0, 1.5, 2.0, 4.0])
+@pytest.mark.parametrize("form,dtype", CASES)
+def test_loss(form, dtype, tau):
+    x, idx, t = problem(form, dtype)
+    loss, lse = distill.forward(x, idx, t, tau)
+    r_loss, off, r_lse, _, _ = bounds(x, idx, t, torch.ones(len(x), device="cuda"), tau)
+    held = torch.isfinite(r_lse.float())        # fp32 holds it
+    within(lse[held, None], r_lse[held, None], (4e-6 + 2e-7 * r_lse.abs())[held, None], "lse")
+    assert torch.isinf(lse[~held]).all()
+    within(loss[:, None], r_loss[:, None], off[:, None], "loss")
+
+
+def test_a_sum_whose_correction_would_leave_the_range():
+    """Values whose product with log2(e) is off by just over 126 powers of two when it is rounded: neither the product's 2^x nor the correction's is infinite."""
+    m = torch.tensor([3000016896.0, 3000146432.0, 3000164352.0, 3000244736.0, 3000293888.0, 3000374272.0, 3000392192.0, 3000521728.0])
+    product = m.double() * torch.tensor(1 / math.log(2)).double()
+    off = (product - product.float().double()).abs()
+    assert (off > 126.2).all() and (off < 127.8).all()
+    found = m.tolist()
+    x, idx, t = make(16, 700, 6)
+    x[:] = torch.tensor(found + [-v for v in found], device="cuda")[:, None]
+    for lists in ((idx, t), padded(x, idx, t)[1:]):
+        loss, lse = distill.forward(x, *lists)
+        r_loss, off, r_lse, _, _ = bounds(x, *lists, torch.ones(16, device="cuda"), 1.0)
+        within(loss[:, None], r_loss[:, None], off[:, None], "loss")
+        within(lse[:, None], r_lse[:, None], (4e-6 + 2e-7 * r_lse.abs())[:, None], "lse")
