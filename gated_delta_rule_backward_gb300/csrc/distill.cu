@@ -53,13 +53,14 @@ __device__ __forceinline__ float2 max_and_sum(const Pack<T, VEC> (&x)[PACKS], fl
     float m = -INFINITY;
 #pragma unroll
     for (int p = 0; p < PACKS; ++p) m = fmaxf(m, pack_max(x[p]));
-    const f2 mm = negative_base(m), ll = pack2(L, L);
+    const float base = base_of(m);
+    const f2 bb = pack2(-base, -base), ll = pack2(L, L);
     f2 s2 = 0;
 #pragma unroll
     for (int p = 0; p < PACKS; ++p)
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
-            const float2 v = unpack2(mul2(add2(x[p].pair(i), mm), ll));
+            const float2 v = unpack2(mul2(add2(x[p].pair(i), bb), ll));
             s2 = add2(s2, pack2(ex2(v.x), ex2(v.y)));
         }
     return make_float2(m, sum2(s2));
@@ -168,11 +169,9 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
             }
         }
         if (MODE == kLoss) return;
-        // q = 2^((x - base) L - off): base is 0 but where m L leaves fp32's range (masks of the type's lowest value)
-        off = log2f(ms.y);
-        if (ms.x == -INFINITY && ms.y == 0.f) off = 0.f;  // every logit is -inf: q = 0
-        else if (isfinite(ms.x * A.L)) off = fmaf(ms.x, A.L, off);
-        else base = ms.x;
+        // q = 2^((x - base) L - off), base the largest logit: one number for both would be off by half an ulp of m L powers of two
+        off = ms.x == -INFINITY && ms.y == 0.f ? 0.f : log2f(ms.y);  // every logit is -inf: q = 0
+        base = base_of(ms.x);
     } else {
         __syncthreads();
         const float lse = A.lse_in[row];

@@ -4,7 +4,6 @@
 #include <cuda_runtime.h>
 
 #include "../../include/distill.h"
-#include "gdn_f32x2.cuh"
 
 namespace gdn {
 
@@ -23,13 +22,9 @@ struct DistillArgs {
 };
 
 #if defined(__CUDACC__)
-// What is added to a row's logits before they are multiplied by L: -m for the largest, m, since 2^(x L - m L) with m L rounded would be off by half an ulp of m L powers of
-// two; 0 for a row of nothing but -inf (and NaN), whose exponentials are 0 (or NaN).  +inf leaves NaN.
-__device__ __forceinline__ f2 negative_base(float m)
-{
-    const float b = m == -INFINITY ? 0.f : -m;
-    return pack2(b, b);
-}
+// What is taken off a row's logits before they are multiplied by L: the largest, m, since 2^(x L - m L) with m L rounded would be off by half an ulp of m L powers of
+// two; nothing of a row of -inf (and NaN) alone, whose exponentials are 0 (or NaN).  +inf leaves NaN.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 #endif
 
 // Rows that CTAs walk (distill_rows.cu); a cudaError_t as int.

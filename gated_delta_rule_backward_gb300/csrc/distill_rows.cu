@@ -34,21 +34,6 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// 2^((x - base) L - off): base is 0 but where m L leaves fp32's range (masks of the type's lowest value).
-struct Exponent {
-    float base, off;
-    __device__ __forceinline__ Exponent(float m, float L)
-    {
-        base = 0.f;
-        off = m * L;
-        if (m == -INFINITY) off = 0.f;  // nothing but -inf: 2^-inf is 0
-        else if (isinf(off) && !isinf(m)) {
-            base = m;
-            off = 0.f;
-        }
-    }
-};
-
 // Two neighbours, rounded together.
 __device__ __forceinline__ void put2(float* y, float a, float b)
 {
@@ -151,16 +136,17 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
         m = warp_max(s_max[0][lane & (WARPS - 1)]);
         const float top = warp_max(s_max[1][lane & (WARPS - 1)]);
         const float tj = (t - top) * A.inv_tau, ej = entry ? expf(tj) : 0.f;
-        const Exponent at_max(m, A.L);
-        float sum = 0.f;
+        // q = 2^((x - base) L - off)
+        float sum = 0.f, base = 0.f, off = 0.f;
         if (MODE != kGradient) {
-            const f2 ll = pack2(A.L, A.L), mm = negative_base(m);
+            base = base_of(m);
+            const f2 ll = pack2(A.L, A.L), bb = pack2(-base, -base);
             f2 s2 = 0;
 #pragma unroll
             for (int p = 0; p < PACKS; ++p)
 #pragma unroll
                 for (int i = 0; i < VEC; i += 2) {
-                    const float2 v = unpack2(mul2(add2(x[p].pair(i), mm), ll));
+                    const float2 v = unpack2(mul2(add2(x[p].pair(i), bb), ll));
                     s2 = add2(s2, pack2(ex2(v.x), ex2(v.y)));
                 }
             sum = warp_sum(sum2(s2));
@@ -180,7 +166,6 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
             esum += __shfl_xor_sync(kFull, esum, o);
         }
         const float pj = ej / esum;
-        float base, off;
         if (MODE != kGradient) {
             const float log_s = logf(sum);
             if (warp * 32 < A.K || warp == 0) {
@@ -190,13 +175,9 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
                 if (lane == 0) s_loss[warp] = l;
             }
             if (tid == 0) A.lse[r] = !any ? 0.f : m == -INFINITY && sum == 0.f ? -INFINITY : fmaf(m, A.inv_tau, log_s);
-            const float log2_s = log2f(sum);
-            base = at_max.base;
-            off = m == -INFINITY && sum == 0.f ? 0.f : base != 0.f ? log2_s : fmaf(m, A.L, log2_s);
-            if (m == -INFINITY && sum != sum) off = sum;  // NaN
+            off = m == -INFINITY && sum == 0.f ? 0.f : log2f(sum);  // nothing but -inf: 2^-inf is 0
         } else {
             const float lse = A.lse_in[r];
-            base = 0.f;
             off = lse * kLog2e;
             if (lse == -INFINITY) off = 0.f;
             else if (!isinf(lse) && isinf(off)) {
@@ -220,29 +201,25 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
             const bool alike = (((uintptr_t)out ^ (uintptr_t)in) & 15) == 0;
             const float shift = off - log2f(fabsf(scale));
             const uint32_t sign = scale < 0.f ? (sizeof(T) == 2 ? 0x80008000u : 0x80000000u) : 0u, keep = any ? 0xffffffffu : 0u;
-            auto dense = [&](auto&& exponents) {
+            const f2 ll = pack2(A.L, A.L), rr = pack2(-shift, -shift), bb = pack2(-base, -base);
 #pragma unroll
-                for (int p = 0; p < PACKS; ++p) {
-                    const int at = (p * THREADS + tid) * VEC;
-                    Pack<T, VEC> y;
+            for (int p = 0; p < PACKS; ++p) {
+                const int at = (p * THREADS + tid) * VEC;
+                Pack<T, VEC> y;
 #pragma unroll
-                    for (int i = 0; i < VEC; i += 2) {
-                        const float2 v = exponents(p, i);
-                        put2(y.x + i, ex2(v.x), ex2(v.y));
-                    }
-                    uint4& w = *reinterpret_cast<uint4*>(&y);
-                    w = make_uint4((w.x ^ sign) & keep, (w.y ^ sign) & keep, (w.z ^ sign) & keep, (w.w ^ sign) & keep);
-                    if (alike && at >= s.lo && at + VEC <= s.end) *reinterpret_cast<uint4*>(to + at) = w;
-                    else {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i)
-                            if (at + i >= s.lo && at + i < s.end) to[at + i] = y.x[i];
-                    }
+                for (int i = 0; i < VEC; i += 2) {
+                    const float2 v = unpack2(fma2(add2(x[p].pair(i), bb), ll, rr));
+                    put2(y.x + i, ex2(v.x), ex2(v.y));
                 }
-            };
-            const f2 ll = pack2(A.L, A.L), rr = pack2(-shift, -shift);
-            if (base == 0.f) dense([&](int p, int i) { return unpack2(fma2(x[p].pair(i), ll, rr)); });
-            else dense([&](int p, int i) { return make_float2(fmaf(x[p].get(i) - base, A.L, -shift), fmaf(x[p].get(i + 1) - base, A.L, -shift)); });
+                uint4& w = *reinterpret_cast<uint4*>(&y);
+                w = make_uint4((w.x ^ sign) & keep, (w.y ^ sign) & keep, (w.z ^ sign) & keep, (w.w ^ sign) & keep);
+                if (alike && at >= s.lo && at + VEC <= s.end) *reinterpret_cast<uint4*>(to + at) = w;
+                else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        if (at + i >= s.lo && at + i < s.end) to[at + i] = y.x[i];
+                }
+            }
         }
         s_p[tid] = pj;
         __syncthreads();

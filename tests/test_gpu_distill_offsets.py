@@ -100,3 +100,36 @@ def test_a_sum_whose_correction_would_leave_the_range():
         r_loss, off, r_lse, _, _ = bounds(x, *lists, torch.ones(16, device="cuda"), 1.0)
         within(loss[:, None], r_loss[:, None], off[:, None], "loss")
         within(lse[:, None], r_lse[:, None], (4e-6 + 2e-7 * r_lse.abs())[:, None], "lse")
+
+
+@pytest.mark.parametrize("tau", [1.0, 1.5, 2.0, 4.0])
+@pytest.mark.parametrize("form,dtype", CASES)
+def test_gradient_with_the_loss(form, dtype, tau):
+    x, idx, t = problem(form, dtype)
+    dloss = torch.linspace(-1.5, 1.0, len(x), device="cuda")
+    loss, lse, d = distill.forward(x, idx, t, tau, dloss=dloss)
+    alone = distill.forward(x, idx, t, tau)
+    assert torch.equal(loss, alone[0]) and torch.equal(lse, alone[1])
+    _, _, _, r_d, bound = bounds(x, idx, t, dloss, tau)
+    within(d, r_d, bound, "dlogits")
+    y = x.clone()
+    distill.forward(y, idx, t, tau, dloss=dloss, in_place=True)
+    assert torch.equal(y, d)
+    if dtype == F32:                                 # what moves all logits alike changes nothing
+        assert (d.double().sum(1).abs() <= bound.sum(1)).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_shift_changes_nothing(dtype):
+    """Logits that are whole multiples of 64 stay exact under shifts by multiples of 2^20 within 24 (bf16: 8) bits: the gradient keeps its bits."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    step = 64.0 if dtype == F32 else 2.0 ** 14
+    x = torch.randint(0, 4, (40, 900), generator=gen, device="cuda").float() * step
+    _, idx, t = make(40, 900, 8)
+    for lists in ((idx, t), padded(x, idx, t)[1:]):
+        want = distill.forward(x.to(dtype), *lists, step, dloss=torch.ones(40, device="cuda"))
+        for shift in (2.0 ** 20, -2.0 ** 20, 2.0 ** 20 + 4 * step):
+            y = (x + shift).to(dtype)
+            assert torch.equal(y.float() - shift, x)
+            got = distill.forward(y, *lists, step, dloss=torch.ones(40, device="cuda"))
+            assert torch.equal(got[2], want[2])
