@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
     const T* in = (const T*)A.logits + row * A.row_stride;
     const long long lead = (long long)(((uintptr_t)in & 15) / sizeof(T));
     const long long lo = (long long)rank * A.chunks * A.seg - lead, hi = lo + (long long)A.chunks * A.seg;  // this CTA's columns
-    if (MODE != kGradient && A.ctas > 1) cluster_arrive();  // the others have started before their shared memory is written
+    if (A.ctas > 1) cluster_arrive();  // the others have started before their shared memory is written
     begin_after();
 
     auto load = [&](Pack<T, VEC>(&x)[PACKS], int c) {
@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
     };
     // Whether the row has an entry is known to the first warp alone, so the first chunk is on its way before.
     Pack<T, VEC> x[PACKS];
+    const float lse = MODE == kGradient ? A.lse_in[row] : 0.f;
     load(x, 0);
     if (warp == 0) {
         const int* idx = A.indices + row * A.K;
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
     }
 
     float base = 0.f, off = 0.f;
-    if (MODE != kGradient) {
+    if (MODE != kGradient || fabsf(lse) > kMostLse) {
         float2 ms = max_and_sum<T, VEC, PACKS>(x, A.L);
         for (int c = 1; c < A.chunks; ++c) {
             load(x, c);
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
         }
         ms = s_cta[0];
         for (int i = 1; i < A.ctas; ++i) ms = join(ms, s_cta[i], A.L);
-        if (rank == 0 && warp == 0) {
+        if (MODE != kGradient && rank == 0 && warp == 0) {
             const bool nothing = ms.x == -INFINITY && ms.y == 0.f;  // every logit is -inf
             const float log_s = logf(ms.y);
             float l = 0.f;
@@ -174,13 +175,8 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
         base = base_of(ms.x);
     } else {
         __syncthreads();
-        const float lse = A.lse_in[row];
+        if (A.ctas > 1) cluster_wait();
         off = lse * kLog2e;
-        if (lse == -INFINITY) off = 0.f;
-        else if (isfinite(lse) && !isfinite(off)) {
-            off = 0.f;
-            base = lse * A.tau;
-        }
     }
 
     // the gradient: scale q, then the listed tokens again
@@ -337,7 +333,6 @@ DistillArgs args_of(const distill_params_t* p, const void* logits, const int32_t
     A.logits = logits; A.indices = indices; A.teacher = teacher; A.dloss = dloss; A.dlogits = dlogits;
     A.row_stride = p->row_stride; A.d_stride = p->d_stride;
     A.V = (int)p->V; A.K = (int)p->K; A.teacher_dtype = p->teacher_dtype;
-    A.tau = p->temperature;
     A.inv_tau = (float)(1.0 / (double)p->temperature);
     A.L = (float)(1.4426950408889634 / (double)p->temperature);
     return A;

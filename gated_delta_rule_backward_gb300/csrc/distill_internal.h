@@ -18,8 +18,12 @@ struct DistillArgs {
     void* dlogits;
     long long row_stride, d_stride;
     int V, K, seg, chunks, ctas, teacher_dtype;
-    float tau, inv_tau, L;
+    float inv_tau, L;
 };
+
+// An lse beyond this (its size) is not what the gradient alone goes by: one fp32 number leaves q off by 2^-24 of it.  The row's largest logit and sum are taken again, from the
+// same reading.
+constexpr float kMostLse = 32.f;
 
 #if defined(__CUDACC__)
 // What is taken off a row's logits before they are multiplied by L: the largest, m, since 2^(x L - m L) with m L rounded would be off by half an ulp of m L powers of

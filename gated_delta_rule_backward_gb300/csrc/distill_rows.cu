@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
         float xj = 0.f;
         if (entry) xj = to_f32(in[idx]);
         list(r + gridDim.x);
-        const float dloss = MODE == kLoss ? 0.f : A.dloss[r];
+        const float dloss = MODE == kLoss ? 0.f : A.dloss[r], lse = MODE == kGradient ? A.lse_in[r] : 0.f;
+        const bool sums = MODE != kGradient || fabsf(lse) > kMostLse;
         // the row, from where its copies have landed; its first and last elements where 16 bytes cut them
         Pack<T, VEC> x[PACKS];
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
             }
         }
         float m = -INFINITY;
-        if (MODE != kGradient) {
+        if (sums) {
 #pragma unroll
             for (int p = 0; p < PACKS; ++p) m = fmaxf(m, pack_max(x[p]));
             m = warp_max(m);
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
         const float tj = (t - top) * A.inv_tau, ej = entry ? expf(tj) : 0.f;
         // q = 2^((x - base) L - off)
         float sum = 0.f, base = 0.f, off = 0.f;
-        if (MODE != kGradient) {
+        if (sums) {
             base = base_of(m);
             const f2 ll = pack2(A.L, A.L), bb = pack2(-base, -base);
             f2 s2 = 0;
@@ -175,20 +176,13 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
                 if (lane == 0) s_loss[warp] = l;
             }
             if (tid == 0) A.lse[r] = !any ? 0.f : m == -INFINITY && sum == 0.f ? -INFINITY : fmaf(m, A.inv_tau, log_s);
-            off = m == -INFINITY && sum == 0.f ? 0.f : log2f(sum);  // nothing but -inf: 2^-inf is 0
-        } else {
-            const float lse = A.lse_in[r];
-            off = lse * kLog2e;
-            if (lse == -INFINITY) off = 0.f;
-            else if (!isinf(lse) && isinf(off)) {
-                off = 0.f;
-                base = lse * A.tau;
-            }
         }
+        if (sums) off = m == -INFINITY && sum == 0.f ? 0.f : log2f(sum);  // nothing but -inf: 2^-inf is 0
+        else off = lse * kLog2e;
         const float scale = dloss * A.inv_tau;
         if (MODE != kLoss) {
             // kept as stored: what the sum made of them would take twice the registers
-            if (MODE == kBoth) {
+            if (MODE != kLoss) {
 #pragma unroll
                 for (int p = 0; p < PACKS; ++p) {
                     uint4& w = reinterpret_cast<uint4&>(x[p]);

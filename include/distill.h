@@ -16,13 +16,14 @@
  *     teacher's.
  *
  * distill_forward gives loss and lse, and with dloss and dlogits the gradient in the same call: rows of up to 512 KB are
- * then read once.  distill_backward gives the gradient from the lse of an earlier forward call.
+ * then read once.  distill_backward gives the gradient from the lse of an earlier forward call: of a row whose lse is beyond 32 in size, where one fp32
+ * number would leave q off by 2^-24 of it, it sums the row again instead.
  *
  * Layouts (device memory): logits [N][V] in dtype, rows row_stride elements apart; dlogits in dtype, rows d_stride
  * apart, and it may be the very buffer of logits (then d_stride = row_stride): the gradient replaces them.  indices int32 [N][K],
  * teacher [N][K] in teacher_dtype, both dense; loss, lse, dloss fp32 [N].
- * Arithmetic: fp32 from the stored numbers; exponentials of the student's logits use the hardware's 2^x (2^-22 relative);
- * dlogits are rounded once.  Sums run in an order fixed by the sizes and each row's place within 16 bytes: the same results run to run.
+ * Arithmetic: fp32 from the stored numbers; exponentials of the student's logits are taken of their distances to the row's largest, however far that lies from zero, and use
+ * the hardware's 2^x (2^-22 relative); dlogits are rounded once.  An lse beyond fp32's range is infinite.  Sums run in an order fixed by the sizes and each row's place within 16 bytes: the same results run to run.
  *
  * Ownership, streams and errors are gdn.h's: work is only enqueued, nothing is allocated or kept.
  *   GDN_ERR_INVALID_ARG  NULL pointer, negative N or K, V < 1, a row stride below V, unknown dtype, a temperature that is not

@@ -2,7 +2,8 @@
 
 Tolerance.  With D = (m - x) / tau >= 0 (m the row's largest logit), a student's exponential is exp(-D): x - m is rounded once, log2(e) / tau once and their product
 once, 3 2^-24 D, and 2^x is off by 2^-22; the sum over the row adds what test_gpu_distill.py derives.  So q is within 1.2e-5 + 2^-22 D relative, and the teacher's
-p within 1.2e-5 + 2^-22 D_t with its own distances.  None of it depends on where the row lies.  lse is one fp32 number: 4e-6 + 2e-7 |lse|.
+p within 1.2e-5 + 2^-22 D_t with its own distances.  None of it depends on where the row lies: the gradient alone
+goes by lse up to 32 in size, where its fp32 number adds 2^-24 |lse| and its product with log2(e) the same, 3.8e-6 within the 1.2e-5.  lse is one fp32 number: 4e-6 + 2e-7 |lse|.
 The loss is the sum of p (log p - log q): p's error times what it weighs, and 2^-22 of the terms D, D_t and log V that make up the logarithms, and 1e-5 for the two sums'."""
 import math
 
@@ -133,3 +134,21 @@ def test_a_shift_changes_nothing(dtype):
             assert torch.equal(y.float() - shift, x)
             got = distill.forward(y, *lists, step, dloss=torch.ones(40, device="cuda"))
             assert torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("tau", [1.0, 1.5, 2.0, 4.0])
+@pytest.mark.parametrize("form,dtype", CASES)
+def test_gradient_alone(form, dtype, tau):
+    x, idx, t = problem(form, dtype)
+    dloss = torch.linspace(-1.5, 1.0, len(x), device="cuda")
+    loss, lse = distill.forward(x, idx, t, tau)
+    d = distill.backward(x, idx, t, lse, dloss, tau)
+    _, _, r_lse, r_d, bound = bounds(x, idx, t, dloss, tau)
+    within(d, r_d, bound, "dlogits")
+    within(distill.backward(x, idx, t, r_lse.float(), dloss, tau), r_d, bound, "dlogits from an lse of 64 bits")
+    y = x.clone()
+    distill.backward(y, idx, t, lse, dloss, tau, in_place=True)
+    assert torch.equal(y, d)
+    lse[::2] = float("nan")
+    d = distill.backward(x, idx, t, lse, dloss, tau)
+    assert torch.isnan(d[::2]).all() and torch.isfinite(d[1::2].float()).all()
