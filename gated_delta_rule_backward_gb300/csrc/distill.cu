@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
             for (int j = lane; j < A.K; j += 32)
                 if (s_idx[j] >= 0 && s_p[j] != 0.f) {
                     const float xj = s_x[j];
-                    l += s_p[j] * (xj == -INFINITY && ms.y == ms.y ? INFINITY : s_log[j] - fmaf(xj - ms.x, A.inv_tau, -log_s));
+                    // p first: a masked token's distance over tau may leave fp32's range where p of it does not
+                    l += xj == -INFINITY && ms.y == ms.y ? INFINITY : s_p[j] * (s_log[j] + log_s) - s_p[j] * (xj - ms.x) * A.inv_tau;
                 }
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kFull, l, o);

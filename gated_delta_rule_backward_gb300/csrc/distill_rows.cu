@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
             const float log_s = logf(sum);
             if (warp * 32 < A.K || warp == 0) {
                 float l = 0.f;
-                if (entry && pj != 0.f) l = pj * (xj == -INFINITY && sum == sum ? INFINITY : (tj - logf(esum)) - fmaf(xj - m, A.inv_tau, -log_s));
+                // p first: a masked token's distance over tau may leave fp32's range where p of it does not
+                if (entry && pj != 0.f) l = xj == -INFINITY && sum == sum ? INFINITY : pj * ((tj - logf(esum)) + log_s) - pj * (xj - m) * A.inv_tau;
                 l = warp_sum(l);
                 if (lane == 0) s_loss[warp] = l;
             }

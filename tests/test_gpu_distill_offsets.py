@@ -67,6 +67,8 @@ def bounds(x, idx, t, dloss, tau):
     # p of an unlisted token is 0; of one listed twice, each entry's error
     err = q * (1.2e-5 + 2.0 ** -22 * D) + p * (1.2e-5 + 2.0 ** -22 * Dt.amax(1, keepdim=True))
     half = 0.0 if x.dtype == F32 else torch.finfo(x.dtype).eps / 2
+    # the hardware's 2^x gives 0 below 2^-126: a q or p of a listed token that is lost there counts |dloss| / tau times
+    err = err + 2.0 ** -125 * dloss.double().abs()[:, None] / tau
     return loss, off, lse + m[:, 0] / tau, d, err * (1 + half) + half * d.abs() + (2.0 ** -24 if x.dtype == F16 else 1e-37)
 
 
@@ -152,3 +154,35 @@ def test_gradient_alone(form, dtype, tau):
     lse[::2] = float("nan")
     d = distill.backward(x, idx, t, lse, dloss, tau)
     assert torch.isnan(d[::2]).all() and torch.isfinite(d[1::2].float()).all()
+
+
+@pytest.mark.parametrize("tau", [0.5, 0.01, 100.0])
+@pytest.mark.parametrize("form,dtype", CASES)
+def test_other_temperatures(form, dtype, tau):
+    """Small ones bring losses of listed but masked tokens near fp32's limit: those that it holds are given, others are infinite."""
+    x, idx, t = problem(form, dtype)
+    dloss = torch.linspace(-1.5, 1.0, len(x), device="cuda")
+    loss, lse, d = distill.forward(x, idx, t, tau, dloss=dloss)
+    r_loss, off, r_lse, r_d, bound = bounds(x, idx, t, dloss, tau)
+    held = r_loss + off < torch.finfo(F32).max
+    within(loss[held, None], r_loss[held, None], off[held, None], "loss")
+    assert (loss[r_loss - off > torch.finfo(F32).max * (1 + 2.0 ** -24)] == math.inf).all()
+    held = torch.isfinite(r_lse.float())
+    within(lse[held, None], r_lse[held, None], (4e-6 + 2e-7 * r_lse.abs())[held, None], "lse")
+    assert torch.isinf(lse[~held]).all()
+    within(d, r_d, bound, "dlogits")
+    within(distill.backward(x, idx, t, lse, dloss, tau), r_d, bound, "dlogits alone")
+
+
+@pytest.mark.parametrize("pad", [False, True])
+def test_a_masked_token_that_counts_for_little(pad):
+    """Its distance to the largest logit, over the temperature, is beyond fp32's range; what it adds to the loss is not."""
+    x, idx, t = make(4, 800, 6)
+    x[torch.arange(4, device="cuda")[:, None], idx[:, 2:3].long()] = torch.finfo(F32).min
+    t[:] = torch.tensor([3.0, 2.0, 1.0, 0.0, -1.0, -2.0], device="cuda")
+    if pad:
+        x, idx, t = padded(x, idx, t)
+    loss = distill.forward(x, idx, t, 0.5)[0]
+    r_loss, off, _, _, _ = bounds(x, idx, t, torch.ones(4, device="cuda"), 0.5)
+    assert (r_loss < 3e38).all() and (r_loss > 1e36).all()
+    within(loss[:, None], r_loss[:, None], off[:, None], "loss")
