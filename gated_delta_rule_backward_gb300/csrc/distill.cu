@@ -15,6 +15,7 @@
 //
 // Bytes bound it, the row in and the gradient out, but about 60 % of the copy rate is what it reaches (4096 fp32 rows of 32000, loss and gradient 294 us): a
 // CTA's registers hold one row, and nothing is under way while it is summed.  For a few rows latency does.
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 
@@ -244,7 +245,9 @@ int check(const distill_params_t* p)
     if (p->N < 0 || p->K < 0 || p->V < 1) return fail(GDN_ERR_INVALID_ARG, "distill: N and K must be >= 0, V >= 1");
     if (p->row_stride < p->V || p->d_stride < p->V) return fail(GDN_ERR_INVALID_ARG, "distill: a row stride is below V");
     if (!known_dtype(p->dtype) || !known_dtype(p->teacher_dtype)) return fail(GDN_ERR_INVALID_ARG, "distill: unknown dtype");
-    if (!(p->temperature > 0.f) || std::isinf(p->temperature)) return fail(GDN_ERR_INVALID_ARG, "distill: the temperature must be positive and finite");
+    // below the smallest normal number log2(e) / tau is infinite, and a distance of 0 times it NaN
+    if (!(p->temperature >= FLT_MIN) || std::isinf(p->temperature))
+        return fail(GDN_ERR_INVALID_ARG, "distill: the temperature must be finite and at least the smallest normal number");
     if (p->K > kMostK) return fail(GDN_ERR_UNSUPPORTED, "distill: more than 1024 entries a row");
     if (p->V > (1 << 30) || p->N > (1 << 30) / kMostCtas) return fail(GDN_ERR_UNSUPPORTED, "distill: V or N is too large");
     return GDN_OK;

@@ -27,7 +27,7 @@
  *
  * Ownership, streams and errors are gdn.h's: work is only enqueued, nothing is allocated or kept.
  *   GDN_ERR_INVALID_ARG  NULL pointer, negative N or K, V < 1, a row stride below V, unknown dtype, a temperature that is not
- *                        positive and finite, a pointer not aligned to its element, one of dloss and dlogits without the other
+ *                        finite or below 2^-126 (the smallest normal number), a pointer not aligned to its element, one of dloss and dlogits without the other
  *   GDN_ERR_UNSUPPORTED  K above 1024, V above 2^30, N above 2^27
  *   GDN_ERR_ALIAS        an output overlaps an input (but for dlogits, as above) or another output
  *   GDN_ERR_CUDA         a launch failed
