@@ -37,8 +37,10 @@
  * the element.  Log decays below -104 (exp = 0 in fp32) count as a = 0.  The same call gives the same bits; in the chunked form
  * they depend on n_seq, T and H_v through the segments.
  *
- * An infinity or NaN in a token's inputs reaches what the formulas say, and in the chunked form also the other outputs of the chunk of 128
- * tokens that it lies in (a masked weight of zero is still multiplied); never another sequence, nor, in the token form, an earlier token.
+ * An infinity or NaN in a token's inputs reaches what the formulas say, and in the chunked form also the other outputs (y and dv) of the chunk of 128
+ * tokens that it lies in, y's counted from the sequence's first token, dv's from its last (a masked weight of zero is still multiplied).  dg is a running
+ * sum over the tokens that follow, so what makes a token's dq or dk infinite or NaN reaches dg of every earlier token of the sequence and value head too.  Never
+ * another sequence, nor, in the token form, an earlier token's y.
  * Decays that grow (g > 0) are fine as long as their products stay within fp32.
  *
  * Within one call, a slot that a sequence writes must not be read or written by another sequence (several may read
