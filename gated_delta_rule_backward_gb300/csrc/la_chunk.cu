@@ -805,7 +805,7 @@ __device__ __forceinline__ void writes(const LaChunkArgs& A, const Work& W, char
     }
 }
 
-// The second group: gates, Y' and the state.
+// The second group: Y' and the state (of y's and dv's runs, whose states lie as the pool's do).
 template <int D>
 __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char* sm, const Shared& sh, const Gates& g)
 {
@@ -834,7 +834,7 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
             } else if (!W.part.last) {
                 load_state<D>(m, state_of(A, D, W.nh, 0), row, c, true);
             } else if (W.q.in >= 0) {
-                load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, row, c, A.run.transposed_in);
+                load_state<D>(m, A.run.s_in + W.q.in * A.run.in_stride + (long long)W.h * D * D, row, c, false);
             }
         }
         uint32_t u[16];
@@ -916,7 +916,7 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
             tc::wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) m[e] *= a;
-            store_state<D>(m, to, row, c, A.run.transposed_out);
+            store_state<D>(m, to, row, c, false);
         }
     }
 }
