@@ -594,10 +594,9 @@ gdn_status_t gdn_device_status(void* stream)
     int a = 0, b = 0, c = 0, t = 0, la = 0;
     int e = gdn::tc_take_status(stream, &a);
     if (!e) e = gdn::tc_grad_take_status(stream, &b);
-    if (!e) e = gdn::la_take_status(stream, true, &t);
     // one code a call: where a wait gave up, what the serving kernels met stays for the next call
+    if (!e) e = gdn::la_take_status(stream, !a && !b, &t, &la);
     if (!e && !a && !b && !t) e = gdn::decode_take_status(stream, &c);
-    if (!e && !a && !b && !t) e = gdn::la_take_status(stream, false, &la);
     if (e) return cuda_status(e, "device status");
     if (!a && !b && !t && !c && !la) return GDN_OK;
     if (!a && !b && !t)

@@ -293,8 +293,9 @@ int launch_widen(const void* src, int in_dtype, const long long s[3], int N, int
 // device).  Returns a cudaError_t as int.
 int decode_take_status(void* stream, int* status);
 
-// Reads and clears linear attention's status words: waits that gave up, or bad slots and token ranges.
-int la_take_status(void* stream, bool timeouts, int* status);
+// Reads and clears linear attention's status words: waits that gave up, and, where there were none and bad_too, bad slots and token ranges.  Before the
+// process's first call of it that launches anything the device is not asked.
+int la_take_status(void* stream, bool bad_too, int* timeout, int* bad);
 
 // Sets the text gdn_last_error() returns on the calling thread.
 void set_last_error(const char* msg);

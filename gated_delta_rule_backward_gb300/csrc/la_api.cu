@@ -7,6 +7,7 @@
 // s_t = dg_{t+1} + scale dy_t . M_t q_t, where both products are q . dq and k . dk.  Of 4096 tokens of 48 heads of 128 over 16
 // key heads, each kernel alone and cold: the joins 37 us each (117 MB from DRAM, at a fifth of whose rate loads wait for loads), the gates 13 us (the
 // latency of a CTA a head).
+#include <atomic>
 #include <climits>
 #include <cstdio>
 
@@ -340,27 +341,30 @@ BackwardPlan plan_of(const la_params_t* p)
 
 }  // namespace
 
-int la_take_word(const void* symbol, void* stream, int* status)
+// Whether a call has launched anything: until then there is nothing to ask the device for.
+static std::atomic<bool> g_la_launched{false};
+
+int la_read_words(const void* symbol, void* stream, int n, int* words)
 {
-    cudaStream_t s = (cudaStream_t)stream;
-    int v = 0;
-    int e = (int)cudaMemcpyFromSymbolAsync(&v, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-    if (!e) e = (int)cudaStreamSynchronize(s);
-    if (!e && v) {
-        const int zero = 0;
-        e = (int)cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-        if (!e) e = (int)cudaStreamSynchronize(s);
-    }
-    *status = v;
-    return e;
+    const int e = (int)cudaMemcpyFromSymbolAsync(words, symbol, n * sizeof(int), 0, cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+    return e ? e : (int)cudaStreamSynchronize((cudaStream_t)stream);
 }
 
-int la_take_status(void* stream, bool timeouts, int* status)
+int la_clear_word(const void* symbol, void* stream, int i)
 {
-    int a = 0, b = 0;
-    int e = timeouts ? la_chunk_take_timeout(stream, &a) : la_token_take_bad(stream, &a);
-    if (!e && !timeouts) e = la_chunk_take_bad(stream, &b);
-    *status = a | b;
+    const int zero = 0;
+    const int e = (int)cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), i * sizeof(int), cudaMemcpyHostToDevice, (cudaStream_t)stream);
+    return e ? e : (int)cudaStreamSynchronize((cudaStream_t)stream);
+}
+
+int la_take_status(void* stream, bool bad_too, int* timeout, int* bad)
+{
+    *timeout = *bad = 0;
+    if (!g_la_launched.load(std::memory_order_relaxed)) return 0;
+    int token = 0;
+    int e = la_chunk_take_status(stream, bad_too, timeout, bad);
+    if (!e && !*timeout && bad_too) e = la_token_take_status(stream, &token);
+    *bad |= token;
     return e;
 }
 
@@ -408,6 +412,7 @@ extern "C" int la_forward(const la_params_t* p, const void* q, const void* k, co
     A.co = p->scale;
     A.out = y;
     A.out_dtype = p->y_dtype;
+    g_la_launched.store(true, std::memory_order_relaxed);
     const int e = launch_run(A, la_chunk_fits(p), p->in_dtype, workspace, (cudaStream_t)stream);
     return e ? cuda_fail(e, "la_forward launch") : GDN_OK;
 }
@@ -459,6 +464,7 @@ extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, c
     // dq and dk token by token, by segments where the chunked form makes their states: dg is a running sum of small differences of both, in which
     // the chunked form's splits leave 3e-5 of dg's norm (4096 tokens) and this 4e-6
     auto precise = [&](const LaRun& R) { return chunked ? launch_la_tokens(R, p->in_dtype, ws + pl.chunk, cs) : launch_la_token(R, p->in_dtype, cs); };
+    g_la_launched.store(true, std::memory_order_relaxed);
     int e = precise(A);
 
     JoinArgs J{};

@@ -47,7 +47,7 @@
 namespace gdn {
 namespace {
 
-__device__ int g_la_chunk_bad, g_la_chunk_timeout;
+__device__ int g_la_chunk_status[2];  // bad slots and token ranges; waits that gave up
 
 constexpr int L = 128;         // tokens of a chunk
 constexpr int kGroup = 256;    // threads of a group
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     }
     tc::fence_before();
     __syncthreads();
-    if (tid == 0 && *sh.failed) atomicOr(&g_la_chunk_timeout, 1);
+    if (tid == 0 && *sh.failed) atomicOr(&g_la_chunk_status[1], 1);
     if (warp == 0) tc::tmem_free(tmem, kTmemCols);
 }
 
@@ -1043,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_cons
     begin_after();
     W.q = la_sequence(A.run, n);
     if (!W.q.ok) {
-        if (threadIdx.x == 0) atomicOr(&g_la_chunk_bad, 1);
+        if (threadIdx.x == 0) atomicOr(&g_la_chunk_status[0], 1);
         return;
     }
     W.part = part_of(A, W.q.hi - W.q.lo, W.segment);
@@ -1062,7 +1062,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_cons
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    if (*sh.failed && threadIdx.x == 0) atomicOr(&g_la_chunk_timeout, 1);
+    if (*sh.failed && threadIdx.x == 0) atomicOr(&g_la_chunk_status[1], 1);
     if (threadIdx.x < 32) tc::tmem_free(W.tmem, kTmemCols);
 }
 
@@ -1205,7 +1205,17 @@ int launch_la_tokens(const LaRun& run, int dtype, void* workspace, cudaStream_t 
     return launch_la_token(B, dtype, st);
 }
 
-int la_chunk_take_bad(void* stream, int* status) { return la_take_word(&g_la_chunk_bad, stream, status); }
-int la_chunk_take_timeout(void* stream, int* status) { return la_take_word(&g_la_chunk_timeout, stream, status); }
+int la_chunk_take_status(void* stream, bool bad_too, int* timeout, int* bad)
+{
+    int words[2] = {0, 0};
+    int e = la_read_words(g_la_chunk_status, stream, 2, words);
+    *timeout = words[1];
+    if (!e && words[1]) e = la_clear_word(g_la_chunk_status, stream, 1);
+    else if (!e && words[0] && bad_too) {
+        *bad = words[0];
+        e = la_clear_word(g_la_chunk_status, stream, 0);
+    }
+    return e;
+}
 
 }  // namespace gdn

@@ -76,10 +76,11 @@ size_t la_tokens_workspace(const LaRun& A);
 int launch_la_tokens(const LaRun& run, int dtype, void* workspace, cudaStream_t st);  // the token form by segments, of the chunked form's sizes
 int launch_la_chunk(const LaRun& A, void* workspace, cudaStream_t stream);
 
-// Read and clear the status words: bad slots and token ranges of either form, and the chunked form's waits that gave up.
-int la_take_word(const void* symbol, void* stream, int* status);  // a __device__ int
-int la_token_take_bad(void* stream, int* status);
-int la_chunk_take_bad(void* stream, int* status);
-int la_chunk_take_timeout(void* stream, int* status);
+// n status words in one copy, and one of them set to 0.
+int la_read_words(const void* symbol, void* stream, int n, int* words);
+int la_clear_word(const void* symbol, void* stream, int i);
+// Read and clear: waits that gave up, and, where there were none and bad_too, bad slots and token ranges.
+int la_chunk_take_status(void* stream, bool bad_too, int* timeout, int* bad);
+int la_token_take_status(void* stream, int* bad);
 
 }  // namespace gdn

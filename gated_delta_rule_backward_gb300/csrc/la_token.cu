@@ -267,6 +267,10 @@ int launch_la_token(const LaRun& A, int dtype, cudaStream_t st)
     return dtype == GDN_F32 ? launch_t<float>(A, st) : dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(A, st) : launch_t<__half>(A, st);
 }
 
-int la_token_take_bad(void* stream, int* status) { return la_take_word(&g_la_token_status, stream, status); }
+int la_token_take_status(void* stream, int* bad)
+{
+    const int e = la_read_words(&g_la_token_status, stream, 1, bad);
+    return e || !*bad ? e : la_clear_word(&g_la_token_status, stream, 0);
+}
 
 }  // namespace gdn
