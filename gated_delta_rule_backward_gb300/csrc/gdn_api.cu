@@ -612,7 +612,7 @@ gdn_status_t gdn_device_status(void* stream)
     return fail(GDN_ERR_TIMEOUT,
                 "a kernel's bounded wait gave up; that call's outputs are invalid (chains: %s, "
                 "wait sites 0x%x; gradient kernel: %s; linear attention: %s)",
-                a ? kernels[ker < 5 ? ker : 0] : "ok", (unsigned)a >> 8, grad, t ? "timed out" : "ok");
+                a ? kernels[ker < 5 ? ker : 0] : "ok", (unsigned)a >> 8, grad, !t ? "ok" : t & 2 ? "timed out, copies or products still in flight at exit" : "timed out");
 }
 
 gdn_status_t gdn_selftest_wait_timeout(void* stream)

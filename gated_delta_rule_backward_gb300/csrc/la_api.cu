@@ -378,9 +378,8 @@ extern "C" size_t la_workspace_bytes(const la_params_t* p) { return check(p, fal
 
 extern "C" size_t la_backward_workspace_bytes(const la_params_t* p) { return check(p, true) == GDN_OK ? plan_of(p).bytes : 0; }
 
-extern "C" int la_forward(const la_params_t* p, const void* q, const void* k, const void* v, const void* g, const int32_t* cu,
-                          float* pool, const int32_t* slot_in, const int32_t* slot_out, void* y, void* workspace,
-                          size_t workspace_bytes, void* stream)
+static int forward(const la_params_t* p, const void* q, const void* k, const void* v, const void* g, const int32_t* cu, float* pool,
+                   const int32_t* slot_in, const int32_t* slot_out, void* y, void* workspace, size_t workspace_bytes, void* stream, bool held)
 {
     int st = check(p, false);
     if (st == GDN_OK) st = check_inputs(p, q, k, v, g, cu, pool, slot_in);
@@ -412,9 +411,25 @@ extern "C" int la_forward(const la_params_t* p, const void* q, const void* k, co
     A.co = p->scale;
     A.out = y;
     A.out_dtype = p->y_dtype;
+    A.held = held;
     g_la_launched.store(true, std::memory_order_relaxed);
     const int e = launch_run(A, la_chunk_fits(p), p->in_dtype, workspace, (cudaStream_t)stream);
     return e ? cuda_fail(e, "la_forward launch") : GDN_OK;
+}
+
+extern "C" int la_forward(const la_params_t* p, const void* q, const void* k, const void* v, const void* g, const int32_t* cu,
+                          float* pool, const int32_t* slot_in, const int32_t* slot_out, void* y, void* workspace,
+                          size_t workspace_bytes, void* stream)
+{
+    return forward(p, q, k, v, g, cu, pool, slot_in, slot_out, y, workspace, workspace_bytes, stream, false);
+}
+
+extern "C" int la_selftest_wait_timeout(const la_params_t* p, const void* q, const void* k, const void* v, const void* g, const int32_t* cu,
+                                        float* pool, const int32_t* slot_in, const int32_t* slot_out, void* y, void* workspace,
+                                        size_t workspace_bytes, void* stream)
+{
+    if (check(p, false) == GDN_OK && !la_chunk_fits(p)) return fail(GDN_ERR_UNSUPPORTED, "la_selftest_wait_timeout: the token form waits for nothing");
+    return forward(p, q, k, v, g, cu, pool, slot_in, slot_out, y, workspace, workspace_bytes, stream, true);
 }
 
 extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, const void* v, const void* g, const int32_t* cu,

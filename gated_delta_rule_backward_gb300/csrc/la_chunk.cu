@@ -107,15 +107,18 @@ struct Shared {
     int* nan;
     uint32_t* tmem;
     volatile int* failed;
+    uint64_t* drain;       // a barrier for what is in flight where a wait has given up
+    volatile int* issued;  // loads (of the first kernel: of stages)
     __device__ __forceinline__ explicit Shared(char* at)
-        : bars((uint64_t*)at), decay((float*)(at + 216)), total((long long*)(at + 224)), nan((int*)(at + 232)), tmem((uint32_t*)(at + 236)), failed((volatile int*)(at + 240))
+        : bars((uint64_t*)at), decay((float*)(at + 216)), total((long long*)(at + 224)), nan((int*)(at + 232)), tmem((uint32_t*)(at + 236)), failed((volatile int*)(at + 240)),
+          drain((uint64_t*)(at + 248)), issued((volatile int*)(at + 256))
     {
         static_assert(kBars * 8 <= 216, "barriers");
     }
-    // Until the barrier's phase is complete; gives up after about 0.2 s (of SM clocks: reading the wall clock takes longer than most
+    // Until the barrier's phase is complete; gives up (false) after about 0.2 s (of SM clocks: reading the wall clock takes longer than most
     // waits here), and soon after another wait has given up: what follows then works on what it finds, which is nobody's
-    // result, and the kernel ends.
-    __device__ __forceinline__ void wait(int bar, uint32_t phase) const
+    // result, no more loads are issued, and the kernel ends (give_up()).
+    __device__ __forceinline__ bool wait(int bar, uint32_t phase) const
     {
         const uint32_t a = tc::smem_addr(bars + bar);
         const uint32_t start = clock();
@@ -125,13 +128,13 @@ struct Shared {
                          : "=r"(done)
                          : "r"(a), "r"(phase & 1)
                          : "memory");
-            if (done) return;
+            if (done) return true;
             const uint32_t now = (uint32_t)clock() - start;
             if (now > kLookClocks) {
-                if (*failed) return;
+                if (*failed) return false;
                 if (now > kWaitClocks) {
                     *failed = 1;
-                    return;
+                    return false;
                 }
             }
         }
@@ -414,6 +417,8 @@ __device__ __forceinline__ uint32_t begin(const Shared& sh, F&& arrivals)
 {
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) tc::mbar_init(sh.bars + i, arrivals(i));
+        tc::mbar_init(sh.drain, 1);
+        *sh.issued = 0;
         tc::mbar_fence_init();
         *sh.failed = 0;
     }
@@ -422,6 +427,42 @@ __device__ __forceinline__ uint32_t begin(const Shared& sh, F&& arrivals)
     __syncthreads();
     tc::fence_after();
     return *sh.tmem;
+}
+
+// The last `buffers` of n loads that took turns at barriers from `bar` on.
+__device__ __forceinline__ bool landed(const Shared& sh, int bar, int buffers, int n)
+{
+    bool done = true;
+    for (int i = n > buffers ? n - buffers : 0; i < n; ++i) done &= tc::mbar_wait(sh.bars + bar + i % buffers, (i / buffers) & 1);
+    return done;
+}
+// Where a wait has given up, products and loads may still be in flight, whose tensor and shared memory are another CTA's once this one is gone: waits for them, each for
+// 0.2 s at most.  Out of line, so that the code that always runs stays short (inlined: a prompt of 32768 tokens 174 us, so 173).
+__device__ __noinline__ void give_up(char* shared, bool segments)
+{
+    const Shared sh(shared);
+    const int warp = warp_of(threadIdx.x), n = *sh.issued;
+    if (threadIdx.x == 0) atomicOr(&g_la_chunk_status[1], 1);
+    bool done = true;
+    if (warp == kIssuer && elect()) {
+        tc::commit(sh.drain);
+        done = tc::mbar_wait(sh.drain, 0);
+    } else if (warp == kLoader && elect()) {
+        if (segments) done = landed(sh, kStage, 3, n);
+        else  // in the order Y, X, Z
+            done = landed(sh, kLoadY, 2, (n + 2) / 3) & landed(sh, kLoadX, 1, (n + 1) / 3) & landed(sh, kLoadZ, 2, n / 3);
+    }
+    if (!done) atomicOr(&g_la_chunk_status[1], 2);
+    __syncthreads();
+}
+// What both kernels end with.
+__device__ __forceinline__ void end(const Shared& sh, uint32_t tmem, int warp, bool segments)
+{
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (*sh.failed) give_up((char*)sh.bars, segments);
+    if (warp == 0) tc::tmem_free(tmem, kTmemCols);
 }
 
 __device__ __forceinline__ float* state_of(const LaChunkArgs& A, int D, int nh, int segment)
@@ -530,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     if (!W.q.ok) return;  // the second kernel reports it
     W.part = part_of(A, W.q.hi - W.q.lo, W.segment);
     if (W.part.none || W.part.last) return;
-    const uint32_t tmem = begin(sh, [](int i) { return i >= kMade && i < kGates ? 16 : 1; }), base = tc::smem_addr(sm);
+    const uint32_t tmem = begin(sh, [&](int i) { return i >= kMade && i < kGates ? 16 : i >= kGates && i < kCarry ? 1 + A.run.held : 1; }), base = tc::smem_addr(sm);
     const int count = (int)(W.part.c1 - W.part.c0), yh = W.h % A.run.yh, zh = W.h % A.run.zh;
     // whole chunks, from the last one back: the sequence's last one is the last segment's
     auto token = [&](int it) { return W.token(count - 1 - it); };
@@ -538,8 +579,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     auto keys = [&](int it) { return tmem + kColY - 128 * (it & 1); };
     if (warp == kLoader) {
         if (A.tma && elect()) {
-            for (int it = 0; it < count; ++it) {
-                if (it >= 3) sh.wait(kRead + it % 3, it / 3 - 1);
+            int it = 0;
+            for (; it < count; ++it) {
+                if (it >= 3 && !sh.wait(kRead + it % 3, it / 3 - 1)) break;
                 uint64_t* bar = sh.bars + kStage + it % 3;
                 tc::mbar_expect_tx(bar, 2 * S::tile);
                 load_tile<D>(base + S::stage(it), &A.y, yh, token(it), bar);
@@ -549,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
                     prefetch_tile<D>(&A.z, zh, token(it + 2));
                 }
             }
+            *sh.issued = it;
         }
         __syncwarp();
     } else if (warp == kIssuer) {
@@ -650,10 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
             if (tid == 0) A.decays[W.nh * A.segments + W.segment + 1] = all;
         }
     }
-    tc::fence_before();
-    __syncthreads();
-    if (tid == 0 && *sh.failed) atomicOr(&g_la_chunk_status[1], 1);
-    if (warp == 0) tc::tmem_free(tmem, kTmemCols);
+    end(sh, tmem, warp, true);
 }
 
 // 32 consecutive bytes.
@@ -1014,16 +1054,17 @@ __device__ __forceinline__ void loads(const LaChunkArgs& A, const Work& W, uint3
     auto load = [&](uint32_t to, const CUtensorMap* map, int head, int i, int bar) {
         tc::mbar_expect_tx(sh.bars + bar, S::tile);
         load_tile<D>(to, map, head, W.token(i), sh.bars + bar);
-
     };
+    auto issued = [&](int n) { *sh.issued = n; };
     for (int i = 0; i < W.count; ++i) {
-        if (i > 1) sh.wait(kFreeY + (i & 1), (i >> 1) - 1);
+        if (i > 1 && !sh.wait(kFreeY + (i & 1), (i >> 1) - 1)) return issued(3 * i);
         load(base + S::y(i), &A.y, yh, i, kLoadY + (i & 1));
-        if (i > 0) sh.wait(kBarXS, i - 1);
+        if (i > 0 && !sh.wait(kBarXS, i - 1)) return issued(3 * i + 1);
         load(base + S::x, &A.x, xh, i, kLoadX);
-        if (i > 1) sh.wait(kFreeZ + (i & 1), (i >> 1) - 1);
+        if (i > 1 && !sh.wait(kFreeZ + (i & 1), (i >> 1) - 1)) return issued(3 * i + 2);
         load(base + S::z(i), &A.z, zh, i, kLoadZ + (i & 1));
     }
+    issued(3 * W.count);
 }
 
 template <int D>
@@ -1049,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_cons
     W.part = part_of(A, W.q.hi - W.q.lo, W.segment);
     if (W.part.none) return;
     W.count = W.part.c1 > W.part.c0 ? (int)(W.part.c1 - W.part.c0) : 0;
-    W.tmem = begin(sh, [](int i) { return i < kSingle || i == kFullG || i == kFullW || i == kFullW + 1 ? 1 : i == kFreeO || i >= kFullOut ? 4 : 8; });
+    W.tmem = begin(sh, [&](int i) { return i < kSingle ? 1 : i == kFullG || i == kFullW || i == kFullW + 1 ? 1 + A.run.held : i == kFreeO || i >= kFullOut ? 4 : 8; });
     const int warp = warp_of(threadIdx.x);
     const uint32_t base = tc::smem_addr(sm);
     if (warp < 8) scores<D>(A, W, sh, g);
@@ -1059,11 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_chunk_kernel(const __grid_cons
     else if (warp == kIssuer && elect()) products<D>(A, W, base, sh);
     else if (warp == kLoader && A.tma && elect()) loads<D>(A, W, base, sh);
     else if (warp == kStorer && elect()) stores<D>(A, W, base, sh);
-    __syncwarp();
-    tc::fence_before();
-    __syncthreads();
-    if (*sh.failed && threadIdx.x == 0) atomicOr(&g_la_chunk_status[1], 1);
-    if (threadIdx.x < 32) tc::tmem_free(W.tmem, kTmemCols);
+    end(sh, W.tmem, warp, false);
 }
 
 // Segments a sequence and head, s of p chunks each: at most as many as leave every SM one, and those of the least p + s, since

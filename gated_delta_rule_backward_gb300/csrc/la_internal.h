@@ -38,6 +38,7 @@ struct LaRun {
     // first's with the state before it) and their decays; states[.][0] is the state before the first.
     int segments, per;
     const float *states, *decays;  // [n_seq H][segments][DK][DV], [n_seq H][segments]
+    int held;  // self-test of the chunked form: 1 for a hand-over, the gates', that waits for an arrival too many
 };
 
 // The token rows of sequence n, and the states that it starts from and leaves (-1: none).

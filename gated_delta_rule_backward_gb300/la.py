@@ -17,7 +17,7 @@ from .decode import _allocating_on, _code, _hand_over, _index, _rows, _stream
 _lib = gdn._lib
 
 # Every symbol include/la.h declares.
-EXPORTS = ["la_form", "la_workspace_bytes", "la_backward_workspace_bytes", "la_forward", "la_backward"]
+EXPORTS = ["la_form", "la_workspace_bytes", "la_backward_workspace_bytes", "la_forward", "la_backward", "la_selftest_wait_timeout"]
 
 FORMS = {0: "token", 1: "chunked"}
 
@@ -38,8 +38,9 @@ _lib.la_form.restype = ctypes.c_int
 for _name in ("la_workspace_bytes", "la_backward_workspace_bytes"):
     getattr(_lib, _name).argtypes = [_P]
     getattr(_lib, _name).restype = ctypes.c_size_t
-_lib.la_forward.argtypes = [_P] + [_vp] * 10 + [ctypes.c_size_t, _vp]
-_lib.la_forward.restype = ctypes.c_int
+for _name in ("la_forward", "la_selftest_wait_timeout"):
+    getattr(_lib, _name).argtypes = [_P] + [_vp] * 10 + [ctypes.c_size_t, _vp]
+    getattr(_lib, _name).restype = ctypes.c_int
 _lib.la_backward.argtypes = [_P] + [_vp] * 15 + [ctypes.c_size_t, _vp]
 _lib.la_backward.restype = ctypes.c_int
 
@@ -121,14 +122,23 @@ def _sequences(p, cu_tokens, *slots):
     return None if cu_tokens is None else _index(cu_tokens, "cu_tokens")
 
 
+def _forward(name, p, q, k, v, g, cu_tokens, pool, slot_in, slot_out, y, workspace, stream):
+    cu = _sequences(p, cu_tokens, slot_in, slot_out)
+    st = getattr(_lib, name)(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), cu, pool.data_ptr(),
+                             _index(slot_in, "slot_in"), _index(slot_out, "slot_out"), y.data_ptr(), _ptr(workspace),
+                             0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != gdn.GDN_OK:
+        raise gdn.GdnError(st, name)
+
+
 def la_forward(p: LaParams, q, k, v, g, cu_tokens, pool, slot_in, slot_out, y, workspace, stream=None):
     """Raw C-ABI call on caller-provided tensors; cu_tokens and the workspace (where it needs no bytes) may be None."""
-    cu = _sequences(p, cu_tokens, slot_in, slot_out)
-    st = _lib.la_forward(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), cu, pool.data_ptr(),
-                         _index(slot_in, "slot_in"), _index(slot_out, "slot_out"), y.data_ptr(), _ptr(workspace),
-                         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
-    if st != gdn.GDN_OK:
-        raise gdn.GdnError(st, "la_forward")
+    _forward("la_forward", p, q, k, v, g, cu_tokens, pool, slot_in, slot_out, y, workspace, stream)
+
+
+def selftest_wait_timeout(p: LaParams, q, k, v, g, cu_tokens, pool, slot_in, slot_out, y, workspace, stream=None):
+    """la_forward's chunked form with a hand-over withheld: its bounded waits run out, and the next device_status says so."""
+    _forward("la_selftest_wait_timeout", p, q, k, v, g, cu_tokens, pool, slot_in, slot_out, y, workspace, stream)
 
 
 def la_backward(p: LaParams, q, k, v, g, cu_tokens, pool, slot_in, dy, dstate_T, dq, dk, dv, dg, dstate_0, workspace, stream=None):

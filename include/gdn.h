@@ -218,7 +218,7 @@ int gdn_timing_stages(const gdn_params_t* p, int backward);
 
 /* Device-side status of the work enqueued so far on the current device.  The
  * tensor-core kernels (head size 128; linear attention's chunked form, la.h) wait on hardware barriers for their operand copies
- * and products; every such wait is bounded (0.2 s of wall clock, far beyond any
+ * and products; every such wait is bounded (about 0.2 s, far beyond any
  * legitimate wait), and a wait that gives up makes its kernel return early and record
  * GDN_ERR_TIMEOUT in a device status word, leaving that call's outputs invalid.  This
  * call synchronises `stream` (a cudaStream_t, NULL = legacy default stream), then reads

@@ -95,6 +95,13 @@ int la_forward(const la_params_t* p, const void* q, const void* k, const void* v
                const int32_t* cu_tokens, float* pool, const int32_t* slot_in, const int32_t* slot_out, void* y,
                void* workspace, size_t workspace_bytes, void* stream);
 
+/* Diagnostic: la_forward (chunked form) with one of its kernels' hand-overs withheld, so that bounded waits run out, the kernels wait for their copies and products in
+ * flight and return, and the next gdn_device_status is GDN_ERR_TIMEOUT.  y is unspecified, the pool keeps what it held
+ * (but for sequences without tokens, which wait for nothing). */
+int la_selftest_wait_timeout(const la_params_t* p, const void* q, const void* k, const void* v, const void* g,
+                             const int32_t* cu_tokens, float* pool, const int32_t* slot_in, const int32_t* slot_out, void* y,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* slot_in and the pool as the forward found them (M_0 unchanged).  dstate_T and dstate_0 may be NULL. */
 int la_backward(const la_params_t* p, const void* q, const void* k, const void* v, const void* g,
                 const int32_t* cu_tokens, const float* pool, const int32_t* slot_in, const void* dy,
