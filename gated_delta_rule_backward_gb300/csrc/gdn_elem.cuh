@@ -16,6 +16,14 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 
+// The hardware's 2^x (2^-22 relative; 0 below 2^-126).
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Two neighbours, widened together.
 __device__ __forceinline__ f2 widen2(const float* p) { return pack2(p[0], p[1]); }
 __device__ __forceinline__ f2 widen2(const __nv_bfloat16* p)

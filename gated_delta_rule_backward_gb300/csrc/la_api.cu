@@ -29,75 +29,62 @@ struct JoinArgs {
     int n_tok, n_seq, H_k, H_v, SK, lower, vec, vec_out;
 };
 
-// LANES lanes a token of one key head (the grid's y), U tokens each; four value heads' rows of them are under way at once.  Two tokens each: 5 us more for both
+// LANES lanes a token of one key head (the grid's y); four value heads' rows of it are under way at once.  Two tokens a warp's turn: 5 us more for both
 // joins of those 4096 tokens, and with the registers of six CTAs an SM 14.
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) la_join_kernel(const JoinArgs A)
 {
-    constexpr int G = 4, U = 1, per_warp = 32 / LANES;
+    constexpr int G = 4, per_warp = 32 / LANES;
     const int lane = threadIdx.x & 31, in_row = lane & (LANES - 1), hk = blockIdx.y, r = A.H_v / A.H_k;
-    const long long first = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * (U * per_warp) + lane / LANES;
+    const long long t = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * per_warp + lane / LANES;
     begin_after();
     long long lo = 0, hi = A.n_tok;
     if (A.cu) {  // rows that no sequence owns
         lo = A.cu[0] > 0 ? A.cu[0] : 0;
         hi = A.cu[A.n_seq] < hi ? A.cu[A.n_seq] : hi;
     }
+    const bool owned = t >= lo && t < hi;
     for (int c0 = 0; c0 < A.SK; c0 += 4 * LANES) {
         const int c = c0 + 4 * in_row;
-        Pack<T, 4> w[U];
-        float sum[U][4];
+        Pack<T, 4> w;
+        float sum[4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long t = first + u * per_warp;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[u].x[e] = from_f32<T>(0.f);
-                sum[u][e] = 0.f;
-            }
-            if (t >= lo && t < hi) w[u] = ld_pack<T, 4>((const T*)A.w + t * A.s0 + hk * A.s1 + c, A.vec);
+        for (int e = 0; e < 4; ++e) {
+            w.x[e] = from_f32<T>(0.f);
+            sum[e] = 0.f;
         }
+        if (owned) w = ld_pack<T, 4>((const T*)A.w + t * A.s0 + hk * A.s1 + c, A.vec);
         for (int i0 = 0; i0 < r; i0 += G) {
-            float4 d[U][G];
-            float before[U][G];
+            float4 d[G];
+            float before[G];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int i = 0; i < G; ++i) {
+                const int h = hk + (i0 + i) * A.H_k;
+                const bool real = owned && i0 + i < r;
+                d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                before[i] = 0.f;
+                if (real) d[i] = *reinterpret_cast<const float4*>(A.heads + (t * A.H_v + h) * A.SK + c);
+                if (real && (A.lower || c0 > 0)) before[i] = A.terms[(long long)h * A.n_tok + t];
+            }
 #pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    const long long t = first + u * per_warp;
-                    const int h = hk + (i0 + i) * A.H_k;
-                    const bool real = t >= lo && t < hi && i0 + i < r;
-                    d[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    before[u][i] = 0.f;
-                    if (real) d[u][i] = *reinterpret_cast<const float4*>(A.heads + (t * A.H_v + h) * A.SK + c);
-                    if (real && (A.lower || c0 > 0)) before[u][i] = A.terms[(long long)h * A.n_tok + t];
-                }
+            for (int i = 0; i < G; ++i) {
+                const float4 v = d[i];
+                sum[0] += v.x;
+                sum[1] += v.y;
+                sum[2] += v.z;
+                sum[3] += v.w;
+                float dot = (w.get(0) * v.x + w.get(1) * v.y) + (w.get(2) * v.z + w.get(3) * v.w);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    const float4 v = d[u][i];
-                    sum[u][0] += v.x;
-                    sum[u][1] += v.y;
-                    sum[u][2] += v.z;
-                    sum[u][3] += v.w;
-                    float dot = (w[u].get(0) * v.x + w[u].get(1) * v.y) + (w[u].get(2) * v.z + w[u].get(3) * v.w);
-#pragma unroll
-                    for (int o = LANES / 2; o >= 1; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-                    const long long t = first + u * per_warp;
-                    if (in_row == 0 && t >= lo && t < hi && i0 + i < r)
-                        A.terms[(long long)(hk + (i0 + i) * A.H_k) * A.n_tok + t] = A.lower ? before[u][i] - dot : before[u][i] + dot;
-                }
+                for (int o = LANES / 2; o >= 1; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+                if (in_row == 0 && owned && i0 + i < r) A.terms[(long long)(hk + (i0 + i) * A.H_k) * A.n_tok + t] = A.lower ? before[i] - dot : before[i] + dot;
+            }
             __syncwarp();
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long t = first + u * per_warp;
-            if (t < lo || t >= hi) continue;
+        if (owned) {
             T* to = (T*)A.out + (t * A.H_k + hk) * A.SK + c;
             Pack<T, 4> y;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y.x[e] = from_f32<T>(sum[u][e]);
+            for (int e = 0; e < 4; ++e) y.x[e] = from_f32<T>(sum[e]);
             if (A.vec_out) *reinterpret_cast<Pack<T, 4>*>(to) = y;
             else {
 #pragma unroll
@@ -111,7 +98,7 @@ __global__ void __launch_bounds__(256) la_join_kernel(const JoinArgs A)
 template <typename T>
 int launch_join(const JoinArgs& A, cudaStream_t st)
 {
-    const int lanes = A.SK >= 128 ? 32 : A.SK / 4, per_cta = 8 * 1 * (32 / lanes);
+    const int lanes = A.SK >= 128 ? 32 : A.SK / 4, per_cta = 8 * (32 / lanes);
     const dim3 grid((unsigned)((A.n_tok + per_cta - 1) / per_cta), (unsigned)A.H_k);
     return launch_after(lanes == 32 ? la_join_kernel<T, 32> : lanes == 16 ? la_join_kernel<T, 16> : lanes == 8 ? la_join_kernel<T, 8> : la_join_kernel<T, 4>, grid,
                         256, 0, st, A);
@@ -477,7 +464,7 @@ extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, c
     A.out = per_head;
     A.out_dtype = GDN_F32;
     // dq and dk token by token, by segments where the chunked form makes their states: dg is a running sum of small differences of both, in which
-    // the chunked form's splits leave 3e-5 of dg's norm (4096 tokens) and this 4e-6
+    // the chunked form's splits leave 3e-5 of dg's norm (4096 tokens) and this 5.9e-6
     auto precise = [&](const LaRun& R) { return chunked ? launch_la_tokens(R, p->in_dtype, ws + pl.chunk, cs) : launch_la_token(R, p->in_dtype, cs); };
     g_la_launched.store(true, std::memory_order_relaxed);
     int e = precise(A);

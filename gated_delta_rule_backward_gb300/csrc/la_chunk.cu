@@ -170,12 +170,6 @@ __device__ __forceinline__ void group_barrier()
 {
     asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(T) : "memory");
 }
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // Two fp32 numbers as bf16 hi and lo words (the first in the low halves).
 __device__ __forceinline__ void split2(f2 x, uint32_t& hi, uint32_t& lo)

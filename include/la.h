@@ -47,7 +47,8 @@
  * one slot).  Rows that no sequence owns are left alone in every output.
  *
  * A slot outside [-1, n_slots), a cu_tokens that falls, leaves [0, n_tok] or gives a sequence more than T tokens is only seen
- * on the device: that sequence is skipped (its outputs keep what they held; in the backward pass, its gradients are unspecified)
+ * on the device: that sequence is skipped (its outputs keep what they held; in the backward pass, its gradients are unspecified, and where cu_tokens
+ * falls or leaves [0, n_tok], those of the whole call)
  * and the next gdn_device_status returns GDN_ERR_INVALID_ARG; GDN_ERR_TIMEOUT where one of the chunked form's bounded waits gave up.
  *
  * Ownership, streams and errors are those of gdn.h: work is only enqueued on `stream`, nothing is allocated or kept, no
