@@ -180,6 +180,14 @@ __device__ __forceinline__ void split2(f2 x, uint32_t& hi, uint32_t& lo)
     lo = tc::pack_bf16x2(r.x, r.y);
 }
 
+// And what both leave out, exactly.
+__device__ __forceinline__ uint32_t rest2(f2 x, uint32_t hi, uint32_t lo)
+{
+    const float2 v = unpack2(x);
+    const float a = (v.x - __uint_as_float(hi << 16)) - __uint_as_float(lo << 16), b = (v.y - __uint_as_float(hi & 0xffff0000u)) - __uint_as_float(lo & 0xffff0000u);
+    return tc::pack_bf16x2(a, b);
+}
+
 // A tile's rows in 128-byte swizzle: 64 columns a row, the next 64 columns 16 KB further.
 __device__ __forceinline__ int swizzled(int row, int kc) { return (kc >> 3) * (L * 128) + row * 128 + (((kc & 7) ^ (row & 7)) << 4); }
 
@@ -318,9 +326,10 @@ __device__ __forceinline__ void put4(float* array, bool reverse, int lane, const
 }
 
 // Y'^T = (w Y)^T as bf16 hi and lo into TMEM, by PARTS x 4 warps: a warp's 32 lanes of TMEM are columns of Y, and it takes 128 / PARTS
-// tokens.  A transposing load of 8 tokens x 8 columns leaves a lane two tokens of one column, which is where TMEM's 16 x 128-bit shape wants them.
-template <int D, int PARTS>
-__device__ __forceinline__ void decayed_keys(uint32_t tile, uint32_t tmem, const float* w, int quarter, int part, int lane)
+// tokens.  A transposing load of 8 tokens x 8 columns leaves a lane two tokens of one column, which is where TMEM's 16 x 128-bit shape wants them.  With THIRD, the rest goes to
+// `third`.
+template <int D, int PARTS, bool THIRD>
+__device__ __forceinline__ void decayed_keys(uint32_t tile, uint32_t tmem, uint32_t third, const float* w, int quarter, int part, int lane)
 {
     if (32 * quarter < D) {
 #pragma unroll 1
@@ -330,7 +339,7 @@ __device__ __forceinline__ void decayed_keys(uint32_t tile, uint32_t tmem, const
             for (int b = 0; b < 4; ++b) ww[b] = *reinterpret_cast<const f2*>(w + t0 + 8 * b + 2 * (lane & 3));
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                uint32_t hi[8], lo[8];
+                uint32_t hi[8], lo[8], rest[8];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const uint32_t at = tile + swizzled(t0 + lane, 4 * quarter + 2 * h + c);
@@ -340,12 +349,16 @@ __device__ __forceinline__ void decayed_keys(uint32_t tile, uint32_t tmem, const
                                  : "r"(at)
                                  : "memory");
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        split2(mul2(pack2(__uint_as_float(v[b] << 16), __uint_as_float(v[b] & 0xffff0000u)), ww[b]), hi[2 * b + c], lo[2 * b + c]);
+                    for (int b = 0; b < 4; ++b) {
+                        const f2 x = mul2(pack2(__uint_as_float(v[b] << 16), __uint_as_float(v[b] & 0xffff0000u)), ww[b]);
+                        split2(x, hi[2 * b + c], lo[2 * b + c]);
+                        if (THIRD) rest[2 * b + c] = rest2(x, hi[2 * b + c], lo[2 * b + c]);
+                    }
                 }
-                const uint32_t to = tmem + ((uint32_t)(32 * quarter + 16 * h) << 16) + t0 / 2;
-                st_16x128b(to, hi);
-                st_16x128b(to + 64, lo);
+                const uint32_t lanes = ((uint32_t)(32 * quarter + 16 * h) << 16) + t0 / 2;
+                st_16x128b(tmem + lanes, hi);
+                st_16x128b(tmem + lanes + 64, lo);
+                if (THIRD) st_16x128b(third + lanes, rest);
             }
         }
         tc::wait_st();
@@ -362,8 +375,8 @@ __device__ __forceinline__ uint64_t step_mn(int s) { return (uint64_t)(s * 2048)
 constexpr uint32_t kTransposedB = 1u << 16;
 
 // dS^T (+)= Y'^T Z.  M is 128 for D = 64 too: lanes 64 .. 127 are nobody's.
-template <int D>
-__device__ __forceinline__ void issue_state(uint32_t to, uint32_t y, uint32_t z, bool accumulate)
+template <int D, bool THIRD>
+__device__ __forceinline__ void issue_state(uint32_t to, uint32_t y, uint32_t third, uint32_t z, bool accumulate)
 {
     constexpr uint32_t idesc = tc::idesc_bf16(D) | kTransposedB;
     const uint64_t b = swizzled_mn(z);
@@ -371,6 +384,7 @@ __device__ __forceinline__ void issue_state(uint32_t to, uint32_t y, uint32_t z,
     for (int s = 0; s < L / 16; ++s) {
         tc::mma_ts16(to, y + 8 * s, b + step_mn(s), idesc, accumulate || s > 0);
         tc::mma_ts16(to, y + 64 + 8 * s, b + step_mn(s), idesc, 1);
+        if (THIRD) tc::mma_ts16(to, third + 8 * s, b + step_mn(s), idesc, 1);
     }
 }
 template <int D>
@@ -544,8 +558,8 @@ __device__ __forceinline__ const __nv_bfloat16* head_of(const void* p, int h, in
     return (const __nv_bfloat16*)p + (h % heads) * stride;
 }
 
-// Segment contributions: segments - 1 CTAs a sequence and head.
-template <int D>
+// Segment contributions: segments - 1 CTAs a sequence and head.  With THIRD, for the token form by segments, to fp32: what its dq and dk are off by adds up in dg.
+template <int D, bool THIRD>
 __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_constant__ LaChunkArgs A)
 {
     using S = Smem<D>;
@@ -571,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
     auto token = [&](int it) { return W.token(count - 1 - it); };
     // two buffers of Y' and of its weights, three stages of Y and Z
     auto keys = [&](int it) { return tmem + kColY - 128 * (it & 1); };
+    auto third = [&](int it) { return tmem + kColO + 64 * (it & 1); };
     if (warp == kLoader) {
         if (A.tma && elect()) {
             int it = 0;
@@ -594,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
             sh.wait(kMade + (it & 3), it >> 2);
             tc::fence_after();
             if (elect()) {
-                issue_state<D>(tmem, keys(it), base + S::stage(it) + S::tile, it > 0);
+                issue_state<D, THIRD>(tmem, keys(it), third(it), base + S::stage(it) + S::tile, it > 0);
                 tc::commit(sh.bars + kProduct + (it & 1));
                 tc::commit(sh.bars + kRead + it % 3);
             }
@@ -653,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_segment_kernel(const __grid_co
             }
             sh.wait(kGates + (it & 3), it >> 2);
             tc::fence_after();
-            decayed_keys<D, 4>(base + S::stage(it), keys(it), w, warp & 3, warp >> 2, lane);
+            decayed_keys<D, 4, THIRD>(base + S::stage(it), keys(it), third(it), w, warp & 3, warp >> 2, lane);
             tc::fence_before();
             sh.arrive(kMade + (it & 3));
         }
@@ -924,7 +939,7 @@ __device__ __forceinline__ void states(const LaChunkArgs& A, const Work& W, char
             tc::fence_async_smem();
         }
         sh.arrive(kFullS);
-        decayed_keys<D, 2>(base + S::y(i), W.tmem + kColY, g.w + L * (i & 1), quarter, half, lane);
+        decayed_keys<D, 2, false>(base + S::y(i), W.tmem + kColY, 0, g.w + L * (i & 1), quarter, half, lane);
         tc::wait_st();
         tc::fence_before();
         sh.arrive(kFullK);
@@ -980,7 +995,7 @@ __device__ __forceinline__ void products(const LaChunkArgs& A, const Work& W, ui
         if (made) sh.wait(kFullZ, A.tma ? 0 : i);
         sh.wait(kFullK, i);
         tc::fence_after();
-        issue_state<D>(W.tmem + kColS, W.tmem + kColY, base + S::z(i), true);
+        issue_state<D, false>(W.tmem + kColS, W.tmem + kColY, 0, base + S::z(i), true);
         tc::commit(sh.bars + kBarS);
         tc::commit(sh.bars + kFreeY + (i & 1));
         sh.wait(kFullP, i);
@@ -1141,18 +1156,18 @@ bool make_map(CUtensorMap* map, const void* ptr, long long s0, long long s1, int
 }
 
 // What the segments leave, but the last.
-template <int D>
+template <int D, bool THIRD>
 int launch_segments(const LaChunkArgs& A, cudaStream_t st)
 {
     if (A.segments < 2) return 0;
-    const int e = (int)cudaFuncSetAttribute(la_segment_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
-    return e ? e : launch_after(la_segment_kernel<D>, (unsigned)(A.run.n_seq * A.run.H * (A.segments - 1)), kThreads, Smem<D>::bytes, st, A);
+    const int e = (int)cudaFuncSetAttribute(la_segment_kernel<D, THIRD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
+    return e ? e : launch_after(la_segment_kernel<D, THIRD>, (unsigned)(A.run.n_seq * A.run.H * (A.segments - 1)), kThreads, Smem<D>::bytes, st, A);
 }
 template <int D>
 int launch(const LaChunkArgs& A, cudaStream_t st)
 {
     int e = (int)cudaFuncSetAttribute(la_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
-    if (!e) e = launch_segments<D>(A, st);
+    if (!e) e = launch_segments<D, false>(A, st);
     if (!e) e = launch_after(la_chunk_kernel<D>, (unsigned)(A.run.n_seq * A.run.H * A.segments), kThreads, Smem<D>::bytes, st, A);
     return e;
 }
@@ -1226,7 +1241,7 @@ int launch_la_tokens(const LaRun& run, int dtype, void* workspace, cudaStream_t 
     plan_tokens(run, &segments, &per);
     if (segments > 1) {
         const LaChunkArgs A = args_of(run, workspace, segments, per);
-        const int e = run.DK == 128 ? launch_segments<128>(A, st) : launch_segments<64>(A, st);
+        const int e = run.DK == 128 ? launch_segments<128, true>(A, st) : launch_segments<64, true>(A, st);
         if (e) return e;
         B.segments = segments;
         B.per = per * L;

@@ -30,3 +30,17 @@ def test_decays_gradient(S, counts, segments):
         assert off(a, b) <= 2.0 ** -8 / 3 ** 0.5
     assert off(got[4], want[4]) <= 3 * 2.0 ** -16
     assert gdn.device_status() == 0
+
+
+@pytest.mark.parametrize("S,T,H", [(128, 1000, 6), (64, 1000, 4), (128, 2048, 2), (64, 4096, 4)])
+def test_segments_are_as_exact_as_one_walk(S, T, H):
+    """The same numbers as fp32 tensors go in one walk of the token form.  The segments' first states are sums in fp32 too, of keys whose weights are split without a rest, so that dg is off
+    by no more than the walk's: errors of one size, drawn anew at eight places; half as much again."""
+    x = P.problem([T], 1, H, S, dtype=torch.bfloat16, slots=1, seed=S + T)
+    want = P.backward(x, [T], [0], S ** -0.5)[3]
+    grads = lambda x: la.backward(x["q"], x["k"], x["v"], x["g"], x["pool"], i32([0]), x["dy"], x["dstate"])[3]
+    off = lambda a: float((a.double() - want).norm() / want.norm())
+    wide = {n: t.float() for n, t in x.items()}
+    assert la.form(la.params_for(wide["q"], wide["k"], wide["v"], wide["g"], wide["pool"], 1)) == "token"
+    assert off(grads(x)) <= 1.5 * off(grads(wide))
+    assert gdn.device_status() == 0
