@@ -10,6 +10,8 @@
 // What bounds it: for a token or a few the states' bytes, 8 S_k S_v a head against 4 S_k S_v flops a token (64 sequences of 48 heads
 // of 128, one token: 64 us, 6.3 TB/s, 94 % of the copy rate); for many tokens the chain of tokens, 0.5 us each (32 heads of 128, 32 tokens: 23 us); for
 // the smallest calls latency (one sequence: 7 us alone and cold, two dependent loads, a barrier and cold instructions).
+#include <type_traits>
+
 #include "gdn_device.cuh"
 #include "gdn_elem.cuh"
 #include "gdn_launch.cuh"
@@ -20,14 +22,17 @@ namespace {
 
 __device__ int g_la_token_status;
 
-// e^g as the sum of two numbers.  One would be off by up to 2^-24 of itself, always the same way for a decay that does not change, so that a state which remembers n tokens
-// would be off by n times that (fp32 prompts of 2000 tokens 2.6e-5 of the state's norm; so 4e-7).  e^g - 1 is exact to 2^-24 of |g|, which n of about 1 / |g| make
-// 2^-24.  Beyond half a token's memory one number does, and e^g - 1 would lose what is left of it.
-__device__ __forceinline__ float2 la_decay(float g)
+// How a state decays: m <- m + (e^g - 1) m, with e^g - 1 off by 2^-24 of |g|, or (past == false), beyond half a token's memory, m <- e^g m.  One number for e^g
+// would be off by up to 2^-24 of itself, always the same way for a decay that does not change, so that a state which remembers n of about 1 / |g| tokens would be off
+// by n times that (fp32 prompts of 2000 tokens 2.6e-5 of the state's norm; so 4e-7).  A strong decay has to leave nothing of what was before, which a sum with it would.
+struct LaDecay {
+    float by;
+    bool past;
+};
+__device__ __forceinline__ LaDecay la_decay(float g)
 {
-    if (!(fabsf(g) <= 0.6875f)) return make_float2(expf(g), 0.f);
-    const float e = expm1f(g), a = 1.f + e;
-    return make_float2(a, e - (a - 1.f));
+    const bool past = fabsf(g) <= 0.6875f;
+    return {past ? expm1f(g) : expf(g), past};
 }
 
 // A token for all warps of a CTA: y and x in fp32, the CTA's rows of cs z, and the decay.
@@ -35,8 +40,7 @@ template <int NV, int RT>
 struct LaStaged {
     float4 y[8 * NV], x[8 * NV];
     float z[16 * RT];
-    float2 a;
-    float inverse;  // by segments: of a.x, 0 where a.y is
+    LaDecay a;
 };
 
 // A lane's share of one token as it arrives.
@@ -114,10 +118,7 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
 #pragma unroll
         for (int b = 0; b < in.ROWS; ++b)
             if (32 * b + lane < rows) S.z[32 * b + lane] = A.cs * to_f32(in.z[b]);
-        if (lane == 0) {
-            S.a = la_decay(in.g);
-            if (SEGMENTS) S.inverse = S.a.y != 0.f ? 1.f / S.a.x : 0.f;
-        }
+        if (lane == 0) S.a = la_decay(in.g);
     };
     if (warp < len) load(warp);
 
@@ -167,9 +168,6 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
     const long long step = (A.reverse ? -1ll : 1ll) * (((long long)A.H * A.DV) << shift);
     char* out = (char*)A.out + ((((A.reverse ? s.hi - 1 - start : s.lo + start) * A.H + h) * A.DV + first + row_in + mine) << shift);
     int set = 0;
-    // By segments, where no call has to give the bits of its tokens one by one, a decay is one number after all, rounded so that the product of those walked is off by one
-    // rounding, `off`: gradients of 4096 tokens 1727 us, with two numbers an element 1920, and 1684 with one that is not.
-    float off = 0.f;
     for (long long t0 = 0; t0 < len; t0 += W, set ^= 1) {
         __syncthreads();
         // the tokens after these W, staged by the warps while they are in them
@@ -180,13 +178,7 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
         const int now = len - t0 < W ? (int)(len - t0) : W;
         for (int i = 0; i < now; ++i) {
             const LaStaged<NV, RT>& S = staged[set][i];
-            float a = S.a.x;
-            if (SEGMENTS) {
-                const float rest = fmaf(-a, off, S.a.y);
-                a += rest;
-                off = ((a - S.a.x) - rest) * S.inverse;
-            }
-            const f2 aa = pack2(a, a), bb = pack2(S.a.y, S.a.y);
+            const f2 aa = pack2(S.a.by, S.a.by);
             f2 zz[RT], o2[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
@@ -194,23 +186,23 @@ __global__ void __launch_bounds__(128, RT * NV >= 16 ? 4 : RT * NV >= 8 ? 5 : 6)
                 zz[r] = pack2(z, z);
                 o2[r] = 0;
             }
+            auto update = [&](auto past) {
 #pragma unroll
-            for (int b = 0; b < NV; ++b) {
-                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(&S.y[8 * b + cl]);
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&S.x[8 * b + cl]);
+                for (int b = 0; b < NV; ++b) {
+                    const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(&S.y[8 * b + cl]);
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&S.x[8 * b + cl]);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    if (SEGMENTS) {
-                        m[r][b][0] = fma2(y.x, zz[r], mul2(m[r][b][0], aa));
-                        m[r][b][1] = fma2(y.y, zz[r], mul2(m[r][b][1], aa));
-                    } else {
-                        m[r][b][0] = fma2(m[r][b][0], aa, fma2(m[r][b][0], bb, mul2(y.x, zz[r])));
-                        m[r][b][1] = fma2(m[r][b][1], aa, fma2(m[r][b][1], bb, mul2(y.y, zz[r])));
+                    for (int r = 0; r < RT; ++r) {
+                        f2 &m0 = m[r][b][0], &m1 = m[r][b][1];
+                        m0 = fma2(m0, aa, past.value ? fma2(y.x, zz[r], m0) : mul2(y.x, zz[r]));
+                        m1 = fma2(m1, aa, past.value ? fma2(y.y, zz[r], m1) : mul2(y.y, zz[r]));
+                        o2[r] = fma2(m0, x.x, o2[r]);
+                        o2[r] = fma2(m1, x.y, o2[r]);
                     }
-                    o2[r] = fma2(m[r][b][0], x.x, o2[r]);
-                    o2[r] = fma2(m[r][b][1], x.y, o2[r]);
                 }
-            }
+            };
+            if (S.a.past) update(std::true_type{});
+            else update(std::false_type{});
             float o[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r) o[r] = sum2(o2[r]);

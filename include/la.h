@@ -28,8 +28,8 @@
  *              NULL: every sequence has T tokens, n_tok = n_seq T
  *   pool   [n_slots][H_v][S_v][S_k] fp32, slots slot_stride elements apart
  *   slot_in, slot_out  int32 [n_seq]
- * Arithmetic: states and sums are fp32 whatever the types.  The token form takes a decay as the sum of two fp32 numbers (CUDA's expm1f; expf beyond
- * half a token's memory), so that its rounding does not add up over the tokens that a state remembers; an infinite state may become NaN by it; the backward pass takes dq and dk in it always, by
+ * Arithmetic: states and sums are fp32 whatever the types.  The token form adds (e^g - 1) times a state to it (CUDA's expm1f; beyond half
+ * a token's memory e^g times it, expf), so that a decay's rounding does not add up over the tokens that a state remembers; an infinite state may become NaN by it; the backward pass takes dq and dk in it always, by
  * segments whose first states the chunked form makes where it fits, and dv in the form that la_form() says.  The chunked form's products take bf16
  * inputs as they are and fp32 operands (states, weighted scores, decayed keys) as the sum of two bf16 numbers, 2^-16 relative,
  * with fp32 accumulation; its sums of log decays are exact in 64-bit fixed point (2^-31 powers of two), each exponential of a difference the
