@@ -5,8 +5,9 @@
 // (maximum, then sum) needs a barrier.  The list is a thread's business each: index and teacher's logit arrive a row ahead, and its softmax takes the same
 // two reductions.
 //
-// Bytes bound it, the row in and the gradient out: 8192 bf16 rows of 32000, loss and gradient 198 us (80 % of the copy rate; issue slots 53 %, two
-// exponentials an element), the gradient alone 171 us (92 %); 4096 fp32 rows of 32000, one CTA an SM, 178 us (88 %) and 163 (97 %).
+// Bytes bound it, the row in and the gradient out: 8192 bf16 rows of 32000, loss and gradient 201 us (78 % of the copy rate; issue slots 56 %, two
+// exponentials an element), the gradient alone 170 us (93 %; 20 more where lse is far from zero and the rows are summed again); 4096 fp32 rows of 32000, one CTA an SM, 177 us (89 %) and
+// 168 (94 %).
 #include "distill_internal.h"
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
@@ -275,8 +276,8 @@ constexpr int kLeastWide = kNumSMs / 2;
 
 // Rows that a CTA of the rows' kernel walks: up to 64 KB, or of many rows 128 KB, with a list of no more entries than it has threads.  Loss and gradient of
 // bf16 rows of 32000, against clusters (with the call's 6 us of an idle GPU): 1 row 11 us and 11, 64 rows 11 and 13, 200 rows 15 and 21, 1216 rows 39 and 48,
-// 4096 rows 107 and 147; rows of 8000: 1 row 9 and 11, 200 rows 9 and 13, 4096 rows 42 and 57.  fp32 rows of 32000, one CTA an SM: 1 row 12 and 11, 64 rows 13
-// and 15 (the gradient alone 12 and 11), 100 rows 13 and 21, 300 rows 21 and 29, 4096 rows 178 and 294.
+// 4096 rows 107 and 147; rows of 8000: 1 row 9 and 11, 200 rows 9 and 13, 4096 rows 42 and 57.  fp32 rows of 32000, one CTA an SM: 1 row 11 and 11, 64 rows 14
+// and 15 (the gradient alone 13 and 13), 100 rows 13 and 21, 300 rows 21 and 29, 4096 rows 177 and 291.
 bool distill_walks_rows(const distill_params_t* p)
 {
     const int vec = 16 / (int)elem_size(p->dtype);

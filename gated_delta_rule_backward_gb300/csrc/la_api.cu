@@ -5,7 +5,7 @@
 // heads of a key head, rounds once, and leaves each token's q . dq - k . dk per value head, whose running sum from the last token on is dg
 // (la_gate_kernel): with s_t = <M_t, D_t>,  dg_t = a_t <D_t, M_{t-1}> = s_t - v_t . D_t k_t  and
 // s_t = dg_{t+1} + scale dy_t . M_t q_t, where both products are q . dq and k . dk.  Of 4096 tokens of 48 heads of 128 over 16
-// key heads, each kernel alone and cold: the joins 37 us each (117 MB from DRAM, at a fifth of whose rate loads wait for loads), the gates 13 us (the
+// key heads, each kernel alone and cold: the joins 35 and 36 us (117 MB from DRAM, at half of whose rate loads wait for loads), the gates 13 us (the
 // latency of a CTA a head).
 #include <atomic>
 #include <climits>
@@ -464,7 +464,7 @@ extern "C" int la_backward(const la_params_t* p, const void* q, const void* k, c
     A.out = per_head;
     A.out_dtype = GDN_F32;
     // dq and dk token by token, by segments where the chunked form makes their states: dg is a running sum of small differences of both, in which
-    // the chunked form's splits leave 3e-5 of dg's norm (4096 tokens) and this 5.9e-6
+    // the chunked form's splits leave 3e-5 of dg's norm (4096 tokens) and this 5.2e-6
     auto precise = [&](const LaRun& R) { return chunked ? launch_la_tokens(R, p->in_dtype, ws + pl.chunk, cs) : launch_la_token(R, p->in_dtype, cs); };
     g_la_launched.store(true, std::memory_order_relaxed);
     int e = precise(A);

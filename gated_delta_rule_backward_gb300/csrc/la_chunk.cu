@@ -1174,9 +1174,9 @@ int launch(const LaChunkArgs& A, cudaStream_t st)
 
 }  // namespace
 
-// From 32 tokens on, a chunk's fixed cost is less than that many steps: 32 heads of 128, 31 tokens 21 us token by token and 17 in a chunk (24 tokens 19
-// and 17), 2048 heads 189 and 177 (24 tokens 152 and 177).  Of many heads of 64, half as wide a step, only from 48 on: 1024 heads, 40 tokens 56 us and
-// 60, 48 tokens 65 and 60; 384 heads, 32 tokens 27 and 29, 40 tokens 31 and 29; 256 heads, 32 tokens 25 and 21; 32 heads, 19 and 13.
+// From 32 tokens on, a chunk's fixed cost is less than that many steps: 32 heads of 128, 31 tokens 23 us token by token and 17 in a chunk (24 tokens 19
+// and 17), 2048 heads 203 and 177 (24 tokens 162 and 177).  Of many heads of 64, half as wide a step, only from 48 on: 1024 heads, 40 tokens 60 us and
+// 60, 48 tokens 70 and 60, 768 heads, 32 tokens 48 and 50; 384 heads, 32 tokens 29 and 29, 40 tokens 33 and 29; 256 heads, 32 tokens 27 and 21; 32 heads, 21 and 13.
 bool la_chunk_fits(const la_params_t* p)
 {
     const int least = p->S_k == 64 && p->n_seq * p->H_v > 4 * kNumSMs ? 48 : 32;
@@ -1213,9 +1213,9 @@ int launch_la_chunk(const LaRun& run, void* workspace, cudaStream_t st)
     return run.DK == 128 ? launch<128>(A, st) : launch<64>(A, st);
 }
 
-// Segments for the token form: as many as fill the places that its CTAs of 64 rows have, of whole chunks, but eight at most: each start
-// from a state of the chunked form's adds to what dg is off by (6 segments 5.9e-6 of its norm, 16 8.6e-6; one 4e-6).  48 heads of 128, gradients of 4096
-// tokens: one segment 4634 us, 6 segments 1547.
+// Segments for the token form: as many as fill the places that its CTAs of 64 rows have, of whole chunks, but eight at most, each of which reads what those before
+// it left.  48 heads of 128, gradients of 4096 tokens: one segment 5012 us, 6 segments 1701; nine sequences of up to 500 tokens, 8 heads of 64: 429 and (4) 247.  More than
+// eight would be faster for few heads: 4 heads of 64, 4096 tokens, 16 segments 305 us and 32 250 against 468, 6 heads of 128 702 and 572 against 669; dg stays as exact.
 static void plan_tokens(const LaRun& A, int* segments, int* per)
 {
     const long long ctas = (long long)A.n_seq * A.H * (A.DV / 64), chunks = ((long long)A.T + L - 1) / L;

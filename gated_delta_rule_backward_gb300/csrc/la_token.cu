@@ -8,7 +8,7 @@
 // Of the backward pass's dq and dk, CTAs of a head may share a sequence by segments (launch_la_tokens).
 //
 // What bounds it: for a token or a few the states' bytes, 8 S_k S_v a head against 4 S_k S_v flops a token (64 sequences of 48 heads
-// of 128, one token: 64 us, 6.3 TB/s, 94 % of the copy rate); for many tokens the chain of tokens, 0.5 us each (32 heads of 128, 32 tokens: 23 us); for
+// of 128, one token: 65 us, 6.2 TB/s, 93 % of the copy rate); for many tokens the chain of tokens, 0.5 us each (32 heads of 128, 32 tokens: 23 us); for
 // the smallest calls latency (one sequence: 7 us alone and cold, two dependent loads, a barrier and cold instructions).
 #include <type_traits>
 
@@ -271,8 +271,8 @@ int launch_t(const LaRun& A, cudaStream_t st)
 {
     const int vec = vec4(A.x, A.xs0, A.xs1, sizeof(T)) && vec4(A.y, A.ys0, A.ys1, sizeof(T));
     // Few heads are spread over more warps of one row a lane; many take more rows a lane, so that a token's x and y
-    // serve them all.  Rows of 128 columns in all, 24 tokens, 4 rows a lane against 1: 4096 rows 21 us and 19, 8192 21 and 21, 12288 23 and 25, 32768 33 and
-    // 54; of 64 columns 8192 rows 19 and 19, 16384 21 and 29; of 256 (2 rows a lane) 4096 rows 23 and 23, 16384 38 and 56.
+    // serve them all.  Rows of 128 columns in all, 24 tokens, 4 rows a lane against 1: 4096 rows 21 us and 19, 8192 21 and 23, 12288 25 and 25, 32768 33 and
+    // 57; of 64 columns 8192 rows 20 and 19, 16384 22 and 23; of 256 (2 rows a lane) 4096 rows 27 and 27, 16384 38 and 62.
     const bool wide = (long long)A.n_seq * A.H * (A.segments ? A.segments : 1) * A.DV >= 16 * 4 * kNumSMs;
     if (A.DK <= 32) return wide ? launch_g<T, 1, 4>(A, vec, st) : launch_g<T, 1, 1>(A, vec, st);
     if (A.DK == 64) return wide ? launch_g<T, 2, 4>(A, vec, st) : launch_g<T, 2, 1>(A, vec, st);
