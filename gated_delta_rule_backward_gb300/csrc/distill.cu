@@ -13,8 +13,8 @@
 // With L = log2(e) / tau, exp((x - m) / tau) = 2^((x - m) L).  The gradient is written dense, q alone; the few
 // listed tokens are written again behind a barrier, from the numbers kept, so that each is rounded once.
 //
-// Bytes bound it, the row in and the gradient out, but 50 % of the copy rate is what it reaches with loss and gradient, 59 with the gradient alone and 40 with the loss (2048 bf16
-// rows of 128257: 317, 265 and 197 us; of 151936, which fill 58 % of eight CTAs' registers, 605, 449 and 377; 2048 fp32 rows of 50001 276, 229 and 178): a
+// Bytes bound it, the row in and the gradient out, but 50 % of the copy rate is what it reaches with loss and gradient, 62 with the gradient alone and 40 with the loss (2048 bf16
+// rows of 128257: 317, 255 and 197 us; of 151936, which fill 58 % of eight CTAs' registers, 606, 425 and 377; 2048 fp32 rows of 50001 277, 220 and 178): a
 // CTA's registers hold one row, and nothing is under way while it is summed.  For a few rows latency does.
 #include <cfloat>
 #include <cmath>
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
     const T* in = (const T*)A.logits + row * A.row_stride;
     const long long lead = (long long)(((uintptr_t)in & 15) / sizeof(T));
     const long long lo = (long long)rank * A.chunks * A.seg - lead, hi = lo + (long long)A.chunks * A.seg;  // this CTA's columns
-    if (A.ctas > 1) cluster_arrive();  // the others have started before their shared memory is written
+    if (MODE != kGradient && A.ctas > 1) cluster_arrive();  // the others have started before their shared memory is written
     begin_after();
 
     auto load = [&](Pack<T, VEC>(&x)[PACKS], int c) {
@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
             for (int o = 8; o >= 1; o >>= 1) ms = join(ms, make_float2(__shfl_xor_sync(kFull, ms.x, o), __shfl_xor_sync(kFull, ms.y, o)), A.L);
         }
         if (A.ctas > 1) {
+            if (MODE == kGradient) cluster_arrive();
             cluster_wait();
             if (warp == 0 && lane < A.ctas) st_cluster(&s_cta[rank], lane, ms);
             cluster_arrive();
@@ -178,7 +179,6 @@ __global__ void __launch_bounds__(kMostThreads, 2) distill_kernel(const DistillA
         base = base_of(ms.x);
     } else {
         __syncthreads();
-        if (A.ctas > 1) cluster_wait();
         off = lse * kLog2e;
     }
 

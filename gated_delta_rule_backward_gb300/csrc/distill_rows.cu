@@ -6,8 +6,8 @@
 // two reductions.
 //
 // Bytes bound it, the row in and the gradient out: 8192 bf16 rows of 32000, loss and gradient 201 us (78 % of the copy rate; issue slots 56 %, two
-// exponentials an element), the gradient alone 170 us (93 %; 20 more where lse is far from zero and the rows are summed again); 4096 fp32 rows of 32000, one CTA an SM, 177 us (89 %) and
-// 168 (94 %).
+// exponentials an element), the gradient alone 161 us (98 %; 28 more where lse is far from zero and the rows are summed again); 4096 fp32 rows of 32000, one CTA an SM, 177 us (89 %) and
+// 165 (96 %).
 #include "distill_internal.h"
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
@@ -71,14 +71,18 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // The gradient alone of large fp32 rows reads lse again, from L2, behind the next row's copies: its stores then come after them and not between, 16384 rows of 8000 164 us
+    // instead of 178, 4096 of 32000 164 instead of 176 (608 of them 35 instead of 32; smaller rows 101 instead of 93, 16-bit ones 177 instead of 167).
+    constexpr bool again = MODE == kGradient && sizeof(T) == 4 && PACKS >= 8;
     int next_idx = -1;
-    float next_t = -INFINITY;
+    float next_t = -INFINITY, next_lse = 0.f;
     auto list = [&](long long r) {
         next_idx = -1;
         if (tid < A.K && r < rows) {
             next_idx = A.indices[r * A.K + tid];
             next_t = ld_any(A.teacher, r * A.K + tid, A.teacher_dtype);
         }
+        if (MODE == kGradient && r < rows) next_lse = __ldcg(A.lse_in + r);
     };
     fetch(blockIdx.x);
     list(blockIdx.x);
@@ -91,8 +95,8 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
         const float t = entry ? next_t : -INFINITY;
         float xj = 0.f;
         if (entry) xj = to_f32(in[idx]);
+        const float dloss = MODE == kLoss ? 0.f : A.dloss[r], lse = next_lse;
         list(r + gridDim.x);
-        const float dloss = MODE == kLoss ? 0.f : A.dloss[r], lse = MODE == kGradient ? A.lse_in[r] : 0.f;
         const bool sums = MODE != kGradient || fabsf(lse) > kMostLse;
         // the row, from where its copies have landed; its first and last elements where 16 bytes cut them
         Pack<T, VEC> x[PACKS];
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, rows_resident(THREADS, PACKS)) distil
             if (tid == 0) A.lse[r] = !any ? 0.f : m == -INFINITY && sum == 0.f ? -INFINITY : fmaf(m, A.inv_tau, log_s);
         }
         if (sums) off = m == -INFINITY && sum == 0.f ? 0.f : log2f(sum);  // nothing but -inf: 2^-inf is 0
-        else off = lse * kLog2e;
+        else off = (again ? __ldcg(A.lse_in + r) : lse) * kLog2e;
         const float scale = dloss * A.inv_tau;
         if (MODE != kLoss) {
             // kept as stored: what the sum made of them would take twice the registers
