@@ -140,6 +140,16 @@ def _index(t, what):
     return t.data_ptr()
 
 
+def _on_device(*tensors):
+    """Refuses tensors that are not on the current device, whose addresses its kernels must not touch."""
+    at = tensors[0].get_device()
+    for t in tensors:  # a loop: any() would take half as long again
+        if t is not None and t.get_device() != at:
+            at = -1
+    if at < 0 or at != torch._C._cuda_getDevice():
+        raise ValueError("every tensor must be on the current CUDA device")
+
+
 def gdn_decode(p: DecodeParams, q, k, v, g, beta, cu_tokens, pool, slot_in, slot_out, y, stream=None):
     """Raw C-ABI call on caller-provided tensors; cu_tokens may be None."""
     if slot_in.numel() != p.n_seq or slot_out.numel() != p.n_seq or (cu_tokens is not None and cu_tokens.numel() != p.n_seq + 1):

@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import gdn
-from .decode import _allocating_on, _code, _hand_over, _index, _stream
+from .decode import _allocating_on, _code, _hand_over, _index, _on_device, _stream
 
 _lib = gdn._lib
 
@@ -63,6 +63,7 @@ def _ptr(t):
 
 def distill_forward(p: DistillParams, logits, indices, teacher, loss, lse, dloss=None, dlogits=None, stream=None):
     """Raw C-ABI call; with dloss and dlogits the gradient comes in the same call."""
+    _on_device(logits, indices, teacher, loss, lse, dloss, dlogits)
     st = _lib.distill_forward(ctypes.byref(p), logits.data_ptr(), indices.data_ptr(), teacher.data_ptr(), loss.data_ptr(), lse.data_ptr(),
                               _ptr(dloss), _ptr(dlogits), _stream(stream))
     if st != gdn.GDN_OK:
@@ -71,6 +72,7 @@ def distill_forward(p: DistillParams, logits, indices, teacher, loss, lse, dloss
 
 def distill_backward(p: DistillParams, logits, indices, teacher, lse, dloss, dlogits, stream=None):
     """Raw C-ABI call."""
+    _on_device(logits, indices, teacher, lse, dloss, dlogits)
     st = _lib.distill_backward(ctypes.byref(p), logits.data_ptr(), indices.data_ptr(), teacher.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
                                dlogits.data_ptr(), _stream(stream))
     if st != gdn.GDN_OK:

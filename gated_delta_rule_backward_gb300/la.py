@@ -12,7 +12,7 @@ import math
 import torch
 
 from . import gdn
-from .decode import _allocating_on, _code, _hand_over, _index, _rows, _stream
+from .decode import _allocating_on, _code, _hand_over, _index, _on_device, _rows, _stream
 
 _lib = gdn._lib
 
@@ -124,8 +124,10 @@ def _sequences(p, cu_tokens, *slots):
 
 def _forward(name, p, q, k, v, g, cu_tokens, pool, slot_in, slot_out, y, workspace, stream):
     cu = _sequences(p, cu_tokens, slot_in, slot_out)
+    slots = _index(slot_in, "slot_in"), _index(slot_out, "slot_out")
+    _on_device(q, k, v, g, cu_tokens, pool, slot_in, slot_out, y, workspace)
     st = getattr(_lib, name)(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), cu, pool.data_ptr(),
-                             _index(slot_in, "slot_in"), _index(slot_out, "slot_out"), y.data_ptr(), _ptr(workspace),
+                             *slots, y.data_ptr(), _ptr(workspace),
                              0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
     if st != gdn.GDN_OK:
         raise gdn.GdnError(st, name)
@@ -144,8 +146,10 @@ def selftest_wait_timeout(p: LaParams, q, k, v, g, cu_tokens, pool, slot_in, slo
 def la_backward(p: LaParams, q, k, v, g, cu_tokens, pool, slot_in, dy, dstate_T, dq, dk, dv, dg, dstate_0, workspace, stream=None):
     """Raw C-ABI call; cu_tokens, dstate_T and dstate_0 may be None."""
     cu = _sequences(p, cu_tokens, slot_in)
+    slots = _index(slot_in, "slot_in")
+    _on_device(q, k, v, g, cu_tokens, pool, slot_in, dy, dstate_T, dq, dk, dv, dg, dstate_0, workspace)
     st = _lib.la_backward(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), cu, pool.data_ptr(),
-                          _index(slot_in, "slot_in"), dy.data_ptr(), _ptr(dstate_T), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
+                          slots, dy.data_ptr(), _ptr(dstate_T), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
                           _ptr(dstate_0), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
     if st != gdn.GDN_OK:
         raise gdn.GdnError(st, "la_backward")
