@@ -32,7 +32,8 @@
  * a token's memory e^g times it, expf), so that a decay's rounding does not add up over the tokens that a state remembers; an infinite state may become NaN by it; the backward pass takes dq and dk in it always, by
  * segments whose first states the chunked form makes where it fits, and dv in the form that la_form() says.  The chunked form's products take bf16
  * inputs as they are and fp32 operands (states, weighted scores, decayed keys) as the sum of two bf16 numbers, 2^-16 relative,
- * with fp32 accumulation; its sums of log decays are exact in 64-bit fixed point (2^-31 powers of two), each exponential of a difference the
+ * with fp32 accumulation, whose sums are cut off, not rounded: a state that remembers n chunks of 128 tokens loses up to n 2^-22 of itself by it (65536 tokens 1.3e-4), where the
+ * token form rounds at random; its sums of log decays are exact in 64-bit fixed point (2^-31 powers of two), each exponential of a difference the
  * hardware's 2^x (2^-22 relative).  Outputs are rounded once.
  * dg is a running sum over the tokens that follow, anchored by <M_T, dM_T>: its error is that of the sum, not of
  * the element.  Log decays below -104 (exp = 0 in fp32) count as a = 0.  The same call gives the same bits; in the chunked form

@@ -68,3 +68,23 @@ def test_decays_gradient_of_chunked_sizes(counts, H, S):
     want = P.backward(x, counts, list(range(len(counts))), S ** -0.5)
     assert off(got[3], want[3]) <= 1e-5
     assert gdn.device_status() == 0
+
+
+@pytest.mark.parametrize("N,H,S,T", [(20, 8, 64, 16384), (1, 16, 128, 32768)])     # one segment, and several
+def test_states_of_long_prompts(N, H, S, T):
+    """Decays that stay the same have a closed form.  The keys' weights and the state are two bf16 terms: 3 2^-18 of its norm at random; and the tensor cores' sums are cut off, as include/la.h
+    says 2^-22 of the state a chunk that it remembers, counted at their weights."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *shape: torch.randn(*shape, generator=gen, device="cuda")
+    q, k, v = rnd(N * T, 1, S).bfloat16(), rnd(N * T, 1, S).bfloat16(), rnd(N * T, H, S).bfloat16()
+    g = -1.1 * 2.0 ** -torch.linspace(8, 17, H, device="cuda")
+    pool = rnd(N, H, S, S)
+    before = pool.double()
+    la.forward(q, k, v, g.expand(N * T, H), pool, i32(range(N)), y_dtype=torch.bfloat16)
+    weights = torch.exp(g.double()[:, None] * torch.arange(T - 1, -1, -1, device="cuda").double())
+    for n in (0, N - 1):
+        at = slice(n * T, (n + 1) * T)
+        want = torch.einsum("thj,ht,ti->hji", v[at].double(), weights, k[at, 0].double()) + torch.exp(g.double() * T)[:, None, None] * before[n]
+        for h in range(H):
+            assert off(pool[n, h], want[h]) <= 3 * 2.0 ** -18 + float(weights[h].sum()) / 128 * 2.0 ** -22, (n, h)
+    assert gdn.device_status() == 0
